@@ -371,6 +371,92 @@ NVFP4_API nvfp4_status_t mxfp4_gemm(const uint8_t* A, const uint8_t* sA, const u
 NVFP4_API nvfp4_status_t mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t R, int64_t C,
                                           uint32_t flags, uint64_t seed, void* y, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Ragged groups: the linear layers of a mixture of experts.  The pages give
+ * the method for one tensor; a group is such a tensor.  (READING: every
+ * group gets its own tensor scale, Eq. 1 over its rows.)
+ *
+ * T rows are sorted by group (expert): group e owns rows offsets[e] ..
+ * offsets[e+1] - 1 of x and D.  offsets is a device int32 array of E + 1
+ * values, 0 <= offsets[0] <= ... <= offsets[E] <= T; the host never reads it,
+ * so a router's output can be used without a synchronisation and inside a
+ * captured graph.  Groups may be empty and have any number of rows; rows
+ * before offsets[0] and from offsets[E] on are neither read nor written.
+ * Offsets that break the rule set NVFP4_ERR_ARG in *status (device, sticky)
+ * and every group is then treated as empty.  1 <= E <= 1024.
+ *
+ * Operand layouts.  With ceil(r / s) s written "r padded to s" and
+ * P_s(e) = the sum of the rows of groups 0 .. e-1, each padded to s:
+ *   row operand (blocks along C): codes [T, C/2], dense; scales in the GEMM
+ *     layout of an operand with nvfp4_grouped_capacity(T, E, 128) rows, row i
+ *     of group e being row P_128(e) + i there.
+ *   column operand (blocks down the rows, transposed): with
+ *     Kcap = nvfp4_grouped_capacity(T, E, 64): codes [C, Kcap/2], scales in
+ *     the GEMM layout of C rows and Kcap columns; group e takes columns
+ *     P_64(e) .. P_64(e+1) - 1, its rows padded to 64 with zeros.
+ * Bytes of these buffers that belong to no group, and the row scales of a
+ * group's padding rows, are not written and need not be.
+ * ------------------------------------------------------------------------ */
+
+/* The most rows that E groups of T rows in all can take up, each padded to a
+ * multiple of `step`: (T + min(T, E) (step - 1)) rounded down to `step`. */
+NVFP4_API int64_t nvfp4_grouped_capacity(int64_t T, int64_t E, int64_t step);
+
+/* Bytes of device workspace nvfp4_quantize_grouped needs (the groups'
+ * maxima).  Calls that may run at the same time, captured graphs among them,
+ * need one each. */
+NVFP4_API size_t nvfp4_grouped_workspace_size(int64_t E);
+
+/* Quantize the groups of the bf16 tensor x [T, C] (row stride ld).  Group e's
+ * codes, scales and alpha are those of nvfp4_quantize (same mode, seed and
+ * flags, stream id stream_id + e) on its rows alone, padded with zero rows to
+ * a multiple of 64; an empty group's alpha is 0.
+ *   flags: NVFP4_ROWWISE and / or NVFP4_COLWISE, optionally NVFP4_RHT and
+ *     NVFP4_HEADROOM; scales are always written in the GEMM layout
+ *     (NVFP4_GEMM_SCALE_LAYOUT is accepted and changes nothing).
+ *   out: codes and scales as above; alpha_row, alpha_col: E floats; amax_out:
+ *     optional, 2 E floats (rows' maxima, then columns'); status: optional.
+ * C % 64 == 0, with NVFP4_COLWISE C % 128 == 0; ld % 8 == 0; x, codes, scales
+ * and the workspace 16-byte aligned; stream_id + E <= 2^31; a NaN or Inf in
+ * any group sets NVFP4_ERR_NONFINITE. */
+NVFP4_API nvfp4_status_t nvfp4_quantize_grouped(const void* x, int64_t T, int64_t C, int64_t ld,
+                                                const int32_t* offsets, int64_t E, nvfp4_mode_t mode, uint32_t flags,
+                                                uint64_t seed, uint32_t stream_id, const nvfp4_qtensor_t* out,
+                                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Decode a grouped operand: y [T, C] (fp32, or bf16 with NVFP4_OUT_BF16),
+ * row-major and contiguous.  flags: exactly one of NVFP4_ROWWISE (row
+ * operand) and NVFP4_COLWISE (column operand, transposed back); optionally
+ * NVFP4_INVERSE_RHT (key `seed`).  alpha: E floats.  Rows of no group are
+ * left as they are. */
+NVFP4_API nvfp4_status_t nvfp4_dequantize_grouped(const uint8_t* codes, const uint8_t* scales, const float* alpha,
+                                                  int64_t T, int64_t C, const int32_t* offsets, int64_t E,
+                                                  uint32_t flags, uint64_t seed, void* y, int32_t* status,
+                                                  void* stream);
+
+/* Products of grouped rows with their group's weight (forward and data
+ * gradient of expert layers), on the tcgen05 tensor cores:
+ *     D[m, n] = alphaA[e] * alphaB[e] * sum_k (qA DeltaA)[m, k] (qB DeltaB)[e, n, k]   for m in group e
+ * A: row operand [T, K/2] with its scales; B: codes [E, N, K/2], scales in
+ * the GEMM layout of E N rows (each expert's operand as nvfp4_quantize writes
+ * it, one after the other); alphaA, alphaB: E floats each.  FP32 accumulation;
+ * D bf16 or fp32, row stride ldd; rows of no group are left as they are.
+ * N % 128 == 0, K % 64 == 0; A, sA, B, sB, D 16-byte aligned, ldd in bytes a
+ * multiple of 16.  status: optional (NVFP4_ERR_TIMEOUT, NVFP4_ERR_ARG). */
+NVFP4_API nvfp4_status_t nvfp4_gemm_grouped(const uint8_t* A, const uint8_t* sA, const float* alphaA, const uint8_t* B,
+                                            const uint8_t* sB, const float* alphaB, const int32_t* offsets, int64_t E,
+                                            int64_t T, int64_t N, int64_t K, void* D, int out_dtype, int64_t ldd,
+                                            int32_t* status, void* stream);
+
+/* Weight gradients of expert layers:
+ *     D[e, m, n] = alphaA[e] * alphaB[e] * sum_{t in group e} (qA DeltaA)[m, t] (qB DeltaB)[n, t]
+ * A, B: column operands of M and N rows over the same groups.  D: [E, M, N],
+ * contiguous; a group without rows gets zeros.  M % 128 == 0, N % 128 == 0. */
+NVFP4_API nvfp4_status_t nvfp4_gemm_grouped_wgrad(const uint8_t* A, const uint8_t* sA, const float* alphaA,
+                                                  const uint8_t* B, const uint8_t* sB, const float* alphaB,
+                                                  const int32_t* offsets, int64_t E, int64_t T, int64_t M, int64_t N,
+                                                  void* D, int out_dtype, int32_t* status, void* stream);
+
 /* Number of kernels this library has launched in the calling process since
  * it was loaded (all devices, all streams).  Instrumentation for callers that
  * account for their launches; not a page-defined operation. */

@@ -33,7 +33,9 @@ NVFP4_OUT_DTYPE_BF16 = 0
 NVFP4_OUT_DTYPE_FP32 = 1
 
 EXPORTED = ("nvfp4_workspace_size", "nvfp4_quantize", "nvfp4_quantize_noalloc", "nvfp4_amax", "nvfp4_dequantize",
-            "nvfp4_gemm", "nvfp4_gemm_vector_scales", "nvfp4_gemm_quantize", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "nvfp4_launch_count",
+            "nvfp4_gemm", "nvfp4_gemm_vector_scales", "nvfp4_gemm_quantize", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm",
+            "nvfp4_grouped_capacity", "nvfp4_grouped_workspace_size", "nvfp4_quantize_grouped",
+            "nvfp4_dequantize_grouped", "nvfp4_gemm_grouped", "nvfp4_gemm_grouped_wgrad", "nvfp4_launch_count",
             "nvfp4_status_string", "nvfp4_version")
 
 
@@ -82,6 +84,19 @@ def load(path=LIB_PATH):
     L.mxfp4_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, ctypes.c_int, i64, vp, sz, vp]
     L.mxfp4_gemm.restype = ctypes.c_int
     L.mxfp4_dequantize.restype = ctypes.c_int
+    L.nvfp4_grouped_capacity.argtypes = [i64, i64, i64]
+    L.nvfp4_grouped_capacity.restype = i64
+    L.nvfp4_grouped_workspace_size.argtypes = [i64]
+    L.nvfp4_grouped_workspace_size.restype = sz
+    L.nvfp4_quantize_grouped.argtypes = [vp, i64, i64, i64, vp, i64, ctypes.c_int, u32, u64, u32,
+                                         ctypes.POINTER(nvfp4_qtensor_t), vp, sz, vp]
+    L.nvfp4_quantize_grouped.restype = ctypes.c_int
+    L.nvfp4_dequantize_grouped.argtypes = [vp, vp, vp, i64, i64, vp, i64, u32, u64, vp, vp, vp]
+    L.nvfp4_dequantize_grouped.restype = ctypes.c_int
+    L.nvfp4_gemm_grouped.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, ctypes.c_int, i64, vp, vp]
+    L.nvfp4_gemm_grouped.restype = ctypes.c_int
+    L.nvfp4_gemm_grouped_wgrad.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, ctypes.c_int, vp, vp]
+    L.nvfp4_gemm_grouped_wgrad.restype = ctypes.c_int
     L.nvfp4_status_string.argtypes = [ctypes.c_int]
     L.nvfp4_status_string.restype = ctypes.c_char_p
     L.nvfp4_version.argtypes = []
@@ -148,6 +163,34 @@ def mxfp4_gemm(A, sA, B, sB, M, N, K, D, out_dtype, ldd, workspace, workspace_by
 
 def mxfp4_dequantize(codes, scales, R, C, flags, seed, y, stream):
     return int(load().mxfp4_dequantize(codes, scales, R, C, flags, seed, y, stream))
+
+
+def nvfp4_grouped_capacity(T, E, step):
+    return int(load().nvfp4_grouped_capacity(T, E, step))
+
+
+def nvfp4_grouped_workspace_size(E):
+    return int(load().nvfp4_grouped_workspace_size(E))
+
+
+def nvfp4_quantize_grouped(x, T, C, ld, offsets, E, mode, flags, seed, stream_id, out, workspace, workspace_bytes,
+                           stream):
+    return int(load().nvfp4_quantize_grouped(x, T, C, ld, offsets, E, mode, flags, seed, stream_id, ctypes.byref(out),
+                                             workspace, workspace_bytes, stream))
+
+
+def nvfp4_dequantize_grouped(codes, scales, alpha, T, C, offsets, E, flags, seed, y, status, stream):
+    return int(load().nvfp4_dequantize_grouped(codes, scales, alpha, T, C, offsets, E, flags, seed, y, status, stream))
+
+
+def nvfp4_gemm_grouped(A, sA, alphaA, B, sB, alphaB, offsets, E, T, N, K, D, out_dtype, ldd, status, stream):
+    return int(load().nvfp4_gemm_grouped(A, sA, alphaA, B, sB, alphaB, offsets, E, T, N, K, D, out_dtype, ldd, status,
+                                         stream))
+
+
+def nvfp4_gemm_grouped_wgrad(A, sA, alphaA, B, sB, alphaB, offsets, E, T, M, N, D, out_dtype, status, stream):
+    return int(load().nvfp4_gemm_grouped_wgrad(A, sA, alphaA, B, sB, alphaB, offsets, E, T, M, N, D, out_dtype, status,
+                                               stream))
 
 
 def nvfp4_status_string(status):

@@ -10,7 +10,7 @@ import torch
 
 from . import _lib as L
 from ._lib import (NVFP4_ALPHA_PROVIDED, NVFP4_AMAX_PROVIDED, NVFP4_BLOCK2D, NVFP4_COLWISE, NVFP4_FOUR_SIX,  # noqa: F401
-                   NVFP4_GEMM_SCALE_LAYOUT, NVFP4_INVERSE_RHT, NVFP4_MS_EDEN, NVFP4_OUT_BF16,
+                   NVFP4_GEMM_SCALE_LAYOUT, NVFP4_HEADROOM, NVFP4_INVERSE_RHT, NVFP4_MS_EDEN, NVFP4_OUT_BF16,
                    NVFP4_OUT_DTYPE_BF16, NVFP4_OUT_DTYPE_FP32, NVFP4_RHT, NVFP4_RHT_SR, NVFP4_RHT_SR_HW,
                    NVFP4_ROWWISE, NVFP4_RTN, NVFP4_SINGLE_PASS, NVFP4_VECTOR_SCALES)
 
@@ -337,4 +337,188 @@ def mxfp4_gemm(A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, sB: torch.Ten
     D = out if out is not None else torch.empty((M, N), dtype=dt, device=A.device)
     st = L.mxfp4_gemm(_p(A), _p(sA), _p(B), _p(sB), M, N, K, _p(D), out_dtype, D.stride(0), None, 0, _stream())
     _check(st, "mxfp4_gemm")
+    return D
+
+
+# ---------------------------------------------------------------------------
+# Ragged groups (the expert layers of a mixture model): rows sorted by group,
+# offsets [E + 1] on the device.
+# ---------------------------------------------------------------------------
+def _check_groups(offsets: torch.Tensor, device) -> int:
+    """Number of groups of an offsets tensor (int32 [E + 1] on `device`)."""
+    if offsets.dtype != torch.int32 or offsets.dim() != 1:
+        raise TypeError("offsets must be a 1D int32 tensor of E + 1 values")
+    if offsets.numel() < 2:
+        raise ValueError("offsets: at least two values (one group) are needed")
+    _need(offsets, 2, torch.int32, "offsets", device)
+    return offsets.numel() - 1
+
+
+def _check_status(status: Optional[torch.Tensor], device):
+    if status is not None:
+        _need(status, 1, torch.int32, "status", device)
+
+
+def _stream_of(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def grouped_alloc_outputs(T: int, C: int, E: int, flags: int, device) -> QTensor:
+    """Output buffers of nvfp4_quantize_grouped: a row operand (codes [T, C/2],
+    scales of the 128-row padded groups) and / or a column operand (codes
+    [C, Kcap/2] and scales over the 64-row padded groups), one alpha per group,
+    amax [2, E]."""
+    q = QTensor()
+    u8 = dict(dtype=torch.uint8, device=device)
+    f32 = dict(dtype=torch.float32, device=device)
+    if flags & NVFP4_ROWWISE:
+        q.codes_row = torch.empty((T, C // 2), **u8)
+        q.scales_row = torch.empty(L.nvfp4_grouped_capacity(T, E, 128) * (C // 16), **u8)
+        q.alpha_row = torch.empty(E, **f32)
+    if flags & NVFP4_COLWISE:
+        kcap = L.nvfp4_grouped_capacity(T, E, 64)
+        q.codes_col = torch.empty((C, kcap // 2), **u8)
+        q.scales_col = torch.empty(C * (kcap // 16), **u8)
+        q.alpha_col = torch.empty(E, **f32)
+    q.amax = torch.empty((2, E), **f32)
+    return q
+
+
+def grouped_check_outputs(q: QTensor, T: int, C: int, E: int, flags: int, device=None):
+    """Raise unless q's buffers can take the outputs of nvfp4_quantize_grouped."""
+    if flags & NVFP4_ROWWISE:
+        _need(q.codes_row, T * (C // 2), torch.uint8, "codes_row", device)
+        _need(q.scales_row, L.nvfp4_grouped_capacity(T, E, 128) * (C // 16), torch.uint8, "scales_row", device)
+        _need(q.alpha_row, E, torch.float32, "alpha_row", device)
+    if flags & NVFP4_COLWISE:
+        kcap = L.nvfp4_grouped_capacity(T, E, 64)
+        _need(q.codes_col, C * (kcap // 2), torch.uint8, "codes_col", device)
+        _need(q.scales_col, C * (kcap // 16), torch.uint8, "scales_col", device)
+        _need(q.alpha_col, E, torch.float32, "alpha_col", device)
+    if q.amax is not None:
+        _need(q.amax, 2 * E, torch.float32, "amax", device)
+
+
+def nvfp4_quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, mode: int, flags: int, seed: int = 0,
+                           stream_id: int = 0, out: Optional[QTensor] = None,
+                           workspace: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None) -> QTensor:
+    """Quantize rows sorted by group (x [T, C] bf16, group e: rows offsets[e]
+    .. offsets[e + 1] - 1) with one tensor scale per group: operands of
+    nvfp4_gemm_grouped (NVFP4_ROWWISE) and nvfp4_gemm_grouped_wgrad
+    (NVFP4_COLWISE).  offsets stays on the device."""
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_cuda:
+        raise TypeError("x must be a 2D bfloat16 CUDA tensor")
+    if x.numel() and x.stride(1) != 1:
+        raise ValueError("x must have unit column stride")
+    T, C = x.shape
+    E = _check_groups(offsets, x.device)
+    ld = x.stride(0) if T > 1 else C
+    _check_status(status, x.device)
+    if out is not None:
+        grouped_check_outputs(out, T, C, E, flags, x.device)
+    need = L.nvfp4_grouped_workspace_size(E)
+    if workspace is not None:
+        _need(workspace, need, torch.uint8, "workspace", x.device)
+    with torch.cuda.device(x.device):
+        q = out if out is not None else grouped_alloc_outputs(T, C, E, flags, x.device)
+        ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=x.device)
+        qt = L.nvfp4_qtensor_t(_p(q.codes_row), _p(q.scales_row), _p(q.alpha_row), _p(q.codes_col), _p(q.scales_col),
+                               _p(q.alpha_col), _p(q.amax), _p(status))
+        st = L.nvfp4_quantize_grouped(_p(x), T, C, ld, _p(offsets), E, mode, flags, seed, stream_id, qt, _p(ws),
+                                      ws.numel(), _stream_of(x.device))
+    _check(st, "nvfp4_quantize_grouped")
+    return q
+
+
+def nvfp4_dequantize_grouped(codes: torch.Tensor, scales: torch.Tensor, alpha: torch.Tensor, offsets: torch.Tensor,
+                             T: int, C: int, flags: int, seed: int = 0, out: Optional[torch.Tensor] = None,
+                             status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Decode a grouped operand (flags: NVFP4_ROWWISE or NVFP4_COLWISE, as it
+    was quantized) to [T, C] fp32, or bf16 with NVFP4_OUT_BF16.  Rows of no
+    group are left as they are in `out` (unspecified in a new tensor)."""
+    dev = codes.device
+    E = _check_groups(offsets, dev)
+    col = bool(flags & NVFP4_COLWISE)
+    cap = L.nvfp4_grouped_capacity(T, E, 64 if col else 128)
+    _need(codes, C * (cap // 2) if col else T * (C // 2), torch.uint8, "codes", dev)
+    _need(scales, cap * (C // 16), torch.uint8, "scales", dev)
+    _need(alpha, E, torch.float32, "alpha", dev)
+    _check_status(status, dev)
+    dtype = torch.bfloat16 if flags & NVFP4_OUT_BF16 else torch.float32
+    if out is not None:
+        _need(out, T * C, dtype, "out", dev)
+    with torch.cuda.device(dev):
+        y = out if out is not None else torch.empty((T, C), dtype=dtype, device=dev)
+        st = L.nvfp4_dequantize_grouped(_p(codes), _p(scales), _p(alpha), T, C, _p(offsets), E, flags, seed, _p(y),
+                                        _p(status), _stream_of(dev))
+    _check(st, "nvfp4_dequantize_grouped")
+    return y
+
+
+def nvfp4_gemm_grouped(A: torch.Tensor, sA: torch.Tensor, alphaA: torch.Tensor, B: torch.Tensor, sB: torch.Tensor,
+                       alphaB: torch.Tensor, offsets: torch.Tensor, out_dtype: int = NVFP4_OUT_DTYPE_BF16,
+                       out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """D[m] = alphaA[e] alphaB[e] A[m] B[e]^T for the rows m of each group e:
+    A codes [T, K/2] and scales as nvfp4_quantize_grouped writes them
+    (NVFP4_ROWWISE), B codes [E, N, K/2] with the experts' GEMM-layout scales
+    one after the other, one alpha per group.  Rows of no group are left as
+    they are in `out` (unspecified in a new tensor)."""
+    dev = A.device
+    if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[2]:
+        raise ValueError("A must be codes [T, K/2] and B codes [E, N, K/2]")
+    E = _check_groups(offsets, dev)
+    T, K2 = A.shape
+    N, K = B.shape[1], 2 * K2
+    if B.shape[0] != E:
+        raise ValueError(f"B holds {B.shape[0]} experts, offsets {E}")
+    _need(A, T * K2, torch.uint8, "A", dev)
+    _need(B, E * N * K2, torch.uint8, "B", dev)
+    _need(sA, L.nvfp4_grouped_capacity(T, E, 128) * (K // 16), torch.uint8, "sA", dev)
+    _need(sB, E * N * (K // 16), torch.uint8, "sB", dev)
+    _need(alphaA, E, torch.float32, "alphaA", dev)
+    _need(alphaB, E, torch.float32, "alphaB", dev)
+    _check_status(status, dev)
+    dt = torch.bfloat16 if out_dtype == NVFP4_OUT_DTYPE_BF16 else torch.float32
+    if out is not None:
+        _need_matrix(out, T, N, dt, "out", dev)
+    with torch.cuda.device(dev):
+        D = out if out is not None else torch.empty((T, N), dtype=dt, device=dev)
+        st = L.nvfp4_gemm_grouped(_p(A), _p(sA), _p(alphaA), _p(B), _p(sB), _p(alphaB), _p(offsets), E, T, N, K, _p(D),
+                                  out_dtype, D.stride(0) if T > 1 else N, _p(status), _stream_of(dev))
+    _check(st, "nvfp4_gemm_grouped")
+    return D
+
+
+def nvfp4_gemm_grouped_wgrad(A: torch.Tensor, sA: torch.Tensor, alphaA: torch.Tensor, B: torch.Tensor,
+                             sB: torch.Tensor, alphaB: torch.Tensor, offsets: torch.Tensor, T: int,
+                             out_dtype: int = NVFP4_OUT_DTYPE_FP32, out: Optional[torch.Tensor] = None,
+                             status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """D[e] = alphaA[e] alphaB[e] A_e B_e^T over the tokens of each group: A
+    codes [M, Kcap/2] (the output gradient) and B codes [N, Kcap/2] (the
+    layer's input) as nvfp4_quantize_grouped writes them (NVFP4_COLWISE) for
+    the same T rows and offsets.  Groups without rows get zeros."""
+    dev = A.device
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("A and B must be codes [M, Kcap/2] and [N, Kcap/2]")
+    E = _check_groups(offsets, dev)
+    M, N = A.shape[0], B.shape[0]
+    kcap = L.nvfp4_grouped_capacity(T, E, 64)
+    if A.shape[1] != kcap // 2 or B.shape[1] != kcap // 2:
+        raise ValueError(f"A and B must have {kcap // 2} bytes per row for T = {T}, E = {E}")
+    _need(A, M * (kcap // 2), torch.uint8, "A", dev)
+    _need(B, N * (kcap // 2), torch.uint8, "B", dev)
+    _need(sA, M * (kcap // 16), torch.uint8, "sA", dev)
+    _need(sB, N * (kcap // 16), torch.uint8, "sB", dev)
+    _need(alphaA, E, torch.float32, "alphaA", dev)
+    _need(alphaB, E, torch.float32, "alphaB", dev)
+    _check_status(status, dev)
+    dt = torch.bfloat16 if out_dtype == NVFP4_OUT_DTYPE_BF16 else torch.float32
+    if out is not None:
+        _need(out, E * M * N, dt, "out", dev)
+    with torch.cuda.device(dev):
+        D = out if out is not None else torch.empty((E, M, N), dtype=dt, device=dev)
+        st = L.nvfp4_gemm_grouped_wgrad(_p(A), _p(sA), _p(alphaA), _p(B), _p(sB), _p(alphaB), _p(offsets), E, T, M, N,
+                                        _p(D), out_dtype, _p(status), _stream_of(dev))
+    _check(st, "nvfp4_gemm_grouped_wgrad")
     return D

@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cstdint>
 
+#include "grouped.cuh"
 #include "nvfp4.h"
 #include "nvfp4_internal.h"
 
@@ -26,6 +27,13 @@ nvfp4_status_t launch_status(cudaError_t e) {
 }
 
 std::atomic<uint64_t> g_launches{0};
+
+// Checks shared by the grouped calls: group count, row count, offsets.
+nvfp4_status_t check_groups(const int32_t* offsets, int64_t E, int64_t T) {
+  if (E < 1 || E > nvfp4::kMaxGroups || T < 0 || T >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
+  if (!offsets) return NVFP4_ERR_ARG;
+  return aligned(offsets, 4) ? NVFP4_OK : NVFP4_ERR_ALIGN;
+}
 
 }  // namespace
 
@@ -264,6 +272,102 @@ nvfp4_status_t nvfp4_gemm_quantize(const uint8_t* A, const uint8_t* sA, const fl
                                                    static_cast<int>(mode), (flags & NVFP4_GEMM_SCALE_LAYOUT) != 0,
                                                    alpha_out, codes, scales, amax_out, status,
                                                    static_cast<cudaStream_t>(stream)));
+}
+
+int64_t nvfp4_grouped_capacity(int64_t T, int64_t E, int64_t step) {
+  return (T < 0 || E < 0 || step < 1) ? 0 : nvfp4::grouped_capacity(T, E, step);
+}
+
+size_t nvfp4_grouped_workspace_size(int64_t E) { return E < 0 ? 0 : nvfp4::grouped_workspace_bytes(E); }
+
+nvfp4_status_t nvfp4_quantize_grouped(const void* x, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int64_t E,
+                                      nvfp4_mode_t mode, uint32_t flags, uint64_t seed, uint32_t stream_id,
+                                      const nvfp4_qtensor_t* out, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  constexpr uint32_t allowed =
+      NVFP4_ROWWISE | NVFP4_COLWISE | NVFP4_RHT | NVFP4_HEADROOM | NVFP4_GEMM_SCALE_LAYOUT;
+  const bool row = flags & NVFP4_ROWWISE, col = flags & NVFP4_COLWISE;
+  if (!out || (flags & ~allowed) || (!row && !col)) return NVFP4_ERR_ARG;
+  if (static_cast<int>(mode) < NVFP4_RTN || static_cast<int>(mode) > NVFP4_RHT_SR_HW) return NVFP4_ERR_ARG;
+  const nvfp4_status_t chk = check_groups(offsets, E, T);
+  if (chk != NVFP4_OK) return chk;
+  if (stream_id >= 0x80000000u - static_cast<uint32_t>(E) + 1u) return NVFP4_ERR_ARG;
+  if (C <= 0 || ld < C || C % (col ? 128 : 64)) return NVFP4_ERR_SHAPE;
+  if (nvfp4::grouped_capacity(T, E, 128) * (C / 16) >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
+  if (row && (!out->alpha_row || (T && (!out->codes_row || !out->scales_row)))) return NVFP4_ERR_ARG;
+  if (col && (!out->alpha_col || (T && (!out->codes_col || !out->scales_col)))) return NVFP4_ERR_ARG;
+  if (T && !x) return NVFP4_ERR_ARG;
+  if (!aligned(x, 16) || ld % 8) return NVFP4_ERR_ALIGN;
+  if (row && (!aligned(out->codes_row, 16) || !aligned(out->scales_row, 16))) return NVFP4_ERR_ALIGN;
+  if (col && (!aligned(out->codes_col, 16) || !aligned(out->scales_col, 16))) return NVFP4_ERR_ALIGN;
+  if (!workspace || workspace_bytes < nvfp4::grouped_workspace_bytes(E) || !aligned(workspace, 16))
+    return NVFP4_ERR_WORKSPACE;
+  const nvfp4::QuantOutputs o{out->codes_row, out->scales_row, out->alpha_row, out->codes_col,
+                              out->scales_col, out->alpha_col, out->amax_out, out->status};
+  return launch_status(nvfp4::grouped_quantize_launch(x, T, C, ld, offsets, E, static_cast<int>(mode), flags, seed,
+                                                      stream_id, o, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status_t nvfp4_dequantize_grouped(const uint8_t* codes, const uint8_t* scales, const float* alpha, int64_t T,
+                                        int64_t C, const int32_t* offsets, int64_t E, uint32_t flags, uint64_t seed,
+                                        void* y, int32_t* status, void* stream) {
+  if (flags & ~(NVFP4_ROWWISE | NVFP4_COLWISE | NVFP4_INVERSE_RHT | NVFP4_OUT_BF16 | NVFP4_GEMM_SCALE_LAYOUT))
+    return NVFP4_ERR_ARG;
+  const bool row = flags & NVFP4_ROWWISE, col = flags & NVFP4_COLWISE;
+  if (row == col) return NVFP4_ERR_ARG;
+  const nvfp4_status_t chk = check_groups(offsets, E, T);
+  if (chk != NVFP4_OK) return chk;
+  if (C <= 0 || C % (col ? 128 : 64)) return NVFP4_ERR_SHAPE;
+  if (nvfp4::grouped_capacity(T, E, 128) * (C / 16) >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
+  if (T == 0) return NVFP4_OK;
+  if (!codes || !scales || !alpha || !y) return NVFP4_ERR_ARG;
+  if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(y, 16)) return NVFP4_ERR_ALIGN;
+  return launch_status(nvfp4::grouped_dequantize_launch(codes, scales, alpha, T, C, offsets, E, flags, seed, y, status,
+                                                        static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status_t nvfp4_gemm_grouped(const uint8_t* A, const uint8_t* sA, const float* alphaA, const uint8_t* B,
+                                  const uint8_t* sB, const float* alphaB, const int32_t* offsets, int64_t E, int64_t T,
+                                  int64_t N, int64_t K, void* D, int out_dtype, int64_t ldd, int32_t* status,
+                                  void* stream) {
+  if (out_dtype != NVFP4_OUT_DTYPE_BF16 && out_dtype != NVFP4_OUT_DTYPE_FP32) return NVFP4_ERR_ARG;
+  const nvfp4_status_t chk = check_groups(offsets, E, T);
+  if (chk != NVFP4_OK) return chk;
+  if (N <= 0 || K <= 0 || N % 128 || K % 64 || ldd < N) return NVFP4_ERR_SHAPE;
+  if (N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
+  // operand rows, scale atoms and tiles are counted in 32 bits
+  if (E * N >= (int64_t(1) << 31) || E * (N / 128) * (K / 64) >= (int64_t(1) << 29) ||
+      nvfp4::grouped_capacity(T, E, 128) / 128 * (K / 64) >= (int64_t(1) << 29) ||
+      nvfp4::grouped_capacity(T, E, 128) / 128 * (N / 128) >= (int64_t(1) << 29))
+    return NVFP4_ERR_SHAPE;
+  if (T == 0) return NVFP4_OK;
+  if (!A || !sA || !alphaA || !B || !sB || !alphaB || !D) return NVFP4_ERR_ARG;
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(sA, 16) || !aligned(sB, 16) || !aligned(D, 16) ||
+      !aligned(alphaA, 4) || !aligned(alphaB, 4) || (ldd * (out_dtype == NVFP4_OUT_DTYPE_BF16 ? 2 : 4)) % 16)
+    return NVFP4_ERR_ALIGN;
+  return launch_status(nvfp4::grouped_gemm_launch(A, sA, alphaA, B, sB, alphaB, offsets, E, T, N, K, D, out_dtype, ldd,
+                                                  status, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status_t nvfp4_gemm_grouped_wgrad(const uint8_t* A, const uint8_t* sA, const float* alphaA, const uint8_t* B,
+                                        const uint8_t* sB, const float* alphaB, const int32_t* offsets, int64_t E,
+                                        int64_t T, int64_t M, int64_t N, void* D, int out_dtype, int32_t* status,
+                                        void* stream) {
+  if (out_dtype != NVFP4_OUT_DTYPE_BF16 && out_dtype != NVFP4_OUT_DTYPE_FP32) return NVFP4_ERR_ARG;
+  const nvfp4_status_t chk = check_groups(offsets, E, T);
+  if (chk != NVFP4_OK) return chk;
+  if (M <= 0 || N <= 0 || M % 128 || N % 128) return NVFP4_ERR_SHAPE;
+  if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
+  const int64_t kblocks = nvfp4::grouped_capacity(T, E, 64) / 64;
+  if (E * M >= (int64_t(1) << 31) || E * (M / 128) * (N / 128) >= (int64_t(1) << 31) ||
+      (M / 128) * kblocks >= (int64_t(1) << 29) || (N / 128) * kblocks >= (int64_t(1) << 29))
+    return NVFP4_ERR_SHAPE;
+  if (!D || (T && (!A || !sA || !alphaA || !B || !sB || !alphaB))) return NVFP4_ERR_ARG;
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(sA, 16) || !aligned(sB, 16) || !aligned(D, 16) ||
+      !aligned(alphaA, 4) || !aligned(alphaB, 4))
+    return NVFP4_ERR_ALIGN;
+  return launch_status(nvfp4::grouped_wgrad_launch(A, sA, alphaA, B, sB, alphaB, offsets, E, T, M, N, D, out_dtype,
+                                                   status, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,427 @@
+// grouped_gemm.cu -- block-scaled NVFP4 products of ragged groups on the
+// sm_100a tensor cores (the expert layers of a mixture model).
+//
+//   rows grouped (forward, data gradient):
+//     D[m, n] = alphaA[e] alphaB[e] sum_k (qA DeltaA)[m, k] (qB DeltaB)[e, n, k],  m in group e
+//   contraction grouped (weight gradient):
+//     D[e, m, n] = alphaA[e] alphaB[e] sum_{t in group e} (qA DeltaA)[m, t] (qB DeltaB)[n, t]
+//
+// One persistent launch covers every group: a CTA pair (cluster of 2)
+// computes 256 x 256 tiles with tcgen05.mma.cta_group::2 as the plain GEMM
+// does, and maps a running tile index to (group, m tile, n tile) with prefix
+// sums of the device-side offsets, so the host never waits for them.
+//   * rows grouped: A's codes are dense, so a group's last tile also loads
+//     rows of the next group; the products of those rows are computed and not
+//     stored.  A's scales sit in 128-row atoms, each group starting a new one.
+//   * contraction grouped: a group's tokens are padded with zero codes to 64
+//     (one MMA's K), and only its own K blocks are multiplied.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "nvfp4_device.cuh"
+#include "gemm_ptx.cuh"
+#include "grouped.cuh"
+#include "launch.cuh"
+#include "nvfp4_internal.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int G_STAGE_AB = 128 * BK_BYTES;          // own 128 rows of one operand, 256 K
+constexpr int G_SF = KB_PER_STAGE * 512;            // scales of 128 rows, 256 K
+constexpr int G_STAGE = 2 * G_STAGE_AB + 3 * G_SF;  // A, B, own A scales, all 256 B rows' scales
+constexpr int G_EPI_WARPS = 8;
+constexpr int G_THREADS = 64 + 32 * G_EPI_WARPS;
+constexpr int G_OUT = G_EPI_WARPS * 2048;
+constexpr int G_TABLE = static_cast<int>(group_table_bytes(kMaxGroups));
+constexpr int G_STAGES = (232448 - G_OUT - 1024 - 512 - G_TABLE) / G_STAGE;
+constexpr int G_SMEM = G_STAGES * G_STAGE + G_OUT + 1024 + 512 + G_TABLE;
+constexpr uint32_t G_SF_W = 12, G_SF_COL = 256, G_TMEM_COLS = 512;
+// M = 256, N = 256, E2M1 x E2M1, E4M3 scales
+constexpr uint32_t G_IDESC = (1u << 7) | (1u << 10) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
+
+struct GroupedGemm {
+  const float* alpha_a;
+  const float* alpha_b;
+  const int32_t* offsets;
+  int E;
+  int64_t T;
+  int M, N, K;        // WGRAD: M x N outputs per group; else N x K weights, M unused
+  int katoms_a;       // scale atoms along K of A (and of B)
+  int group_m;        // m tiles per raster group
+  void* D;
+  int64_t ldd;        // rows grouped: row stride of D; WGRAD: N
+  int32_t* status;
+};
+
+// Where a tile's operands and outputs are.
+struct TileAt {
+  int e;
+  int a_row, b_row;     // first operand row (TMA y)
+  int x0;               // first byte along K (TMA x)
+  int sfa, sfb;         // first scale atom of A's and of B's 128 rows
+  int kblocks;          // K / 64
+  int row0, rows;       // first output row of D, rows that are stored
+  int col0, cols;       // first output column, columns that are stored
+};
+
+template <bool WGRAD>
+__device__ __forceinline__ TileAt locate(const GroupTable& g, const GroupedGemm& p, int tile, int n_tiles) {
+  TileAt t;
+  int tm, tn;
+  if constexpr (!WGRAD) {
+    // prefix pa counts 256-row tiles, pb 128-row scale atoms
+    t.e = find_group(g.pa, g.E, tile / n_tiles);
+    const int m_tiles = g.pa[t.e + 1] - g.pa[t.e];
+    pair_tile_coords(tile - g.pa[t.e] * n_tiles, m_tiles, n_tiles, min(p.group_m, m_tiles), tm, tn);
+    t.a_row = g.off[t.e] + 256 * tm;
+    t.b_row = t.e * p.N + 256 * tn;
+    t.x0 = 0;
+    t.sfa = (g.pb[t.e] + 2 * tm) * p.katoms_a;
+    t.sfb = (t.e * (p.N / 128) + 2 * tn) * p.katoms_a;
+    t.kblocks = p.K / 64;
+    t.row0 = t.a_row;
+    t.rows = min(256, g.rows(t.e) - 256 * tm);
+  } else {
+    // prefix pb counts 64-token K blocks
+    const int m_tiles = (p.M + 255) / 256, per = m_tiles * n_tiles;
+    t.e = tile / per;
+    pair_tile_coords(tile - t.e * per, m_tiles, n_tiles, min(p.group_m, m_tiles), tm, tn);
+    const int k0 = g.pb[t.e];
+    t.a_row = 256 * tm;
+    t.b_row = 256 * tn;
+    t.x0 = 32 * k0;
+    t.sfa = 2 * tm * p.katoms_a + k0;
+    t.sfb = 2 * tn * p.katoms_a + k0;
+    t.kblocks = g.pb[t.e + 1] - k0;
+    t.row0 = t.e * p.M + 256 * tm;
+    t.rows = min(256, p.M - 256 * tm);
+  }
+  t.col0 = 256 * tn;
+  t.cols = min(256, p.N - 256 * tn);
+  return t;
+}
+
+template <bool WGRAD, bool FP32>
+__global__ void __launch_bounds__(G_THREADS, 1)
+    nvfp4_grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                              const __grid_constant__ CUtensorMap tmap_d, const __grid_constant__ CUtensorMap tmap_sfa,
+                              const __grid_constant__ CUtensorMap tmap_sfb, const GroupedGemm p) {
+  pdl_entry();
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + G_STAGES * G_STAGE_AB;
+  uint8_t* sSFA = sB + G_STAGES * G_STAGE_AB;
+  uint8_t* sSFB = sSFA + G_STAGES * G_SF;
+  uint8_t* sOut = sSFB + G_STAGES * 2 * G_SF;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + G_OUT);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + G_STAGES;
+  uint64_t* acc_full = bars + 2 * G_STAGES;
+  uint64_t* acc_empty = bars + 2 * G_STAGES + 1;
+  uint64_t* drain = bars + 2 * G_STAGES + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * G_STAGES + 3);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* table_mem = reinterpret_cast<int*>(sOut + G_OUT + 512);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = static_cast<int>(blockIdx.x) >> 1, num_pairs = static_cast<int>(gridDim.x) >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < G_STAGES; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(acc_full), 1);
+    mbar_init(smem_u32(acc_empty), 2 * G_EPI_WARPS);
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(G_TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  const GroupTable g = build_group_table<G_THREADS>(p.offsets, p.E, p.T, WGRAD ? 64 : 256, WGRAD ? 64 : 128, table_mem,
+                                                    p.status, blockIdx.x == 0);
+  fence_before();
+  __syncwarp();
+  cluster_sync();   // barriers of both CTAs initialised, TMEM allocated
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int n_tiles = (p.N + 255) / 256;
+  const int num_tiles = WGRAD ? p.E * ((p.M + 255) / 256) * n_tiles : g.pa[p.E] * n_tiles;
+
+  if (warp == 0) {
+    // ---------------- producer (both CTAs, one elected lane) ----------------
+    if (elect_one()) {
+      int it = 0, s = 0;
+      uint32_t ph = 0;
+      bool stop = false;
+      for (int tile = pair; tile < num_tiles && !stop; tile += num_pairs) {
+        const TileAt t = locate<WGRAD>(g, p, tile, n_tiles);
+        const int kstages = (t.kblocks + KB_PER_STAGE - 1) / KB_PER_STAGE;
+        const int r = static_cast<int>(rank);
+        for (int kt = 0; kt < kstages; ++kt, ++it) {
+          if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1, abort_flag)) {
+            stop = true;
+            break;
+          }
+          const uint32_t fb = map_to_rank(smem_u32(&full[s]), 0);
+          const uint32_t dSB = smem_u32(sSFB + s * 2 * G_SF);
+          // scale atoms viewed as rows of 256 bytes (two per atom)
+          const int ysa = (t.sfa + r * p.katoms_a + KB_PER_STAGE * kt) * 2;
+          const int ysb = (t.sfb + KB_PER_STAGE * kt) * 2;
+          if (leader) mbar_expect_tx(smem_u32(&full[s]), 2 * G_STAGE);
+          tma_load_2d_pair(smem_u32(sA + s * G_STAGE_AB), &tmap_a, t.x0 + kt * BK_BYTES, t.a_row + 128 * r, fb);
+          tma_load_2d_pair(smem_u32(sB + s * G_STAGE_AB), &tmap_b, t.x0 + kt * BK_BYTES, t.b_row + 128 * r, fb);
+          tma_load_2d_pair(smem_u32(sSFA + s * G_SF), &tmap_sfa, 0, ysa, fb);
+          tma_load_2d_pair(dSB, &tmap_sfb, 0, ysb, fb);
+          tma_load_2d_pair(dSB + G_SF, &tmap_sfb, 0, ysb + 2 * p.katoms_a, fb);
+          if (++s == G_STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (*abort_flag && leader) {
+        // a wait gave up somewhere: let the copies already issued land
+        // before the CTA exits (each wait again bounded)
+        for (int i = (it > G_STAGES ? it - G_STAGES : 0); i < it; ++i)
+          mbar_wait_bounded(smem_u32(&full[i % G_STAGES]), (i / G_STAGES) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (leader CTA, one elected lane) ----------------
+    if (leader && elect_one()) {
+      int s = 0;
+      uint32_t full_ph = 0, acc_ph = 0, set = 0;
+      bool stop = false;
+      for (int tile = pair; tile < num_tiles && !stop; tile += num_pairs) {
+        const TileAt t = locate<WGRAD>(g, p, tile, n_tiles);
+        if (t.kblocks == 0) continue;   // a group without tokens: the epilogue writes zeros
+        // the epilogue must have drained the previous accumulator
+        if (!mbar_wait(smem_u32(acc_empty), acc_ph ^ 1, abort_flag)) break;
+        acc_ph ^= 1;
+        fence_after();
+        for (int kb = 0; kb < t.kblocks; kb += KB_PER_STAGE) {
+          if (!mbar_wait(smem_u32(&full[s]), full_ph, abort_flag)) {
+            stop = true;
+            break;
+          }
+          fence_after();
+          const uint32_t sfa_s = smem_u32(sSFA + s * G_SF), sfb_s = smem_u32(sSFB + s * 2 * G_SF);
+          const int nk = min(KB_PER_STAGE, t.kblocks - kb);
+          const uint64_t adesc = desc_sw128(smem_u32(sA + s * G_STAGE_AB));
+          const uint64_t bdesc = desc_sw128(smem_u32(sB + s * G_STAGE_AB));
+          for (int kk = 0; kk < nk; ++kk) {
+            // this K block's scales right before its MMA, in the slot set the
+            // previous stage did not use
+            const uint32_t col = tmem + G_SF_COL + (set + kk) * G_SF_W;
+            tmem_cp_sf_pair(col, desc_sf(sfa_s + 512 * kk));
+            tmem_cp_sf_pair(col + 4, desc_sf(sfb_s + 512 * kk));
+            tmem_cp_sf_pair(col + 8, desc_sf(sfb_s + G_SF + 512 * kk));
+            mma_mxf4nvf4_pair(tmem, adesc + 2 * kk, bdesc + 2 * kk, G_IDESC, (kb > 0 || kk > 0) ? 1u : 0u, col, col + 4);
+          }
+          set ^= KB_PER_STAGE;
+          umma_commit_pair(smem_u32(&empty[s]));
+          if (kb + KB_PER_STAGE >= t.kblocks) umma_commit_pair(smem_u32(acc_full));
+          if (++s == G_STAGES) {
+            s = 0;
+            full_ph ^= 1;
+          }
+        }
+      }
+      if (*abort_flag) {
+        // MMAs already issued may still run: let them finish (bounded) before
+        // TMEM is freed
+        umma_commit_pair(smem_u32(drain));
+        mbar_wait_bounded(smem_u32(drain), 0);
+      }
+    }
+  } else {
+    // ---------------- epilogue (warps 2..9 of both CTAs) ----------------
+    const int q = warp & 3, h = (warp - 2) >> 2;
+    uint8_t* buf = sOut + (warp - 2) * 2048;
+    const uint32_t acc_empty_leader = map_to_rank(smem_u32(acc_empty), 0);
+    uint32_t acc_ph = 0;
+    for (int tile = pair; tile < num_tiles; tile += num_pairs) {
+      const TileAt t = locate<WGRAD>(g, p, tile, n_tiles);
+      const bool zero = t.kblocks == 0;
+      if (!zero) {
+        if (!mbar_wait(smem_u32(acc_full), acc_ph, abort_flag)) break;
+        acc_ph ^= 1;
+        fence_after();
+      }
+      const float ab = zero ? 0.0f : __fmul_rn(__ldg(p.alpha_a + t.e), __ldg(p.alpha_b + t.e));
+      const int lrow = 128 * static_cast<int>(rank) + 32 * q;   // this warp's first row within the tile
+      const int row0 = t.row0 + lrow, left = t.rows - lrow;     // rows of this warp that are stored
+      const int col0 = t.col0 + 128 * h;
+      const bool store = 128 * h < t.cols && left > 0;
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * h;
+      // one 16-row x 128-byte box (w: this lane's 32 words): a whole box by
+      // TMA through the warp's staging buffer, a ragged one lane by lane
+      auto put = [&](const uint32_t* w, int col, int64_t byte_col) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (left >= 16 * half + 16) {
+            if (lane == 0) bulk_wait_read<0>();   // the previous box has been read
+            __syncwarp();
+            if ((lane >> 4) == half) {
+              uint8_t* rowp = buf + (lane & 15) * 128;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) =
+                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tmap_d, smem_u32(buf), col, row0 + 16 * half);
+              bulk_commit();
+            }
+          } else if ((lane >> 4) == half && lane < left) {
+            uint8_t* dst = static_cast<uint8_t*>(p.D) + (static_cast<int64_t>(row0) + lane) * p.ldd * (FP32 ? 4 : 2) + byte_col;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              reinterpret_cast<uint4*>(dst)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          }
+        }
+      };
+      if constexpr (!FP32) {
+        uint32_t packed[64];
+        if (zero) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) packed[j] = 0u;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 128; c += 64) {
+            uint32_t r[64];
+            tmem_ld32_nowait(taddr + c, r);
+            tmem_ld32_nowait(taddr + c + 32, r + 32);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float2 v = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])),
+                                          make_float2(ab, ab));
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(v.x, v.y);
+              packed[c / 2 + j] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
+        }
+        if (store) {
+          put(packed, col0, 2 * static_cast<int64_t>(col0));
+          put(packed + 32, col0 + 64, 2 * static_cast<int64_t>(col0 + 64));
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t r[32];
+          if (zero) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = 0u;
+          } else {
+            tmem_ld32_nowait(taddr + c, r);
+            tmem_ld_wait();
+            if (c + 32 == 128) {
+              fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__fmul_rn(__uint_as_float(r[j]), ab));
+          }
+          if (store) put(r, col0 + c, 4 * static_cast<int64_t>(col0 + c));
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  fence_before();
+  __syncwarp();
+  // neither CTA may leave (or free TMEM) while its peer can still touch its
+  // shared memory or its TMEM
+  cluster_sync();
+  if (threadIdx.x == 0 && *abort_flag && p.status) *p.status = kStatusTimeout;
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G_TMEM_COLS) : "memory");
+  }
+}
+
+template <bool WGRAD, bool FP32>
+cudaError_t launch_grouped(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md, const CUtensorMap& msa,
+                           const CUtensorMap& msb, const GroupedGemm& p, int64_t most_tiles, cudaStream_t st) {
+  auto fn = nvfp4_grouped_gemm_kernel<WGRAD, FP32>;
+  static bool done[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !done[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, G_SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev] = true;
+  }
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(most_tiles, sm_count() / 2));
+  const cudaError_t e = launch_k(fn, dim3(static_cast<unsigned>(2 * pairs)), dim3(G_THREADS), G_SMEM, st, 2u, ma, mb, md,
+                                 msa, msb, p);
+  note_launch();
+  return e;
+}
+
+// m tiles per raster group, as the plain GEMM chooses them: the group's A
+// panels and all of B within about 64 MB of L2 (k: the contraction's length)
+int raster_group(int64_t k, int64_t n_tiles) {
+  const int64_t panel = 256 * (k / 2 + k / 16);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(1 << 20, (int64_t(64) << 20) / panel - n_tiles)));
+}
+
+}  // namespace
+
+cudaError_t grouped_gemm_launch(const uint8_t* A, const uint8_t* sA, const float* alphaA, const uint8_t* B,
+                                const uint8_t* sB, const float* alphaB, const int32_t* offsets, int64_t E, int64_t T,
+                                int64_t N, int64_t K, void* D, int out_dtype, int64_t ldd, int32_t* status,
+                                cudaStream_t st) {
+  const bool fp32 = out_dtype == NVFP4_OUT_DTYPE_FP32;
+  CUtensorMap ma, mb, md, msa, msb;
+  if (!make_map(&ma, A, T, K / 2, 128) || !make_map(&mb, B, E * N, K / 2, 128) ||
+      !make_sf_map(&msa, sA, grouped_capacity(T, E, 128), K) || !make_sf_map(&msb, sB, E * N, K) ||
+      !make_out_map(&md, D, T, N, ldd, fp32))
+    return cudaErrorInvalidValue;
+  const int64_t n_tiles = (N + 255) / 256;
+  GroupedGemm p{alphaA, alphaB, offsets, static_cast<int>(E), T, 0, static_cast<int>(N), static_cast<int>(K),
+                static_cast<int>(K / 64), raster_group(K, n_tiles), D, ldd, status};
+  const int64_t most = grouped_capacity(T, E, 256) / 256 * n_tiles;
+  return fp32 ? launch_grouped<false, true>(ma, mb, md, msa, msb, p, most, st)
+              : launch_grouped<false, false>(ma, mb, md, msa, msb, p, most, st);
+}
+
+cudaError_t grouped_wgrad_launch(const uint8_t* A, const uint8_t* sA, const float* alphaA, const uint8_t* B,
+                                 const uint8_t* sB, const float* alphaB, const int32_t* offsets, int64_t E, int64_t T,
+                                 int64_t M, int64_t N, void* D, int out_dtype, int32_t* status, cudaStream_t st) {
+  const bool fp32 = out_dtype == NVFP4_OUT_DTYPE_FP32;
+  const int64_t kcap = grouped_capacity(T, E, 64);
+  if (kcap == 0) return cudaMemsetAsync(D, 0, static_cast<size_t>(E * M * N) * (fp32 ? 4 : 2), st);   // no token at all
+  CUtensorMap ma, mb, md, msa, msb;
+  if (!make_map(&ma, A, M, kcap / 2, 128) || !make_map(&mb, B, N, kcap / 2, 128) || !make_sf_map(&msa, sA, M, kcap) ||
+      !make_sf_map(&msb, sB, N, kcap) || !make_out_map(&md, D, E * M, N, N, fp32))
+    return cudaErrorInvalidValue;
+  const int64_t n_tiles = (N + 255) / 256, m_tiles = (M + 255) / 256;
+  GroupedGemm p{alphaA, alphaB, offsets, static_cast<int>(E), T, static_cast<int>(M), static_cast<int>(N), 0,
+                static_cast<int>(kcap / 64), raster_group(std::max<int64_t>(64, T / E), n_tiles), D, N, status};
+  const int64_t most = E * m_tiles * n_tiles;
+  return fp32 ? launch_grouped<true, true>(ma, mb, md, msa, msb, p, most, st)
+              : launch_grouped<true, false>(ma, mb, md, msa, msb, p, most, st);
+}
+
+}  // namespace nvfp4

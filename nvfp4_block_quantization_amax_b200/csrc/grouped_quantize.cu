@@ -1,0 +1,613 @@
+// grouped_quantize.cu -- NVFP4 quantization of rows sorted by group (the
+// tokens of each expert of a mixture layer), and its inverse.
+//
+// Every group is a tensor of its own (Four Over Six §2.1 Eq. 1-3 per group):
+// alpha_e from the group's amax, blocks of 16 along the rows' elements and /
+// or down the group's rows.  Group e gets exactly the codes and scales that
+// nvfp4_quantize writes for its rows alone, padded with zero rows to a
+// multiple of 64, with stream id stream_id + e.
+//
+// Two launches, as for one tensor: an amax pass folds each tile's maximum
+// into its group's word, then the tiles are encoded.  Both walk 64 x 128
+// tiles of the groups' own row frames, a contiguous run per CTA, so the
+// group changes rarely within a CTA.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <algorithm>
+#include <cstdint>
+
+#include "nvfp4_device.cuh"
+#include "block_modes.cuh"
+#include "grouped.cuh"
+#include "launch.cuh"
+#include "nvfp4_internal.h"
+#include "tile.cuh"
+
+namespace nvfp4 {
+namespace {
+
+struct GroupedArgs {
+  const uint16_t* x;
+  int64_t T, C, ld;
+  const int32_t* offsets;
+  int E;
+  uint64_t seed;
+  uint32_t stream_id, flags;
+  uint32_t* amax_r;      // [E] float bits (or kNonFinite)
+  uint32_t* amax_c;      // [E] (== amax_r when not rotated)
+  uint8_t* codes_row;
+  uint8_t* scales_row;
+  float* alpha_row;
+  uint8_t* codes_col;
+  uint8_t* scales_col;
+  float* alpha_col;
+  float* amax_out;       // [2, E] or null
+  int32_t* status;
+  uint32_t tiles_c;
+  int64_t kcap;          // columns of codes_col in elements (a multiple of 64)
+};
+
+__device__ __forceinline__ void cp_async16_or_zero(void* smem, const void* gmem, bool valid) {
+  const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  const int bytes = valid ? 16 : 0;   // 0: nothing is read, the 16 bytes become zero
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(gmem), "r"(bytes) : "memory");
+}
+
+// One 64 x 128 tile of a group whose first row is x (rows x C valid): chunks
+// outside it become zeros, so that a block that the group's end cuts holds
+// the zero rows of its padding.
+template <int NT>
+__device__ __forceinline__ void load_group_tile(uint4 (*buf)[TC / 8], const uint16_t* x, int rows, int64_t C,
+                                                int64_t ld, int tr, uint32_t tc) {
+  constexpr int kRowStep = NT / 16, kPasses = TR / kRowStep;
+  const int row0 = static_cast<int>(threadIdx.x) >> 4, cc = static_cast<int>(threadIdx.x) & 15;
+  const int64_t c0 = static_cast<int64_t>(tc) * TC + 8 * cc;
+  const int left = rows - tr * TR;
+  const uint16_t* src = x + (static_cast<int64_t>(tr) * TR + row0) * ld + c0;
+  const bool col_ok = c0 < C;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int row = row0 + kRowStep * i;
+    const bool ok = col_ok && row < left;
+    cp_async16_or_zero(&buf[row][tile_chunk(row, cc)], ok ? src + static_cast<int64_t>(kRowStep * i) * ld : x, ok);
+  }
+  cp_async_commit();
+}
+
+// A CTA's run of tiles: [first, last) of the total, the runs differing by at
+// most one tile.
+struct TileRun {
+  uint32_t tile, end;
+  __device__ __forceinline__ TileRun(uint32_t total, uint32_t cta, uint32_t ncta) {
+    tile = static_cast<uint32_t>(static_cast<uint64_t>(total) * cta / ncta);
+    end = static_cast<uint32_t>(static_cast<uint64_t>(total) * (cta + 1) / ncta);
+  }
+};
+
+// Tile -> (group, tile row within the group, tile column).
+struct GroupTile {
+  int e, tr;
+  uint32_t tc;
+};
+__device__ __forceinline__ GroupTile group_tile(const GroupTable& g, uint32_t tile, uint32_t tiles_c) {
+  const uint32_t u = tile / tiles_c;
+  const int e = find_group(g.pa, g.E, static_cast<int>(u));
+  return GroupTile{e, static_cast<int>(u) - g.pa[e], tile - u * tiles_c};
+}
+__device__ __forceinline__ void next_tile(const GroupTable& g, GroupTile& t, uint32_t tiles_c) {
+  if (++t.tc < tiles_c) return;
+  t.tc = 0;
+  ++t.tr;
+  while (t.e + 1 < g.E && g.pa[t.e] + t.tr >= g.pa[t.e + 1]) {   // past this group's last tile row
+    ++t.e;
+    t.tr = 0;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// amax per group
+// ---------------------------------------------------------------------------
+// Fold the CTA's running maximum (float bits) into a group's word.
+template <int NT>
+__device__ __forceinline__ void flush_max(uint32_t m, uint32_t* dst, uint32_t* red, int32_t* status) {
+  m = block_max_u32<NT>(m, red);
+  if (threadIdx.x == 0 && m) {
+    atomicMax(dst, m);   // the order of a maximum does not matter
+    if (m == kNonFinite && status) *status = kStatusNonFinite;
+  }
+}
+
+constexpr int kPlainNT = 256;
+
+__global__ void __launch_bounds__(kPlainNT) grouped_amax_plain_kernel(const GroupedArgs a) {
+  pdl_entry();
+  extern __shared__ int table_mem[];
+  __shared__ uint32_t red[kPlainNT / 32];
+  const GroupTable g = build_group_table<kPlainNT>(a.offsets, a.E, a.T, TR, 128, table_mem, a.status, blockIdx.x == 0);
+  TileRun run(static_cast<uint32_t>(g.pa[a.E]) * a.tiles_c, blockIdx.x, gridDim.x);
+  if (run.tile >= run.end) return;
+  GroupTile t = group_tile(g, run.tile, a.tiles_c);
+  int e = t.e;
+  uint32_t hm = 0;
+  auto flush = [&]() {
+    const uint32_t h = max(hm & 0xFFFFu, hm >> 16);
+    flush_max<kPlainNT>(h >= 0x7F80u ? kNonFinite : (h << 16), a.amax_r + e, red, a.status);
+    hm = 0;
+  };
+  for (; run.tile < run.end; ++run.tile, next_tile(g, t, a.tiles_c)) {
+    if (t.e != e) {   // uniform over the CTA
+      flush();
+      e = t.e;
+    }
+    const int left = g.rows(t.e) - t.tr * TR;
+    const int row0 = static_cast<int>(threadIdx.x) >> 4, cc = static_cast<int>(threadIdx.x) & 15;
+    const int64_t c0 = static_cast<int64_t>(t.tc) * TC + 8 * cc;
+    const uint16_t* src = a.x + (static_cast<int64_t>(g.off[t.e]) + t.tr * TR + row0) * a.ld + c0;
+    uint4 u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (c0 < a.C && row0 + 16 * i < left)
+        u[i] = __ldg(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(16 * i) * a.ld));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hm = __vmaxu2(hm, u[i].x & 0x7FFF7FFFu);
+      hm = __vmaxu2(hm, u[i].y & 0x7FFF7FFFu);
+      hm = __vmaxu2(hm, u[i].z & 0x7FFF7FFFu);
+      hm = __vmaxu2(hm, u[i].w & 0x7FFF7FFFu);
+    }
+  }
+  flush();
+}
+
+// Rotated maxima, rows and / or columns.  The transform's final 1/4 commutes
+// with the maximum and is applied at the end.
+template <bool ROW, bool COL>
+__global__ void __launch_bounds__(TNT) grouped_amax_rot_kernel(const GroupedArgs a) {
+  pdl_entry();
+  extern __shared__ int table_mem[];
+  __shared__ __align__(16) uint4 tiles[2][TR][TC / 8];
+  __shared__ uint32_t red[TNT / 32];
+  const GroupTable g = build_group_table<TNT>(a.offsets, a.E, a.T, TR, 128, table_mem, a.status, blockIdx.x == 0);
+  TileRun run(static_cast<uint32_t>(g.pa[a.E]) * a.tiles_c, blockIdx.x, gridDim.x);
+  if (run.tile >= run.end) return;
+  const SignMasks sm = sign_masks(sign_bits(philox_keys(a.seed)));
+  GroupTile t = group_tile(g, run.tile, a.tiles_c), ahead = t;
+  auto load = [&](int b) {
+    load_group_tile<TNT>(tiles[b], a.x + static_cast<int64_t>(g.off[ahead.e]) * a.ld, g.rows(ahead.e), a.C, a.ld,
+                         ahead.tr, ahead.tc);
+    next_tile(g, ahead, a.tiles_c);
+  };
+  load(0);
+  int e = t.e, buf = 0;
+  float mr = 0.0f, mc = 0.0f;
+  uint32_t hm = 0;
+  auto flush = [&]() {
+    const bool inf = max(hm & 0xFFFFu, hm >> 16) >= 0x7F80u;
+    if constexpr (ROW)
+      flush_max<TNT>(inf ? kNonFinite : __float_as_uint(__fmul_rn(mr, 0.25f)), a.amax_r + e, red, a.status);
+    if constexpr (COL)
+      flush_max<TNT>(inf ? kNonFinite : __float_as_uint(__fmul_rn(mc, 0.25f)), a.amax_c + e, red, a.status);
+    mr = mc = 0.0f;
+    hm = 0;
+  };
+  const int th = threadIdx.x;
+  for (; run.tile < run.end; ++run.tile, next_tile(g, t, a.tiles_c), buf ^= 1) {
+    if (t.e != e) {
+      flush();
+      e = t.e;
+    }
+    if (run.tile + 1 < run.end) load(buf ^ 1);
+    else cp_async_commit();
+    cp_async_wait<1>();
+    __syncthreads();
+    const uint4 (*s)[TC / 8] = tiles[buf];
+    if constexpr (ROW) {
+      const int row = th >> 3, cb = th & 7;
+      const uint4 a0 = s[row][tile_chunk(row, 2 * cb)], a1 = s[row][tile_chunk(row, 2 * cb + 1)];
+      const uint4 b0 = s[row + 32][tile_chunk(row + 32, 2 * cb)], b1 = s[row + 32][tile_chunk(row + 32, 2 * cb + 1)];
+      const uint32_t w[16] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w,
+                              b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+      for (int i = 0; i < 16; ++i) hm = __vmaxu2(hm, w[i] & 0x7FFF7FFFu);
+      float2 v[16];
+      unpack16x2_signed(a0, a1, b0, b1, sm, v);
+      hadamard16x2(v);
+      float ma, mb;
+      max_abs16x2(v, ma, mb);
+      mr = max3(mr, ma, mb);
+    }
+    if constexpr (COL) {
+      const int cp = th >> 2, rb = th & 3;
+      const uint32_t* base = reinterpret_cast<const uint32_t*>(&s[16 * rb][0]);
+      const int wofs = tile_word(16 * rb, cp);
+      float2 v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t w = base[i * (TC / 2) + wofs];
+        if constexpr (!ROW) hm = __vmaxu2(hm, w & 0x7FFF7FFFu);
+        v[i] = make_float2(bf16lo_flip(w, sm.m[i]), bf16hi_flip(w, sm.m[i]));
+      }
+      hadamard16x2(v);
+      float ma, mb;
+      max_abs16x2(v, ma, mb);
+      mc = max3(mc, ma, mb);
+    }
+    __syncthreads();   // the buffer is refilled two iterations on
+  }
+  cp_async_wait<0>();
+  flush();
+}
+
+// ---------------------------------------------------------------------------
+// encode
+// ---------------------------------------------------------------------------
+struct GroupStaging {
+  uint8_t colcodes[TC][48];        // transposed codes of one tile (32 bytes used per column)
+  uint8_t colscale[TC][TR / 16];
+  uint4 words[TNT / 32][32];       // scale-SR words shared by a warp (MS-EDEN)
+  float2 tab_r[kScaleTab];
+  float2 tab_c[kScaleTab];
+};
+
+__device__ __forceinline__ float group_alpha(const GroupedArgs& a, const uint32_t* amax, int e) {
+  const uint32_t m = __ldcg(amax + e);
+  return __fdiv_rn(m == kNonFinite ? 0.0f : __uint_as_float(m), (a.flags & kHeadroom) ? 1792.0f : 2688.0f);
+}
+
+template <int MODE, bool ROT, bool ROW, bool COL>
+__global__ void __launch_bounds__(TNT, 3) grouped_quantize_kernel(const GroupedArgs a) {
+  pdl_entry();
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ __align__(16) GroupStaging stg;
+  auto tiles = reinterpret_cast<uint4(*)[TR][TC / 8]>(dyn);
+  int* table_mem = reinterpret_cast<int*>(dyn + 2 * TR * TC * 2);
+  const GroupTable g = build_group_table<TNT>(a.offsets, a.E, a.T, TR, 128, table_mem, a.status, blockIdx.x == 0);
+  const int th = threadIdx.x;
+  if (blockIdx.x == 0) {
+    for (int e = th; e < a.E; e += TNT) {
+      if constexpr (ROW) a.alpha_row[e] = group_alpha(a, a.amax_r, e);
+      if constexpr (COL) a.alpha_col[e] = group_alpha(a, a.amax_c, e);
+      if (a.amax_out) {
+        const uint32_t r = __ldcg(a.amax_r + e), c = __ldcg(a.amax_c + e);
+        if constexpr (ROW) a.amax_out[e] = r == kNonFinite ? 0.0f : __uint_as_float(r);
+        if constexpr (COL) a.amax_out[a.E + e] = c == kNonFinite ? 0.0f : __uint_as_float(c);
+      }
+    }
+  }
+  TileRun run(static_cast<uint32_t>(g.pa[a.E]) * a.tiles_c, blockIdx.x, gridDim.x);
+  if (run.tile >= run.end) return;
+
+  const PhiloxKeys K = philox_keys(a.seed);
+  SignMasks sm;
+  if constexpr (ROT) {
+    sm = sign_masks(sign_bits(K));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sm.m[i] = 0u;
+  }
+  const int64_t nbr = a.C / 16;
+  const int trow = th >> 3, tcb = th & 7, tcp = th >> 2, trb = th & 3, lane = th & 31, j4 = th & 3;
+
+  GroupTile t = group_tile(g, run.tile, a.tiles_c), ahead = t;
+  auto load = [&](int b) {
+    load_group_tile<TNT>(tiles[b], a.x + static_cast<int64_t>(g.off[ahead.e]) * a.ld, g.rows(ahead.e), a.C, a.ld,
+                         ahead.tr, ahead.tc);
+    next_tile(g, ahead, a.tiles_c);
+  };
+  load(0);
+  int e = -1, buf = 0;
+  TabScales scr{}, scc{};
+  for (; run.tile < run.end; ++run.tile, next_tile(g, t, a.tiles_c), buf ^= 1) {
+    if (run.tile + 1 < run.end) load(buf ^ 1);
+    else cp_async_commit();
+    if (t.e != e) {   // the scale tables of this group; the barrier below publishes them
+      e = t.e;
+      if constexpr (ROW) {
+        const float al = group_alpha(a, a.amax_r, e);
+        build_scale_tab<TNT>(stg.tab_r, al);
+        scr = make_scale_ctx(stg.tab_r, al);
+      }
+      if constexpr (COL) {
+        const float al = group_alpha(a, a.amax_c, e);
+        build_scale_tab<TNT>(stg.tab_c, al);
+        scc = make_scale_ctx(stg.tab_c, al);
+      }
+    }
+    cp_async_wait<1>();
+    __syncthreads();
+    const uint4 (*s)[TC / 8] = tiles[buf];
+    const int left = g.rows(e) - t.tr * TR;
+    const int rows = left < TR ? left : TR;
+    const int64_t c0 = static_cast<int64_t>(t.tc) * TC;
+    const int cols = static_cast<int>(a.C - c0 < TC ? a.C - c0 : TC);
+    const uint32_t c2r = (a.stream_id + static_cast<uint32_t>(e)) * 2u, c2c = c2r + 1u;
+    // blocks down the rows, in the group's own frame padded to 64 rows
+    const int64_t nbc = static_cast<int64_t>(g.pa[e + 1] - g.pa[e]) * (TR / 16);
+    const int64_t rblk = (static_cast<int64_t>(t.tr) * TR + trow) * nbr + c0 / 16 + tcb;
+    const int64_t cblk = (c0 + 2 * tcp) * nbc + t.tr * (TR / 16) + trb;
+
+    // MS-EDEN: lanes 4k .. 4k + 3 hold blocks of the same two row units and
+    // two column units (C and the padded rows are multiples of 64); each
+    // draws one unit's four words and they are exchanged in shared memory.
+    uint32_t w_ra = 0, w_rb = 0, w_ca = 0, w_cb = 0;
+    if constexpr (MODE == kModeMsEden) {
+      const int64_t unit_r = rblk - (tcb & 3) + (j4 & 1) * 32 * nbr;
+      const int64_t unit_c = (c0 + 2 * tcp + (j4 & 1)) * nbc + t.tr * (TR / 16);
+      const uint64_t unit = static_cast<uint64_t>(j4 < 2 ? unit_r : unit_c) >> 2;
+      uint4* xs = stg.words[th >> 5];
+      xs[lane] = philox(K, static_cast<uint32_t>(unit), static_cast<uint32_t>(unit >> 32), j4 < 2 ? c2r : c2c, kTagScaleSR);
+      __syncwarp();
+      const uint32_t* xw = reinterpret_cast<const uint32_t*>(xs + (lane & ~3)) + j4;
+      w_ra = xw[0];
+      w_rb = xw[4];
+      w_ca = xw[8];
+      w_cb = xw[12];
+      __syncwarp();
+    }
+
+    if constexpr (ROW) {
+      const int row = trow, cb = tcb;
+      const bool va = row < rows && 16 * cb < cols, vb = row + 32 < rows && 16 * cb < cols;
+      if (va || vb) {
+        const uint4 a0 = s[row][tile_chunk(row, 2 * cb)], a1 = s[row][tile_chunk(row, 2 * cb + 1)];
+        const uint4 b0 = s[row + 32][tile_chunk(row + 32, 2 * cb)];
+        const uint4 b1 = s[row + 32][tile_chunk(row + 32, 2 * cb + 1)];
+        float2 v[16];
+        unpack16x2_signed(a0, a1, b0, b1, sm, v);
+        if constexpr (ROT) rht16x2_presigned(v);
+        Packed16 pa, pb;
+        uint32_t sa, sb;
+        quantize_pair<MODE>(v, scr, K, c2r, static_cast<uint64_t>(rblk), static_cast<uint64_t>(rblk + 32 * nbr), pa, pb,
+                            sa, sb, MODE == kModeMsEden, w_ra, w_rb);
+        uint8_t* crow = a.codes_row + (static_cast<int64_t>(g.off[e]) + t.tr * TR + row) * (a.C / 2) + c0 / 2 + 8 * cb;
+        if (va) *reinterpret_cast<uint2*>(crow) = make_uint2(pa.lo, pa.hi);
+        if (vb) *reinterpret_cast<uint2*>(crow + 32 * (a.C / 2)) = make_uint2(pb.lo, pb.hi);
+        uint8_t* srow = a.scales_row + gemm_scale_tile_row(2 * static_cast<int64_t>(g.pb[e]) + t.tr, t.tc, nbr) +
+                        gemm_scale_thread_row(row, cb);
+        if (va) srow[0] = static_cast<uint8_t>(sa);
+        if (vb) srow[4] = static_cast<uint8_t>(sb);
+      }
+    }
+    if constexpr (COL) {
+      {
+        const uint32_t* base = reinterpret_cast<const uint32_t*>(&s[16 * trb][0]);
+        const int wofs = tile_word(16 * trb, tcp);
+        float2 v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t w = base[i * (TC / 2) + wofs];
+          v[i] = make_float2(bf16lo_flip(w, sm.m[i]), bf16hi_flip(w, sm.m[i]));
+        }
+        if constexpr (ROT) rht16x2_presigned(v);
+        Packed16 qa, qb;
+        uint32_t sa, sb;
+        quantize_pair<MODE>(v, scc, K, c2c, static_cast<uint64_t>(cblk), static_cast<uint64_t>(cblk + nbc), qa, qb, sa,
+                            sb, MODE == kModeMsEden, w_ca, w_cb);
+        *reinterpret_cast<uint2*>(&stg.colcodes[2 * tcp][8 * trb]) = make_uint2(qa.lo, qa.hi);
+        *reinterpret_cast<uint2*>(&stg.colcodes[2 * tcp + 1][8 * trb]) = make_uint2(qb.lo, qb.hi);
+        stg.colscale[2 * tcp][trb] = static_cast<uint8_t>(sa);
+        stg.colscale[2 * tcp + 1][trb] = static_cast<uint8_t>(sb);
+      }
+      __syncthreads();
+      // 16 code bytes of column th / 2 and column th's four scales: whole
+      // tiles of the padded frame (C % 128 == 0 with columns)
+      const int64_t kt = g.pa[e] + t.tr;   // 64-row tile of the padded frame
+      const int c = th >> 1, h = th & 1;
+      *reinterpret_cast<uint4*>(a.codes_col + (c0 + c) * (a.kcap / 2) + 32 * kt + 16 * h) =
+          *reinterpret_cast<const uint4*>(&stg.colcodes[c][16 * h]);
+      if (th < TC)
+        *reinterpret_cast<uint32_t*>(a.scales_col + gemm_scale_tile_col(kt, t.tc, a.kcap / 16) +
+                                     gemm_scale_thread_col(th)) = *reinterpret_cast<const uint32_t*>(&stg.colscale[th][0]);
+    }
+    __syncthreads();   // the tile buffer, the staging and the tables are free again
+  }
+  cp_async_wait<0>();
+}
+
+// ---------------------------------------------------------------------------
+// decode
+// ---------------------------------------------------------------------------
+// 64 x 64 tiles of a group: a thread decodes one block of 16 (a row's or a
+// column's), the values pass through shared memory so that rows are written
+// in 16-byte pieces.
+template <bool INV, bool BF16, bool COL>
+__global__ void __launch_bounds__(256) grouped_dequantize_kernel(const uint8_t* __restrict__ codes,
+                                                                 const uint8_t* __restrict__ scales,
+                                                                 const float* __restrict__ alpha, int64_t T, int64_t C,
+                                                                 const int32_t* __restrict__ offsets, int E,
+                                                                 int64_t kcap, uint64_t seed, void* __restrict__ y,
+                                                                 int32_t* status) {
+  pdl_entry();
+  extern __shared__ int table_mem[];
+  __shared__ __align__(16) float vals[64][68];
+  const GroupTable g = build_group_table<256>(offsets, E, T, TR, 128, table_mem, status, blockIdx.x == 0);
+  const uint32_t tiles_c = static_cast<uint32_t>(C / 64);
+  TileRun run(static_cast<uint32_t>(g.pa[E]) * tiles_c, blockIdx.x, gridDim.x);
+  if (run.tile >= run.end) return;
+  uint32_t signs = 0;
+  if constexpr (INV) signs = sign_bits(philox_keys(seed));
+  GroupTile t = group_tile(g, run.tile, tiles_c);
+  const int th = threadIdx.x;
+  for (; run.tile < run.end; ++run.tile, next_tile(g, t, tiles_c)) {
+    const int left = g.rows(t.e) - t.tr * TR;
+    const int rows = left < TR ? left : TR;
+    const int64_t c0 = static_cast<int64_t>(t.tc) * 64;
+    const int i = th >> 2, b = th & 3;   // row (COL: column) i of the tile, its block b
+    if (COL || i < rows) {
+      uint2 p;
+      uint32_t sb;
+      if constexpr (COL) {
+        const int64_t kt = g.pa[t.e] + t.tr;
+        p = __ldg(reinterpret_cast<const uint2*>(codes + (c0 + i) * (kcap / 2) + 32 * kt + 8 * b));
+        sb = __ldg(scales + gemm_scale_offset(c0 + i, 4 * kt + b, kcap / 16));
+      } else {
+        const int64_t r = static_cast<int64_t>(t.tr) * TR + i;
+        p = __ldg(reinterpret_cast<const uint2*>(codes + (g.off[t.e] + r) * (C / 2) + c0 / 2 + 8 * b));
+        sb = __ldg(scales + gemm_scale_offset(128 * static_cast<int64_t>(g.pb[t.e]) + r, c0 / 16 + b, C / 16));
+      }
+      const float s = __fmul_rn(__ldg(alpha + t.e), e4m3_value(sb));
+      float v[16];
+      e2m1x8_values(p.x, v);
+      e2m1x8_values(p.y, v + 8);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], s);
+      if constexpr (INV) irht16(v, signs);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if constexpr (COL) vals[16 * b + j][i] = v[j];
+        else vals[i][16 * b + j] = v[j];
+      }
+    }
+    __syncthreads();
+    const int64_t row0 = static_cast<int64_t>(g.off[t.e]) + t.tr * TR;
+    if (i < rows) {   // 16 values of row i
+      const float* src = &vals[i][16 * b];
+      const int64_t off = (row0 + i) * C + c0 + 16 * b;
+      if constexpr (BF16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(src[2 * j], src[2 * j + 1]);
+          w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + off);
+        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(y) + off);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dst[j] = make_float4(src[4 * j], src[4 * j + 1], src[4 * j + 2], src[4 * j + 3]);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// Persistent grid: enough CTAs for every tile that T rows in E groups can
+// make, at most `per_sm` on each SM.
+int grid_for(int64_t T, int64_t E, int64_t tiles_c, int per_sm) {
+  const int64_t most = grouped_capacity(T, E, TR) / TR * tiles_c;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, static_cast<int64_t>(sm_count()) * per_sm)));
+}
+
+// Once per kernel and device: raise the dynamic shared memory limit.
+template <class F>
+cudaError_t allow_smem(F fn, int bytes, bool* done) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
+
+template <int MODE, bool ROT, bool ROW, bool COL>
+cudaError_t launch_encode(const GroupedArgs& a, cudaStream_t st) {
+  auto fn = grouped_quantize_kernel<MODE, ROT, ROW, COL>;
+  static bool done[64] = {false};
+  constexpr int ring = 2 * TR * TC * 2;
+  cudaError_t e = allow_smem(fn, ring + static_cast<int>(group_table_bytes(kMaxGroups)), done);
+  if (e != cudaSuccess) return e;
+  e = launch_k(fn, dim3(grid_for(a.T, a.E, a.tiles_c, 3)), dim3(TNT), ring + group_table_bytes(a.E), st, 1u, a);
+  note_launch();
+  return e;
+}
+
+template <int MODE, bool ROT>
+cudaError_t dispatch_encode(const GroupedArgs& a, bool row, bool col, cudaStream_t st) {
+  if (row && col) return launch_encode<MODE, ROT, true, true>(a, st);
+  return row ? launch_encode<MODE, ROT, true, false>(a, st) : launch_encode<MODE, ROT, false, true>(a, st);
+}
+
+cudaError_t launch_group_amax(const GroupedArgs& a, bool row, bool col, bool rot, cudaStream_t st) {
+  const size_t tab = group_table_bytes(a.E);
+  cudaError_t e;
+  if (!rot) e = launch_k(grouped_amax_plain_kernel, dim3(grid_for(a.T, a.E, a.tiles_c, 8)), dim3(kPlainNT), tab, st, 1u, a);
+  else {
+    const dim3 grid(grid_for(a.T, a.E, a.tiles_c, 4));
+    if (row && col) e = launch_k(grouped_amax_rot_kernel<true, true>, grid, dim3(TNT), tab, st, 1u, a);
+    else if (row) e = launch_k(grouped_amax_rot_kernel<true, false>, grid, dim3(TNT), tab, st, 1u, a);
+    else e = launch_k(grouped_amax_rot_kernel<false, true>, grid, dim3(TNT), tab, st, 1u, a);
+  }
+  note_launch();
+  return e;
+}
+
+template <bool INV, bool BF16>
+cudaError_t launch_decode(const uint8_t* codes, const uint8_t* scales, const float* alpha, int64_t T, int64_t C,
+                          const int32_t* offsets, int E, bool col, uint64_t seed, void* y, int32_t* status,
+                          cudaStream_t st) {
+  const int64_t kcap = grouped_capacity(T, E, 64);
+  const dim3 grid(grid_for(T, E, C / 64, 8));
+  const size_t tab = group_table_bytes(E);
+  const cudaError_t e =
+      col ? launch_k(grouped_dequantize_kernel<INV, BF16, true>, grid, dim3(256), tab, st, 1u, codes, scales, alpha, T, C,
+                     offsets, E, kcap, seed, y, status)
+          : launch_k(grouped_dequantize_kernel<INV, BF16, false>, grid, dim3(256), tab, st, 1u, codes, scales, alpha, T, C,
+                     offsets, E, kcap, seed, y, status);
+  note_launch();
+  return e;
+}
+
+}  // namespace
+
+size_t grouped_workspace_bytes(int64_t E) { return static_cast<size_t>(2 * E) * sizeof(uint32_t); }
+
+cudaError_t grouped_quantize_launch(const void* x, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int64_t E,
+                                    int mode, uint32_t flags, uint64_t seed, uint32_t stream_id, const QuantOutputs& o,
+                                    void* workspace, cudaStream_t st) {
+  const bool row = flags & kRowwise, col = flags & kColwise;
+  const bool rot = mode == kModeRhtSR || mode == kModeMsEden || mode == kModeRhtSRHw || (flags & kRht);
+  GroupedArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.T = T;
+  a.C = C;
+  a.ld = ld;
+  a.offsets = offsets;
+  a.E = static_cast<int>(E);
+  a.seed = seed;
+  a.stream_id = stream_id;
+  a.flags = flags;
+  a.amax_r = static_cast<uint32_t*>(workspace);
+  a.amax_c = rot ? a.amax_r + E : a.amax_r;
+  a.codes_row = o.codes_row;
+  a.scales_row = o.scales_row;
+  a.alpha_row = o.alpha_row;
+  a.codes_col = o.codes_col;
+  a.scales_col = o.scales_col;
+  a.alpha_col = o.alpha_col;
+  a.amax_out = o.amax_out;
+  a.status = o.status;
+  a.tiles_c = static_cast<uint32_t>((C + TC - 1) / TC);
+  a.kcap = grouped_capacity(T, E, 64);
+  cudaError_t e = cudaMemsetAsync(workspace, 0, grouped_workspace_bytes(E), st);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_group_amax(a, row, col, rot, st)) != cudaSuccess) return e;
+  switch (mode) {
+    case kModeRTN: return rot ? dispatch_encode<kModeRTN, true>(a, row, col, st) : dispatch_encode<kModeRTN, false>(a, row, col, st);
+    case kModeFourSix:
+      return rot ? dispatch_encode<kModeFourSix, true>(a, row, col, st) : dispatch_encode<kModeFourSix, false>(a, row, col, st);
+    case kModeRhtSR: return dispatch_encode<kModeRhtSR, true>(a, row, col, st);
+    case kModeRhtSRHw: return dispatch_encode<kModeRhtSRHw, true>(a, row, col, st);
+    default: return dispatch_encode<kModeMsEden, true>(a, row, col, st);
+  }
+}
+
+cudaError_t grouped_dequantize_launch(const uint8_t* codes, const uint8_t* scales, const float* alpha, int64_t T,
+                                      int64_t C, const int32_t* offsets, int64_t E, uint32_t flags, uint64_t seed,
+                                      void* y, int32_t* status, cudaStream_t st) {
+  const bool col = flags & kColwise, inv = flags & kInverseRht, bf = flags & kOutBf16;
+  const int e = static_cast<int>(E);
+  if (inv)
+    return bf ? launch_decode<true, true>(codes, scales, alpha, T, C, offsets, e, col, seed, y, status, st)
+              : launch_decode<true, false>(codes, scales, alpha, T, C, offsets, e, col, seed, y, status, st);
+  return bf ? launch_decode<false, true>(codes, scales, alpha, T, C, offsets, e, col, seed, y, status, st)
+            : launch_decode<false, false>(codes, scales, alpha, T, C, offsets, e, col, seed, y, status, st);
+}
+
+}  // namespace nvfp4

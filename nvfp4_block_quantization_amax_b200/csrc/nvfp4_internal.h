@@ -96,4 +96,21 @@ cudaError_t mx_quantize_launch(const void* x, int64_t R, int64_t C, int64_t ld, 
 cudaError_t mx_dequantize_launch(const uint8_t* codes, const uint8_t* scales, int64_t R, int64_t C, uint32_t flags,
                                  uint64_t seed, void* y, cudaStream_t st);
 
+// Ragged groups (grouped_quantize.cu, grouped_gemm.cu): T rows sorted by
+// group, offsets [E + 1] on the device.
+size_t grouped_workspace_bytes(int64_t E);
+cudaError_t grouped_quantize_launch(const void* x, int64_t T, int64_t C, int64_t ld, const int32_t* offsets, int64_t E,
+                                    int mode, uint32_t flags, uint64_t seed, uint32_t stream_id, const QuantOutputs& o,
+                                    void* workspace, cudaStream_t st);
+cudaError_t grouped_dequantize_launch(const uint8_t* codes, const uint8_t* scales, const float* alpha, int64_t T,
+                                      int64_t C, const int32_t* offsets, int64_t E, uint32_t flags, uint64_t seed,
+                                      void* y, int32_t* status, cudaStream_t st);
+cudaError_t grouped_gemm_launch(const uint8_t* A, const uint8_t* sA, const float* alphaA, const uint8_t* B,
+                                const uint8_t* sB, const float* alphaB, const int32_t* offsets, int64_t E, int64_t T,
+                                int64_t N, int64_t K, void* D, int out_dtype, int64_t ldd, int32_t* status,
+                                cudaStream_t st);
+cudaError_t grouped_wgrad_launch(const uint8_t* A, const uint8_t* sA, const float* alphaA, const uint8_t* B,
+                                 const uint8_t* sB, const float* alphaB, const int32_t* offsets, int64_t E, int64_t T,
+                                 int64_t M, int64_t N, void* D, int out_dtype, int32_t* status, cudaStream_t st);
+
 }  // namespace nvfp4
