@@ -457,6 +457,53 @@ NVFP4_API nvfp4_status_t nvfp4_gemm_grouped_wgrad(const uint8_t* A, const uint8_
                                                   const int32_t* offsets, int64_t E, int64_t T, int64_t M, int64_t N,
                                                   void* D, int out_dtype, int32_t* status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Low-rank adapters beside a shared projection (no page defines them): the
+ * projection's weight stays frozen in NVFP4 (nvfp4_gemm), and each token adds
+ * the low-rank product of its own request's adapter in bf16.
+ *
+ * A: bf16 [n, r, K], B: bf16 [n, N, r], scaling: n floats; ids: device int32
+ * [T], the adapter of each token, -1 for none.  Any order of ids is right;
+ * tokens of one adapter that stand together (a request's tokens) share one
+ * pass over its weights, in tiles of 64 tokens.  An id outside -1 .. n - 1
+ * sets NVFP4_ERR_ARG in *status and counts as -1.
+ * r % 8 == 0, 8 <= r <= 128; K % 8 == 0, N % 8 == 0, at most 2^22; n <= 65535.
+ * Rows x, y, out, dy, dx: bf16, 16-byte aligned, row strides (ld, elements) a
+ * multiple of 8; A, B, h, dA, dB and the workspace 16-byte aligned.
+ * Sums are held in fp32, in an order that depends on the sizes alone: the
+ * same call gives the same bits.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of device workspace of nvfp4_lora_apply (backward = 0) or
+ * nvfp4_lora_backward (backward != 0).  Calls that may run at the same time,
+ * captured graphs among them, need one each. */
+NVFP4_API size_t nvfp4_lora_workspace_size(int64_t T, int64_t K, int64_t N, int64_t r, int64_t n, int backward);
+
+/*     h[t] = A_a x[t],   out[t] = y[t] + scaling[a] B_a h[t],   a = ids[t]
+ * out is rounded once, to bf16; a token without an adapter gets y[t] as it is
+ * (0 without y) and h[t] = 0.  y may be NULL (out is then the adapters' part
+ * alone) and may be out itself, otherwise they must not overlap.  h: optional,
+ * fp32 [T, r], for nvfp4_lora_backward. */
+NVFP4_API nvfp4_status_t nvfp4_lora_apply(const void* x, int64_t ldx, const void* A, const void* B,
+                                          const float* scaling, const int32_t* ids, int64_t T, int64_t K, int64_t N,
+                                          int64_t r, int64_t n, const void* y, int64_t ldy, void* out, int64_t ldo,
+                                          float* h, void* workspace, size_t workspace_bytes, int32_t* status,
+                                          void* stream);
+
+/* Gradients of nvfp4_lora_apply for the output gradient dy [T, N]:
+ *     g[t] = B_a^T dy[t],   dx[t] = dx_in[t] + scaling[a] A_a^T g[t]
+ *     dA_a = scaling[a] sum_{ids[t] = a} g[t] x[t]^T
+ *     dB_a = scaling[a] sum_{ids[t] = a} dy[t] h[t]^T
+ * h: as nvfp4_lora_apply wrote it (needed for dB).  dx (bf16 [T, K]), dA
+ * [n, r, K] and dB [n, N, r] (fp32 or bf16 by out_dtype, contiguous) are each
+ * optional, one at least.  dx_in (the shared projection's input gradient) may
+ * be NULL and may be dx itself.  An adapter without tokens gets zeros. */
+NVFP4_API nvfp4_status_t nvfp4_lora_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* h,
+                                             const void* A, const void* B, const float* scaling, const int32_t* ids,
+                                             int64_t T, int64_t K, int64_t N, int64_t r, int64_t n, const void* dx_in,
+                                             int64_t ld_in, void* dx, int64_t lddx, void* dA, void* dB, int out_dtype,
+                                             void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
 /* Number of kernels this library has launched in the calling process since
  * it was loaded (all devices, all streams).  Instrumentation for callers that
  * account for their launches; not a page-defined operation. */

@@ -35,7 +35,8 @@ NVFP4_OUT_DTYPE_FP32 = 1
 EXPORTED = ("nvfp4_workspace_size", "nvfp4_quantize", "nvfp4_quantize_noalloc", "nvfp4_amax", "nvfp4_dequantize",
             "nvfp4_gemm", "nvfp4_gemm_vector_scales", "nvfp4_gemm_quantize", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm",
             "nvfp4_grouped_capacity", "nvfp4_grouped_workspace_size", "nvfp4_quantize_grouped",
-            "nvfp4_dequantize_grouped", "nvfp4_gemm_grouped", "nvfp4_gemm_grouped_wgrad", "nvfp4_launch_count",
+            "nvfp4_dequantize_grouped", "nvfp4_gemm_grouped", "nvfp4_gemm_grouped_wgrad",
+            "nvfp4_lora_workspace_size", "nvfp4_lora_apply", "nvfp4_lora_backward", "nvfp4_launch_count",
             "nvfp4_status_string", "nvfp4_version")
 
 
@@ -97,6 +98,13 @@ def load(path=LIB_PATH):
     L.nvfp4_gemm_grouped.restype = ctypes.c_int
     L.nvfp4_gemm_grouped_wgrad.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, ctypes.c_int, vp, vp]
     L.nvfp4_gemm_grouped_wgrad.restype = ctypes.c_int
+    L.nvfp4_lora_workspace_size.argtypes = [i64, i64, i64, i64, i64, ctypes.c_int]
+    L.nvfp4_lora_workspace_size.restype = sz
+    L.nvfp4_lora_apply.argtypes = [vp, i64, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, sz, vp, vp]
+    L.nvfp4_lora_apply.restype = ctypes.c_int
+    L.nvfp4_lora_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, i64, vp, i64,
+                                      vp, vp, ctypes.c_int, vp, sz, vp, vp]
+    L.nvfp4_lora_backward.restype = ctypes.c_int
     L.nvfp4_status_string.argtypes = [ctypes.c_int]
     L.nvfp4_status_string.restype = ctypes.c_char_p
     L.nvfp4_version.argtypes = []
@@ -191,6 +199,22 @@ def nvfp4_gemm_grouped(A, sA, alphaA, B, sB, alphaB, offsets, E, T, N, K, D, out
 def nvfp4_gemm_grouped_wgrad(A, sA, alphaA, B, sB, alphaB, offsets, E, T, M, N, D, out_dtype, status, stream):
     return int(load().nvfp4_gemm_grouped_wgrad(A, sA, alphaA, B, sB, alphaB, offsets, E, T, M, N, D, out_dtype, status,
                                                stream))
+
+
+def nvfp4_lora_workspace_size(T, K, N, r, n, backward):
+    return int(load().nvfp4_lora_workspace_size(T, K, N, r, n, int(backward)))
+
+
+def nvfp4_lora_apply(x, ldx, A, B, scaling, ids, T, K, N, r, n, y, ldy, out, ldo, h, workspace, workspace_bytes, status,
+                     stream):
+    return int(load().nvfp4_lora_apply(x, ldx, A, B, scaling, ids, T, K, N, r, n, y, ldy, out, ldo, h, workspace,
+                                       workspace_bytes, status, stream))
+
+
+def nvfp4_lora_backward(dy, lddy, x, ldx, h, A, B, scaling, ids, T, K, N, r, n, dx_in, ld_in, dx, lddx, dA, dB,
+                        out_dtype, workspace, workspace_bytes, status, stream):
+    return int(load().nvfp4_lora_backward(dy, lddy, x, ldx, h, A, B, scaling, ids, T, K, N, r, n, dx_in, ld_in, dx, lddx,
+                                          dA, dB, out_dtype, workspace, workspace_bytes, status, stream))
 
 
 def nvfp4_status_string(status):

@@ -522,3 +522,104 @@ def nvfp4_gemm_grouped_wgrad(A: torch.Tensor, sA: torch.Tensor, alphaA: torch.Te
                                         _p(D), out_dtype, _p(status), _stream_of(dev))
     _check(st, "nvfp4_gemm_grouped_wgrad")
     return D
+
+
+# ---------------------------------------------------------------------------
+# Low-rank adapters of many requests beside a shared projection.
+# ---------------------------------------------------------------------------
+def _rows(t: torch.Tensor, T: int, cols: int, what: str, device):
+    """Row stride of a bf16 matrix [T, cols] with unit column stride."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {torch.bfloat16}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if tuple(t.shape) != (T, cols) or (t.numel() and t.stride(1) != 1):
+        raise ValueError(f"{what}: shape {tuple(t.shape)} / strides {t.stride()}, need a row-major [{T}, {cols}] matrix")
+    return t.stride(0) if T > 1 else cols
+
+
+def _check_lora(A, B, scaling, ids, T, device):
+    """(K, N, r, n) of adapters A [n, r, K], B [n, N, r] and the tokens' ids [T]."""
+    if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
+        raise ValueError("A must be [n, r, K] and B [n, N, r]")
+    n, r, K = A.shape
+    N = B.shape[1]
+    _need(A, n * r * K, torch.bfloat16, "A", device)
+    _need(B, n * N * r, torch.bfloat16, "B", device)
+    _need(scaling, n, torch.float32, "scaling", device)
+    if ids.dim() != 1 or ids.numel() != T:
+        raise ValueError(f"ids: shape {tuple(ids.shape)}, need [{T}]")
+    _need(ids, T, torch.int32, "ids", device)
+    return K, N, r, n
+
+
+def _lora_workspace(workspace, T, K, N, r, n, backward, device):
+    need = L.nvfp4_lora_workspace_size(T, K, N, r, n, backward)
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    _need(workspace, need, torch.uint8, "workspace", device)
+    return workspace
+
+
+def nvfp4_lora_apply(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scaling: torch.Tensor, ids: torch.Tensor,
+                     y: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     h: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None):
+    """out[t] = y[t] + scaling[a] B[a] (A[a] x[t]) with a = ids[t] (-1: y[t]
+    alone), beside the shared projection y = nvfp4_gemm(x, frozen weight).
+    x [T, K], y and out [T, N] bf16 (out may be y); A [n, r, K], B [n, N, r]
+    bf16; scaling [n] fp32; ids [T] int32.  Returns (out, h) with h = A[a] x[t]
+    (fp32 [T, r]), which nvfp4_lora_backward takes."""
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_cuda:
+        raise TypeError("x must be a 2D bfloat16 CUDA tensor")
+    dev, T = x.device, x.shape[0]
+    K, N, r, n = _check_lora(A, B, scaling, ids, T, dev)
+    ldx = _rows(x, T, K, "x", dev)
+    ldy = 0 if y is None else _rows(y, T, N, "y", dev)
+    ldo = N if out is None else _rows(out, T, N, "out", dev)
+    if h is not None:
+        _need(h, T * r, torch.float32, "h", dev)
+    _check_status(status, dev)
+    with torch.cuda.device(dev):
+        ws = _lora_workspace(workspace, T, K, N, r, n, False, dev)
+        if out is None:
+            out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        if h is None:
+            h = torch.empty((T, r), dtype=torch.float32, device=dev)
+        st = L.nvfp4_lora_apply(_p(x), ldx, _p(A), _p(B), _p(scaling), _p(ids), T, K, N, r, n, _p(y), ldy, _p(out), ldo,
+                                _p(h), _p(ws), ws.numel(), _p(status), _stream_of(dev))
+    _check(st, "nvfp4_lora_apply")
+    return out, h
+
+
+def nvfp4_lora_backward(dy: torch.Tensor, x: torch.Tensor, h: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                        scaling: torch.Tensor, ids: torch.Tensor, dx: Optional[torch.Tensor] = None,
+                        dx_out: Optional[torch.Tensor] = None, out_dtype: int = NVFP4_OUT_DTYPE_BF16,
+                        workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+    """Gradients of nvfp4_lora_apply: returns (dx, dA, dB) for the output
+    gradient dy [T, N].  dx (bf16 [T, K], the shared projection's input
+    gradient, optional) is added to the adapters' part; the sum goes to dx_out
+    (which may be dx) or a new tensor.  h as the forward call returned it.  dA
+    [n, r, K] and dB [n, N, r] are bf16 or fp32 (out_dtype); an adapter
+    without tokens gets zeros."""
+    if dy.dtype != torch.bfloat16 or dy.dim() != 2 or not dy.is_cuda:
+        raise TypeError("dy must be a 2D bfloat16 CUDA tensor")
+    dev, T = dy.device, dy.shape[0]
+    K, N, r, n = _check_lora(A, B, scaling, ids, T, dev)
+    lddy, ldx = _rows(dy, T, N, "dy", dev), _rows(x, T, K, "x", dev)
+    _need(h, T * r, torch.float32, "h", dev)
+    ld_in = 0 if dx is None else _rows(dx, T, K, "dx", dev)
+    lddx = K if dx_out is None else _rows(dx_out, T, K, "dx_out", dev)
+    _check_status(status, dev)
+    dt = torch.bfloat16 if out_dtype == NVFP4_OUT_DTYPE_BF16 else torch.float32
+    with torch.cuda.device(dev):
+        ws = _lora_workspace(workspace, T, K, N, r, n, True, dev)
+        if dx_out is None:
+            dx_out = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+        dA = torch.empty((n, r, K), dtype=dt, device=dev)
+        dB = torch.empty((n, N, r), dtype=dt, device=dev)
+        st = L.nvfp4_lora_backward(_p(dy), lddy, _p(x), ldx, _p(h), _p(A), _p(B), _p(scaling), _p(ids), T, K, N, r, n,
+                                   _p(dx), ld_in, _p(dx_out) if T else None, lddx, _p(dA), _p(dB), out_dtype, _p(ws),
+                                   ws.numel(), _p(status), _stream_of(dev))
+    _check(st, "nvfp4_lora_backward")
+    return dx_out, dA, dB

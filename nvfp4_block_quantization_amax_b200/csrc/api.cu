@@ -35,6 +35,24 @@ nvfp4_status_t check_groups(const int32_t* offsets, int64_t E, int64_t T) {
   return aligned(offsets, 4) ? NVFP4_OK : NVFP4_ERR_ALIGN;
 }
 
+// Checks shared by the adapter calls: sizes, the adapters, the token list.
+nvfp4_status_t check_lora(const void* A, const void* B, const float* scaling, const int32_t* ids, int64_t T, int64_t K,
+                          int64_t N, int64_t r, int64_t n) {
+  constexpr int64_t most = int64_t(1) << 22;
+  if (T < 0 || T >= (int64_t(1) << 31) || K < 8 || N < 8 || K > most || N > most || K % 8 || N % 8 || r < 8 || r > 128 ||
+      r % 8 || n < 1 || n > 65535)
+    return NVFP4_ERR_SHAPE;
+  if (!A || !B || !scaling || (T && !ids)) return NVFP4_ERR_ARG;
+  return aligned(A, 16) && aligned(B, 16) && aligned(scaling, 4) && aligned(ids, 4) ? NVFP4_OK : NVFP4_ERR_ALIGN;
+}
+
+// A bf16 matrix of T rows: present, 16-byte aligned, rows of at least `cols`.
+nvfp4_status_t check_rows(const void* p, int64_t ld, int64_t cols) {
+  if (!p) return NVFP4_ERR_ARG;
+  if (ld < cols) return NVFP4_ERR_SHAPE;
+  return aligned(p, 16) && ld % 8 == 0 ? NVFP4_OK : NVFP4_ERR_ALIGN;
+}
+
 }  // namespace
 
 namespace nvfp4 {
@@ -368,6 +386,88 @@ nvfp4_status_t nvfp4_gemm_grouped_wgrad(const uint8_t* A, const uint8_t* sA, con
     return NVFP4_ERR_ALIGN;
   return launch_status(nvfp4::grouped_wgrad_launch(A, sA, alphaA, B, sB, alphaB, offsets, E, T, M, N, D, out_dtype,
                                                    status, static_cast<cudaStream_t>(stream)));
+}
+
+size_t nvfp4_lora_workspace_size(int64_t T, int64_t K, int64_t N, int64_t r, int64_t n, int backward) {
+  return (T < 0 || K < 1 || N < 1 || r < 1 || n < 1) ? 0 : nvfp4::lora_workspace_bytes(T, K, N, r, n, backward != 0);
+}
+
+nvfp4_status_t nvfp4_lora_apply(const void* x, int64_t ldx, const void* A, const void* B, const float* scaling,
+                                const int32_t* ids, int64_t T, int64_t K, int64_t N, int64_t r, int64_t n,
+                                const void* y, int64_t ldy, void* out, int64_t ldo, float* h, void* workspace,
+                                size_t workspace_bytes, int32_t* status, void* stream) {
+  nvfp4_status_t chk = check_lora(A, B, scaling, ids, T, K, N, r, n);
+  if (chk != NVFP4_OK) return chk;
+  if (T == 0) return NVFP4_OK;
+  if ((chk = check_rows(x, ldx, K)) != NVFP4_OK || (chk = check_rows(out, ldo, N)) != NVFP4_OK) return chk;
+  if (y && (chk = check_rows(y, ldy, N)) != NVFP4_OK) return chk;
+  if (!aligned(h, 16)) return NVFP4_ERR_ALIGN;
+  if (!workspace || workspace_bytes < nvfp4::lora_workspace_bytes(T, K, N, r, n, false) || !aligned(workspace, 16))
+    return NVFP4_ERR_WORKSPACE;
+  nvfp4::LoraArgs l{};
+  l.x = static_cast<const __nv_bfloat16*>(x);
+  l.ldx = ldx;
+  l.A = static_cast<const __nv_bfloat16*>(A);
+  l.B = static_cast<const __nv_bfloat16*>(B);
+  l.scaling = scaling;
+  l.ids = ids;
+  l.T = T;
+  l.K = K;
+  l.N = N;
+  l.r = r;
+  l.n = n;
+  l.in = static_cast<const __nv_bfloat16*>(y);
+  l.ldi = ldy;
+  l.out = static_cast<__nv_bfloat16*>(out);
+  l.ldo = ldo;
+  l.h = h;
+  l.status = status;
+  return launch_status(nvfp4::lora_forward_launch(l, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status_t nvfp4_lora_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* h,
+                                   const void* A, const void* B, const float* scaling, const int32_t* ids, int64_t T,
+                                   int64_t K, int64_t N, int64_t r, int64_t n, const void* dx_in, int64_t ld_in, void* dx,
+                                   int64_t lddx, void* dA, void* dB, int out_dtype, void* workspace,
+                                   size_t workspace_bytes, int32_t* status, void* stream) {
+  if (out_dtype != NVFP4_OUT_DTYPE_BF16 && out_dtype != NVFP4_OUT_DTYPE_FP32) return NVFP4_ERR_ARG;
+  nvfp4_status_t chk = check_lora(A, B, scaling, ids, T, K, N, r, n);
+  if (chk != NVFP4_OK) return chk;
+  if (!dx && !dA && !dB) return NVFP4_ERR_ARG;
+  if (T) {
+    if ((chk = check_rows(dy, lddy, N)) != NVFP4_OK) return chk;
+    if (dx && (chk = check_rows(dx, lddx, K)) != NVFP4_OK) return chk;
+    if (dx && dx_in && (chk = check_rows(dx_in, ld_in, K)) != NVFP4_OK) return chk;
+    if (dA && (chk = check_rows(x, ldx, K)) != NVFP4_OK) return chk;
+    if (dB && !h) return NVFP4_ERR_ARG;
+  }
+  if (!aligned(h, 16) || !aligned(dA, 16) || !aligned(dB, 16)) return NVFP4_ERR_ALIGN;
+  if (T && (!workspace || workspace_bytes < nvfp4::lora_workspace_bytes(T, K, N, r, n, true) || !aligned(workspace, 16)))
+    return NVFP4_ERR_WORKSPACE;
+  nvfp4::LoraArgs l{};
+  l.dy = static_cast<const __nv_bfloat16*>(dy);
+  l.lddy = lddy;
+  l.x = static_cast<const __nv_bfloat16*>(x);
+  l.ldx = ldx;
+  l.h = const_cast<float*>(h);
+  l.A = static_cast<const __nv_bfloat16*>(A);
+  l.B = static_cast<const __nv_bfloat16*>(B);
+  l.scaling = scaling;
+  l.ids = ids;
+  l.T = T;
+  l.K = K;
+  l.N = N;
+  l.r = r;
+  l.n = n;
+  l.in = dx ? static_cast<const __nv_bfloat16*>(dx_in) : nullptr;
+  l.ldi = ld_in;
+  l.out = static_cast<__nv_bfloat16*>(dx);
+  l.ldo = lddx;
+  l.dA = dA;
+  l.dB = dB;
+  l.fp32 = out_dtype == NVFP4_OUT_DTYPE_FP32;
+  l.status = status;
+  return launch_status(nvfp4::lora_backward_launch(l, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,5 +1,6 @@
 // nvfp4_internal.h -- declarations shared by the library's translation units.
 #pragma once
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -112,5 +113,31 @@ cudaError_t grouped_gemm_launch(const uint8_t* A, const uint8_t* sA, const float
 cudaError_t grouped_wgrad_launch(const uint8_t* A, const uint8_t* sA, const float* alphaA, const uint8_t* B,
                                  const uint8_t* sB, const float* alphaB, const int32_t* offsets, int64_t E, int64_t T,
                                  int64_t M, int64_t N, void* D, int out_dtype, int32_t* status, cudaStream_t st);
+
+// Low-rank adapters (lora.cu).  Forward: x, in (y) -> out, h.  Backward: dy,
+// x, h, in (dx0) -> out (dx), dA, dB.  Members not used are null.
+struct LoraArgs {
+  const __nv_bfloat16* x;
+  int64_t ldx;
+  const __nv_bfloat16* dy;
+  int64_t lddy;
+  const __nv_bfloat16* A;
+  const __nv_bfloat16* B;
+  const float* scaling;
+  const int32_t* ids;
+  int64_t T, K, N, r, n;
+  const __nv_bfloat16* in;
+  int64_t ldi;
+  __nv_bfloat16* out;
+  int64_t ldo;
+  float* h;
+  void* dA;
+  void* dB;
+  bool fp32;
+  int32_t* status;
+};
+size_t lora_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t r, int64_t n, bool backward);
+cudaError_t lora_forward_launch(const LoraArgs& l, void* workspace, cudaStream_t st);
+cudaError_t lora_backward_launch(const LoraArgs& l, void* workspace, cudaStream_t st);
 
 }  // namespace nvfp4

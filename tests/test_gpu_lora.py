@@ -1,0 +1,312 @@
+"""Low-rank adapters beside a shared projection: nvfp4_lora_apply and
+nvfp4_lora_backward against 64-bit products.
+
+Tolerances, element by element.  A product of two bf16 numbers is exact in
+fp32; a sum of k of them in fp32 is off by at most k steps of 2^-23 of the sum
+of magnitudes (truncating adds included).  So with u = 2^-23 and |.| taken
+element by element:
+  h:  E_h = (K + 32) u |x| |A|^T        (32: the partial sums of the splits)
+  h enters a product as two bf16 numbers: + 2^-17 |h|
+  out: s (E_h + 2^-17 |h|) |B|^T + s (2 r + 3) u |h| |B|^T, then one rounding
+       to bf16 of the sum with y: half a step, 2^-8 of its magnitude
+and the same for g, dx; dA and dB are sums over at most T tokens (2 T + 16).
+"""
+import pytest
+import torch
+
+from nvfp4_block_quantization_amax_b200 import synthetic
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -23
+HALF = torch.finfo(torch.bfloat16).eps / 2
+FP32, BF16 = 1, 0
+
+
+@pytest.fixture(scope="module")
+def api():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from nvfp4_block_quantization_amax_b200 import api as _api
+    return _api
+
+
+def ids_of(kind, T, n, seed):
+    g = torch.Generator().manual_seed(seed)
+    if kind == "none":
+        return torch.full((T,), -1, dtype=torch.int32)
+    if kind == "one":
+        return torch.full((T,), n - 1, dtype=torch.int32)
+    if kind == "random":
+        return torch.randint(-1, n, (T,), generator=g).to(torch.int32)
+    cuts = torch.sort(torch.randint(0, T + 1, (n + 1,), generator=g)).values.tolist()
+    order = torch.randperm(n + 2, generator=g) - 1                 # runs, one without an adapter, one id twice
+    order[order == n] = 0
+    lengths = [b - a for a, b in zip([0] + cuts, cuts + [T])]
+    return torch.repeat_interleave(order, torch.tensor(lengths)).to(torch.int32)
+
+
+def problem(T, K, N, r, n, kind, seed=0):
+    g = torch.Generator().manual_seed(1000 + seed)
+    rnd = lambda *s: torch.randn(s, generator=g)   # noqa: E731
+    return dict(x=rnd(T, K).bfloat16().cuda(), A=(rnd(n, r, K) / K ** 0.5).bfloat16().cuda(),
+                B=(rnd(n, N, r) * 0.1).bfloat16().cuda(), scaling=(torch.rand(n, generator=g) + 0.5).cuda(),
+                ids=ids_of(kind, T, n, seed).cuda(), y=rnd(T, N).bfloat16().cuda(), dy=(rnd(T, N) * 1e-2).bfloat16().cuda(),
+                dx=(rnd(T, K) * 1e-2).bfloat16().cuda())
+
+
+def within(got, ref, bound, what):
+    over = (got.double() - ref).abs() - bound
+    assert bool((over <= 0).all()), f"{what}: {float(over.max()):.3g} over the bound"
+
+
+def reference(p, h=None):
+    """64-bit results and bounds of both directions; h: the forward's h as the backward was given it."""
+    x, A, B, s, y, dy, dx = (p[k].double() for k in ("x", "A", "B", "scaling", "y", "dy", "dx"))
+    T, K = x.shape
+    n, N, r = B.shape
+    f = dict(h=torch.zeros((T, r), dtype=torch.float64, device="cuda"), out=y.clone(), dx=dx.clone(),
+             dA=torch.zeros_like(A), dB=torch.zeros_like(B))
+    e = {k: torch.zeros_like(v) for k, v in f.items()}
+    for a in range(n):
+        t = torch.nonzero(p["ids"] == a).view(-1)
+        if len(t) == 0:
+            continue
+        f["h"][t] = x[t] @ A[a].t()
+        e["h"][t] = (K + 32) * U * (x[t].abs() @ A[a].abs().t())
+        habs = f["h"][t].abs()
+        f["out"][t] += s[a] * (f["h"][t] @ B[a].t())
+        e["out"][t] = s[a] * ((e["h"][t] + (2.0 ** -17 + (2 * r + 3) * U) * habs) @ B[a].abs().t())
+        g = dy[t] @ B[a]
+        eg = (N + 32) * U * (dy[t].abs() @ B[a].abs())
+        gb = eg + 2.0 ** -17 * g.abs()
+        f["dx"][t] += s[a] * (g @ A[a])
+        e["dx"][t] = s[a] * ((gb + (2 * r + 3) * U * g.abs()) @ A[a].abs())
+        f["dA"][a] = s[a] * (g.t() @ x[t])
+        e["dA"][a] = s[a] * ((gb + (2 * T + 16) * U * g.abs()).t() @ x[t].abs())
+        hh = (f["h"] if h is None else h.double())[t]
+        f["dB"][a] = s[a] * (dy[t].t() @ hh)
+        e["dB"][a] = s[a] * (dy[t].abs().t() @ ((2.0 ** -17 + (2 * T + 16) * U) * hh.abs()))
+    for k in ("out", "dx"):
+        e[k] += HALF * (f[k].abs() + e[k])
+    return f, e
+
+
+def check(api, p, out_dtype=FP32):
+    none = p["ids"] < 0
+    out, h = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"], y=p["y"])
+    f, e = reference(p, h)
+    within(h, f["h"], e["h"], "h")
+    within(out, f["out"], e["out"], "out")
+    assert torch.equal(out[none], p["y"][none]) and not bool(h[none].any())
+    dx, dA, dB = api.nvfp4_lora_backward(p["dy"], p["x"], h, p["A"], p["B"], p["scaling"], p["ids"], dx=p["dx"],
+                                         out_dtype=out_dtype)
+    within(dx, f["dx"], e["dx"], "dx")
+    assert torch.equal(dx[none], p["dx"][none])
+    for got, k in ((dA, "dA"), (dB, "dB")):
+        assert got.dtype == (torch.float32 if out_dtype == FP32 else torch.bfloat16)
+        within(got, f[k], e[k] + (HALF if out_dtype == BF16 else 2.0 ** -24) * (f[k].abs() + e[k]), k)
+    return out, h, dx, dA, dB
+
+
+@pytest.mark.parametrize("T,K,N,r,n,kind", [
+    (1, 64, 64, 16, 1, "one"), (1, 8, 8, 8, 3, "random"), (3, 72, 136, 8, 2, "random"), (16, 512, 256, 16, 40, "random"),
+    (63, 128, 128, 24, 4, "runs"), (64, 200, 264, 32, 5, "random"), (65, 256, 128, 40, 3, "runs"),
+    (130, 136, 520, 64, 4, "runs"), (200, 320, 1032, 128, 3, "random"), (300, 1000, 2056, 16, 6, "runs"),
+    (517, 384, 200, 72, 9, "random"), (70, 64, 64, 16, 4, "none"), (129, 2048, 384, 16, 1, "one"),
+    (1030, 640, 384, 104, 2, "runs"), (2, 4096, 128, 128, 2, "random"),
+])
+def test_shapes_and_orders(api, T, K, N, r, n, kind):
+    check(api, problem(T, K, N, r, n, kind, seed=T))
+
+
+@pytest.mark.parametrize("T,n,kind", [(5000, 2, "runs"), (4100, 3, "random"), (900, 200, "random")])
+def test_many_tokens_and_many_adapters(api, T, n, kind):
+    check(api, problem(T, 136, 264, 16, n, kind, seed=3))
+
+
+def test_bf16_gradients(api):
+    check(api, problem(300, 256, 384, 16, 3, "runs"), out_dtype=BF16)
+
+
+def test_without_a_base_and_in_place(api):
+    p = problem(150, 256, 264, 16, 3, "runs", seed=5)
+    args = (p["x"], p["A"], p["B"], p["scaling"], p["ids"])
+    want, h = api.nvfp4_lora_apply(*args, y=p["y"])
+    y = p["y"].clone()
+    got, _ = api.nvfp4_lora_apply(*args, y=y, out=y)
+    assert got is y and torch.equal(y, want)
+    alone, _ = api.nvfp4_lora_apply(*args)
+    zero, _ = api.nvfp4_lora_apply(*args, y=torch.zeros_like(y))
+    assert torch.equal(alone, zero)
+    back = (p["dy"], p["x"], h, p["A"], p["B"], p["scaling"], p["ids"])
+    want = api.nvfp4_lora_backward(*back, dx=p["dx"])
+    dx = p["dx"].clone()
+    got = api.nvfp4_lora_backward(*back, dx=dx, dx_out=dx)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    alone = api.nvfp4_lora_backward(*back)
+    zero = api.nvfp4_lora_backward(*back, dx=torch.zeros_like(dx))
+    assert all(torch.equal(a, b) for a, b in zip(alone, zero))
+
+
+def test_strided_rows(api):
+    p = problem(90, 256, 136, 24, 3, "random", seed=6)
+    want = check(api, p)
+    wide = {k: torch.full((90, p[k].shape[1] + 40), float("nan"), dtype=torch.bfloat16, device="cuda")
+            for k in ("x", "y", "dy", "dx")}
+    q = dict(p)
+    for k, w in wide.items():
+        q[k] = w[:, 16:16 + p[k].shape[1]]
+        q[k].copy_(p[k])
+    got = check(api, q)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    out = torch.full((90, 200), 3.0, dtype=torch.bfloat16, device="cuda")
+    api.nvfp4_lora_apply(q["x"], q["A"], q["B"], q["scaling"], q["ids"], y=q["y"], out=out[:, 32:168])
+    assert torch.equal(out[:, 32:168], want[0]) and bool((out[:, :32] == 3).all()) and bool((out[:, 168:] == 3).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_token_reaches_no_other_adapter(api, bad):
+    p = problem(140, 136, 128, 16, 3, "random", seed=7)
+    p["ids"][70], p["ids"][71] = 1, -1
+    for k in ("x", "y", "dy", "dx"):
+        p[k][70:72] = bad
+    clean = dict(p, **{k: p[k].clone() for k in ("x", "y", "dy", "dx")})
+    for k in ("x", "y", "dy", "dx"):
+        clean[k][70:72] = 0
+    def run(q):
+        out, h = api.nvfp4_lora_apply(q["x"], q["A"], q["B"], q["scaling"], q["ids"], y=q["y"])
+        return (out, h) + api.nvfp4_lora_backward(q["dy"], q["x"], h, q["A"], q["B"], q["scaling"], q["ids"], dx=q["dx"])
+    got, want = run(p), run(clean)
+    keep = torch.ones(140, dtype=torch.bool, device="cuda")
+    keep[70:72] = False
+    for i in (0, 1, 2):
+        assert torch.equal(got[i][keep], want[i][keep])
+    for i in (3, 4):
+        assert torch.equal(got[i][[0, 2]], want[i][[0, 2]])
+        assert not bool(torch.isfinite(got[i][1]).all())
+
+
+def test_an_infinite_h_gives_infinities_where_the_formula_does(api):
+    p = problem(1, 64, 64, 16, 1, "one", seed=8)
+    p["A"].zero_()
+    p["A"][0, 0] = 1.0
+    p["x"].fill_(3e38)                       # h[0] overflows to +inf, the other h are 0
+    p["B"].fill_(0.0)
+    p["B"][0, :, 0] = 1.0
+    out, h = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"])
+    assert h[0, 0] == float("inf") and bool((out == float("inf")).all())
+
+
+def test_bad_ids_set_the_status(api):
+    p = problem(80, 128, 128, 16, 3, "one", seed=9)
+    for bad in (3, -2, 1 << 30):
+        ids = p["ids"].clone()
+        ids[41] = bad
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, h = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], ids, y=p["y"], status=st)
+        assert st.item() == -1 and torch.equal(out[41], p["y"][41])
+        st.zero_()
+        api.nvfp4_lora_backward(p["dy"], p["x"], h, p["A"], p["B"], p["scaling"], ids, status=st)
+        assert st.item() == -1
+
+
+def test_no_tokens(api):
+    p = problem(0, 128, 64, 16, 2, "none")
+    out, h = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"], y=p["y"])
+    assert out.shape == (0, 64) and h.shape == (0, 16)
+    dx, dA, dB = api.nvfp4_lora_backward(p["dy"], p["x"], h, p["A"], p["B"], p["scaling"], p["ids"])
+    assert dx.shape == (0, 128) and not bool(dA.any()) and not bool(dB.any())
+
+
+def test_same_call_same_bits(api):
+    p = problem(700, 512, 384, 24, 4, "random", seed=10)
+    first = check(api, p)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(check(api, p), first))
+
+
+def test_gradients_against_differences(api):
+    """out is linear in A for fixed B and the other way round, so a finite
+    step gives the derivative without truncation error; steps and weights are
+    small dyadic numbers, exact in bf16.  What is left is the rounding of the
+    two outputs to bf16 (half a step each), weighted by dy."""
+    T, K, N, r, n = 90, 64, 72, 16, 3
+    p = problem(T, K, N, r, n, "runs", seed=11)
+    g = torch.Generator().manual_seed(12)
+    for k in ("A", "B"):
+        p[k] = (torch.randint(-8, 9, p[k].shape, generator=g) / 8).bfloat16().cuda()
+    out, h = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"])
+    dx, dA, dB = api.nvfp4_lora_backward(p["dy"], p["x"], h, p["A"], p["B"], p["scaling"], p["ids"], out_dtype=FP32)
+    dy = p["dy"].double()
+    for k, grad in (("A", dA), ("B", dB), ("x", dx)):
+        d = torch.randint(-1, 2, p[k].shape, generator=g).cuda() / 8
+        q = dict(p)
+        if k == "x":
+            q["x"] = (p["x"].double() + d).bfloat16()
+            d = q["x"].double() - p["x"].double()
+        else:
+            q[k] = (p[k].double() + d).bfloat16()
+            assert torch.equal(q[k].double(), p[k].double() + d)
+        moved, _ = api.nvfp4_lora_apply(q["x"], q["A"], q["B"], q["scaling"], q["ids"])
+        diff = float((dy * (moved.double() - out.double())).sum())
+        noise = float((dy.abs() * HALF * (moved.double().abs() + out.double().abs())).sum()) * 1.01
+        if k == "x":
+            noise += float((HALF * dx.double().abs() * d.abs()).sum())
+        assert abs(diff - float((grad.double() * d).sum())) <= noise
+
+
+def test_beside_the_shared_projection_forward_and_backward(api):
+    """As a layer uses them: y = x W^T in NVFP4, the adapters added in place;
+    backward: dx of the frozen NVFP4 weight, the adapters' part on top."""
+    T, K, N, r, n = 256, 512, 768, 16, 3
+    p = problem(T, K, N, r, n, "runs", seed=13)
+    w = synthetic.weight(N, K, seed=14).cuda()
+    ROW, COL, GEMM = api.NVFP4_ROWWISE, api.NVFP4_COLWISE, api.NVFP4_GEMM_SCALE_LAYOUT
+    qw = api.nvfp4_quantize(w, 0, ROW | COL | GEMM)
+    qx = api.nvfp4_quantize(p["x"], 1, ROW | GEMM)
+    y = api.nvfp4_gemm(qx.codes_row, qx.scales_row, qx.alpha_row, qw.codes_row, qw.scales_row, qw.alpha_row)
+    base = y.clone()
+    out, h = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"], y=y, out=y)
+    qd = api.nvfp4_quantize(p["dy"], 1, ROW | GEMM)
+    dx0 = api.nvfp4_gemm(qd.codes_row, qd.scales_row, qd.alpha_row, qw.codes_col, qw.scales_col, qw.alpha_col)
+    dx, dA, dB = api.nvfp4_lora_backward(p["dy"], p["x"], h, p["A"], p["B"], p["scaling"], p["ids"], dx=dx0,
+                                         out_dtype=FP32)
+    f, e = reference(dict(p, y=base, dx=dx0), h)
+    within(out, f["out"], e["out"], "out")
+    within(dx, f["dx"], e["dx"], "dx")
+    within(dA, f["dA"], e["dA"] + 2.0 ** -24 * f["dA"].abs(), "dA")
+    within(dB, f["dB"], e["dB"] + 2.0 ** -24 * f["dB"].abs(), "dB")
+
+
+def test_captured_and_on_two_streams(api):
+    p = problem(300, 256, 384, 16, 4, "runs", seed=15)
+
+    def step(q):
+        out, h = api.nvfp4_lora_apply(q["x"], q["A"], q["B"], q["scaling"], q["ids"], y=q["y"])
+        return (out, h) + api.nvfp4_lora_backward(q["dy"], q["x"], h, q["A"], q["B"], q["scaling"], q["ids"], dx=q["dx"])
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(p)
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(p)
+    for kind, s in (("random", 16), ("none", 17), ("one", 18)):
+        q = problem(300, 256, 384, 16, 4, kind, seed=s)
+        for k in p:
+            p[k].copy_(q[k])
+        g.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, step(q)))
+    qs = [problem(300, 256, 384, 16, 4, "random", seed=s) for s in (19, 20)]
+    want = [step(q) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        res = []
+        for q, s in zip(qs, streams):
+            with torch.cuda.stream(s):
+                res.append(step(q))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for u, v in zip(res, want) for a, b in zip(u, v))
