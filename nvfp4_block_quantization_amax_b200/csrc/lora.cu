@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kRows = 64;      // tokens of a tile
 constexpr int kNT = 256;       // threads of the tile kernels
-constexpr int kCols = 256;     // columns of an expand tile (512 bytes of a row)
+constexpr int kCols = 128;     // columns of an expand tile
 constexpr int kFewTokens = 256;   // up to here the tokens are gathered by adapter
 
 struct AdapterIds {
@@ -80,6 +80,11 @@ __device__ __forceinline__ void copy16(void* smem, const void* gmem, bool valid)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_addr(smem)), "l"(gmem), "r"(bytes) : "memory");
 }
 
+__device__ __forceinline__ void copy4(void* smem, const void* gmem, bool valid) {
+  const int bytes = valid ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(smem_addr(smem)), "l"(gmem), "r"(bytes) : "memory");
+}
+
 // v = hi + lo up to 2^-17 |v| (an infinity or NaN is all in hi: its lo would
 // be a NaN of its own)
 __device__ __forceinline__ float rest_of(float v, float hi) {
@@ -101,17 +106,11 @@ __device__ __forceinline__ uint32_t pack_bf16(__nv_bfloat16 a, __nv_bfloat16 b) 
   return static_cast<uint32_t>(__bfloat16_as_ushort(a)) | (static_cast<uint32_t>(__bfloat16_as_ushort(b)) << 16);
 }
 
-// base + d of eight columns, rounded once to bf16
-__device__ __forceinline__ uint4 add_round(const uint4 y, const float* d) {
-  const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
-  uint32_t o[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(__fadd_rn(__uint_as_float(yw[j] << 16), d[2 * j]),
-                                                   __fadd_rn(__uint_as_float(yw[j] & 0xFFFF0000u), d[2 * j + 1]));
-    o[j] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+// base + d of two columns, rounded once to bf16
+__device__ __forceinline__ uint32_t add_round(uint32_t y, float d0, float d1) {
+  const float2 v = __fadd2_rn(make_float2(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u)), make_float2(d0, d1));
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&b);
 }
 
 // Column order of a 32-column group in the expand products: thread c of a
@@ -127,19 +126,17 @@ __device__ __forceinline__ int slot_col(int slot) {   // and back
 }
 
 // The adapters of a tile of 64 tokens: ids[64] (-1: none) and the list of the
-// distinct ones.  All threads call it (at least two warps); ends with a
-// barrier.
+// distinct ones.  All threads call it (at least two warps), thread t < 64 with
+// token t's adapter; ends with a barrier.
 struct TileAdapters {
   int ids[kRows];
   int list[kRows];
   int head, count;   // distinct ones of the first 32 tokens, and in all
 };
-__device__ __forceinline__ void tile_adapters(TileAdapters& ta, const AdapterIds& a, int64_t row0, bool report) {
+__device__ __forceinline__ void tile_adapters(TileAdapters& ta, int id) {
   const int t = threadIdx.x, lane = t & 31;
-  int id = -1;
   bool first = false;
   if (t < kRows) {
-    id = adapter_of(a, row0 + t, report);
     ta.ids[t] = id;
     const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);   // by every lane, whatever its id
     first = id >= 0 && __ffs(same) - 1 == lane;
@@ -161,30 +158,45 @@ __device__ __forceinline__ void tile_adapters(TileAdapters& ta, const AdapterIds
   __syncthreads();
 }
 
+// The bf16 numbers that make up w [T, r] (TERMS of them), rows padded to R
+// with zeros: operands of the outer products.  terms[x][t][j].
+template <int RP>
+__device__ __forceinline__ void write_terms(__nv_bfloat16* terms, int n_terms, int64_t T, int64_t t, int j, float v) {
+  constexpr int R = 16 * RP;
+  __nv_bfloat16 s[3];
+  if (n_terms == 3) split_bf16(v, s[0], s[1], s[2]);
+  else split_bf16(v, s[0], s[1]);
+  for (int x = 0; x < n_terms; ++x) terms[(x * T + t) * R + j] = s[x];
+}
+
 // ---------------------------------------------------------------------------
 // shrink: part[split][t][j] = sum over this split's columns of z[t, c] W[j, c]
 // TRANS: W is stored [C, r] (c-major), else [r, C].
-// A stage is 64 rows x 256 columns: every warp's copy is 512 contiguous bytes
-// of one row.  (64 x 64 stages, 128 bytes of a row at a time, ran at 2.9 TB/s
-// on 8192 x 14336: scattered short reads.)  Warp w multiplies rows 16 (w % 4)
-// over half w / 4 of the stage's columns; the halves are added at the end.
+// 64 rows x 128 columns a stage; warp w multiplies rows 16 (w % 4) over half
+// w / 4 of the stage's columns, the halves are added at the end.  The rows'
+// traffic bounds it; what it takes is warps and copies in flight, so the ring
+// is sized for three CTAs per SM.
+// In the backward pass the first split also writes h's terms for dB.
 // ---------------------------------------------------------------------------
 template <int RP, bool TRANS>
 struct ShrinkCfg {
   static constexpr int R = 16 * RP;
-  static constexpr int KC = RP == 8 ? 128 : 256;   // columns of a stage (RP = 8: the weights' stage is as large)
+  static constexpr int KC = 128;   // columns of a stage
   static constexpr int ZB = kRows * (KC + 8) * 2;
   static constexpr int WB = (TRANS ? KC * (R + 8) : R * (KC + 8)) * 2;
-  static constexpr int BYTES = 2 * (ZB + WB);
+  static constexpr int CTAS = RP == 1 ? 3 : (RP <= 4 ? 2 : 1);   // per SM
+  static constexpr int STAGES = 224 * 1024 / CTAS / (ZB + WB);
+  static constexpr int BYTES = STAGES * (ZB + WB);
 };
 
 template <int RP, bool TRANS>
-__global__ void __launch_bounds__(kNT, RP <= 2 ? 2 : 1)
+__global__ void __launch_bounds__(kNT, ShrinkCfg<RP, TRANS>::CTAS)
     lora_shrink_kernel(const __nv_bfloat16* __restrict__ z, int64_t ldz, const __nv_bfloat16* __restrict__ W,
-                       const AdapterIds a, int64_t C, int r, int64_t per_split, float* __restrict__ part) {
+                       const AdapterIds a, int64_t C, int r, int64_t per_split, float* __restrict__ part,
+                       const float* __restrict__ h, __nv_bfloat16* __restrict__ h_terms, int n_terms) {
   pdl_entry();
   using S = ShrinkCfg<RP, TRANS>;
-  constexpr int R = S::R, KC = S::KC;
+  constexpr int R = S::R, KC = S::KC, ST = S::STAGES;
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ TileAdapters ta;
   const int th = threadIdx.x, lane = th & 31, warp = th >> 5, rg = warp & 3, kh = warp >> 2;
@@ -192,29 +204,32 @@ __global__ void __launch_bounds__(kNT, RP <= 2 ? 2 : 1)
   const int64_t c_begin = blockIdx.y * per_split;
   const int64_t c_end = c_begin + per_split < C ? c_begin + per_split : C;
   const int steps = static_cast<int>((c_end - c_begin + KC - 1) / KC);
-  tile_adapters(ta, a, row0, blockIdx.y == 0);
+  tile_adapters(ta, th < kRows ? adapter_of(a, row0 + th, blockIdx.y == 0) : -1);
   float* mine = part + static_cast<int64_t>(blockIdx.y) * a.T * r;
 
-  auto load = [&](int step, const __nv_bfloat16* w) {
-    uint8_t* base = dyn + (step & 1) * (S::ZB + S::WB);
-    const int64_t c0 = c_begin + static_cast<int64_t>(step) * KC;
+  // this thread copies chunk zch of rows zrow, zrow + 16, ..
+  const int zrow = th >> 4, zch = th & 15;
+  const __nv_bfloat16* zsrc = z + (row0 + zrow) * ldz + c_begin + 8 * zch;
+  uint32_t zok = 0;
 #pragma unroll
-    for (int i = 0; i < kRows * KC / 8 / kNT; ++i) {
-      const int k = th + kNT * i, row = k / (KC / 8), ch = k % (KC / 8);
-      const bool ok = c0 + 8 * ch < c_end && ta.ids[row] >= 0;
-      copy16(base + row * (KC + 8) * 2 + 16 * ch, ok ? z + (row0 + row) * ldz + c0 + 8 * ch : z, ok);
+  for (int i = 0; i < kRows / 16; ++i) zok |= (ta.ids[zrow + 16 * i] >= 0 ? 1u : 0u) << i;
+  auto load = [&](int step, int slot, const __nv_bfloat16* w) {
+    uint8_t* base = dyn + slot * (S::ZB + S::WB);
+    const int64_t off = static_cast<int64_t>(step) * KC, c0 = c_begin + off;
+    const uint32_t ok4 = c0 + 8 * zch < c_end ? zok : 0u;
+#pragma unroll
+    for (int i = 0; i < kRows / 16; ++i) {
+      const bool ok = ok4 >> i & 1u;
+      copy16(base + (zrow + 16 * i) * (KC + 8) * 2 + 16 * zch, ok ? zsrc + off + 16 * i * ldz : z, ok);
     }
     uint8_t* wb = base + S::ZB;
-    if constexpr (!TRANS) {
 #pragma unroll
-      for (int i = 0; i < (R * KC / 8 + kNT - 1) / kNT; ++i) {
-        const int k = th + kNT * i, j = k / (KC / 8), ch = k % (KC / 8);
-        const bool ok = j < r && c0 + 8 * ch < c_end;
-        copy16(wb + j * (KC + 8) * 2 + 16 * ch, ok ? w + j * C + c0 + 8 * ch : w, ok);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < (KC * R / 8 + kNT - 1) / kNT; ++i) {
+    for (int i = 0; i < RP; ++i) {
+      if constexpr (!TRANS) {   // ranks zrow + 16 i, chunk zch
+        const int j = zrow + 16 * i;
+        const bool ok = j < r && c0 + 8 * zch < c_end;
+        copy16(wb + j * (KC + 8) * 2 + 16 * zch, ok ? w + j * C + c0 + 8 * zch : w, ok);
+      } else {
         const int k = th + kNT * i, c = k / (R / 8), ch = k % (R / 8);
         const bool ok = c0 + c < c_end && 8 * ch < r;
         copy16(wb + c * (R + 8) * 2 + 16 * ch, ok ? w + (c0 + c) * r + 8 * ch : w, ok);
@@ -229,13 +244,20 @@ __global__ void __launch_bounds__(kNT, RP <= 2 ? 2 : 1)
     float sum[2 * RP][4];
 #pragma unroll
     for (int i = 0; i < 2 * RP; ++i) sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.0f;
-    load(0, w);
-    for (int s = 0; s < steps; ++s) {
-      if (s + 1 < steps) load(s + 1, w);
+#pragma unroll
+    for (int p = 0; p < ST - 1; ++p) {
+      if (p < steps) load(p, p, w);
       else cp_async_commit();
-      cp_async_wait<1>();
-      __syncthreads();
-      const uint8_t* base = dyn + (s & 1) * (S::ZB + S::WB);
+    }
+    int slot = 0, ahead = ST - 1;
+    for (int s = 0; s < steps; ++s) {
+      cp_async_wait<ST - 2>();   // this stage has landed
+      __syncthreads();           // for every thread, and the stage before it has been read
+      if (s + ST - 1 < steps) load(s + ST - 1, ahead, w);
+      else cp_async_commit();
+      const uint8_t* base = dyn + slot * (S::ZB + S::WB);
+      if (++slot == ST) slot = 0;
+      if (++ahead == ST) ahead = 0;
       const __nv_bfloat16* zs = reinterpret_cast<const __nv_bfloat16*>(base);
       const __nv_bfloat16* ws = reinterpret_cast<const __nv_bfloat16*>(base + S::ZB);
       // this stage's sums start from zero and are added to the running ones:
@@ -243,29 +265,39 @@ __global__ void __launch_bounds__(kNT, RP <= 2 ? 2 : 1)
       float acc[2 * RP][4];
 #pragma unroll
       for (int i = 0; i < 2 * RP; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+      // fragments of kBatch products of 16 columns are loaded together, so
+      // their latencies overlap
+      constexpr int kBatch = RP <= 2 ? 4 : 2;
 #pragma unroll
-      for (int k8 = 0; k8 < KC / 2; k8 += 16) {
-        const int kk = kh * (KC / 2) + k8;
-        uint32_t af[4];
-        ldsm4(af, zs + (16 * rg + (lane & 15)) * (KC + 8) + kk + (lane >> 4) * 8);
+      for (int k8 = 0; k8 < KC / 2; k8 += 16 * kBatch) {
+        uint32_t af[kBatch][4], bf[kBatch][RP][4];
 #pragma unroll
-        for (int p = 0; p < RP; ++p) {
-          uint32_t bf[4];
-          if constexpr (!TRANS)
-            ldsm4(bf, ws + (16 * p + (lane & 7) + ((lane >> 4) << 3)) * (KC + 8) + kk + ((lane >> 3) & 1) * 8);
-          else
-            ldsm4_t(bf, ws + (kk + (lane & 7) + ((lane >> 3) & 1) * 8) * (R + 8) + 16 * p + (lane >> 4) * 8);
-          mma16(acc[2 * p], af, bf);
-          mma16(acc[2 * p + 1], af, bf + 2);
+        for (int b = 0; b < kBatch; ++b) {
+          const int kk = kh * (KC / 2) + k8 + 16 * b;
+          ldsm4(af[b], zs + (16 * rg + (lane & 15)) * (KC + 8) + kk + (lane >> 4) * 8);
+#pragma unroll
+          for (int p = 0; p < RP; ++p) {
+            if constexpr (!TRANS)
+              ldsm4(bf[b][p], ws + (16 * p + (lane & 7) + ((lane >> 4) << 3)) * (KC + 8) + kk + ((lane >> 3) & 1) * 8);
+            else
+              ldsm4_t(bf[b][p], ws + (kk + (lane & 7) + ((lane >> 3) & 1) * 8) * (R + 8) + 16 * p + (lane >> 4) * 8);
+          }
         }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+          for (int p = 0; p < RP; ++p) {
+            mma16(acc[2 * p], af[b], bf[b][p]);
+            mma16(acc[2 * p + 1], af[b], bf[b][p] + 2);
+          }
       }
 #pragma unroll
       for (int i = 0; i < 2 * RP; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[i][e] = __fadd_rn(sum[i][e], acc[i][e]);
-      __syncthreads();   // this buffer is refilled in the next round
     }
-    // add the second half's sums (the ring is free: every copy has landed)
+    __syncthreads();   // the ring is free: every copy has landed and been read
+    // add the second half's sums
     float* other = reinterpret_cast<float*>(dyn);
     if (kh == 1) {
 #pragma unroll
@@ -297,32 +329,46 @@ __global__ void __launch_bounds__(kNT, RP <= 2 ? 2 : 1)
     const int row = k / r;
     if (ta.ids[row] < 0 && row0 + row < a.T) mine[(row0 + row) * r + (k - row * r)] = 0.0f;
   }
+  if (h_terms && blockIdx.y == 0) {
+    for (int k = th; k < kRows * R; k += kNT) {
+      const int64_t t = row0 + k / R;
+      const int j = k % R;
+      if (t < a.T) write_terms<RP>(h_terms, n_terms, a.T, t, j, j < r ? __ldg(h + t * r + j) : 0.0f);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
 // expand: out[t, c] = base[t, c] + s_a sum_j w[t, j] W[c, j], w = sum of the
-// partials; w itself goes to w_out.  TRANS: W is stored [r, C], else [C, r].
-// A CTA takes 64 tokens and `per_cta` tiles of 256 columns; warp w rows
-// 16 (w % 4), columns 128 (w / 4).  A thread's products land on the 16 bytes
+// partials; w itself goes to w_out, its terms to w_terms.  TRANS: W is stored
+// [r, C], else [C, r].
+// A CTA takes 64 tokens and `per_cta` tiles of 128 columns; warp w rows
+// 16 (w % 4), columns 64 (w / 4).  A thread's products land on the 16 bytes
 // of base it has loaded (see mma_slot), so neither base nor result passes
-// through shared memory.
+// through shared memory.  Instructions and their latencies bound it before
+// memory does: the scale is folded into w, base is added in pairs, and tiles
+// are narrow so that four CTAs (32 warps) fit an SM.  Measured at 8192 x
+// 14336, r = 16: 256-column tiles, three CTAs and 632 instructions per warp
+// and 256 columns 105 us; a persistent form that prefetched the next tile with
+// two CTAs 120 us.
 // ---------------------------------------------------------------------------
-template <int RP>
+template <int RP, bool TRANS>
 struct ExpandCfg {
   static constexpr int R = 16 * RP;
   static constexpr int HB = kRows * (R + 8) * 2;
-  static constexpr int WB = kCols * (R + 8) * 2;
+  static constexpr int WB = (TRANS ? R * (kCols + 8) : kCols * (R + 8)) * 2;
   static constexpr int BYTES = 2 * HB + WB;
+  static constexpr int CTAS = RP <= 4 ? 4 : 2;   // per SM
 };
 
 template <int RP, bool TRANS>
-__global__ void __launch_bounds__(kNT, RP <= 4 ? 3 : 2)
+__global__ void __launch_bounds__(kNT, ExpandCfg<RP, TRANS>::CTAS)
     lora_expand_kernel(const float* __restrict__ part, int splits, const __nv_bfloat16* __restrict__ W,
-                       const float* __restrict__ scaling, const AdapterIds a, int64_t C, int r, int per_cta,
+                       const float* __restrict__ scaling, const AdapterIds a, int64_t C, int r, int per_cta, int groups,
                        const __nv_bfloat16* in, int64_t ldi, __nv_bfloat16* out, int64_t ldo,
-                       float* __restrict__ w_out) {
+                       float* __restrict__ w_out, __nv_bfloat16* __restrict__ w_terms, int n_terms) {
   pdl_entry();
-  using S = ExpandCfg<RP>;
+  using S = ExpandCfg<RP, TRANS>;
   constexpr int R = S::R;
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ TileAdapters ta;
@@ -330,82 +376,95 @@ __global__ void __launch_bounds__(kNT, RP <= 4 ? 3 : 2)
   __nv_bfloat16* hl = reinterpret_cast<__nv_bfloat16*>(dyn + S::HB);
   __nv_bfloat16* ws = reinterpret_cast<__nv_bfloat16*>(dyn + 2 * S::HB);
   const int th = threadIdx.x, lane = th & 31, warp = th >> 5, rg = warp & 3, ch = warp >> 2;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
-  const int64_t ta_row = row0 + 16 * rg + (lane >> 2);   // this thread's rows: ta_row and ta_row + 8
-  const int piece = lane & 3;
-  tile_adapters(ta, a, row0, false);
-  // the sum of the partials, in their order
-  for (int k = th; k < kRows * R; k += kNT) {
-    const int row = k / R, j = k % R;
-    float v = 0.0f;
-    if (row0 + row < a.T && j < r) {
-      const int64_t at = (row0 + row) * r + j;
-      for (int s = 0; s < splits; ++s) v = __fadd_rn(v, __ldcg(part + s * a.T * r + at));
-      if (w_out && blockIdx.y == 0) w_out[at] = v;
-    }
-    split_bf16(v, hh[row * (R + 8) + j], hl[row * (R + 8) + j]);
-  }
-  if (!out) return;   // only the sum was asked for
-  const int id_lo = ta.ids[16 * rg + (lane >> 2)], id_hi = ta.ids[16 * rg + (lane >> 2) + 8];
-
-  for (int i = 0; i < per_cta; ++i) {
-    const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * per_cta + i) * kCols;
-    if (c0 >= C) break;
-    const int64_t c_mine = c0 + 128 * ch + 8 * piece;   // + 32 per column group
-    uint4 y[4][2];
+  // neighbouring CTAs take neighbouring columns of the same rows
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / groups) * kRows;
+  const int group = blockIdx.x % groups;
+  const int my_row = 16 * rg + (lane >> 2);        // this thread's rows of the tile: my_row and my_row + 8
+  const int my_col = 64 * ch + 8 * (lane & 3);     // and its columns: 8 from here on, and 32 further
+  uint4 y[2][2];
+  auto load_base = [&](int64_t c0) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int64_t t = ta_row + 8 * half, c = c_mine + 32 * q;
+        const int64_t t = row0 + my_row + 8 * half, c = c0 + my_col + 32 * q;
         y[q][half] = make_uint4(0u, 0u, 0u, 0u);
         if (in && c < C && t < a.T) y[q][half] = __ldcs(reinterpret_cast<const uint4*>(in + t * ldi + c));
       }
     }
+  };
+  // loads that do not depend on the adapters first
+  const int id_mine = th < kRows ? adapter_of(a, row0 + th, false) : -1;
+  if (out) load_base(static_cast<int64_t>(group) * per_cta * kCols);
+  tile_adapters(ta, id_mine);
+  // the sum of the partials, in their order
+#pragma unroll 4
+  for (int k = th; k < kRows * R; k += kNT) {
+    const int row = k / R, j = k % R;
+    float v = 0.0f;
+    if (row0 + row < a.T) {
+      const int64_t at = (row0 + row) * r + j;
+      if (j < r)
+        for (int s = 0; s < splits; ++s) v = __fadd_rn(v, __ldcg(part + s * a.T * r + at));
+      if (group == 0) {
+        if (w_out && j < r) w_out[at] = v;
+        if (w_terms) write_terms<RP>(w_terms, n_terms, a.T, row0 + row, j, v);
+      }
+    }
+    const int id = ta.ids[row];
+    split_bf16(id >= 0 ? __fmul_rn(__ldg(scaling + id), v) : 0.0f, hh[row * (R + 8) + j], hl[row * (R + 8) + j]);
+  }
+  if (!out) return;   // only the sum was asked for
+  const int id_lo = ta.ids[my_row], id_hi = ta.ids[my_row + 8];
+
+  for (int i = 0; i < per_cta; ++i) {
+    const int64_t c0 = (static_cast<int64_t>(group) * per_cta + i) * kCols;
+    if (c0 >= C) break;
+    if (i > 0) load_base(c0);
     for (int u = 0; u < ta.count; ++u) {
       const int id = ta.list[u];
       const __nv_bfloat16* w = W + static_cast<int64_t>(id) * r * C;
-      __syncthreads();   // the previous weights have been read
+      if (i > 0 || u > 0) __syncthreads();   // the previous weights have been read
       if constexpr (!TRANS) {
-        for (int k = th; k < kCols * (R / 8); k += kNT) {
-          const int c = k / (R / 8), c8 = k % (R / 8);
+#pragma unroll
+        for (int x = 0; x < RP; ++x) {
+          const int k = th + kNT * x, c = k / (R / 8), c8 = k % (R / 8);
           const bool ok = c0 + c < C && 8 * c8 < r;
           copy16(ws + mma_slot(c) * (R + 8) + 8 * c8, ok ? w + (c0 + c) * r + 8 * c8 : w, ok);
         }
-        cp_async_commit();
-        cp_async_wait<0>();
       } else {
-        // transposed on the way: two rows j, j + 1 of eight columns give
-        // eight words (j, j + 1) of those columns
-        for (int k = th; k < (R / 2) * (kCols / 8); k += kNT) {
-          const int j = 2 * (k / (kCols / 8)), c8 = k % (kCols / 8);
-          uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-          if (j < r && c0 + 8 * c8 < C) {   // r is even
-            lo = __ldg(reinterpret_cast<const uint4*>(w + j * C + c0 + 8 * c8));
-            hi = __ldg(reinterpret_cast<const uint4*>(w + (j + 1) * C + c0 + 8 * c8));
-          }
-          const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
+        // pairs of columns, each to its slot
+        const int c = 2 * (th & 63), slot = mma_slot(c);
+        const bool col_ok = c0 + c < C;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint32_t*>(ws + mma_slot(8 * c8 + e) * (R + 8) + j) =
-                __byte_perm(l[e >> 1], h[e >> 1], (e & 1) ? 0x7632 : 0x5410);
+        for (int x = 0; x < R / 4; ++x) {
+          const int j = (th >> 6) + 4 * x;
+          const bool ok = col_ok && j < r;
+          copy4(ws + j * (kCols + 8) + slot, ok ? w + j * C + c0 + c : w, ok);
         }
       }
+      cp_async_commit();
+      cp_async_wait<0>();
       __syncthreads();
       const bool lo_mine = id_lo == id, hi_mine = id_hi == id;
       if (!__any_sync(0xFFFFFFFFu, lo_mine || hi_mine)) continue;
-      const float s = __ldg(scaling + id);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {   // 32 columns each
+      for (int q = 0; q < 2; ++q) {   // 32 columns each
         float acc[4][4] = {};
 #pragma unroll
         for (int kk = 0; kk < R; kk += 16) {
           uint32_t ah[4], al[4], b0[4], b1[4];
           ldsm4(ah, hh + (16 * rg + (lane & 15)) * (R + 8) + kk + (lane >> 4) * 8);
           ldsm4(al, hl + (16 * rg + (lane & 15)) * (R + 8) + kk + (lane >> 4) * 8);
-          const __nv_bfloat16* wq = ws + (128 * ch + 32 * q + (lane & 7) + ((lane >> 4) << 3)) * (R + 8) + kk + ((lane >> 3) & 1) * 8;
-          ldsm4(b0, wq);
-          ldsm4(b1, wq + 16 * (R + 8));
+          if constexpr (!TRANS) {
+            const __nv_bfloat16* wq = ws + (64 * ch + 32 * q + (lane & 7) + ((lane >> 4) << 3)) * (R + 8) + kk + ((lane >> 3) & 1) * 8;
+            ldsm4(b0, wq);
+            ldsm4(b1, wq + 16 * (R + 8));
+          } else {
+            const __nv_bfloat16* wq = ws + (kk + (lane & 7) + ((lane >> 3) & 1) * 8) * (kCols + 8) + 64 * ch + 32 * q + (lane >> 4) * 8;
+            ldsm4_t(b0, wq);
+            ldsm4_t(b1, wq + 16);
+          }
           mma16(acc[0], al, b0);
           mma16(acc[1], al, b0 + 2);
           mma16(acc[2], al, b1);
@@ -415,26 +474,24 @@ __global__ void __launch_bounds__(kNT, RP <= 4 ? 3 : 2)
           mma16(acc[2], ah, b1);
           mma16(acc[3], ah, b1 + 2);
         }
+        // a token without an adapter keeps the base's bits (a NaN's payload, a zero's sign)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          // a token without an adapter keeps the base's bits (a NaN's payload, a zero's sign)
           if (half ? hi_mine : lo_mine) {
-            float d[8];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              d[2 * m] = __fmul_rn(s, acc[m][2 * half]);
-              d[2 * m + 1] = __fmul_rn(s, acc[m][2 * half + 1]);
-            }
-            y[q][half] = add_round(y[q][half], d);
+            uint4& v = y[q][half];
+            v.x = add_round(v.x, acc[0][2 * half], acc[0][2 * half + 1]);
+            v.y = add_round(v.y, acc[1][2 * half], acc[1][2 * half + 1]);
+            v.z = add_round(v.z, acc[2][2 * half], acc[2][2 * half + 1]);
+            v.w = add_round(v.w, acc[3][2 * half], acc[3][2 * half + 1]);
           }
         }
       }
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 2; ++q) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int64_t t = ta_row + 8 * half, c = c_mine + 32 * q;
+        const int64_t t = row0 + my_row + 8 * half, c = c0 + my_col + 32 * q;
         if (c < C && t < a.T) __stcs(reinterpret_cast<uint4*>(out + t * ldo + c), y[q][half]);
       }
     }
@@ -620,7 +677,7 @@ __global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __res
         const float vv[4] = {v.x, v.y, v.z, v.w};
         __nv_bfloat16 h[4], l[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split_bf16(vv[e], h[e], l[e]);
+        for (int e = 0; e < 4; ++e) split_bf16(__fmul_rn(s, vv[e]), h[e], l[e]);
         ah[p][half] = pack_bf16(h[0], h[1]);
         ah[p][2 + half] = pack_bf16(h[2], h[3]);
         al[p][half] = pack_bf16(l[0], l[1]);
@@ -646,13 +703,11 @@ __global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __res
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        float d[8];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          d[2 * m] = __fmul_rn(s, acc[m][2 * half]);
-          d[2 * m + 1] = __fmul_rn(s, acc[m][2 * half + 1]);
-        }
-        y[q][half] = add_round(y[q][half], d);
+        uint4& v = y[q][half];
+        v.x = add_round(v.x, acc[0][2 * half], acc[0][2 * half + 1]);
+        v.y = add_round(v.y, acc[1][2 * half], acc[1][2 * half + 1]);
+        v.z = add_round(v.z, acc[2][2 * half], acc[2][2 * half + 1]);
+        v.w = add_round(v.w, acc[3][2 * half], acc[3][2 * half + 1]);
       }
     }
   }
@@ -673,10 +728,11 @@ __global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __res
 // stored [r, C]) and dB (z = dy, w = h, stored [C, r]).
 // grid: column tiles of both products, adapter, split of the rows.
 // TERMS: bf16 numbers that w enters as: 3 (all of fp32) for fp32 gradients,
-// 2 (2^-17) for bf16 ones.
+// 2 (2^-17) for bf16 ones.  They were written by the kernels before this one,
+// once for all column tiles.
 // ---------------------------------------------------------------------------
 struct OuterProduct {
-  const float* w;
+  const __nv_bfloat16* w;   // [TERMS][T][16 RP]
   const __nv_bfloat16* z;
   int64_t ldz, C;
   void* dst;
@@ -698,10 +754,11 @@ struct OuterCfg {
   static constexpr int NQ = RP <= 2 ? 2 : 1;          // 16-column groups of a warp
   static constexpr int COLS = 8 * 16 * NQ;            // columns of a tile
   static constexpr int ZB = kRows * (COLS + 8) * 2;
-  static constexpr int FB = kRows * R * 4;            // w as it is in memory
   static constexpr int HB = kRows * (R + 8) * 2;
-  static constexpr int STAGES = 2;
-  static constexpr int BYTES = STAGES * (ZB + FB) + TERMS * HB;
+  static constexpr int STAGE = ZB + TERMS * HB;
+  static constexpr int CTAS = RP <= 2 ? 2 : 1;        // per SM
+  static constexpr int STAGES = (CTAS == 2 ? 104 : 208) * 1024 / STAGE;
+  static constexpr int BYTES = STAGES * STAGE;
 };
 constexpr int kWindow = 2048;   // rows whose ids a CTA looks at together
 
@@ -711,10 +768,11 @@ __device__ __forceinline__ void store_out(void* dst, int64_t at, float v, bool f
 }
 
 template <int RP, int TERMS>
-__global__ void __launch_bounds__(kNT, RP <= 2 ? 2 : 1) lora_outer_kernel(const OuterArgs o) {
+__global__ void __launch_bounds__(kNT, OuterCfg<RP, TERMS>::CTAS) lora_outer_kernel(const OuterArgs o) {
   pdl_entry();
   using S = OuterCfg<RP, TERMS>;
-  constexpr int R = S::R, COLS = S::COLS, NQ = S::NQ;
+  constexpr int R = S::R, COLS = S::COLS, NQ = S::NQ, ST = S::STAGES;
+  static_assert(ST >= 2, "a ring");
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ __align__(16) int ids[kWindow];
   __shared__ int list[kWindow / kRows];
@@ -727,7 +785,12 @@ __global__ void __launch_bounds__(kNT, RP <= 2 ? 2 : 1) lora_outer_kernel(const 
   const int tiles = static_cast<int>((o.a.T + kRows - 1) / kRows);
   const int first = static_cast<int>(static_cast<int64_t>(tiles) * split / splits);
   const int last = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / splits);
-  __nv_bfloat16* wb = reinterpret_cast<__nv_bfloat16*>(dyn + S::STAGES * (S::ZB + S::FB));
+  // this thread copies one 16-byte chunk of rows zrow, zrow + kRowStep, ..
+  constexpr int kRowStep = kNT / (COLS / 8);
+  const int zrow = th / (COLS / 8), zch = th % (COLS / 8);
+  const bool zcol_ok = c0 + 8 * zch < p.C;
+  const __nv_bfloat16* zbase = p.z + c0 + 8 * zch;
+  const int64_t zstep = kRowStep * p.ldz;
 
   float sum[RP][2 * NQ][4];
 #pragma unroll
@@ -758,48 +821,42 @@ __global__ void __launch_bounds__(kNT, RP <= 2 ? 2 : 1) lora_outer_kernel(const 
     const int count = listed;
     any |= count > 0;
 
-    auto load = [&](int k) {
+    auto load = [&](int k, int slot) {
       const int tile = list[k];
-      uint8_t* st = dyn + (k & 1) * (S::ZB + S::FB);
+      uint8_t* st = dyn + slot * S::STAGE;
       const int64_t row0 = row_base + static_cast<int64_t>(tile) * kRows;
+      const __nv_bfloat16* src = zbase + (row0 + zrow) * p.ldz;
+      const int* idr = ids + tile * kRows + zrow;
+      uint8_t* to = st + zrow * (COLS + 8) * 2 + 16 * zch;
 #pragma unroll
-      for (int i = 0; i < kRows * COLS / 8 / kNT; ++i) {
-        const int e = th + kNT * i, row = e / (COLS / 8), ch = e % (COLS / 8);
-        const bool ok = ids[tile * kRows + row] == id && c0 + 8 * ch < p.C;
-        copy16(st + row * (COLS + 8) * 2 + 16 * ch, ok ? p.z + (row0 + row) * p.ldz + c0 + 8 * ch : p.z, ok);
+      for (int i = 0; i < kRows / kRowStep; ++i) {
+        const bool ok = zcol_ok && idr[kRowStep * i] == id;
+        copy16(to + i * kRowStep * (COLS + 8) * 2, ok ? src + i * zstep : p.z, ok);
       }
-      for (int e = th; e < kRows * (R / 4); e += kNT) {
-        const int row = e / (R / 4), j4 = e % (R / 4);
-        const bool ok = ids[tile * kRows + row] == id && 4 * j4 < r;
-        copy16(st + S::ZB + row * R * 4 + 16 * j4, ok ? p.w + (row0 + row) * r + 4 * j4 : p.w, ok);
+      for (int e = th; e < TERMS * kRows * (R / 8); e += kNT) {
+        const int x = e / (kRows * (R / 8)), row = e / (R / 8) % kRows, ch = e % (R / 8);
+        const bool ok = ids[tile * kRows + row] == id;
+        copy16(st + S::ZB + x * S::HB + row * (R + 8) * 2 + 16 * ch,
+               ok ? p.w + (x * o.a.T + row0 + row) * R + 8 * ch : p.w, ok);
       }
       cp_async_commit();
     };
-    if (count > 0) load(0);
-    for (int k = 0; k < count; ++k) {
-      if (k + 1 < count) load(k + 1);
-      else cp_async_commit();
-      cp_async_wait<1>();
-      __syncthreads();
-      const uint8_t* st = dyn + (k & 1) * (S::ZB + S::FB);
-      const float* wf = reinterpret_cast<const float*>(st + S::ZB);
-      for (int e = th; e < kRows * R / 2; e += kNT) {   // pairs of ranks
-        const int row = e / (R / 2), j = 2 * (e % (R / 2));
-        const float2 v = *reinterpret_cast<const float2*>(wf + row * R + j);
-        __nv_bfloat16 s0[3], s1[3];
-        if constexpr (TERMS == 3) {
-          split_bf16(v.x, s0[0], s0[1], s0[2]);
-          split_bf16(v.y, s1[0], s1[1], s1[2]);
-        } else {
-          split_bf16(v.x, s0[0], s0[1]);
-          split_bf16(v.y, s1[0], s1[1]);
-        }
 #pragma unroll
-        for (int x = 0; x < TERMS; ++x)
-          *reinterpret_cast<uint32_t*>(wb + x * (S::HB / 2) + row * (R + 8) + j) = pack_bf16(s0[x], s1[x]);
-      }
-      __syncthreads();
+    for (int k = 0; k < ST - 1; ++k) {
+      if (k < count) load(k, k);
+      else cp_async_commit();
+    }
+    int slot = 0, ahead = ST - 1;
+    for (int k = 0; k < count; ++k) {
+      cp_async_wait<ST - 2>();   // this tile has landed
+      __syncthreads();           // for every thread, and the tile before it has been read
+      if (k + ST - 1 < count) load(k + ST - 1, ahead);
+      else cp_async_commit();
+      const uint8_t* st = dyn + slot * S::STAGE;
+      if (++slot == ST) slot = 0;
+      if (++ahead == ST) ahead = 0;
       const __nv_bfloat16* zs = reinterpret_cast<const __nv_bfloat16*>(st);
+      const __nv_bfloat16* wb = reinterpret_cast<const __nv_bfloat16*>(st + S::ZB);
 #pragma unroll
       for (int m = 0; m < RP; ++m) {
         float acc[2 * NQ][4];
@@ -827,7 +884,6 @@ __global__ void __launch_bounds__(kNT, RP <= 2 ? 2 : 1) lora_outer_kernel(const 
 #pragma unroll
           for (int e = 0; e < 4; ++e) sum[m][q][e] = __fadd_rn(sum[m][q][e], acc[q][e]);
       }
-      __syncthreads();   // this stage and wb are rewritten in the next round
     }
     cp_async_wait<0>();
   }
@@ -895,20 +951,20 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Units that T tokens and n adapters (and "none") can make.
 int64_t most_units(int64_t T, int64_t n) { return std::min<int64_t>(n + 1, T) + T / 16; }
 
-// Columns per shrink split: one wave of two CTAs per SM, whole stages; with
-// few tokens about eight small CTAs per SM, whole 128-column rounds.
+// Columns per shrink split: one wave of three CTAs per SM, with few tokens
+// about eight small CTAs per SM; whole 128-column stages.
 int64_t shrink_per_split(int64_t T, int64_t C, int64_t n) {
   const bool few = T <= kFewTokens;
   const int64_t rows = few ? most_units(T, n) : ceil_div(T, kRows);
-  const int64_t step = few ? 128 : 256;
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(few ? 16 : 32, (few ? 8 : 2) * sm_count() / rows));
+  const int64_t step = 128;
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(few ? 16 : 32, (few ? 8 : 3) * sm_count() / rows));
   return ceil_div(ceil_div(C, splits), step) * step;
 }
 int shrink_splits(int64_t T, int64_t C, int64_t n) { return static_cast<int>(ceil_div(C, shrink_per_split(T, C, n))); }
 // The backward pass shrinks with the tile kernel for any T.
 int64_t tile_per_split(int64_t T, int64_t C) {
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(32, 2 * sm_count() / ceil_div(T, kRows)));
-  return ceil_div(ceil_div(C, splits), 256) * 256;
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(32, 3 * sm_count() / ceil_div(T, kRows)));
+  return ceil_div(ceil_div(C, splits), 128) * 128;
 }
 int tile_splits(int64_t T, int64_t C) { return static_cast<int>(ceil_div(C, tile_per_split(T, C))); }
 
@@ -919,16 +975,19 @@ int outer_splits(int64_t T) { return static_cast<int>(std::max<int64_t>(1, std::
 
 // Parts of the workspace, in 16-byte steps.
 struct LoraWorkspace {
-  size_t part, sum, outer_a, outer_b, used, total;
+  size_t part, g_terms, h_terms, outer_a, outer_b, used, total;
 };
 size_t up16(size_t v) { return (v + 15) & ~static_cast<size_t>(15); }
+int64_t padded_rank(int64_t r) { return r <= 16 ? 16 : (r <= 32 ? 32 : (r <= 64 ? 64 : 128)); }
 LoraWorkspace lora_workspace(int64_t T, int64_t K, int64_t N, int64_t r, int64_t n, bool backward) {
   LoraWorkspace w{};
   w.part = 0;
-  w.sum = up16(static_cast<size_t>(backward ? tile_splits(T, N) : shrink_splits(T, K, n)) * T * r * 4);
-  w.total = w.sum;
+  w.total = up16(static_cast<size_t>(backward ? tile_splits(T, N) : shrink_splits(T, K, n)) * T * r * 4);
   if (backward) {
-    w.outer_a = w.sum + up16(static_cast<size_t>(T) * r * 4);
+    const size_t terms = up16(static_cast<size_t>(3 * T) * padded_rank(r) * 2);
+    w.g_terms = w.total;
+    w.h_terms = w.g_terms + terms;
+    w.outer_a = w.h_terms + terms;
     const int s = outer_splits(T);
     const size_t each = s > 1 ? static_cast<size_t>(s) * n * r * 4 : 0;
     w.outer_b = w.outer_a + up16(each * K);
@@ -950,14 +1009,15 @@ cudaError_t allow_smem(F fn, int bytes, bool* done) {
 
 template <int RP, bool TRANS>
 cudaError_t shrink(const __nv_bfloat16* z, int64_t ldz, const __nv_bfloat16* W, const AdapterIds& a, int64_t C, int r,
-                   float* part, cudaStream_t st) {
+                   float* part, const float* h, __nv_bfloat16* h_terms, int n_terms, cudaStream_t st) {
   auto fn = lora_shrink_kernel<RP, TRANS>;
   constexpr int smem = ShrinkCfg<RP, TRANS>::BYTES;
   static bool done[64] = {false};
   cudaError_t e = allow_smem(fn, smem, done);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(ceil_div(a.T, kRows)), static_cast<unsigned>(tile_splits(a.T, C)));
-  e = launch_k(fn, grid, dim3(kNT), smem, st, 1u, z, ldz, W, a, C, r, tile_per_split(a.T, C), part);
+  e = launch_k(fn, grid, dim3(kNT), smem, st, 1u, z, ldz, W, a, C, r, tile_per_split(a.T, C), part, h,
+               h_terms, n_terms);
   note_launch();
   return e;
 }
@@ -965,18 +1025,19 @@ cudaError_t shrink(const __nv_bfloat16* z, int64_t ldz, const __nv_bfloat16* W, 
 template <int RP, bool TRANS>
 cudaError_t expand(const float* part, int splits, const __nv_bfloat16* W, const float* scaling, const AdapterIds& a,
                    int64_t C, int r, const __nv_bfloat16* in, int64_t ldi, __nv_bfloat16* out, int64_t ldo, float* w_out,
-                   cudaStream_t st) {
+                   __nv_bfloat16* w_terms, int n_terms, cudaStream_t st) {
   auto fn = lora_expand_kernel<RP, TRANS>;
-  constexpr int smem = ExpandCfg<RP>::BYTES;
+  constexpr int smem = ExpandCfg<RP, TRANS>::BYTES;
   static bool done[64] = {false};
   cudaError_t e = allow_smem(fn, smem, done);
   if (e != cudaSuccess) return e;
-  // up to four column tiles share one sum of the partials, as long as the
+  // up to eight column tiles share one sum of the partials, as long as the
   // grid still fills the GPU a few times over
   const int64_t rows = ceil_div(a.T, kRows), cols = ceil_div(C, kCols);
-  const int per = out ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, rows * cols / (12 * sm_count())))) : 1;
-  const dim3 grid(static_cast<unsigned>(rows), out ? static_cast<unsigned>(ceil_div(cols, per)) : 1u);
-  e = launch_k(fn, grid, dim3(kNT), smem, st, 1u, part, splits, W, scaling, a, C, r, per, in, ldi, out, ldo, w_out);
+  const int per = out ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, rows * cols / (8 * sm_count())))) : 1;
+  const int64_t groups = out ? ceil_div(cols, per) : 1;
+  e = launch_k(fn, dim3(static_cast<unsigned>(rows * groups)), dim3(kNT), smem, st, 1u, part, splits, W, scaling, a, C, r, per,
+               static_cast<int>(groups), in, ldi, out, ldo, w_out, w_terms, n_terms);
   note_launch();
   return e;
 }
@@ -1005,9 +1066,10 @@ cudaError_t forward(const LoraArgs& l, float* part, cudaStream_t st) {
   const AdapterIds a{l.ids, l.T, static_cast<int>(l.n), l.status};
   const int r = static_cast<int>(l.r);
   if (l.T > kFewTokens) {
-    const cudaError_t e = shrink<RP, false>(l.x, l.ldx, l.A, a, l.K, r, part, st);
+    const cudaError_t e = shrink<RP, false>(l.x, l.ldx, l.A, a, l.K, r, part, nullptr, nullptr, 0, st);
     if (e != cudaSuccess) return e;
-    return expand<RP, false>(part, tile_splits(l.T, l.K), l.B, l.scaling, a, l.N, r, l.in, l.ldi, l.out, l.ldo, l.h, st);
+    return expand<RP, false>(part, tile_splits(l.T, l.K), l.B, l.scaling, a, l.N, r, l.in, l.ldi, l.out, l.ldo, l.h,
+                             nullptr, 0, st);
   }
   const unsigned units = static_cast<unsigned>(most_units(l.T, l.n));
   const int splits = shrink_splits(l.T, l.K, l.n);
@@ -1024,21 +1086,24 @@ cudaError_t forward(const LoraArgs& l, float* part, cudaStream_t st) {
 template <int RP>
 cudaError_t backward(const LoraArgs& l, uint8_t* ws, const LoraWorkspace& w, cudaStream_t st) {
   const AdapterIds a{l.ids, l.T, static_cast<int>(l.n), l.status};
-  const int r = static_cast<int>(l.r);
+  const int r = static_cast<int>(l.r), n_terms = l.fp32 ? 3 : 2;
   float* part = reinterpret_cast<float*>(ws + w.part);
-  float* g = reinterpret_cast<float*>(ws + w.sum);
+  __nv_bfloat16* g_terms = reinterpret_cast<__nv_bfloat16*>(ws + w.g_terms);
+  __nv_bfloat16* h_terms = reinterpret_cast<__nv_bfloat16*>(ws + w.h_terms);
+  // the shrink also writes h's terms, so it runs even where dB alone is asked for
+  cudaError_t e = shrink<RP, true>(l.dy, l.lddy, l.B, a, l.N, r, part, l.h, l.dB ? h_terms : nullptr, n_terms, st);
+  if (e != cudaSuccess) return e;
   if (l.out || l.dA) {
-    cudaError_t e = shrink<RP, true>(l.dy, l.lddy, l.B, a, l.N, r, part, st);
-    if (e != cudaSuccess) return e;
-    e = expand<RP, true>(part, tile_splits(l.T, l.N), l.A, l.scaling, a, l.K, r, l.in, l.ldi, l.out, l.ldo, g, st);
+    e = expand<RP, true>(part, tile_splits(l.T, l.N), l.A, l.scaling, a, l.K, r, l.in, l.ldi, l.out, l.ldo, nullptr,
+                         l.dA ? g_terms : nullptr, n_terms, st);
     if (e != cudaSuccess) return e;
   }
   if (!l.dA && !l.dB) return cudaSuccess;
   const int cols = outer_cols(l.r);
   OuterArgs o{};
-  o.p[0] = OuterProduct{g, l.x, l.ldx, l.K, l.dA, reinterpret_cast<float*>(ws + w.outer_a),
+  o.p[0] = OuterProduct{g_terms, l.x, l.ldx, l.K, l.dA, reinterpret_cast<float*>(ws + w.outer_a),
                         l.dA ? static_cast<int>(ceil_div(l.K, cols)) : 0, 0};
-  o.p[1] = OuterProduct{l.h, l.dy, l.lddy, l.N, l.dB, reinterpret_cast<float*>(ws + w.outer_b),
+  o.p[1] = OuterProduct{h_terms, l.dy, l.lddy, l.N, l.dB, reinterpret_cast<float*>(ws + w.outer_b),
                         l.dB ? static_cast<int>(ceil_div(l.N, cols)) : 0, 1};
   o.scaling = l.scaling;
   o.a = a;
