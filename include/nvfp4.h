@@ -415,7 +415,8 @@ NVFP4_API size_t nvfp4_grouped_workspace_size(int64_t E);
  *     NVFP4_HEADROOM; scales are always written in the GEMM layout
  *     (NVFP4_GEMM_SCALE_LAYOUT is accepted and changes nothing).
  *   out: codes and scales as above; alpha_row, alpha_col: E floats; amax_out:
- *     optional, 2 E floats (rows' maxima, then columns'); status: optional.
+ *     optional, 2 E floats (rows' maxima, then columns'), may be the
+ *     workspace; status: optional.
  * C % 64 == 0, with NVFP4_COLWISE C % 128 == 0; ld % 8 == 0; x, codes, scales
  * and the workspace 16-byte aligned; stream_id + E <= 2^31; a NaN or Inf in
  * any group sets NVFP4_ERR_NONFINITE. */

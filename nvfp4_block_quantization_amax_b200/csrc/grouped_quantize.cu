@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "nvfp4_device.cuh"
 #include "block_modes.cuh"
@@ -84,24 +85,50 @@ struct TileRun {
   }
 };
 
-// Tile -> (group, tile row within the group, tile column).
+// Tile -> (group, tile row within the group, tile column).  A group's tiles
+// are walked in bands of four tile rows, down a band's rows first, then along
+// its columns: four 32-byte pieces of a column's codes and, two columns on,
+// two 64-byte pieces of a row's complete 128-byte lines within a few tiles of
+// one CTA.  (Row by row, columns first, each column piece was a partial line
+// of its own: decoding 16301 x 14336 column codes took 202 us.)
+constexpr int kBand = 4;
 struct GroupTile {
   int e, tr;
   uint32_t tc;
 };
 __device__ __forceinline__ GroupTile group_tile(const GroupTable& g, uint32_t tile, uint32_t tiles_c) {
-  const uint32_t u = tile / tiles_c;
-  const int e = find_group(g.pa, g.E, static_cast<int>(u));
-  return GroupTile{e, static_cast<int>(u) - g.pa[e], tile - u * tiles_c};
+  const int e = find_group(g.pa, g.E, static_cast<int>(tile / tiles_c));
+  const uint32_t local = tile - static_cast<uint32_t>(g.pa[e]) * tiles_c;
+  const uint32_t n_tr = static_cast<uint32_t>(g.pa[e + 1] - g.pa[e]);
+  const uint32_t band = local / (kBand * tiles_c), in = local - band * kBand * tiles_c;
+  const uint32_t h = min(static_cast<uint32_t>(kBand), n_tr - band * kBand);
+  return GroupTile{e, static_cast<int>(band * kBand + in % h), in / h};
 }
 __device__ __forceinline__ void next_tile(const GroupTable& g, GroupTile& t, uint32_t tiles_c) {
+  const int n_tr = g.pa[t.e + 1] - g.pa[t.e];
+  const int start = t.tr & ~(kBand - 1);
+  if (++t.tr < min(start + kBand, n_tr)) return;
+  t.tr = start;
   if (++t.tc < tiles_c) return;
   t.tc = 0;
-  ++t.tr;
-  while (t.e + 1 < g.E && g.pa[t.e] + t.tr >= g.pa[t.e + 1]) {   // past this group's last tile row
+  t.tr = start + kBand;
+  while (t.e + 1 < g.E && t.tr >= g.pa[t.e + 1] - g.pa[t.e]) {   // past this group's last tile row
     ++t.e;
     t.tr = 0;
   }
+}
+
+// All threads of the cluster; what they wrote to shared memory before is
+// visible to the others after.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The word at this shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t load_cluster_u32(const uint32_t* p, int rank) {
+  uint32_t addr, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 // ---------------------------------------------------------------------------
@@ -407,78 +434,294 @@ __global__ void __launch_bounds__(TNT, 3) grouped_quantize_kernel(const GroupedA
 }
 
 // ---------------------------------------------------------------------------
-// decode
+// Few rows (a decode step's tokens), rowwise: one launch.  A cluster of eight
+// CTAs takes a group, each CTA an eighth of its columns; the CTAs' maxima are
+// exchanged through distributed shared memory and the rows, still in
+// registers where they fit, are encoded at once.  What it saves are launches:
+// clearing the maxima, the amax pass and the encoding pass were three of
+// 2 to 7 us each for 16 rows of 4096.
 // ---------------------------------------------------------------------------
-// 64 x 64 tiles of a group: a thread decodes one block of 16 (a row's or a
-// column's), the values pass through shared memory so that rows are written
-// in 16-byte pieces.
-template <bool INV, bool BF16, bool COL>
-__global__ void __launch_bounds__(256) grouped_dequantize_kernel(const uint8_t* __restrict__ codes,
-                                                                 const uint8_t* __restrict__ scales,
-                                                                 const float* __restrict__ alpha, int64_t T, int64_t C,
-                                                                 const int32_t* __restrict__ offsets, int E,
-                                                                 int64_t kcap, uint64_t seed, void* __restrict__ y,
-                                                                 int32_t* status) {
+constexpr int kFewRows = 64;        // rows (of all groups) up to which this path is taken
+constexpr int kFewGroups = 128;     // and groups: each costs a cluster, rows or not
+constexpr int kFewSplit = 8;        // CTAs of a cluster (the portable size)
+constexpr int kFewNT = 256;
+constexpr int kFewKept = 2;         // block pairs of a thread that stay in registers
+
+template <int MODE, bool ROT>
+__global__ void __launch_bounds__(kFewNT) grouped_quantize_few_kernel(const GroupedArgs a) {
   pdl_entry();
   extern __shared__ int table_mem[];
-  __shared__ __align__(16) float vals[64][68];
+  __shared__ uint32_t red[kFewNT / 32];
+  __shared__ uint32_t cta_max;
+  const GroupTable g = build_group_table<kFewNT>(a.offsets, a.E, a.T, TR, 128, table_mem, a.status, blockIdx.x == 0);
+  const int e = static_cast<int>(blockIdx.x) / kFewSplit, rank = static_cast<int>(blockIdx.x) % kFewSplit;
+  const int rows = g.rows(e), th = threadIdx.x;
+  if (rows == 0) {   // every CTA of the cluster leaves here
+    if (rank == 0 && th == 0) {
+      a.alpha_row[e] = 0.0f;
+      if (a.amax_out) a.amax_out[e] = 0.0f;
+    }
+    return;
+  }
+  const PhiloxKeys K = philox_keys(a.seed);
+  SignMasks sm;
+  if constexpr (ROT) {
+    sm = sign_masks(sign_bits(K));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sm.m[i] = 0u;
+  }
+  // pairs of neighbouring blocks (32 elements); C is a multiple of 64
+  const int pairs_row = static_cast<int>(a.C / 32);
+  const int first = pairs_row * rank / kFewSplit, width = pairs_row * (rank + 1) / kFewSplit - first;
+  const int total = rows * width;
+  const uint16_t* x = a.x + static_cast<int64_t>(g.off[e]) * a.ld;
+  auto load = [&](int k, uint4* u) {
+    const int r = k / width, p = first + k - r * width;
+    const uint4* src = reinterpret_cast<const uint4*>(x + r * a.ld + 32 * p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = __ldg(src + i);
+  };
+  auto values = [&](const uint4* u, float2* v) {
+    unpack16x2_signed(u[0], u[1], u[2], u[3], sm, v);
+    if constexpr (ROT) rht16x2_presigned(v);
+  };
+  uint4 kept[kFewKept][4];
+  uint32_t m = 0;
+  auto take_max = [&](const uint4* u) {
+    uint32_t hm = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hm = __vmaxu2(hm, u[i].x & 0x7FFF7FFFu);
+      hm = __vmaxu2(hm, u[i].y & 0x7FFF7FFFu);
+      hm = __vmaxu2(hm, u[i].z & 0x7FFF7FFFu);
+      hm = __vmaxu2(hm, u[i].w & 0x7FFF7FFFu);
+    }
+    const uint32_t h = max(hm & 0xFFFFu, hm >> 16);
+    uint32_t b = h << 16;
+    if constexpr (ROT) {
+      float2 v[16];
+      values(u, v);
+      float ma, mb;
+      max_abs16x2(v, ma, mb);
+      b = __float_as_uint(fmaxf(ma, mb));
+    }
+    m = max(m, h >= 0x7F80u ? kNonFinite : b);
+  };
+#pragma unroll
+  for (int i = 0; i < kFewKept; ++i)
+    if (th + i * kFewNT < total) load(th + i * kFewNT, kept[i]);
+#pragma unroll
+  for (int i = 0; i < kFewKept; ++i)
+    if (th + i * kFewNT < total) take_max(kept[i]);
+  for (int k = th + kFewKept * kFewNT; k < total; k += kFewNT) {
+    uint4 u[4];
+    load(k, u);
+    take_max(u);
+  }
+  m = block_max_u32<kFewNT>(m, red);
+  if (th == 0) cta_max = m;
+  cluster_barrier();
+  if (th < kFewSplit) m = max(m, load_cluster_u32(&cta_max, th));
+  m = block_max_u32<kFewNT>(m, red);
+  cluster_barrier();   // no CTA leaves while another may still read its word
+  const float amax = m == kNonFinite ? 0.0f : __uint_as_float(m);
+  const float al = __fdiv_rn(amax, (a.flags & kHeadroom) ? 1792.0f : 2688.0f);
+  if (rank == 0 && th == 0) {
+    a.alpha_row[e] = al;
+    if (a.amax_out) a.amax_out[e] = amax;
+    if (m == kNonFinite && a.status) *a.status = kStatusNonFinite;
+  }
+  const VecScales sc = make_vec_scales(al, al);
+  const uint32_t c2 = (a.stream_id + static_cast<uint32_t>(e)) * 2u;
+  const int64_t nbr = a.C / 16;
+  auto encode = [&](int k, const uint4* u) {
+    const int r = k / width, p = first + k - r * width;
+    float2 v[16];
+    values(u, v);
+    const int64_t blk = r * nbr + 2 * p;
+    Packed16 pa, pb;
+    uint32_t sa, sb;
+    quantize_pair<MODE>(v, sc, K, c2, static_cast<uint64_t>(blk), static_cast<uint64_t>(blk + 1), pa, pb, sa, sb);
+    *reinterpret_cast<uint4*>(a.codes_row + (static_cast<int64_t>(g.off[e]) + r) * (a.C / 2) + 16 * p) =
+        make_uint4(pa.lo, pa.hi, pb.lo, pb.hi);
+    // both scales lie in one 16-bit half of the four-scale word
+    *reinterpret_cast<uint16_t*>(a.scales_row + gemm_scale_offset(128 * static_cast<int64_t>(g.pb[e]) + r, 2 * p, nbr)) =
+        static_cast<uint16_t>(sa | (sb << 8));
+  };
+#pragma unroll
+  for (int i = 0; i < kFewKept; ++i)
+    if (th + i * kFewNT < total) encode(th + i * kFewNT, kept[i]);
+  for (int k = th + kFewKept * kFewNT; k < total; k += kFewNT) {
+    uint4 u[4];
+    load(k, u);
+    encode(k, u);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// decode.  Memory bounds it (0.5625 bytes in, 2 or 4 out per element); what
+// counts is that every warp store is whole and contiguous.
+// ---------------------------------------------------------------------------
+template <bool BF16>
+__device__ __forceinline__ void store8(void* y, int64_t at, const float* v) {   // eight values of a row
+  if constexpr (BF16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(y) + at);
+    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// Row operands: 64 x 256 tiles, a warp takes one row at a time, lane l the
+// elements 8 l .. 8 l + 7 (a 16-byte bf16 store).  With INV a lane takes two
+// rows' worth of one 16-element block instead, since the rotation mixes it.
+template <bool INV, bool BF16>
+__global__ void __launch_bounds__(256) grouped_dequantize_rows_kernel(const uint8_t* __restrict__ codes,
+                                                                      const uint8_t* __restrict__ scales,
+                                                                      const float* __restrict__ alpha, int64_t T,
+                                                                      int64_t C, const int32_t* __restrict__ offsets,
+                                                                      int E, uint64_t seed, void* __restrict__ y,
+                                                                      int32_t* status) {
+  pdl_entry();
+  extern __shared__ int table_mem[];
   const GroupTable g = build_group_table<256>(offsets, E, T, TR, 128, table_mem, status, blockIdx.x == 0);
-  const uint32_t tiles_c = static_cast<uint32_t>(C / 64);
+  const uint32_t tiles_c = static_cast<uint32_t>((C + 255) / 256);
   TileRun run(static_cast<uint32_t>(g.pa[E]) * tiles_c, blockIdx.x, gridDim.x);
   if (run.tile >= run.end) return;
   uint32_t signs = 0;
   if constexpr (INV) signs = sign_bits(philox_keys(seed));
   GroupTile t = group_tile(g, run.tile, tiles_c);
-  const int th = threadIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t katoms = C / 64;
   for (; run.tile < run.end; ++run.tile, next_tile(g, t, tiles_c)) {
     const int left = g.rows(t.e) - t.tr * TR;
     const int rows = left < TR ? left : TR;
-    const int64_t c0 = static_cast<int64_t>(t.tc) * 64;
-    const int i = th >> 2, b = th & 3;   // row (COL: column) i of the tile, its block b
-    if (COL || i < rows) {
-      uint2 p;
-      uint32_t sb;
-      if constexpr (COL) {
-        const int64_t kt = g.pa[t.e] + t.tr;
-        p = __ldg(reinterpret_cast<const uint2*>(codes + (c0 + i) * (kcap / 2) + 32 * kt + 8 * b));
-        sb = __ldg(scales + gemm_scale_offset(c0 + i, 4 * kt + b, kcap / 16));
-      } else {
-        const int64_t r = static_cast<int64_t>(t.tr) * TR + i;
-        p = __ldg(reinterpret_cast<const uint2*>(codes + (g.off[t.e] + r) * (C / 2) + c0 / 2 + 8 * b));
-        sb = __ldg(scales + gemm_scale_offset(128 * static_cast<int64_t>(g.pb[t.e]) + r, c0 / 16 + b, C / 16));
+    const float al = __ldg(alpha + t.e);
+    const int64_t row0 = static_cast<int64_t>(g.off[t.e]) + t.tr * TR;                  // in codes and y
+    const int64_t srow0 = 128 * static_cast<int64_t>(g.pb[t.e]) + t.tr * TR;            // in the scale layout
+    const uint8_t* sbase = scales + (srow0 >> 7) * katoms * 512 + ((srow0 >> 5) & 3) * 4;
+    if constexpr (!INV) {
+      const int64_t c = static_cast<int64_t>(t.tc) * 256 + 8 * lane;
+      const bool col_ok = c < C;
+      uint32_t w[8], sw[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {   // rows warp + 8 i
+        const int r = warp + 8 * i;
+        w[i] = sw[i] = 0u;
+        if (col_ok && r < rows) {
+          w[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + (row0 + r) * (C / 2) + c / 2));
+          // the four scales of 64 elements; row r of the half atom
+          sw[i] = __ldg(reinterpret_cast<const uint32_t*>(sbase + (c >> 6) * 512 + (r & 31) * 16 + (r >> 5) * 4));
+        }
       }
-      const float s = __fmul_rn(__ldg(alpha + t.e), e4m3_value(sb));
-      float v[16];
-      e2m1x8_values(p.x, v);
-      e2m1x8_values(p.y, v + 8);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], s);
-      if constexpr (INV) irht16(v, signs);
+      for (int i = 0; i < 8; ++i) {
+        const int r = warp + 8 * i;
+        const float s = __fmul_rn(al, e4m3_value((sw[i] >> (8 * ((lane >> 1) & 3))) & 0xFFu));
+        float v[8];
+        e2m1x8_values(w[i], v);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        if constexpr (COL) vals[16 * b + j][i] = v[j];
-        else vals[i][16 * b + j] = v[j];
+        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], s);
+        if (col_ok && r < rows) store8<BF16>(y, (row0 + r) * C + c, v);
+      }
+    } else {
+      const int64_t c = static_cast<int64_t>(t.tc) * 256 + 16 * (lane & 15);
+      if (c < C) {
+#pragma unroll 2
+        for (int r = 2 * warp + (lane >> 4); r < rows; r += 16) {
+          const uint2 p = __ldg(reinterpret_cast<const uint2*>(codes + (row0 + r) * (C / 2) + c / 2));
+          const float s = __fmul_rn(al, e4m3_value(__ldg(sbase + (c >> 6) * 512 + (r & 31) * 16 + (r >> 5) * 4 + ((c >> 4) & 3))));
+          float v[16];
+          e2m1x8_values(p.x, v);
+          e2m1x8_values(p.y, v + 8);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], s);
+          irht16(v, signs);
+          store8<BF16>(y, (row0 + r) * C + c, v);
+          store8<BF16>(y, (row0 + r) * C + c + 8, v + 8);
+        }
+      }
+    }
+  }
+}
+
+// Column operands: 64 x 128 tiles of the rows' frame.  A thread decodes one
+// 16-row block of two neighbouring columns and leaves them in shared memory
+// pairwise (a warp's stores cover 32 neighbouring pairs of one row), from
+// where rows are written whole.
+template <bool INV, bool BF16>
+__global__ void __launch_bounds__(256) grouped_dequantize_cols_kernel(const uint8_t* __restrict__ codes,
+                                                                      const uint8_t* __restrict__ scales,
+                                                                      const float* __restrict__ alpha, int64_t T,
+                                                                      int64_t C, const int32_t* __restrict__ offsets,
+                                                                      int E, int64_t kcap, uint64_t seed,
+                                                                      void* __restrict__ y, int32_t* status) {
+  using Pair = typename std::conditional<BF16, uint32_t, float2>::type;
+  constexpr int kPitch = TC / 2 + (BF16 ? 4 : 2);   // pairs: rows stay 16-byte aligned, and shift by a few banks
+  pdl_entry();
+  extern __shared__ int table_mem[];
+  __shared__ __align__(16) Pair vals[TR][kPitch];
+  const GroupTable g = build_group_table<256>(offsets, E, T, TR, 128, table_mem, status, blockIdx.x == 0);
+  const uint32_t tiles_c = static_cast<uint32_t>(C / TC);
+  TileRun run(static_cast<uint32_t>(g.pa[E]) * tiles_c, blockIdx.x, gridDim.x);
+  if (run.tile >= run.end) return;
+  uint32_t signs = 0;
+  if constexpr (INV) signs = sign_bits(philox_keys(seed));
+  GroupTile t = group_tile(g, run.tile, tiles_c);
+  const int th = threadIdx.x, warp = th >> 5, lane = th & 31;
+  const int pair = 32 * (warp >> 2) + lane, b = warp & 3;   // column pair and 16-row block
+  for (; run.tile < run.end; ++run.tile, next_tile(g, t, tiles_c)) {
+    const int left = g.rows(t.e) - t.tr * TR;
+    const int rows = left < TR ? left : TR;
+    const int64_t c0 = static_cast<int64_t>(t.tc) * TC, c = c0 + 2 * pair, kt = g.pa[t.e] + t.tr;
+    const float al = __ldg(alpha + t.e);
+    const uint8_t* src = codes + c * (kcap / 2) + 32 * kt + 8 * b;
+    const uint2 pa = __ldg(reinterpret_cast<const uint2*>(src)), pb = __ldg(reinterpret_cast<const uint2*>(src + kcap / 2));
+    const int64_t so = gemm_scale_offset(c, 4 * kt + b, kcap / 16);   // column c + 1: the next 16-byte line
+    const float sa = __fmul_rn(al, e4m3_value(__ldg(scales + so))), sb = __fmul_rn(al, e4m3_value(__ldg(scales + so + 16)));
+    float va[16], vb[16];
+    e2m1x8_values(pa.x, va);
+    e2m1x8_values(pa.y, va + 8);
+    e2m1x8_values(pb.x, vb);
+    e2m1x8_values(pb.y, vb + 8);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      va[j] = __fmul_rn(va[j], sa);
+      vb[j] = __fmul_rn(vb[j], sb);
+    }
+    if constexpr (INV) {
+      irht16(va, signs);
+      irht16(vb, signs);
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if constexpr (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(va[j], vb[j]);
+        vals[16 * b + j][pair] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        vals[16 * b + j][pair] = make_float2(va[j], vb[j]);
       }
     }
     __syncthreads();
+    constexpr int kPieces = TC * (BF16 ? 2 : 4) / 16;   // 16-byte pieces of a row
+    constexpr int kEach = 16 / (BF16 ? 2 : 4);          // their elements
     const int64_t row0 = static_cast<int64_t>(g.off[t.e]) + t.tr * TR;
-    if (i < rows) {   // 16 values of row i
-      const float* src = &vals[i][16 * b];
-      const int64_t off = (row0 + i) * C + c0 + 16 * b;
-      if constexpr (BF16) {
-        uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(src[2 * j], src[2 * j + 1]);
-          w[j] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + off);
-        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      } else {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(y) + off);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dst[j] = make_float4(src[4 * j], src[4 * j + 1], src[4 * j + 2], src[4 * j + 3]);
+    for (int i = 0; i < TR * kPieces / 256; ++i) {
+      const int k = th + 256 * i, r = k / kPieces, piece = k % kPieces;
+      if (r < rows) {
+        const int64_t at = (row0 + r) * C + c0 + kEach * piece;
+        uint4* dst = BF16 ? reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + at)
+                          : reinterpret_cast<uint4*>(static_cast<float*>(y) + at);
+        *dst = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(&vals[r][0]) + 16 * piece);
       }
     }
     __syncthreads();
@@ -538,18 +781,30 @@ cudaError_t launch_group_amax(const GroupedArgs& a, bool row, bool col, bool rot
   return e;
 }
 
+template <int MODE, bool ROT>
+cudaError_t launch_few(const GroupedArgs& a, cudaStream_t st) {
+  const cudaError_t e = launch_k(grouped_quantize_few_kernel<MODE, ROT>, dim3(static_cast<unsigned>(kFewSplit * a.E)),
+                                 dim3(kFewNT), group_table_bytes(a.E), st, kFewSplit, a);
+  note_launch();
+  return e;
+}
+
 template <bool INV, bool BF16>
 cudaError_t launch_decode(const uint8_t* codes, const uint8_t* scales, const float* alpha, int64_t T, int64_t C,
                           const int32_t* offsets, int E, bool col, uint64_t seed, void* y, int32_t* status,
                           cudaStream_t st) {
-  const int64_t kcap = grouped_capacity(T, E, 64);
-  const dim3 grid(grid_for(T, E, C / 64, 8));
   const size_t tab = group_table_bytes(E);
-  const cudaError_t e =
-      col ? launch_k(grouped_dequantize_kernel<INV, BF16, true>, grid, dim3(256), tab, st, 1u, codes, scales, alpha, T, C,
-                     offsets, E, kcap, seed, y, status)
-          : launch_k(grouped_dequantize_kernel<INV, BF16, false>, grid, dim3(256), tab, st, 1u, codes, scales, alpha, T, C,
-                     offsets, E, kcap, seed, y, status);
+  cudaError_t e;
+  if (col) {
+    static bool done[64] = {false};
+    auto fn = grouped_dequantize_cols_kernel<INV, BF16>;
+    if ((e = allow_smem(fn, static_cast<int>(group_table_bytes(kMaxGroups)), done)) != cudaSuccess) return e;
+    e = launch_k(fn, dim3(grid_for(T, E, C / TC, 8)), dim3(256), tab, st, 1u, codes, scales, alpha, T, C, offsets, E,
+                 grouped_capacity(T, E, 64), seed, y, status);
+  } else {
+    e = launch_k(grouped_dequantize_rows_kernel<INV, BF16>, dim3(grid_for(T, E, (C + 255) / 256, 8)), dim3(256), tab, st, 1u,
+                 codes, scales, alpha, T, C, offsets, E, seed, y, status);
+  }
   note_launch();
   return e;
 }
@@ -585,6 +840,15 @@ cudaError_t grouped_quantize_launch(const void* x, int64_t T, int64_t C, int64_t
   a.status = o.status;
   a.tiles_c = static_cast<uint32_t>((C + TC - 1) / TC);
   a.kcap = grouped_capacity(T, E, 64);
+  if (row && !col && T <= kFewRows && E <= kFewGroups) {
+    switch (mode) {
+      case kModeRTN: return rot ? launch_few<kModeRTN, true>(a, st) : launch_few<kModeRTN, false>(a, st);
+      case kModeFourSix: return rot ? launch_few<kModeFourSix, true>(a, st) : launch_few<kModeFourSix, false>(a, st);
+      case kModeRhtSR: return launch_few<kModeRhtSR, true>(a, st);
+      case kModeRhtSRHw: return launch_few<kModeRhtSRHw, true>(a, st);
+      default: return launch_few<kModeMsEden, true>(a, st);
+    }
+  }
   cudaError_t e = cudaMemsetAsync(workspace, 0, grouped_workspace_bytes(E), st);
   if (e != cudaSuccess) return e;
   if ((e = launch_group_amax(a, row, col, rot, st)) != cudaSuccess) return e;

@@ -135,6 +135,34 @@ def test_quantize_row_widths(api, C):
     check_quantize(api, rows_of(100, C, 13), [3, 97], MODES["rtn"], ROW)
 
 
+@pytest.mark.parametrize("mode", list(MODES))
+@pytest.mark.parametrize("counts,C", [([1], 64), ([3, 0, 1, 20], 192), ([0, 0, 64, 0], 4096), ([2] * 30, 14336 // 7),
+                                      ([5, 0, 40], 14336)])
+def test_quantize_few_rows(api, mode, counts, C):
+    """Rowwise and at most 64 rows: the single-launch path, every mode."""
+    x = rows_of(sum(counts) + 2, C, 17)
+    check_quantize(api, x, counts, MODES[mode], ROW, first=1)
+    check_quantize(api, x, counts, MODES[mode], ROW | RHT | HEADROOM, first=1)
+
+
+def test_quantize_few_rows_strided_and_nonfinite(api):
+    x = rows_of(12, 512, 18)
+    wide = torch.zeros((12, 648), dtype=torch.bfloat16, device="cuda")
+    wide[:, 64:576] = x.cuda()
+    got = api.nvfp4_quantize_grouped(wide[:, 64:576], offsets_of([5, 0, 7]), 1, ROW)
+    want = check_quantize(api, x, [5, 0, 7], 1, ROW, seed=0, sid=0)
+    assert torch.equal(got.codes_row, want.codes_row) and torch.equal(got.alpha_row, want.alpha_row)
+    for flags in (ROW, ROW | RHT):
+        y = x.clone()
+        y[9, 500] = float("nan")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        q = api.nvfp4_quantize_grouped(y.cuda(), offsets_of([5, 0, 7]), 0, flags, status=st)
+        assert st.item() == -4 and float(q.alpha_row[0]) > 0.0
+        st.zero_()
+        api.nvfp4_quantize_grouped(y.cuda(), offsets_of([5, 0, 4]), 0, flags, status=st)
+        assert st.item() == 0
+
+
 def test_quantize_strided_rows_and_rows_of_no_group(api):
     x = rows_of(90, 512, 14)
     wide = torch.zeros((90, 640), dtype=torch.bfloat16, device="cuda")
