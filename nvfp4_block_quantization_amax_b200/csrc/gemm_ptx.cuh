@@ -293,15 +293,15 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t kbytes, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 2D map over the output D [M, N] (row stride ldd elements): boxes of 16 rows
-// x 128 bytes (64 bf16 or 32 fp32 columns), 128-byte swizzle, for TMA stores.
-bool make_out_map(CUtensorMap* map, void* base, int64_t M, int64_t N, int64_t ldd, bool fp32) {
+// 2D map over the output D [M, N] (row stride ldd elements): boxes of 16 (or
+// box_rows) rows x 128 bytes (64 bf16 or 32 fp32 columns), 128-byte swizzle, for TMA stores.
+bool make_out_map(CUtensorMap* map, void* base, int64_t M, int64_t N, int64_t ldd, bool fp32, int box_rows = 16) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t esize = fp32 ? 4 : 2;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldd) * esize};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esize), 16};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esize), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,

@@ -35,10 +35,18 @@ constexpr int G_SF = KB_PER_STAGE * 512;            // scales of 128 rows, 256 K
 constexpr int G_STAGE = 2 * G_STAGE_AB + 3 * G_SF;  // A, B, own A scales, all 256 B rows' scales
 constexpr int G_EPI_WARPS = 8;
 constexpr int G_THREADS = 64 + 32 * G_EPI_WARPS;
-constexpr int G_OUT = G_EPI_WARPS * 2048;
 constexpr int G_TABLE = static_cast<int>(group_table_bytes(kMaxGroups));
-constexpr int G_STAGES = (232448 - G_OUT - 1024 - 512 - G_TABLE) / G_STAGE;
-constexpr int G_SMEM = G_STAGES * G_STAGE + G_OUT + 1024 + 512 + G_TABLE;
+// Output staging.  Where the output outweighs the operands (fp32 results,
+// weight gradients of few tokens each) a warp has two 32-row boxes and the
+// ring gives up a stage for them; otherwise one 16-row box.
+template <bool WGRAD, bool FP32>
+struct GroupedCfg {
+  static constexpr bool WIDE = WGRAD || FP32;
+  static constexpr int BOX = WIDE ? 4096 : 2048;
+  static constexpr int OUT = G_EPI_WARPS * BOX * (WIDE ? 2 : 1);
+  static constexpr int STAGES = (232448 - OUT - 1024 - 512 - 1024 - G_TABLE) / G_STAGE;
+  static constexpr int SMEM = STAGES * G_STAGE + OUT + 1024 + 512 + G_TABLE;
+};
 constexpr uint32_t G_SF_W = 12, G_SF_COL = 256, G_TMEM_COLS = 512;
 // M = 256, N = 256, E2M1 x E2M1, E4M3 scales
 constexpr uint32_t G_IDESC = (1u << 7) | (1u << 10) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
@@ -111,6 +119,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                               const __grid_constant__ CUtensorMap tmap_d, const __grid_constant__ CUtensorMap tmap_sfa,
                               const __grid_constant__ CUtensorMap tmap_sfb, const GroupedGemm p) {
   pdl_entry();
+  using GC = GroupedCfg<WGRAD, FP32>;
+  constexpr int G_STAGES = GC::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -118,7 +128,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   uint8_t* sSFA = sB + G_STAGES * G_STAGE_AB;
   uint8_t* sSFB = sSFA + G_STAGES * G_SF;
   uint8_t* sOut = sSFB + G_STAGES * 2 * G_SF;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + G_OUT);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + GC::OUT);
   uint64_t* full = bars;
   uint64_t* empty = bars + G_STAGES;
   uint64_t* acc_full = bars + 2 * G_STAGES;
@@ -126,7 +136,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   uint64_t* drain = bars + 2 * G_STAGES + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * G_STAGES + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* table_mem = reinterpret_cast<int*>(sOut + G_OUT + 512);
+  int* table_mem = reinterpret_cast<int*>(sOut + GC::OUT + 512);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -250,7 +260,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   } else {
     // ---------------- epilogue (warps 2..9 of both CTAs) ----------------
     const int q = warp & 3, h = (warp - 2) >> 2;
-    uint8_t* buf = sOut + (warp - 2) * 2048;
+    uint8_t* buf = sOut + (warp - 2) * (GC::OUT / G_EPI_WARPS);
+    uint32_t box = 0;   // WIDE: the staging box used next
     const uint32_t acc_empty_leader = map_to_rank(smem_u32(acc_empty), 0);
     uint32_t acc_ph = 0;
     for (int tile = pair; tile < num_tiles; tile += num_pairs) {
@@ -267,33 +278,56 @@ __global__ void __launch_bounds__(G_THREADS, 1)
       const int col0 = t.col0 + 128 * h;
       const bool store = 128 * h < t.cols && left > 0;
       const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * h;
-      // one 16-row x 128-byte box (w: this lane's 32 words): a whole box by
-      // TMA through the warp's staging buffer, a ragged one lane by lane
+      // 128 bytes of each of the warp's rows (w: this lane's row): whole boxes
+      // by TMA through the staging, ragged ones lane by lane
       auto put = [&](const uint32_t* w, int col, int64_t byte_col) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (left >= 16 * half + 16) {
-            if (lane == 0) bulk_wait_read<0>();   // the previous box has been read
+        if constexpr (GC::WIDE) {
+          if (left >= 32) {
+            if (lane == 0) bulk_wait_read<1>();   // the box before the previous one has been read
             __syncwarp();
-            if ((lane >> 4) == half) {
-              uint8_t* rowp = buf + (lane & 15) * 128;
+            uint8_t* rowp = buf + box * GC::BOX + lane * 128;
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) =
-                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-            }
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) =
+                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&tmap_d, smem_u32(buf), col, row0 + 16 * half);
+              tma_store_2d(&tmap_d, smem_u32(buf + box * GC::BOX), col, row0);
               bulk_commit();
             }
-          } else if ((lane >> 4) == half && lane < left) {
-            uint8_t* dst = static_cast<uint8_t*>(p.D) + (static_cast<int64_t>(row0) + lane) * p.ldd * (FP32 ? 4 : 2) + byte_col;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              reinterpret_cast<uint4*>(dst)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            box ^= 1;
+            return;
           }
+        } else {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (left >= 16 * half + 16) {
+              if (lane == 0) bulk_wait_read<0>();   // the previous box has been read
+              __syncwarp();
+              if ((lane >> 4) == half) {
+                uint8_t* rowp = buf + (lane & 15) * 128;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) =
+                      make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(&tmap_d, smem_u32(buf), col, row0 + 16 * half);
+                bulk_commit();
+              }
+            }
+          }
+        }
+        // the rows of a box that is not whole
+        const int boxed = GC::WIDE ? 0 : (left >= 32 ? 32 : (left >= 16 ? 16 : 0));
+        if (lane >= boxed && lane < left) {
+          uint8_t* dst = static_cast<uint8_t*>(p.D) + (static_cast<int64_t>(row0) + lane) * p.ldd * (FP32 ? 4 : 2) + byte_col;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            reinterpret_cast<uint4*>(dst)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         }
       };
       if constexpr (!FP32) {
@@ -325,24 +359,25 @@ __global__ void __launch_bounds__(G_THREADS, 1)
           put(packed + 32, col0 + 64, 2 * static_cast<int64_t>(col0 + 64));
         }
       } else {
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t r[32];
-          if (zero) {
+        // the whole row goes to registers, so the accumulator is handed back
+        // before anything is stored
+        uint32_t r[128];
+        if (zero) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = 0u;
-          } else {
-            tmem_ld32_nowait(taddr + c, r);
-            tmem_ld_wait();
-            if (c + 32 == 128) {
-              fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
-            }
+          for (int j = 0; j < 128; ++j) r[j] = 0u;
+        } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__fmul_rn(__uint_as_float(r[j]), ab));
-          }
-          if (store) put(r, col0 + c, 4 * static_cast<int64_t>(col0 + c));
+          for (int c = 0; c < 128; c += 32) tmem_ld32_nowait(taddr + c, r + c);
+          tmem_ld_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
+#pragma unroll
+          for (int j = 0; j < 128; ++j) r[j] = __float_as_uint(__fmul_rn(__uint_as_float(r[j]), ab));
+        }
+        if (store) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) put(r + c, col0 + c, 4 * static_cast<int64_t>(col0 + c));
         }
       }
     }
@@ -368,12 +403,12 @@ cudaError_t launch_grouped(const CUtensorMap& ma, const CUtensorMap& mb, const C
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !done[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, G_SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, GroupedCfg<WGRAD, FP32>::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev] = true;
   }
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(most_tiles, sm_count() / 2));
-  const cudaError_t e = launch_k(fn, dim3(static_cast<unsigned>(2 * pairs)), dim3(G_THREADS), G_SMEM, st, 2u, ma, mb, md,
+  const cudaError_t e = launch_k(fn, dim3(static_cast<unsigned>(2 * pairs)), dim3(G_THREADS), GroupedCfg<WGRAD, FP32>::SMEM, st, 2u, ma, mb, md,
                                  msa, msb, p);
   note_launch();
   return e;
@@ -396,7 +431,7 @@ cudaError_t grouped_gemm_launch(const uint8_t* A, const uint8_t* sA, const float
   CUtensorMap ma, mb, md, msa, msb;
   if (!make_map(&ma, A, T, K / 2, 128) || !make_map(&mb, B, E * N, K / 2, 128) ||
       !make_sf_map(&msa, sA, grouped_capacity(T, E, 128), K) || !make_sf_map(&msb, sB, E * N, K) ||
-      !make_out_map(&md, D, T, N, ldd, fp32))
+      !make_out_map(&md, D, T, N, ldd, fp32, fp32 ? 32 : 16))
     return cudaErrorInvalidValue;
   const int64_t n_tiles = (N + 255) / 256;
   GroupedGemm p{alphaA, alphaB, offsets, static_cast<int>(E), T, 0, static_cast<int>(N), static_cast<int>(K),
@@ -414,7 +449,7 @@ cudaError_t grouped_wgrad_launch(const uint8_t* A, const uint8_t* sA, const floa
   if (kcap == 0) return cudaMemsetAsync(D, 0, static_cast<size_t>(E * M * N) * (fp32 ? 4 : 2), st);   // no token at all
   CUtensorMap ma, mb, md, msa, msb;
   if (!make_map(&ma, A, M, kcap / 2, 128) || !make_map(&mb, B, N, kcap / 2, 128) || !make_sf_map(&msa, sA, M, kcap) ||
-      !make_sf_map(&msb, sB, N, kcap) || !make_out_map(&md, D, E * M, N, N, fp32))
+      !make_sf_map(&msb, sB, N, kcap) || !make_out_map(&md, D, E * M, N, N, fp32, 32))
     return cudaErrorInvalidValue;
   const int64_t n_tiles = (N + 255) / 256, m_tiles = (M + 255) / 256;
   GroupedGemm p{alphaA, alphaB, offsets, static_cast<int>(E), T, static_cast<int>(M), static_cast<int>(N), 0,

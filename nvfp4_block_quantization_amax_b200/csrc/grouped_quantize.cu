@@ -678,15 +678,32 @@ __global__ void __launch_bounds__(256) grouped_dequantize_cols_kernel(const uint
   GroupTile t = group_tile(g, run.tile, tiles_c);
   const int th = threadIdx.x, warp = th >> 5, lane = th & 31;
   const int pair = 32 * (warp >> 2) + lane, b = warp & 3;   // column pair and 16-row block
-  for (; run.tile < run.end; ++run.tile, next_tile(g, t, tiles_c)) {
+  // the next tile's codes and scales are on their way while this one is
+  // written (8 bytes per column and thread leave little in flight otherwise)
+  struct Column {
+    uint2 p;
+    uint32_t s;
+  } na, nb;
+  auto fetch = [&](const GroupTile& f) {
+    const int64_t c = static_cast<int64_t>(f.tc) * TC + 2 * pair, kt = g.pa[f.e] + f.tr;
+    const uint8_t* src = codes + c * (kcap / 2) + 32 * kt + 8 * b;
+    const uint8_t* sc = scales + gemm_scale_offset(c, 4 * kt + b, kcap / 16);   // column c + 1: the next 16-byte line
+    na.p = __ldg(reinterpret_cast<const uint2*>(src));
+    nb.p = __ldg(reinterpret_cast<const uint2*>(src + kcap / 2));
+    na.s = __ldg(sc);
+    nb.s = __ldg(sc + 16);
+  };
+  fetch(t);
+  GroupTile ahead = t;
+  for (; run.tile < run.end; ++run.tile, t = ahead) {
     const int left = g.rows(t.e) - t.tr * TR;
     const int rows = left < TR ? left : TR;
-    const int64_t c0 = static_cast<int64_t>(t.tc) * TC, c = c0 + 2 * pair, kt = g.pa[t.e] + t.tr;
+    const int64_t c0 = static_cast<int64_t>(t.tc) * TC;
     const float al = __ldg(alpha + t.e);
-    const uint8_t* src = codes + c * (kcap / 2) + 32 * kt + 8 * b;
-    const uint2 pa = __ldg(reinterpret_cast<const uint2*>(src)), pb = __ldg(reinterpret_cast<const uint2*>(src + kcap / 2));
-    const int64_t so = gemm_scale_offset(c, 4 * kt + b, kcap / 16);   // column c + 1: the next 16-byte line
-    const float sa = __fmul_rn(al, e4m3_value(__ldg(scales + so))), sb = __fmul_rn(al, e4m3_value(__ldg(scales + so + 16)));
+    const uint2 pa = na.p, pb = nb.p;
+    const float sa = __fmul_rn(al, e4m3_value(na.s)), sb = __fmul_rn(al, e4m3_value(nb.s));
+    next_tile(g, ahead, tiles_c);
+    if (run.tile + 1 < run.end) fetch(ahead);
     float va[16], vb[16];
     e2m1x8_values(pa.x, va);
     e2m1x8_values(pa.y, va + 8);
