@@ -293,8 +293,9 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t kbytes, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 2D map over the output D [M, N] (row stride ldd elements): boxes of 16 (or
-// box_rows) rows x 128 bytes (64 bf16 or 32 fp32 columns), 128-byte swizzle, for TMA stores.
+// 2D map over the output D [M, N] (row stride ldd elements): boxes of box_rows
+// rows x 128 bytes (64 bf16 or 32 fp32 columns), 128-byte swizzle, for TMA
+// stores.
 bool make_out_map(CUtensorMap* map, void* base, int64_t M, int64_t N, int64_t ldd, bool fp32, int box_rows = 16) {
   auto fn = encode_fn();
   if (!fn) return false;

@@ -36,17 +36,22 @@ constexpr int G_STAGE = 2 * G_STAGE_AB + 3 * G_SF;  // A, B, own A scales, all 2
 constexpr int G_EPI_WARPS = 8;
 constexpr int G_THREADS = 64 + 32 * G_EPI_WARPS;
 constexpr int G_TABLE = static_cast<int>(group_table_bytes(kMaxGroups));
-// Output staging.  Where the output outweighs the operands (fp32 results,
-// weight gradients of few tokens each) a warp has two 32-row boxes and the
-// ring gives up a stage for them; otherwise one 16-row box.
-template <bool WGRAD, bool FP32>
+// Output staging: a 16-row x 128-byte box per epilogue warp, or (WIDE) two of
+// 32 rows, for which the operand ring gives up one of its five stages.
+// Measured, narrow against wide, 14336 x 4096 outputs per group: weight
+// gradient of 8 x 2048 tokens fp32 614 / 707 us, bf16 475 / 551; of 8 x 256
+// tokens fp32 385 / 410, bf16 236 / 214; 64 groups of 62 tokens, 1408 x 2048,
+// fp32 171 / 164, bf16 111 / 88.  So the wide form is for bf16 weight
+// gradients of few tokens per group.  (Plain stores of whole 128-byte lines
+// by the threads were slower than the narrow boxes nearly everywhere.)
+template <bool WIDE>
 struct GroupedCfg {
-  static constexpr bool WIDE = WGRAD || FP32;
   static constexpr int BOX = WIDE ? 4096 : 2048;
   static constexpr int OUT = G_EPI_WARPS * BOX * (WIDE ? 2 : 1);
   static constexpr int STAGES = (232448 - OUT - 1024 - 512 - 1024 - G_TABLE) / G_STAGE;
   static constexpr int SMEM = STAGES * G_STAGE + OUT + 1024 + 512 + G_TABLE;
 };
+constexpr int64_t kWideTokens = 512;   // tokens per group, on average, up to which bf16 weight gradients are wide
 constexpr uint32_t G_SF_W = 12, G_SF_COL = 256, G_TMEM_COLS = 512;
 // M = 256, N = 256, E2M1 x E2M1, E4M3 scales
 constexpr uint32_t G_IDESC = (1u << 7) | (1u << 10) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
@@ -113,13 +118,13 @@ __device__ __forceinline__ TileAt locate(const GroupTable& g, const GroupedGemm&
   return t;
 }
 
-template <bool WGRAD, bool FP32>
+template <bool WGRAD, bool FP32, bool WIDE>
 __global__ void __launch_bounds__(G_THREADS, 1)
     nvfp4_grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                               const __grid_constant__ CUtensorMap tmap_d, const __grid_constant__ CUtensorMap tmap_sfa,
                               const __grid_constant__ CUtensorMap tmap_sfb, const GroupedGemm p) {
   pdl_entry();
-  using GC = GroupedCfg<WGRAD, FP32>;
+  using GC = GroupedCfg<WIDE>;
   constexpr int G_STAGES = GC::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -263,6 +268,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     uint8_t* buf = sOut + (warp - 2) * (GC::OUT / G_EPI_WARPS);
     uint32_t box = 0;   // WIDE: the staging box used next
     const uint32_t acc_empty_leader = map_to_rank(smem_u32(acc_empty), 0);
+    const int64_t row_bytes = p.ldd * (FP32 ? 4 : 2);
     uint32_t acc_ph = 0;
     for (int tile = pair; tile < num_tiles; tile += num_pairs) {
       const TileAt t = locate<WGRAD>(g, p, tile, n_tiles);
@@ -278,18 +284,21 @@ __global__ void __launch_bounds__(G_THREADS, 1)
       const int col0 = t.col0 + 128 * h;
       const bool store = 128 * h < t.cols && left > 0;
       const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * h;
-      // 128 bytes of each of the warp's rows (w: this lane's row): whole boxes
-      // by TMA through the staging, ragged ones lane by lane
-      auto put = [&](const uint32_t* w, int col, int64_t byte_col) {
-        if constexpr (GC::WIDE) {
+      // 128 bytes of each of the warp's rows (w: this lane's row)
+      auto put = [&](const uint32_t* w, int col) {
+        auto stage = [&](uint8_t* rowp) {   // this lane's row into a box, 16-byte chunks swizzled by the row
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        };
+        uint8_t* out = static_cast<uint8_t*>(p.D) + static_cast<int64_t>(row0) * row_bytes + (FP32 ? 4 : 2) * static_cast<int64_t>(col);
+        int boxed = 0;   // rows that left as whole boxes
+        if constexpr (WIDE) {
           if (left >= 32) {
             if (lane == 0) bulk_wait_read<1>();   // the box before the previous one has been read
             __syncwarp();
-            uint8_t* rowp = buf + box * GC::BOX + lane * 128;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) =
-                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            stage(buf + box * GC::BOX + lane * 128);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -297,7 +306,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
               bulk_commit();
             }
             box ^= 1;
-            return;
+            boxed = 32;
           }
         } else {
 #pragma unroll
@@ -305,29 +314,21 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             if (left >= 16 * half + 16) {
               if (lane == 0) bulk_wait_read<0>();   // the previous box has been read
               __syncwarp();
-              if ((lane >> 4) == half) {
-                uint8_t* rowp = buf + (lane & 15) * 128;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) =
-                      make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-              }
+              if ((lane >> 4) == half) stage(buf + (lane & 15) * 128);
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
                 tma_store_2d(&tmap_d, smem_u32(buf), col, row0 + 16 * half);
                 bulk_commit();
               }
+              boxed = 16 * half + 16;
             }
           }
         }
-        // the rows of a box that is not whole
-        const int boxed = GC::WIDE ? 0 : (left >= 32 ? 32 : (left >= 16 ? 16 : 0));
-        if (lane >= boxed && lane < left) {
-          uint8_t* dst = static_cast<uint8_t*>(p.D) + (static_cast<int64_t>(row0) + lane) * p.ldd * (FP32 ? 4 : 2) + byte_col;
+        if (lane >= boxed && lane < left) {   // the rows of a box that is not whole, lane by lane
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            reinterpret_cast<uint4*>(dst)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            reinterpret_cast<uint4*>(out + lane * row_bytes)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         }
       };
       if constexpr (!FP32) {
@@ -355,8 +356,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
           if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
         }
         if (store) {
-          put(packed, col0, 2 * static_cast<int64_t>(col0));
-          put(packed + 32, col0 + 64, 2 * static_cast<int64_t>(col0 + 64));
+          put(packed, col0);
+          put(packed + 32, col0 + 64);
         }
       } else {
         // the whole row goes to registers, so the accumulator is handed back
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         }
         if (store) {
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) put(r + c, col0 + c, 4 * static_cast<int64_t>(col0 + c));
+          for (int c = 0; c < 128; c += 32) put(r + c, col0 + c);
         }
       }
     }
@@ -395,21 +396,21 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   }
 }
 
-template <bool WGRAD, bool FP32>
+template <bool WGRAD, bool FP32, bool WIDE>
 cudaError_t launch_grouped(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md, const CUtensorMap& msa,
                            const CUtensorMap& msb, const GroupedGemm& p, int64_t most_tiles, cudaStream_t st) {
-  auto fn = nvfp4_grouped_gemm_kernel<WGRAD, FP32>;
+  auto fn = nvfp4_grouped_gemm_kernel<WGRAD, FP32, WIDE>;
   static bool done[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !done[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, GroupedCfg<WGRAD, FP32>::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, GroupedCfg<WIDE>::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev] = true;
   }
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(most_tiles, sm_count() / 2));
-  const cudaError_t e = launch_k(fn, dim3(static_cast<unsigned>(2 * pairs)), dim3(G_THREADS), GroupedCfg<WGRAD, FP32>::SMEM, st, 2u, ma, mb, md,
-                                 msa, msb, p);
+  const cudaError_t e = launch_k(fn, dim3(static_cast<unsigned>(2 * pairs)), dim3(G_THREADS), GroupedCfg<WIDE>::SMEM, st, 2u, ma,
+                                 mb, md, msa, msb, p);
   note_launch();
   return e;
 }
@@ -431,14 +432,14 @@ cudaError_t grouped_gemm_launch(const uint8_t* A, const uint8_t* sA, const float
   CUtensorMap ma, mb, md, msa, msb;
   if (!make_map(&ma, A, T, K / 2, 128) || !make_map(&mb, B, E * N, K / 2, 128) ||
       !make_sf_map(&msa, sA, grouped_capacity(T, E, 128), K) || !make_sf_map(&msb, sB, E * N, K) ||
-      !make_out_map(&md, D, T, N, ldd, fp32, fp32 ? 32 : 16))
+      !make_out_map(&md, D, T, N, ldd, fp32))
     return cudaErrorInvalidValue;
   const int64_t n_tiles = (N + 255) / 256;
   GroupedGemm p{alphaA, alphaB, offsets, static_cast<int>(E), T, 0, static_cast<int>(N), static_cast<int>(K),
                 static_cast<int>(K / 64), raster_group(K, n_tiles), D, ldd, status};
   const int64_t most = grouped_capacity(T, E, 256) / 256 * n_tiles;
-  return fp32 ? launch_grouped<false, true>(ma, mb, md, msa, msb, p, most, st)
-              : launch_grouped<false, false>(ma, mb, md, msa, msb, p, most, st);
+  return fp32 ? launch_grouped<false, true, false>(ma, mb, md, msa, msb, p, most, st)
+              : launch_grouped<false, false, false>(ma, mb, md, msa, msb, p, most, st);
 }
 
 cudaError_t grouped_wgrad_launch(const uint8_t* A, const uint8_t* sA, const float* alphaA, const uint8_t* B,
@@ -447,16 +448,19 @@ cudaError_t grouped_wgrad_launch(const uint8_t* A, const uint8_t* sA, const floa
   const bool fp32 = out_dtype == NVFP4_OUT_DTYPE_FP32;
   const int64_t kcap = grouped_capacity(T, E, 64);
   if (kcap == 0) return cudaMemsetAsync(D, 0, static_cast<size_t>(E * M * N) * (fp32 ? 4 : 2), st);   // no token at all
+  const bool wide = !fp32 && T <= kWideTokens * E;
   CUtensorMap ma, mb, md, msa, msb;
   if (!make_map(&ma, A, M, kcap / 2, 128) || !make_map(&mb, B, N, kcap / 2, 128) || !make_sf_map(&msa, sA, M, kcap) ||
-      !make_sf_map(&msb, sB, N, kcap) || !make_out_map(&md, D, E * M, N, N, fp32, 32))
+      !make_sf_map(&msb, sB, N, kcap) ||
+      !make_out_map(&md, D, E * M, N, N, fp32, wide ? 32 : 16))
     return cudaErrorInvalidValue;
   const int64_t n_tiles = (N + 255) / 256, m_tiles = (M + 255) / 256;
   GroupedGemm p{alphaA, alphaB, offsets, static_cast<int>(E), T, static_cast<int>(M), static_cast<int>(N), 0,
                 static_cast<int>(kcap / 64), raster_group(std::max<int64_t>(64, T / E), n_tiles), D, N, status};
   const int64_t most = E * m_tiles * n_tiles;
-  return fp32 ? launch_grouped<true, true>(ma, mb, md, msa, msb, p, most, st)
-              : launch_grouped<true, false>(ma, mb, md, msa, msb, p, most, st);
+  if (fp32) return launch_grouped<true, true, false>(ma, mb, md, msa, msb, p, most, st);
+  return wide ? launch_grouped<true, false, true>(ma, mb, md, msa, msb, p, most, st)
+              : launch_grouped<true, false, false>(ma, mb, md, msa, msb, p, most, st);
 }
 
 }  // namespace nvfp4
