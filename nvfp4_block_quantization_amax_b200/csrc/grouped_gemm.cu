@@ -396,6 +396,257 @@ __global__ void __launch_bounds__(G_THREADS, 1)
   }
 }
 
+// ===========================================================================
+// Few rows per group (decode, small experts): the roles are swapped.  128 rows
+// of the weight are the MMA's M and up to 128 tokens of a group its N, so no
+// tensor-core row and no load is spent on tokens that are not there: N is
+// rounded up to 16 tile by tile, and a tile of up to 32 tokens loads 32 rows.
+// One CTA per SM; what bounds it is the weights' stream from memory, so the
+// ring holds as many stages as fit, and two accumulators let the next tile
+// start while the epilogue drains this one.
+// D^T comes out of the MMA: lane n of the accumulator is a weight row, column
+// j a token; a warp stores 64 (bf16) or 128 (fp32) contiguous bytes per token.
+// ===========================================================================
+constexpr int F_STAGE_W = 128 * BK_BYTES, F_STAGE_X = 128 * BK_BYTES;   // weight rows, token rows
+constexpr int F_STAGE = F_STAGE_W + F_STAGE_X + 2 * G_SF;
+constexpr int F_STAGES = (232448 - 1024 - 512 - 1024 - G_TABLE) / F_STAGE;
+constexpr int F_SMEM = F_STAGES * F_STAGE + 1024 + 512 + G_TABLE;
+constexpr int F_THREADS = 192;      // producer, MMA, four epilogue warps
+constexpr int F_SMALL = 32;         // tokens up to which a tile loads F_SMALL rows
+constexpr uint32_t F_ACC = 128;     // columns of an accumulator
+constexpr uint32_t F_SF_COL = 2 * F_ACC, F_SF_W = 8, F_TMEM_COLS = 512;
+constexpr uint32_t F_IDESC = (1u << 7) | (1u << 10) | ((128u >> 4) << 24);   // M = 128; N >> 3 at bit 17
+
+struct FewAt {
+  int e, tn, tokens;    // group, weight tile, tokens of this tile
+  int w_row, x_row;     // first rows of the operands
+  int sfw, sfx;         // first scale atoms
+};
+
+__device__ __forceinline__ FewAt locate_few(const GroupTable& g, const GroupedGemm& p, int tile, int n_tiles) {
+  FewAt t;
+  t.e = find_group(g.pb, g.E, tile / n_tiles);
+  const int m_tiles = g.pb[t.e + 1] - g.pb[t.e], local = tile - g.pb[t.e] * n_tiles;
+  t.tn = local / m_tiles;
+  const int tm = local - t.tn * m_tiles;   // token tiles of one weight tile follow one another: it stays in L2
+  t.tokens = min(128, g.rows(t.e) - 128 * tm);
+  t.w_row = t.e * p.N + 128 * t.tn;
+  t.x_row = g.off[t.e] + 128 * tm;
+  t.sfw = (t.e * n_tiles + t.tn) * p.katoms_a;
+  t.sfx = (g.pb[t.e] + tm) * p.katoms_a;
+  return t;
+}
+
+template <bool FP32>
+__global__ void __launch_bounds__(F_THREADS, 1)
+    nvfp4_grouped_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+                                  const __grid_constant__ CUtensorMap tmap_x_small,
+                                  const __grid_constant__ CUtensorMap tmap_sfw,
+                                  const __grid_constant__ CUtensorMap tmap_sfx, const GroupedGemm p) {
+  pdl_entry();
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sW = smem;
+  uint8_t* sX = sW + F_STAGES * F_STAGE_W;
+  uint8_t* sSFW = sX + F_STAGES * F_STAGE_X;
+  uint8_t* sSFX = sSFW + F_STAGES * G_SF;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sSFX + F_STAGES * G_SF);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + F_STAGES;
+  uint64_t* acc_full = bars + 2 * F_STAGES;        // [2]
+  uint64_t* acc_empty = bars + 2 * F_STAGES + 2;   // [2]
+  uint64_t* drain = bars + 2 * F_STAGES + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * F_STAGES + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* table_mem = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 512);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < F_STAGES; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&acc_full[i]), 1);
+      mbar_init(smem_u32(&acc_empty[i]), 4);   // one arrival per epilogue warp
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(F_TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  const GroupTable g =
+      build_group_table<F_THREADS>(p.offsets, p.E, p.T, 128, 128, table_mem, p.status, blockIdx.x == 0);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int n_tiles = p.N / 128, num_tiles = g.pb[p.E] * n_tiles;
+  const int kblocks = p.K / 64, kstages = (kblocks + KB_PER_STAGE - 1) / KB_PER_STAGE;
+
+  if (warp == 0) {
+    // ---------------- producer ----------------
+    if (elect_one()) {
+      int it = 0, s = 0;
+      uint32_t ph = 0;
+      bool stop = false;
+      for (int tile = blockIdx.x; tile < num_tiles && !stop; tile += gridDim.x) {
+        const FewAt t = locate_few(g, p, tile, n_tiles);
+        const bool small = t.tokens <= F_SMALL;
+        const uint32_t bytes = F_STAGE_W + 2 * G_SF + (small ? F_SMALL : 128) * BK_BYTES;
+        for (int kt = 0; kt < kstages; ++kt, ++it) {
+          if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1, abort_flag)) {
+            stop = true;
+            break;
+          }
+          const uint32_t fb = smem_u32(&full[s]);
+          mbar_expect_tx(fb, bytes);
+          tma_load_2d(smem_u32(sW + s * F_STAGE_W), &tmap_w, kt * BK_BYTES, t.w_row, fb);
+          tma_load_2d(smem_u32(sX + s * F_STAGE_X), small ? &tmap_x_small : &tmap_x, kt * BK_BYTES, t.x_row, fb);
+          tma_load_2d(smem_u32(sSFW + s * G_SF), &tmap_sfw, 0, (t.sfw + KB_PER_STAGE * kt) * 2, fb);
+          tma_load_2d(smem_u32(sSFX + s * G_SF), &tmap_sfx, 0, (t.sfx + KB_PER_STAGE * kt) * 2, fb);
+          if (++s == F_STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (*abort_flag) {
+        // a wait gave up somewhere: let the copies already issued land before
+        // the CTA exits (each wait again bounded)
+        for (int i = (it > F_STAGES ? it - F_STAGES : 0); i < it; ++i)
+          mbar_wait_bounded(smem_u32(&full[i % F_STAGES]), (i / F_STAGES) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    if (elect_one()) {
+      int s = 0, buf = 0;
+      uint32_t full_ph = 0, acc_ph = 0, set = 0;
+      bool stop = false;
+      for (int tile = blockIdx.x; tile < num_tiles && !stop; tile += gridDim.x) {
+        const FewAt t = locate_few(g, p, tile, n_tiles);
+        const uint32_t idesc = F_IDESC | ((static_cast<uint32_t>((t.tokens + 15) & ~15) >> 3) << 17);
+        // the epilogue must have drained this accumulator's previous tile
+        if (!mbar_wait(smem_u32(&acc_empty[buf]), acc_ph ^ 1, abort_flag)) break;
+        fence_after();
+        const uint32_t acc = tmem + buf * F_ACC;
+        for (int kt = 0; kt < kstages; ++kt) {
+          if (!mbar_wait(smem_u32(&full[s]), full_ph, abort_flag)) {
+            stop = true;
+            break;
+          }
+          fence_after();
+          const uint32_t sfw = smem_u32(sSFW + s * G_SF), sfx = smem_u32(sSFX + s * G_SF);
+          const uint64_t wdesc = desc_sw128(smem_u32(sW + s * F_STAGE_W));
+          const uint64_t xdesc = desc_sw128(smem_u32(sX + s * F_STAGE_X));
+          const int nk = min(KB_PER_STAGE, kblocks - KB_PER_STAGE * kt);
+          for (int kk = 0; kk < nk; ++kk) {
+            const uint32_t col = tmem + F_SF_COL + (set + kk) * F_SF_W;
+            tmem_cp_sf(col, desc_sf(sfw + 512 * kk));
+            tmem_cp_sf(col + 4, desc_sf(sfx + 512 * kk));
+            mma_mxf4nvf4(acc, wdesc + 2 * kk, xdesc + 2 * kk, idesc, (kt > 0 || kk > 0) ? 1u : 0u, col, col + 4);
+          }
+          set ^= KB_PER_STAGE;
+          umma_commit(smem_u32(&empty[s]));
+          if (kt == kstages - 1) umma_commit(smem_u32(&acc_full[buf]));
+          if (++s == F_STAGES) {
+            s = 0;
+            full_ph ^= 1;
+          }
+        }
+        buf ^= 1;
+        if (buf == 0) acc_ph ^= 1;
+      }
+      if (*abort_flag) {
+        // MMAs already issued may still run: let them finish (bounded) before
+        // TMEM is freed
+        umma_commit(smem_u32(drain));
+        mbar_wait_bounded(smem_u32(drain), 0);
+      }
+    }
+  } else {
+    // ---------------- epilogue (warps 2..5) ----------------
+    const int q = warp & 3;
+    int buf = 0;
+    uint32_t acc_ph = 0;
+    for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
+      const FewAt t = locate_few(g, p, tile, n_tiles);
+      const float ab = __fmul_rn(__ldg(p.alpha_a + t.e), __ldg(p.alpha_b + t.e));
+      if (!mbar_wait(smem_u32(&acc_full[buf]), acc_ph, abort_flag)) break;
+      fence_after();
+      const uint32_t taddr = tmem + buf * F_ACC + (static_cast<uint32_t>(32 * q) << 16);
+      const int64_t n = 128 * static_cast<int64_t>(t.tn) + 32 * q + lane;   // this lane's output column
+      for (int c = 0; c < t.tokens; c += 32) {
+        uint32_t r[32];
+        tmem_ld32_nowait(taddr + c, r);
+        tmem_ld_wait();
+        if (c + 32 >= t.tokens) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&acc_empty[buf]));
+        }
+        const int64_t row = t.x_row + c;
+        if constexpr (FP32) {
+          float* out = static_cast<float*>(p.D) + row * p.ldd + n;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c + j < t.tokens) out[j * p.ldd] = __fmul_rn(__uint_as_float(r[j]), ab);
+        } else {
+          // neighbouring lanes exchange, so that an even lane holds two
+          // columns of token j and an odd one of token j + 1
+          const bool odd = lane & 1;
+          uint16_t* out = static_cast<uint16_t*>(p.D) + row * p.ldd + (n & ~int64_t(1));
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float v0 = __fmul_rn(__uint_as_float(r[j]), ab), v1 = __fmul_rn(__uint_as_float(r[j + 1]), ab);
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
+            const __nv_bfloat162 b2 = odd ? __floats2bfloat162_rn(got, v1) : __floats2bfloat162_rn(v0, got);
+            const int tok = j + (odd ? 1 : 0);
+            if (c + tok < t.tokens) *reinterpret_cast<uint32_t*>(out + tok * p.ldd) = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+        }
+      }
+      buf ^= 1;
+      if (buf == 0) acc_ph ^= 1;
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag && p.status) *p.status = kStatusTimeout;
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(F_TMEM_COLS) : "memory");
+  }
+}
+
+// Tokens per group, on average, up to which the swapped form is taken.
+constexpr int64_t kFewTokensPerGroup = 160;
+
+template <bool FP32>
+cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& mxs, const CUtensorMap& msw,
+                       const CUtensorMap& msx, const GroupedGemm& p, int64_t most_tiles, cudaStream_t st) {
+  auto fn = nvfp4_grouped_gemm_few_kernel<FP32>;
+  static bool done[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !done[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, F_SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev] = true;
+  }
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(most_tiles, sm_count()));
+  const cudaError_t e =
+      launch_k(fn, dim3(static_cast<unsigned>(grid)), dim3(F_THREADS), F_SMEM, st, 1u, mw, mx, mxs, msw, msx, p);
+  note_launch();
+  return e;
+}
+
 template <bool WGRAD, bool FP32, bool WIDE>
 cudaError_t launch_grouped(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md, const CUtensorMap& msa,
                            const CUtensorMap& msb, const GroupedGemm& p, int64_t most_tiles, cudaStream_t st) {
@@ -429,6 +680,16 @@ cudaError_t grouped_gemm_launch(const uint8_t* A, const uint8_t* sA, const float
                                 int64_t N, int64_t K, void* D, int out_dtype, int64_t ldd, int32_t* status,
                                 cudaStream_t st) {
   const bool fp32 = out_dtype == NVFP4_OUT_DTYPE_FP32;
+  if (T <= kFewTokensPerGroup * E) {
+    CUtensorMap mw, mx, mxs, msw, msx;
+    if (!make_map(&mw, B, E * N, K / 2, 128) || !make_map(&mx, A, T, K / 2, 128) || !make_map(&mxs, A, T, K / 2, F_SMALL) ||
+        !make_sf_map(&msw, sB, E * N, K) || !make_sf_map(&msx, sA, grouped_capacity(T, E, 128), K))
+      return cudaErrorInvalidValue;
+    const GroupedGemm p{alphaA, alphaB, offsets, static_cast<int>(E), T, 0, static_cast<int>(N), static_cast<int>(K),
+                        static_cast<int>(K / 64), 0, D, ldd, status};
+    const int64_t most = grouped_capacity(T, E, 128) / 128 * (N / 128);
+    return fp32 ? launch_few<true>(mw, mx, mxs, msw, msx, p, most, st) : launch_few<false>(mw, mx, mxs, msw, msx, p, most, st);
+  }
   CUtensorMap ma, mb, md, msa, msb;
   if (!make_map(&ma, A, T, K / 2, 128) || !make_map(&mb, B, E * N, K / 2, 128) ||
       !make_sf_map(&msa, sA, grouped_capacity(T, E, 128), K) || !make_sf_map(&msb, sB, E * N, K) ||
