@@ -484,7 +484,7 @@ NVFP4_API size_t nvfp4_lora_workspace_size(int64_t T, int64_t K, int64_t N, int6
  * out is rounded once, to bf16; a token without an adapter gets y[t] as it is
  * (0 without y) and h[t] = 0.  y may be NULL (out is then the adapters' part
  * alone) and may be out itself, otherwise they must not overlap.  h: optional,
- * fp32 [T, r], for nvfp4_lora_backward. */
+ * fp32 [T, r], for nvfp4_lora_backward; the workspace may be h itself. */
 NVFP4_API nvfp4_status_t nvfp4_lora_apply(const void* x, int64_t ldx, const void* A, const void* B,
                                           const float* scaling, const int32_t* ids, int64_t T, int64_t K, int64_t N,
                                           int64_t r, int64_t n, const void* y, int64_t ldy, void* out, int64_t ldo,

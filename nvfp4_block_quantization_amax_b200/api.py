@@ -579,8 +579,8 @@ def _check_lora(A, B, scaling, ids, T, device):
     return K, N, r, n
 
 
-def _lora_workspace(workspace, T, K, N, r, n, backward, device):
-    need = L.nvfp4_lora_workspace_size(T, K, N, r, n, backward)
+def _lora_workspace(workspace, T, K, N, r, n, device):
+    need = L.nvfp4_lora_workspace_size(T, K, N, r, n, True)
     if workspace is None:
         return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
     _need(workspace, need, torch.uint8, "workspace", device)
@@ -589,8 +589,7 @@ def _lora_workspace(workspace, T, K, N, r, n, backward, device):
 
 def nvfp4_lora_apply(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scaling: torch.Tensor, ids: torch.Tensor,
                      y: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-                     h: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                     status: Optional[torch.Tensor] = None):
+                     h: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
     """out[t] = y[t] + scaling[a] B[a] (A[a] x[t]) with a = ids[t] (-1: y[t]
     alone), beside the shared projection y = nvfp4_gemm(x, frozen weight).
     x [T, K], y and out [T, N] bf16 (out may be y); A [n, r, K], B [n, N, r]
@@ -607,13 +606,13 @@ def nvfp4_lora_apply(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scaling:
         _need(h, T * r, torch.float32, "h", dev)
     _check_status(status, dev)
     with _guard(dev):
-        ws = _lora_workspace(workspace, T, K, N, r, n, False, dev)
         if out is None:
             out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
         if h is None:
             h = torch.empty((T, r), dtype=torch.float32, device=dev)
+        # h serves as the workspace, whose only use is to hold h
         st = L.nvfp4_lora_apply(_p(x), ldx, _p(A), _p(B), _p(scaling), _p(ids), T, K, N, r, n, _p(y), ldy, _p(out), ldo,
-                                _p(h), _p(ws), ws.numel(), _p(status), _stream_of(dev))
+                                _p(h), _p(h), 4 * T * r, _p(status), _stream_of(dev))
     _check(st, "nvfp4_lora_apply")
     return out, h
 
@@ -639,7 +638,7 @@ def nvfp4_lora_backward(dy: torch.Tensor, x: torch.Tensor, h: torch.Tensor, A: t
     _check_status(status, dev)
     dt = torch.bfloat16 if out_dtype == NVFP4_OUT_DTYPE_BF16 else torch.float32
     with _guard(dev):
-        ws = _lora_workspace(workspace, T, K, N, r, n, True, dev)
+        ws = _lora_workspace(workspace, T, K, N, r, n, dev)
         if dx_out is None:
             dx_out = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
         dA = torch.empty((n, r, K), dtype=dt, device=dev)

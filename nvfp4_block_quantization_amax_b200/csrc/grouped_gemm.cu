@@ -625,8 +625,11 @@ __global__ void __launch_bounds__(F_THREADS, 1)
   }
 }
 
-// Tokens per group, on average, up to which the swapped form is taken.
-constexpr int64_t kFewTokensPerGroup = 160;
+// Tokens per group, on average, up to which the swapped form is taken.  Timed
+// by themselves, pair form against swapped, bf16 results: 64 groups, 1408 x
+// 2112: 44 / 40 us at 4 tokens each, 52 / 49 at 64, 53 / 57 at 96; 8 groups,
+// 14336 x 4096: 81 / 66, 75 / 72, 77 / 74, and 79 / 84 at 128.
+constexpr int64_t kFewTokensPerGroup = 80;
 
 template <bool FP32>
 cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mx, const CUtensorMap& mxs, const CUtensorMap& msw,

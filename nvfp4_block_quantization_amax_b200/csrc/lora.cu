@@ -9,11 +9,19 @@
 //
 // Three kernels, each used in both directions:
 //   shrink  (x, A) -> h and (dy, B) -> g: contraction over the long axis,
-//           split over CTAs into fp32 partial sums;
+//           split over the CTAs of a cluster, which add their sums through
+//           distributed shared memory;
 //   expand  (h, B) + y -> out and (g, A) + dx0 -> dx: contraction over the
-//           rank; sums the partials first, in their order;
+//           rank;
 //   outer   (g, x) -> dA and (h, dy) -> dB: contraction over one adapter's
 //           tokens.
+// What bounds them are the long rows that pass through memory once (shrink,
+// outer) or twice (expand).  They stream through rings of shared memory that
+// one producer warp fills with TMA, so that the copies in flight do not depend
+// on how many warps fit an SM: with copies issued by the computing threads
+// the same products ran at 2.2 to 4.5 TB/s (a plain copy kernel needs six
+// 256-thread CTAs per SM to reach 6 TB/s, and these have registers for two to
+// four).
 // The products are small (2 T r (K + N) flops) beside the rows that pass
 // through memory, so they run on mma.sync with bf16 operands and fp32 sums.
 // h and g are kept in fp32; where they are an operand of a product they enter
@@ -28,16 +36,14 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "gemm_ptx.cuh"
 #include "launch.cuh"
 #include "nvfp4_internal.h"
-#include "tile.cuh"
 
 namespace nvfp4 {
 namespace {
 
 constexpr int kRows = 64;      // tokens of a tile
-constexpr int kNT = 256;       // threads of the tile kernels
-constexpr int kCols = 128;     // columns of an expand tile
 constexpr int kFewTokens = 256;   // up to here the tokens are gathered by adapter
 
 struct AdapterIds {
@@ -75,16 +81,6 @@ __device__ __forceinline__ void mma16(float* d, const uint32_t* a, const uint32_
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-__device__ __forceinline__ void copy16(void* smem, const void* gmem, bool valid) {
-  const int bytes = valid ? 16 : 0;   // 0: the 16 bytes become zero, nothing is read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_addr(smem)), "l"(gmem), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void copy4(void* smem, const void* gmem, bool valid) {
-  const int bytes = valid ? 4 : 0;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(smem_addr(smem)), "l"(gmem), "r"(bytes) : "memory");
-}
-
 // v = hi + lo up to 2^-17 |v| (an infinity or NaN is all in hi: its lo would
 // be a NaN of its own)
 __device__ __forceinline__ float rest_of(float v, float hi) {
@@ -113,17 +109,88 @@ __device__ __forceinline__ uint32_t add_round(uint32_t y, float d0, float d1) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// Column order of a 32-column group in the expand products: thread c of a
+// Column order of a 32-column group in the few-token expand: thread c of a
 // quad owns columns 8c .. 8c + 7 of its rows (16 bytes of bf16) when column
 // 8 (n / 2) + 2 q + n % 2 of the group is column n of the group's MMA q.
-// Weights are staged in that order, 8 q + n.
-__device__ __forceinline__ int mma_slot(int col) {   // column -> slot of its 32-group
-  return (col & ~31) + 8 * ((col & 7) >> 1) + 2 * ((col & 31) >> 3) + (col & 1);
-}
-__device__ __forceinline__ int slot_col(int slot) {   // and back
+__device__ __forceinline__ int slot_col(int slot) {
   const int q = (slot & 31) >> 3, n = slot & 7;
   return (slot & ~31) + 8 * (n >> 1) + 2 * q + (n & 1);
 }
+
+// ---- rings of shared memory, filled by TMA --------------------------------
+// A ring's barriers: full[s] completes when a slot's bytes have landed,
+// empty[s] when every consumer warp has arrived.  All waits are bounded (see
+// mbar_wait): one that gives up raises `abort`, every role leaves its loop,
+// and the kernel reports NVFP4_ERR_TIMEOUT.
+constexpr int kConsumers = 8;                      // warps
+constexpr int kThreads = 32 * (kConsumers + 1);    // and the producer warp
+
+struct Ring {
+  uint64_t* full;
+  uint64_t* empty;
+  int slots, slot;
+  uint32_t phase;   // of the current pass over the slots
+  __device__ __forceinline__ void init() const {   // one thread
+    for (int i = 0; i < slots; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), kConsumers);
+    }
+  }
+  __device__ __forceinline__ void next() {
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+  __device__ __forceinline__ bool wait_full(volatile int* abort) const { return mbar_wait(smem_u32(&full[slot]), phase, abort); }
+  __device__ __forceinline__ bool wait_empty(volatile int* abort) const { return mbar_wait(smem_u32(&empty[slot]), phase ^ 1, abort); }
+  // After an abort the producer lets the copies it has issued land before its
+  // CTA goes: `issued` slots in all.
+  __device__ __forceinline__ void drain(int issued) const {
+    for (int i = issued > slots ? issued - slots : 0; i < issued; ++i)
+      mbar_wait_bounded(smem_u32(&full[i % slots]), (i / slots) & 1);
+  }
+};
+// A consumer warp is done with a slot.
+__device__ __forceinline__ void release(uint64_t* empty) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(empty)) : "memory");
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory"); }
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// Shared-memory tiles as TMA writes them: rows of ROW bytes (32, 64 or 128)
+// whose 16-byte chunks are swizzled by the row, so that eight rows of one
+// chunk lie in different banks.  Wider tiles are several boxes, one behind
+// the other.
+template <int ROW>
+__device__ __forceinline__ const uint8_t* chunk_at(const uint8_t* tile, int row, int chunk) {
+  constexpr int kShift = ROW == 128 ? 0 : (ROW == 64 ? 1 : 2);
+  return tile + row * ROW + ((chunk ^ ((row >> kShift) & (ROW / 16 - 1))) << 4);
+}
+template <int ROW>
+__device__ __forceinline__ uint8_t* chunk_at(uint8_t* tile, int row, int chunk) {
+  return const_cast<uint8_t*>(chunk_at<ROW>(static_cast<const uint8_t*>(tile), row, chunk));
+}
+
+// A tile of rank vectors: ROWS rows of R = 16 RP ranks (R = 128: two boxes).
+template <int RP>
+struct RankTile {
+  static constexpr int R = 16 * RP;
+  static constexpr int ROW = RP == 8 ? 128 : 2 * R;
+  static constexpr int BOXES = RP == 8 ? 2 : 1;
+  template <int ROWS>
+  static __device__ __forceinline__ const uint8_t* at(const uint8_t* tile, int row, int chunk) {   // chunk: 8 ranks
+    if constexpr (BOXES == 1) return chunk_at<ROW>(tile, row, chunk);
+    else return chunk_at<ROW>(tile + (chunk >> 3) * (ROWS * ROW), row, chunk & 7);
+  }
+};
 
 // The adapters of a tile of 64 tokens: ids[64] (-1: none) and the list of the
 // distinct ones.  All threads call it (at least two warps), thread t < 64 with
@@ -158,344 +225,377 @@ __device__ __forceinline__ void tile_adapters(TileAdapters& ta, int id) {
   __syncthreads();
 }
 
-// The bf16 numbers that make up w [T, r] (TERMS of them), rows padded to R
+// The bf16 numbers that make up w [T, r] (n_terms of them), rows padded to R
 // with zeros: operands of the outer products.  terms[x][t][j].
-template <int RP>
-__device__ __forceinline__ void write_terms(__nv_bfloat16* terms, int n_terms, int64_t T, int64_t t, int j, float v) {
-  constexpr int R = 16 * RP;
+__device__ __forceinline__ void write_terms(__nv_bfloat16* terms, int n_terms, int64_t T, int R, int64_t t, int j, float v) {
   __nv_bfloat16 s[3];
   if (n_terms == 3) split_bf16(v, s[0], s[1], s[2]);
   else split_bf16(v, s[0], s[1]);
   for (int x = 0; x < n_terms; ++x) terms[(x * T + t) * R + j] = s[x];
 }
 
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The float at this shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ float load_cluster(const float* p, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to_rank(smem_u32(p), static_cast<uint32_t>(rank))) : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------------------
-// shrink: part[split][t][j] = sum over this split's columns of z[t, c] W[j, c]
+// shrink: w[t][j] = sum over the columns of z[t, c] W[j, c], fp32.
 // TRANS: W is stored [C, r] (c-major), else [r, C].
-// 64 rows x 128 columns a stage; warp w multiplies rows 16 (w % 4) over half
-// w / 4 of the stage's columns, the halves are added at the end.  The rows'
-// traffic bounds it; what it takes is warps and copies in flight, so the ring
-// is sized for three CTAs per SM.
-// In the backward pass the first split also writes h's terms for dB.
+// A cluster of S CTAs takes 64 rows, each CTA a share of the columns in stages
+// of 128 (16 KB of z, 4 to 32 KB of weights).  Warp w multiplies rows
+// 16 (w % 4) over half w / 4 of a stage.  Sums of the cluster are added in
+// rank order.  In the backward pass the terms of w and of h are written here.
 // ---------------------------------------------------------------------------
 template <int RP, bool TRANS>
 struct ShrinkCfg {
   static constexpr int R = 16 * RP;
-  static constexpr int KC = 128;   // columns of a stage
-  static constexpr int ZB = kRows * (KC + 8) * 2;
-  static constexpr int WB = (TRANS ? KC * (R + 8) : R * (KC + 8)) * 2;
-  static constexpr int CTAS = RP == 1 ? 3 : (RP <= 4 ? 2 : 1);   // per SM
-  static constexpr int STAGES = 224 * 1024 / CTAS / (ZB + WB);
-  static constexpr int BYTES = STAGES * (ZB + WB);
+  static constexpr int KC = 128;                     // columns of a stage
+  static constexpr int ZB = kRows * KC * 2;          // two boxes of 64 columns
+  static constexpr int WB = R * KC * 2;
+  static constexpr int SUM = kRows * R * 4;
+  static constexpr int CTAS = RP <= 2 ? 2 : 1;       // per SM
+  static constexpr int STAGES = ((CTAS == 2 ? 110 : 224) * 1024 - SUM) / (ZB + WB);
+  static constexpr int BYTES = 1024 + STAGES * (ZB + WB) + SUM + 256;
 };
 
 template <int RP, bool TRANS>
-__global__ void __launch_bounds__(kNT, ShrinkCfg<RP, TRANS>::CTAS)
-    lora_shrink_kernel(const __nv_bfloat16* __restrict__ z, int64_t ldz, const __nv_bfloat16* __restrict__ W,
-                       const AdapterIds a, int64_t C, int r, int64_t per_split, float* __restrict__ part,
-                       const float* __restrict__ h, __nv_bfloat16* __restrict__ h_terms, int n_terms) {
+__global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
+    lora_shrink_kernel(const __grid_constant__ CUtensorMap tmap_z, const __grid_constant__ CUtensorMap tmap_w,
+                       const AdapterIds a, int64_t C, int r, int split, int per_split, float* __restrict__ w_out,
+                       __nv_bfloat16* __restrict__ w_terms, const float* __restrict__ h,
+                       __nv_bfloat16* __restrict__ h_terms, int n_terms) {
   pdl_entry();
   using S = ShrinkCfg<RP, TRANS>;
-  constexpr int R = S::R, KC = S::KC, ST = S::STAGES;
-  extern __shared__ __align__(16) uint8_t dyn[];
+  [[maybe_unused]] constexpr int R = S::R, KC = S::KC;
+  extern __shared__ uint8_t dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+  uint8_t* zs = smem;
+  uint8_t* wsm = zs + S::STAGES * S::ZB;
+  float* sums = reinterpret_cast<float*>(wsm + S::STAGES * S::WB);   // [64][R]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sums) + S::SUM);
+  Ring ring{bars, bars + S::STAGES, S::STAGES, 0, 0u};
+  volatile int* abort = reinterpret_cast<volatile int*>(bars + 2 * S::STAGES);
   __shared__ TileAdapters ta;
-  const int th = threadIdx.x, lane = th & 31, warp = th >> 5, rg = warp & 3, kh = warp >> 2;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
-  const int64_t c_begin = blockIdx.y * per_split;
+  const int th = threadIdx.x, lane = th & 31, warp = th >> 5;
+  const int rank = static_cast<int>(blockIdx.x) % split;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / split) * kRows;
+  const int64_t c_begin = static_cast<int64_t>(rank) * per_split;
   const int64_t c_end = c_begin + per_split < C ? c_begin + per_split : C;
-  const int steps = static_cast<int>((c_end - c_begin + KC - 1) / KC);
-  tile_adapters(ta, th < kRows ? adapter_of(a, row0 + th, blockIdx.y == 0) : -1);
-  float* mine = part + static_cast<int64_t>(blockIdx.y) * a.T * r;
+  const int steps = c_end > c_begin ? static_cast<int>((c_end - c_begin + KC - 1) / KC) : 0;
+  if (th == 0) {
+    ring.init();
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  for (int k = th; k < kRows * R; k += kThreads) sums[k] = 0.0f;
+  tile_adapters(ta, th < kRows ? adapter_of(a, row0 + th, rank == 0) : -1);   // ends with a barrier
 
-  // this thread copies chunk zch of rows zrow, zrow + 16, ..
-  const int zrow = th >> 4, zch = th & 15;
-  const __nv_bfloat16* zsrc = z + (row0 + zrow) * ldz + c_begin + 8 * zch;
-  uint32_t zok = 0;
-#pragma unroll
-  for (int i = 0; i < kRows / 16; ++i) zok |= (ta.ids[zrow + 16 * i] >= 0 ? 1u : 0u) << i;
-  auto load = [&](int step, int slot, const __nv_bfloat16* w) {
-    uint8_t* base = dyn + slot * (S::ZB + S::WB);
-    const int64_t off = static_cast<int64_t>(step) * KC, c0 = c_begin + off;
-    const uint32_t ok4 = c0 + 8 * zch < c_end ? zok : 0u;
-#pragma unroll
-    for (int i = 0; i < kRows / 16; ++i) {
-      const bool ok = ok4 >> i & 1u;
-      copy16(base + (zrow + 16 * i) * (KC + 8) * 2 + 16 * zch, ok ? zsrc + off + 16 * i * ldz : z, ok);
-    }
-    uint8_t* wb = base + S::ZB;
-#pragma unroll
-    for (int i = 0; i < RP; ++i) {
-      if constexpr (!TRANS) {   // ranks zrow + 16 i, chunk zch
-        const int j = zrow + 16 * i;
-        const bool ok = j < r && c0 + 8 * zch < c_end;
-        copy16(wb + j * (KC + 8) * 2 + 16 * zch, ok ? w + j * C + c0 + 8 * zch : w, ok);
-      } else {
-        const int k = th + kNT * i, c = k / (R / 8), ch = k % (R / 8);
-        const bool ok = c0 + c < c_end && 8 * ch < r;
-        copy16(wb + c * (R + 8) * 2 + 16 * ch, ok ? w + (c0 + c) * r + 8 * ch : w, ok);
-      }
-    }
-    cp_async_commit();
-  };
-
-  for (int u = 0; u < ta.count; ++u) {
-    const int id = ta.list[u];
-    const __nv_bfloat16* w = W + static_cast<int64_t>(id) * r * C;
-    float sum[2 * RP][4];
-#pragma unroll
-    for (int i = 0; i < 2 * RP; ++i) sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.0f;
-#pragma unroll
-    for (int p = 0; p < ST - 1; ++p) {
-      if (p < steps) load(p, p, w);
-      else cp_async_commit();
-    }
-    int slot = 0, ahead = ST - 1;
-    for (int s = 0; s < steps; ++s) {
-      cp_async_wait<ST - 2>();   // this stage has landed
-      __syncthreads();           // for every thread, and the stage before it has been read
-      if (s + ST - 1 < steps) load(s + ST - 1, ahead, w);
-      else cp_async_commit();
-      const uint8_t* base = dyn + slot * (S::ZB + S::WB);
-      if (++slot == ST) slot = 0;
-      if (++ahead == ST) ahead = 0;
-      const __nv_bfloat16* zs = reinterpret_cast<const __nv_bfloat16*>(base);
-      const __nv_bfloat16* ws = reinterpret_cast<const __nv_bfloat16*>(base + S::ZB);
-      // this stage's sums start from zero and are added to the running ones:
-      // the tensor core truncates as it adds, so its runs are kept short
-      float acc[2 * RP][4];
-#pragma unroll
-      for (int i = 0; i < 2 * RP; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-      // fragments of kBatch products of 16 columns are loaded together, so
-      // their latencies overlap
-      constexpr int kBatch = RP <= 2 ? 4 : 2;
-#pragma unroll
-      for (int k8 = 0; k8 < KC / 2; k8 += 16 * kBatch) {
-        uint32_t af[kBatch][4], bf[kBatch][RP][4];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int kk = kh * (KC / 2) + k8 + 16 * b;
-          ldsm4(af[b], zs + (16 * rg + (lane & 15)) * (KC + 8) + kk + (lane >> 4) * 8);
-#pragma unroll
-          for (int p = 0; p < RP; ++p) {
-            if constexpr (!TRANS)
-              ldsm4(bf[b][p], ws + (16 * p + (lane & 7) + ((lane >> 4) << 3)) * (KC + 8) + kk + ((lane >> 3) & 1) * 8);
-            else
-              ldsm4_t(bf[b][p], ws + (kk + (lane & 7) + ((lane >> 3) & 1) * 8) * (R + 8) + 16 * p + (lane >> 4) * 8);
-          }
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-          for (int p = 0; p < RP; ++p) {
-            mma16(acc[2 * p], af[b], bf[b][p]);
-            mma16(acc[2 * p + 1], af[b], bf[b][p] + 2);
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < 2 * RP; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum[i][e] = __fadd_rn(sum[i][e], acc[i][e]);
-    }
-    __syncthreads();   // the ring is free: every copy has landed and been read
-    // add the second half's sums
-    float* other = reinterpret_cast<float*>(dyn);
-    if (kh == 1) {
-#pragma unroll
-      for (int i = 0; i < 2 * RP; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) other[((rg * 2 * RP + i) * 4 + e) * 32 + lane] = sum[i][e];
-    }
-    __syncthreads();
-    if (kh == 0) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int row = 16 * rg + (lane >> 2) + 8 * half;
-        if (ta.ids[row] == id) {
-#pragma unroll
-          for (int i = 0; i < 2 * RP; ++i) {
-            const int j = 8 * i + 2 * (lane & 3);
-            const float* o = other + ((rg * 2 * RP + i) * 4 + 2 * half) * 32 + lane;
-            if (j < r)
-              *reinterpret_cast<float2*>(mine + (row0 + row) * r + j) =
-                  make_float2(__fadd_rn(sum[i][2 * half], o[0]), __fadd_rn(sum[i][2 * half + 1], o[32]));
+  if (warp == kConsumers) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int u = 0; u < ta.count && !*abort; ++u) {
+        for (int s = 0; s < steps; ++s, ++issued, ring.next()) {
+          if (!ring.wait_empty(abort)) break;
+          const uint32_t bar = smem_u32(&ring.full[ring.slot]);
+          const uint32_t zd = smem_u32(zs + ring.slot * S::ZB), wd = smem_u32(wsm + ring.slot * S::WB);
+          const int c = static_cast<int>(c_begin) + s * KC;
+          mbar_expect_tx(bar, S::ZB + S::WB);
+          tma_load_2d(zd, &tmap_z, c, static_cast<int>(row0), bar);
+          tma_load_2d(zd + S::ZB / 2, &tmap_z, c + 64, static_cast<int>(row0), bar);
+          if constexpr (!TRANS) {
+            tma_load_3d(wd, &tmap_w, c, 0, ta.list[u], bar);
+            tma_load_3d(wd + S::WB / 2, &tmap_w, c + 64, 0, ta.list[u], bar);
+          } else {
+            tma_load_3d(wd, &tmap_w, 0, c, ta.list[u], bar);
+            if constexpr (RP == 8) tma_load_3d(wd + S::WB / 2, &tmap_w, 64, c, ta.list[u], bar);
           }
         }
       }
+      if (*abort) ring.drain(issued);
     }
-    __syncthreads();   // before the next adapter's copies
-  }
-  // tokens without an adapter
-  for (int k = th; k < kRows * r; k += kNT) {
-    const int row = k / r;
-    if (ta.ids[row] < 0 && row0 + row < a.T) mine[(row0 + row) * r + (k - row * r)] = 0.0f;
-  }
-  if (h_terms && blockIdx.y == 0) {
-    for (int k = th; k < kRows * R; k += kNT) {
-      const int64_t t = row0 + k / R;
-      const int j = k % R;
-      if (t < a.T) write_terms<RP>(h_terms, n_terms, a.T, t, j, j < r ? __ldg(h + t * r + j) : 0.0f);
+    __syncwarp();
+  } else {
+    const int rg = warp & 3, kh = warp >> 2;
+    for (int u = 0; u < ta.count; ++u) {
+      const int id = ta.list[u];
+      float sum[2 * RP][4];
+#pragma unroll
+      for (int i = 0; i < 2 * RP; ++i) sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.0f;
+      for (int s = 0; s < steps; ++s) {
+        if (!ring.wait_full(abort)) break;
+        const uint8_t* zt = zs + ring.slot * S::ZB + kh * (S::ZB / 2);   // this half's box of 64 columns
+        const uint8_t* wt = wsm + ring.slot * S::WB;
+        // this stage's sums start from zero and are added to the running ones:
+        // the tensor core truncates as it adds, so its runs are kept short
+        float acc[2 * RP][4];
+#pragma unroll
+        for (int i = 0; i < 2 * RP; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+        // fragments of kBatch products of 16 columns are loaded together, so
+        // their latencies overlap
+        constexpr int kBatch = RP <= 2 ? 4 : 2;
+#pragma unroll
+        for (int k8 = 0; k8 < KC / 2; k8 += 16 * kBatch) {
+          uint32_t af[kBatch][4], bf[kBatch][RP][4];
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int kk = k8 + 16 * b;   // within this half
+            ldsm4(af[b], chunk_at<128>(zt, 16 * rg + (lane & 15), kk / 8 + (lane >> 4)));
+#pragma unroll
+            for (int p = 0; p < RP; ++p) {
+              if constexpr (!TRANS)
+                ldsm4(bf[b][p], chunk_at<128>(wt + kh * (S::WB / 2), 16 * p + (lane & 7) + ((lane >> 4) << 3), kk / 8 + ((lane >> 3) & 1)));
+              else
+                ldsm4_t(bf[b][p], RankTile<RP>::template at<KC>(wt, 64 * kh + kk + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * p + (lane >> 4)));
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int p = 0; p < RP; ++p) {
+              mma16(acc[2 * p], af[b], bf[b][p]);
+              mma16(acc[2 * p + 1], af[b], bf[b][p] + 2);
+            }
+        }
+        release(&ring.empty[ring.slot]);
+        ring.next();
+#pragma unroll
+        for (int i = 0; i < 2 * RP; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[i][e] = __fadd_rn(sum[i][e], acc[i][e]);
+      }
+      // this adapter's rows: the second half's sums, then the first's on top
+#pragma unroll
+      for (int turn = 1; turn >= 0; --turn) {
+        if (kh == turn) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int row = 16 * rg + (lane >> 2) + 8 * half;
+            if (ta.ids[row] == id) {
+#pragma unroll
+              for (int i = 0; i < 2 * RP; ++i) {
+                float2* at = reinterpret_cast<float2*>(sums + row * R + 8 * i + 2 * (lane & 3));
+                float2 v = make_float2(sum[i][2 * half], sum[i][2 * half + 1]);
+                if (turn == 0) v = make_float2(__fadd_rn(v.x, at->x), __fadd_rn(v.y, at->y));
+                *at = v;
+              }
+            }
+          }
+        }
+        consumers_sync();
+      }
     }
   }
+  // the cluster's sums, in rank order; each CTA finishes a share of the rows
+  if (split > 1) cluster_barrier();
+  else __syncthreads();
+  const int first = kRows * rank / split, rows = kRows * (rank + 1) / split - first;
+  for (int k = th; k < rows * R; k += kThreads) {
+    const int row = first + k / R, j = k % R;
+    const int64_t t = row0 + row;
+    if (t >= a.T) continue;
+    float v = 0.0f;
+    if (split == 1) v = sums[row * R + j];
+    else
+      for (int q = 0; q < split; ++q) v = __fadd_rn(v, load_cluster(sums + row * R + j, q));
+    if (w_out && j < r) w_out[t * r + j] = v;
+    if (w_terms) write_terms(w_terms, n_terms, a.T, R, t, j, v);
+    if (h_terms) write_terms(h_terms, n_terms, a.T, R, t, j, j < r ? __ldg(h + t * r + j) : 0.0f);
+  }
+  if (th == 0 && *abort && a.status) *a.status = kStatusTimeout;
+  if (split > 1) cluster_barrier();   // no CTA leaves while another may still read its sums
 }
 
 // ---------------------------------------------------------------------------
-// expand: out[t, c] = base[t, c] + s_a sum_j w[t, j] W[c, j], w = sum of the
-// partials; w itself goes to w_out, its terms to w_terms.  TRANS: W is stored
-// [r, C], else [C, r].
-// A CTA takes 64 tokens and `per_cta` tiles of 128 columns; warp w rows
-// 16 (w % 4), columns 64 (w / 4).  A thread's products land on the 16 bytes
-// of base it has loaded (see mma_slot), so neither base nor result passes
-// through shared memory.  Instructions and their latencies bound it before
-// memory does: the scale is folded into w, base is added in pairs, and tiles
-// are narrow so that four CTAs (32 warps) fit an SM.  Measured at 8192 x
-// 14336, r = 16: 256-column tiles, three CTAs and 632 instructions per warp
-// and 256 columns 105 us; a persistent form that prefetched the next tile with
-// two CTAs 120 us.
+// expand: out[t, c] = base[t, c] + s_a sum_j w[t, j] W[c, j].
+// TRANS: W is stored [r, C], else [C, r].
+// Persistent CTAs walk runs of 64 x 128 tiles, columns fastest.  One ring
+// holds base tiles (TMA in, changed in place, TMA out), another the weights
+// of the tile's adapters, one slot each; w stays in registers while the row
+// tile does, its scale folded in.  Warp w: rows 16 (w % 4), columns 64 (w / 4).
 // ---------------------------------------------------------------------------
-template <int RP, bool TRANS>
+template <int RP>
 struct ExpandCfg {
   static constexpr int R = 16 * RP;
-  static constexpr int HB = kRows * (R + 8) * 2;
-  static constexpr int WB = (TRANS ? R * (kCols + 8) : kCols * (R + 8)) * 2;
-  static constexpr int BYTES = 2 * HB + WB;
-  static constexpr int CTAS = RP <= 4 ? 4 : 2;   // per SM
+  static constexpr int KC = 128;                  // columns of a tile
+  static constexpr int YB = kRows * KC * 2;       // two boxes of 64 columns
+  static constexpr int WB = R * KC * 2;
+  static constexpr int CTAS = RP <= 4 ? 2 : 1;    // per SM
+  static constexpr int WSLOTS = RP <= 2 ? 3 : 2;
+  static constexpr int YSLOTS = ((CTAS == 2 ? 110 : 224) * 1024 - WSLOTS * WB) / YB;
+  static constexpr int BYTES = 1024 + YSLOTS * YB + WSLOTS * WB + 512;
 };
 
 template <int RP, bool TRANS>
-__global__ void __launch_bounds__(kNT, ExpandCfg<RP, TRANS>::CTAS)
-    lora_expand_kernel(const float* __restrict__ part, int splits, const __nv_bfloat16* __restrict__ W,
-                       const float* __restrict__ scaling, const AdapterIds a, int64_t C, int r, int per_cta, int groups,
-                       const __nv_bfloat16* in, int64_t ldi, __nv_bfloat16* out, int64_t ldo,
-                       float* __restrict__ w_out, __nv_bfloat16* __restrict__ w_terms, int n_terms) {
+__global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
+    lora_expand_kernel(const __grid_constant__ CUtensorMap tmap_in, const __grid_constant__ CUtensorMap tmap_w,
+                       const __grid_constant__ CUtensorMap tmap_out, const float* __restrict__ w,
+                       const float* __restrict__ scaling, const AdapterIds a, int64_t C, int r, int has_in) {
   pdl_entry();
-  using S = ExpandCfg<RP, TRANS>;
-  constexpr int R = S::R;
-  extern __shared__ __align__(16) uint8_t dyn[];
+  using S = ExpandCfg<RP>;
+  [[maybe_unused]] constexpr int R = S::R, KC = S::KC;
+  extern __shared__ uint8_t dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+  uint8_t* ys = smem;
+  uint8_t* wsm = ys + S::YSLOTS * S::YB;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(wsm + S::WSLOTS * S::WB);
+  Ring yr{bars, bars + S::YSLOTS, S::YSLOTS, 0, 0u};
+  Ring wr{bars + 2 * S::YSLOTS, bars + 2 * S::YSLOTS + S::WSLOTS, S::WSLOTS, 0, 0u};
+  volatile int* abort = reinterpret_cast<volatile int*>(bars + 2 * (S::YSLOTS + S::WSLOTS));
   __shared__ TileAdapters ta;
-  __nv_bfloat16* hh = reinterpret_cast<__nv_bfloat16*>(dyn);
-  __nv_bfloat16* hl = reinterpret_cast<__nv_bfloat16*>(dyn + S::HB);
-  __nv_bfloat16* ws = reinterpret_cast<__nv_bfloat16*>(dyn + 2 * S::HB);
-  const int th = threadIdx.x, lane = th & 31, warp = th >> 5, rg = warp & 3, ch = warp >> 2;
-  // neighbouring CTAs take neighbouring columns of the same rows
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x / groups) * kRows;
-  const int group = blockIdx.x % groups;
-  const int my_row = 16 * rg + (lane >> 2);        // this thread's rows of the tile: my_row and my_row + 8
-  const int my_col = 64 * ch + 8 * (lane & 3);     // and its columns: 8 from here on, and 32 further
-  uint4 y[2][2];
-  auto load_base = [&](int64_t c0) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int64_t t = row0 + my_row + 8 * half, c = c0 + my_col + 32 * q;
-        y[q][half] = make_uint4(0u, 0u, 0u, 0u);
-        if (in && c < C && t < a.T) y[q][half] = __ldcs(reinterpret_cast<const uint4*>(in + t * ldi + c));
-      }
-    }
-  };
-  // loads that do not depend on the adapters first
-  const int id_mine = th < kRows ? adapter_of(a, row0 + th, false) : -1;
-  if (out) load_base(static_cast<int64_t>(group) * per_cta * kCols);
-  tile_adapters(ta, id_mine);
-  // the sum of the partials, in their order
-#pragma unroll 4
-  for (int k = th; k < kRows * R; k += kNT) {
-    const int row = k / R, j = k % R;
-    float v = 0.0f;
-    if (row0 + row < a.T) {
-      const int64_t at = (row0 + row) * r + j;
-      if (j < r)
-        for (int s = 0; s < splits; ++s) v = __fadd_rn(v, __ldcg(part + s * a.T * r + at));
-      if (group == 0) {
-        if (w_out && j < r) w_out[at] = v;
-        if (w_terms) write_terms<RP>(w_terms, n_terms, a.T, row0 + row, j, v);
-      }
-    }
-    const int id = ta.ids[row];
-    split_bf16(id >= 0 ? __fmul_rn(__ldg(scaling + id), v) : 0.0f, hh[row * (R + 8) + j], hl[row * (R + 8) + j]);
+  const int th = threadIdx.x, lane = th & 31, warp = th >> 5;
+  const int64_t col_tiles = (C + KC - 1) / KC, total = (a.T + kRows - 1) / kRows * col_tiles;
+  const int64_t begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+  if (th == 0) {
+    yr.init();
+    wr.init();
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (!out) return;   // only the sum was asked for
-  const int id_lo = ta.ids[my_row], id_hi = ta.ids[my_row + 8];
-
-  for (int i = 0; i < per_cta; ++i) {
-    const int64_t c0 = (static_cast<int64_t>(group) * per_cta + i) * kCols;
-    if (c0 >= C) break;
-    if (i > 0) load_base(c0);
-    for (int u = 0; u < ta.count; ++u) {
-      const int id = ta.list[u];
-      const __nv_bfloat16* w = W + static_cast<int64_t>(id) * r * C;
-      if (i > 0 || u > 0) __syncthreads();   // the previous weights have been read
-      if constexpr (!TRANS) {
-#pragma unroll
-        for (int x = 0; x < RP; ++x) {
-          const int k = th + kNT * x, c = k / (R / 8), c8 = k % (R / 8);
-          const bool ok = c0 + c < C && 8 * c8 < r;
-          copy16(ws + mma_slot(c) * (R + 8) + 8 * c8, ok ? w + (c0 + c) * r + 8 * c8 : w, ok);
-        }
-      } else {
-        // pairs of columns, each to its slot
-        const int c = 2 * (th & 63), slot = mma_slot(c);
-        const bool col_ok = c0 + c < C;
-#pragma unroll
-        for (int x = 0; x < R / 4; ++x) {
-          const int j = (th >> 6) + 4 * x;
-          const bool ok = col_ok && j < r;
-          copy4(ws + j * (kCols + 8) + slot, ok ? w + j * C + c0 + c : w, ok);
-        }
-      }
-      cp_async_commit();
-      cp_async_wait<0>();
-      __syncthreads();
-      const bool lo_mine = id_lo == id, hi_mine = id_hi == id;
-      if (!__any_sync(0xFFFFFFFFu, lo_mine || hi_mine)) continue;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {   // 32 columns each
-        float acc[4][4] = {};
-#pragma unroll
-        for (int kk = 0; kk < R; kk += 16) {
-          uint32_t ah[4], al[4], b0[4], b1[4];
-          ldsm4(ah, hh + (16 * rg + (lane & 15)) * (R + 8) + kk + (lane >> 4) * 8);
-          ldsm4(al, hl + (16 * rg + (lane & 15)) * (R + 8) + kk + (lane >> 4) * 8);
-          if constexpr (!TRANS) {
-            const __nv_bfloat16* wq = ws + (64 * ch + 32 * q + (lane & 7) + ((lane >> 4) << 3)) * (R + 8) + kk + ((lane >> 3) & 1) * 8;
-            ldsm4(b0, wq);
-            ldsm4(b1, wq + 16 * (R + 8));
+  __syncthreads();
+  // Row tile by row tile: all threads agree on its adapters, then the producer
+  // and the consumers walk its column tiles at their own pace.
+  int64_t tile = begin;
+  int y_issued = 0, w_issued = 0;
+  int held = -1;   // base slot whose store may still be reading it
+  while (tile < end) {
+    const int64_t row_tile = tile / col_tiles, row0 = row_tile * kRows;
+    const int64_t stop = min(end, (row_tile + 1) * col_tiles);
+    // the previous row tile's adapters have been read; after an abort all leave
+    if (__syncthreads_or(*abort != 0)) break;
+    tile_adapters(ta, th < kRows ? adapter_of(a, row0 + th, false) : -1);
+    if (warp == kConsumers) {
+      if (lane == 0) {
+        for (int64_t k = tile; k < stop && !*abort; ++k) {
+          const int c = static_cast<int>(k - row_tile * col_tiles) * KC;
+          if (!yr.wait_empty(abort)) break;
+          const uint32_t yb = smem_u32(&yr.full[yr.slot]), yd = smem_u32(ys + yr.slot * S::YB);
+          if (has_in) {
+            mbar_expect_tx(yb, S::YB);
+            tma_load_2d(yd, &tmap_in, c, static_cast<int>(row0), yb);
+            tma_load_2d(yd + S::YB / 2, &tmap_in, c + 64, static_cast<int>(row0), yb);
           } else {
-            const __nv_bfloat16* wq = ws + (kk + (lane & 7) + ((lane >> 3) & 1) * 8) * (kCols + 8) + 64 * ch + 32 * q + (lane >> 4) * 8;
-            ldsm4_t(b0, wq);
-            ldsm4_t(b1, wq + 16);
+            mbar_expect_tx(yb, 0);
           }
-          mma16(acc[0], al, b0);
-          mma16(acc[1], al, b0 + 2);
-          mma16(acc[2], al, b1);
-          mma16(acc[3], al, b1 + 2);
-          mma16(acc[0], ah, b0);
-          mma16(acc[1], ah, b0 + 2);
-          mma16(acc[2], ah, b1);
-          mma16(acc[3], ah, b1 + 2);
-        }
-        // a token without an adapter keeps the base's bits (a NaN's payload, a zero's sign)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (half ? hi_mine : lo_mine) {
-            uint4& v = y[q][half];
-            v.x = add_round(v.x, acc[0][2 * half], acc[0][2 * half + 1]);
-            v.y = add_round(v.y, acc[1][2 * half], acc[1][2 * half + 1]);
-            v.z = add_round(v.z, acc[2][2 * half], acc[2][2 * half + 1]);
-            v.w = add_round(v.w, acc[3][2 * half], acc[3][2 * half + 1]);
+          yr.next();
+          ++y_issued;
+          for (int u = 0; u < ta.count; ++u) {
+            if (!wr.wait_empty(abort)) break;
+            const uint32_t wb = smem_u32(&wr.full[wr.slot]), wd = smem_u32(wsm + wr.slot * S::WB);
+            mbar_expect_tx(wb, S::WB);
+            if constexpr (!TRANS) {
+              tma_load_3d(wd, &tmap_w, 0, c, ta.list[u], wb);
+              if constexpr (RP == 8) tma_load_3d(wd + S::WB / 2, &tmap_w, 64, c, ta.list[u], wb);
+            } else {
+              tma_load_3d(wd, &tmap_w, c, 0, ta.list[u], wb);
+              tma_load_3d(wd + S::WB / 2, &tmap_w, c + 64, 0, ta.list[u], wb);
+            }
+            wr.next();
+            ++w_issued;
           }
         }
       }
-    }
+      __syncwarp();
+    } else {
+      const int rg = warp & 3, ch = warp >> 2;
+      const int my_row = 16 * rg + (lane >> 2);   // this thread's rows of the tile: my_row and my_row + 8
+      const int id_lo = ta.ids[my_row], id_hi = ta.ids[my_row + 8];
+      // w of this warp's rows as MMA operands: hi and lo parts of s_a w
+      uint32_t ah[RP][4], al[RP][4];
+      const float s_lo = id_lo >= 0 ? __ldg(scaling + id_lo) : 0.0f, s_hi = id_hi >= 0 ? __ldg(scaling + id_hi) : 0.0f;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+      for (int p = 0; p < RP; ++p)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int64_t t = row0 + my_row + 8 * half, c = c0 + my_col + 32 * q;
-        if (c < C && t < a.T) __stcs(reinterpret_cast<uint4*>(out + t * ldo + c), y[q][half]);
+        for (int e = 0; e < 4; ++e) {   // row + 8 (e % 2), ranks 16 p + 2 (lane % 4) + 8 (e / 2), + 1
+          const int id = e & 1 ? id_hi : id_lo, j = 16 * p + 2 * (lane & 3) + 8 * (e >> 1);
+          float2 v = make_float2(0.0f, 0.0f);
+          if (id >= 0 && j < r) v = __ldcg(reinterpret_cast<const float2*>(w + (row0 + my_row + 8 * (e & 1)) * r + j));
+          const float s = e & 1 ? s_hi : s_lo;
+          __nv_bfloat16 h0, l0, h1, l1;
+          split_bf16(id >= 0 ? __fmul_rn(s, v.x) : 0.0f, h0, l0);
+          split_bf16(id >= 0 ? __fmul_rn(s, v.y) : 0.0f, h1, l1);
+          ah[p][e] = pack_bf16(h0, h1);
+          al[p][e] = pack_bf16(l0, l1);
+        }
+      for (int64_t k = tile; k < stop; ++k) {
+        const int c0 = static_cast<int>(k - row_tile * col_tiles) * KC;
+        if (held >= 0) {   // the previous tile's store has read its slot
+          if (lane == 0) bulk_wait_read<0>();
+          release(&yr.empty[held]);
+          held = -1;
+        }
+        if (!yr.wait_full(abort)) break;
+        uint8_t* yt = ys + yr.slot * S::YB + ch * (S::YB / 2);   // this half's box of 64 columns
+        if (!has_in) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(yt + (16 * rg) * 128 + 16 * (lane + 32 * i)) = make_uint4(0u, 0u, 0u, 0u);
+          __syncwarp();
+        }
+        bool ok = true;
+        for (int u = 0; u < ta.count && ok; ++u) {
+          ok = wr.wait_full(abort);
+          if (!ok) break;
+          const int id = ta.list[u];
+          const uint8_t* wt = wsm + wr.slot * S::WB;
+          const bool lo_mine = id_lo == id, hi_mine = id_hi == id;
+          if (__any_sync(0xFFFFFFFFu, lo_mine || hi_mine)) {
+#pragma unroll
+            for (int n = 0; n < 64; n += 16) {   // columns of this half
+              float acc[2][4] = {};
+#pragma unroll
+              for (int p = 0; p < RP; ++p) {
+                uint32_t bf[4];
+                if constexpr (!TRANS)
+                  ldsm4(bf, RankTile<RP>::template at<KC>(wt, 64 * ch + n + (lane & 7) + ((lane >> 4) << 3), 2 * p + ((lane >> 3) & 1)));
+                else
+                  ldsm4_t(bf, chunk_at<128>(wt + ch * (S::WB / 2), 16 * p + (lane & 7) + ((lane >> 3) & 1) * 8, n / 8 + (lane >> 4)));
+                mma16(acc[0], al[p], bf);
+                mma16(acc[1], al[p], bf + 2);
+                mma16(acc[0], ah[p], bf);
+                mma16(acc[1], ah[p], bf + 2);
+              }
+              // a token without an adapter keeps the base's bits (a NaN's payload, a zero's sign)
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                  if (half ? hi_mine : lo_mine) {
+                    uint32_t* at = reinterpret_cast<uint32_t*>(chunk_at<128>(yt, my_row + 8 * half, n / 8 + q)) + (lane & 3);
+                    *at = add_round(*at, acc[q][2 * half], acc[q][2 * half + 1]);
+                  }
+            }
+          }
+          release(&wr.empty[wr.slot]);
+          wr.next();
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && c0 + 64 * ch < C && row0 + 16 * rg < a.T) {
+          tma_store_2d(&tmap_out, smem_u32(yt + 16 * rg * 128), c0 + 64 * ch, static_cast<int>(row0) + 16 * rg);
+          bulk_commit();
+        }
+        held = yr.slot;
+        yr.next();
       }
     }
+    tile = stop;
   }
+  if (warp == kConsumers) {
+    if (lane == 0 && *abort) {
+      yr.drain(y_issued);
+      wr.drain(w_issued);
+    }
+  } else if (lane == 0) {
+    bulk_wait_all();
+  }
+  if (th == 0 && *abort && a.status) *a.status = kStatusTimeout;
 }
 
 // ---------------------------------------------------------------------------
@@ -572,23 +672,25 @@ __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p, bool ok) {
   return ok ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
 }
 
-// grid: split, unit.  Warp w takes the 32-column blocks w, w + 4, .. of the
-// split; thread c of a quad holds columns 8c .. 8c + 7 of a block.
+// grid: split (a cluster), unit.  Warp w takes the 32-column blocks w, w + 4,
+// .. of the split; thread c of a quad holds columns 8c .. 8c + 7 of a block.
+// The cluster's sums are added in rank order.
 template <int RP>
 __global__ void __launch_bounds__(128) lora_shrink_few_kernel(const __nv_bfloat16* __restrict__ z, int64_t ldz,
                                                               const __nv_bfloat16* __restrict__ W, const AdapterIds a,
                                                               int64_t C, int r, int64_t per_split,
-                                                              float* __restrict__ part) {
+                                                              float* __restrict__ h) {
   pdl_entry();
   constexpr int R = 16 * RP;
   __shared__ __align__(16) Unit un;
   __shared__ float sums[4][16][R + 4];
+  __shared__ float total[16][R];
   const int th = threadIdx.x, lane = th & 31, warp = th >> 5, g = lane >> 2, c = lane & 3;
   if (!find_unit(un, a, blockIdx.y, blockIdx.x == 0)) return;
-  float* mine = part + static_cast<int64_t>(blockIdx.x) * a.T * r;
-  if (un.id < 0) {
-    for (int k = th; k < 16 * r; k += 128)
-      if (un.member[k / r] >= 0) mine[static_cast<int64_t>(un.member[k / r]) * r + k % r] = 0.0f;
+  if (un.id < 0) {   // tokens without an adapter; the whole cluster leaves
+    if (blockIdx.x == 0)
+      for (int k = th; k < 16 * r; k += 128)
+        if (un.member[k / r] >= 0) h[static_cast<int64_t>(un.member[k / r]) * r + k % r] = 0.0f;
     return;
   }
   const __nv_bfloat16* w = W + static_cast<int64_t>(un.id) * r * C;
@@ -618,23 +720,32 @@ __global__ void __launch_bounds__(128) lora_shrink_few_kernel(const __nv_bfloat1
 #pragma unroll
     for (int e = 0; e < 4; ++e) sums[warp][g + 8 * (e >> 1)][8 * i + 2 * c + (e & 1)] = acc[i][e];
   __syncthreads();
-  for (int k = th; k < 16 * r; k += 128) {
-    const int row = k / r, j = k - row * r, t = un.member[row];
-    if (t >= 0)
-      mine[static_cast<int64_t>(t) * r + j] = __fadd_rn(__fadd_rn(sums[0][row][j], sums[1][row][j]),
-                                                        __fadd_rn(sums[2][row][j], sums[3][row][j]));
+  for (int k = th; k < 16 * R; k += 128) {
+    const int row = k / R, j = k % R;
+    total[row][j] = __fadd_rn(__fadd_rn(sums[0][row][j], sums[1][row][j]), __fadd_rn(sums[2][row][j], sums[3][row][j]));
   }
+  const int split = gridDim.x, rank = blockIdx.x;
+  cluster_barrier();
+  const int begin = 16 * R * rank / split, end = 16 * R * (rank + 1) / split;
+  for (int k = begin + th; k < end; k += 128) {
+    const int row = k / R, j = k % R, t = un.member[row];
+    if (t < 0 || j >= r) continue;
+    float v = 0.0f;
+    for (int q = 0; q < split; ++q) v = __fadd_rn(v, load_cluster(&total[row][j], q));
+    h[static_cast<int64_t>(t) * r + j] = v;
+  }
+  cluster_barrier();   // no CTA leaves while another may still read its sums
 }
 
 // grid: 512 columns, unit.  Warp w takes 128 of the columns.
 constexpr int kFewCols = 512;
 
 template <int RP>
-__global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __restrict__ part, int splits,
+__global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __restrict__ h,
                                                               const __nv_bfloat16* __restrict__ W,
                                                               const float* __restrict__ scaling, const AdapterIds a,
                                                               int64_t C, int r, const __nv_bfloat16* in, int64_t ldi,
-                                                              __nv_bfloat16* out, int64_t ldo, float* __restrict__ w_out) {
+                                                              __nv_bfloat16* out, int64_t ldo) {
   pdl_entry();
   constexpr int R = 16 * RP;
   __shared__ __align__(16) Unit un;
@@ -655,12 +766,7 @@ __global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __res
     }
   for (int k = th; k < 16 * R; k += 128) {
     const int row = k / R, j = k % R, t = un.member[row];
-    float v = 0.0f;
-    if (t >= 0 && j < r) {
-      const int64_t at = static_cast<int64_t>(t) * r + j;
-      for (int s = 0; s < splits; ++s) v = __fadd_rn(v, __ldcg(part + s * a.T * r + at));
-      if (w_out && blockIdx.x == 0) w_out[at] = v;
-    }
+    const float v = (t >= 0 && j < r) ? __ldcg(h + static_cast<int64_t>(t) * r + j) : 0.0f;
     hs[row][j] = v;
   }
   __syncthreads();
@@ -675,13 +781,13 @@ __global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __res
       for (int half = 0; half < 2; ++half) {
         const float4 v = *reinterpret_cast<const float4*>(&hs[g + 8 * half][16 * p + 4 * c]);
         const float vv[4] = {v.x, v.y, v.z, v.w};
-        __nv_bfloat16 h[4], l[4];
+        __nv_bfloat16 hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split_bf16(__fmul_rn(s, vv[e]), h[e], l[e]);
-        ah[p][half] = pack_bf16(h[0], h[1]);
-        ah[p][2 + half] = pack_bf16(h[2], h[3]);
-        al[p][half] = pack_bf16(l[0], l[1]);
-        al[p][2 + half] = pack_bf16(l[2], l[3]);
+        for (int e = 0; e < 4; ++e) split_bf16(__fmul_rn(s, vv[e]), hi[e], lo[e]);
+        ah[p][half] = pack_bf16(hi[0], hi[1]);
+        ah[p][2 + half] = pack_bf16(hi[2], hi[3]);
+        al[p][half] = pack_bf16(lo[0], lo[1]);
+        al[p][2 + half] = pack_bf16(lo[2], lo[3]);
       }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -723,18 +829,16 @@ __global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __res
 
 // ---------------------------------------------------------------------------
 // outer: P[a][j, c] = s_a sum_{ids[t] = a} w[t, j] z[t, c] over a range of
-// row tiles.  Rows of other adapters are not read (their slots are zero, so a
-// NaN there reaches nothing).  Two products share a launch: dA (z = x, w = g,
-// stored [r, C]) and dB (z = dy, w = h, stored [C, r]).
+// rows, in tiles of 32.  Rows of other adapters in a tile are made zero before
+// it is used, w's too, so that a NaN there reaches nothing.  Two products
+// share a launch: dA (z = x, w = g, stored [r, C]) and dB (z = dy, w = h,
+// stored [C, r]).
 // grid: column tiles of both products, adapter, split of the rows.
 // TERMS: bf16 numbers that w enters as: 3 (all of fp32) for fp32 gradients,
-// 2 (2^-17) for bf16 ones.  They were written by the kernels before this one,
-// once for all column tiles.
+// 2 (2^-17) for bf16 ones, as the shrink kernel wrote them.
 // ---------------------------------------------------------------------------
 struct OuterProduct {
-  const __nv_bfloat16* w;   // [TERMS][T][16 RP]
-  const __nv_bfloat16* z;
-  int64_t ldz, C;
+  int64_t C;
   void* dst;
   float* part;
   int tiles;         // column tiles, 0: this product is not asked for
@@ -748,19 +852,22 @@ struct OuterArgs {
   int32_t* used;     // [adapter][split][column tile of both]: the split saw a token
 };
 
+constexpr int kRowsO = 32;                   // rows of a tile
+constexpr int kWindow = 32 * kRowsO;         // rows whose ids a CTA looks at together
+
 template <int RP, int TERMS>
 struct OuterCfg {
   static constexpr int R = 16 * RP;
   static constexpr int NQ = RP <= 2 ? 2 : 1;          // 16-column groups of a warp
-  static constexpr int COLS = 8 * 16 * NQ;            // columns of a tile
-  static constexpr int ZB = kRows * (COLS + 8) * 2;
-  static constexpr int HB = kRows * (R + 8) * 2;
+  static constexpr int COLS = kConsumers * 16 * NQ;   // columns of a tile
+  static constexpr int ZBOX = kRowsO * 128;           // 64 columns
+  static constexpr int ZB = COLS / 64 * ZBOX;
+  static constexpr int HB = kRowsO * R * 2;
   static constexpr int STAGE = ZB + TERMS * HB;
   static constexpr int CTAS = RP <= 2 ? 2 : 1;        // per SM
-  static constexpr int STAGES = (CTAS == 2 ? 104 : 208) * 1024 / STAGE;
-  static constexpr int BYTES = STAGES * STAGE;
+  static constexpr int STAGES = (CTAS == 2 ? 104 : 200) * 1024 / STAGE;
+  static constexpr int BYTES = 1024 + STAGES * STAGE + 256;
 };
-constexpr int kWindow = 2048;   // rows whose ids a CTA looks at together
 
 __device__ __forceinline__ void store_out(void* dst, int64_t at, float v, bool fp32) {
   if (fp32) static_cast<float*>(dst)[at] = v;
@@ -768,29 +875,37 @@ __device__ __forceinline__ void store_out(void* dst, int64_t at, float v, bool f
 }
 
 template <int RP, int TERMS>
-__global__ void __launch_bounds__(kNT, OuterCfg<RP, TERMS>::CTAS) lora_outer_kernel(const OuterArgs o) {
+__global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
+    lora_outer_kernel(const __grid_constant__ CUtensorMap tmap_z0, const __grid_constant__ CUtensorMap tmap_w0,
+                      const __grid_constant__ CUtensorMap tmap_z1, const __grid_constant__ CUtensorMap tmap_w1,
+                      const OuterArgs o) {
   pdl_entry();
   using S = OuterCfg<RP, TERMS>;
-  constexpr int R = S::R, COLS = S::COLS, NQ = S::NQ, ST = S::STAGES;
-  static_assert(ST >= 2, "a ring");
-  extern __shared__ __align__(16) uint8_t dyn[];
+  using Ranks = RankTile<RP>;
+  [[maybe_unused]] constexpr int R = S::R, COLS = S::COLS, NQ = S::NQ;
+  extern __shared__ uint8_t dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::STAGES * S::STAGE);
+  Ring ring{bars, bars + S::STAGES, S::STAGES, 0, 0u};
+  volatile int* abort = reinterpret_cast<volatile int*>(bars + 2 * S::STAGES);
   __shared__ __align__(16) int ids[kWindow];
-  __shared__ int list[kWindow / kRows];
+  __shared__ int list[kWindow / kRowsO];   // tiles with a token of this adapter; bit 8: all tokens are its
   __shared__ int listed;
   const int th = threadIdx.x, lane = th & 31, warp = th >> 5;
   const bool second = static_cast<int>(blockIdx.x) >= o.p[0].tiles;
   const OuterProduct& p = o.p[second ? 1 : 0];
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x - (second ? o.p[0].tiles : 0)) * COLS;
+  const CUtensorMap* map_z = second ? &tmap_z1 : &tmap_z0;
+  const CUtensorMap* map_w = second ? &tmap_w1 : &tmap_w0;
+  const int c0 = (static_cast<int>(blockIdx.x) - (second ? o.p[0].tiles : 0)) * COLS;
   const int id = blockIdx.y, splits = gridDim.z, split = blockIdx.z, r = o.r;
-  const int tiles = static_cast<int>((o.a.T + kRows - 1) / kRows);
-  const int first = static_cast<int>(static_cast<int64_t>(tiles) * split / splits);
-  const int last = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / splits);
-  // this thread copies one 16-byte chunk of rows zrow, zrow + kRowStep, ..
-  constexpr int kRowStep = kNT / (COLS / 8);
-  const int zrow = th / (COLS / 8), zch = th % (COLS / 8);
-  const bool zcol_ok = c0 + 8 * zch < p.C;
-  const __nv_bfloat16* zbase = p.z + c0 + 8 * zch;
-  const int64_t zstep = kRowStep * p.ldz;
+  const int64_t tiles = (o.a.T + kRowsO - 1) / kRowsO;
+  const int64_t first = tiles * split / splits, last = tiles * (split + 1) / splits;
+  if (th == 0) {
+    ring.init();
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
 
   float sum[RP][2 * NQ][4];
 #pragma unroll
@@ -798,95 +913,105 @@ __global__ void __launch_bounds__(kNT, OuterCfg<RP, TERMS>::CTAS) lora_outer_ker
 #pragma unroll
     for (int q = 0; q < 2 * NQ; ++q) sum[m][q][0] = sum[m][q][1] = sum[m][q][2] = sum[m][q][3] = 0.0f;
   bool any = false;
+  int issued = 0;
 
-  for (int base = first; base < last; base += kWindow / kRows) {
-    const int n_tiles = min(kWindow / kRows, last - base);
-    const int64_t row_base = static_cast<int64_t>(base) * kRows;
-    __syncthreads();   // the previous window's ids and list have been read
-    for (int k = th; k < n_tiles * kRows; k += kNT) ids[k] = adapter_of(o.a, row_base + k, false);
+  for (int64_t base = first; base < last; base += kWindow / kRowsO) {
+    const int n_tiles = static_cast<int>(last - base < kWindow / kRowsO ? last - base : kWindow / kRowsO);
+    const int64_t row_base = base * kRowsO;
+    // the previous window's ids and list have been read; after an abort all leave
+    if (__syncthreads_or(*abort != 0)) break;
+    for (int k = th; k < n_tiles * kRowsO; k += kThreads) ids[k] = adapter_of(o.a, row_base + k, false);
     __syncthreads();
-    if (warp == 0) {   // the tiles that hold a token of this adapter
-      bool mine = false;
+    if (warp == 0) {
+      bool some = false, all = true;
       if (lane < n_tiles)
-        for (int k = 0; k < kRows / 4; ++k) {
-          // lanes start at different places: no bank conflicts
-          const int4 v = *reinterpret_cast<const int4*>(&ids[lane * kRows + 4 * ((k + lane) % (kRows / 4))]);
-          mine |= v.x == id || v.y == id || v.z == id || v.w == id;
+        for (int k = 0; k < kRowsO / 4; ++k) {
+          // lanes start at different places: fewer bank conflicts
+          const int4 v = *reinterpret_cast<const int4*>(&ids[lane * kRowsO + 4 * ((k + lane) % (kRowsO / 4))]);
+          some |= v.x == id || v.y == id || v.z == id || v.w == id;
+          all &= v.x == id && v.y == id && v.z == id && v.w == id;
         }
-      const uint32_t m = __ballot_sync(0xFFFFFFFFu, mine);
-      if (mine) list[__popc(m & ((1u << lane) - 1u))] = lane;
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, some);
+      if (some) list[__popc(m & ((1u << lane) - 1u))] = lane | (all ? 256 : 0);
       if (lane == 0) listed = __popc(m);
     }
     __syncthreads();
     const int count = listed;
     any |= count > 0;
 
-    auto load = [&](int k, int slot) {
-      const int tile = list[k];
-      uint8_t* st = dyn + slot * S::STAGE;
-      const int64_t row0 = row_base + static_cast<int64_t>(tile) * kRows;
-      const __nv_bfloat16* src = zbase + (row0 + zrow) * p.ldz;
-      const int* idr = ids + tile * kRows + zrow;
-      uint8_t* to = st + zrow * (COLS + 8) * 2 + 16 * zch;
+    if (warp == kConsumers) {
+      if (lane == 0) {
+        for (int k = 0; k < count; ++k, ++issued, ring.next()) {
+          if (!ring.wait_empty(abort)) break;
+          const uint32_t bar = smem_u32(&ring.full[ring.slot]), zd = smem_u32(smem + ring.slot * S::STAGE), wd = zd + S::ZB;
+          const int row = static_cast<int>(row_base) + (list[k] & 255) * kRowsO;
+          mbar_expect_tx(bar, S::STAGE);
 #pragma unroll
-      for (int i = 0; i < kRows / kRowStep; ++i) {
-        const bool ok = zcol_ok && idr[kRowStep * i] == id;
-        copy16(to + i * kRowStep * (COLS + 8) * 2, ok ? src + i * zstep : p.z, ok);
+          for (int b = 0; b < COLS / 64; ++b) tma_load_2d(zd + b * S::ZBOX, map_z, c0 + 64 * b, row, bar);
+#pragma unroll
+          for (int x = 0; x < TERMS; ++x)
+#pragma unroll
+            for (int b = 0; b < Ranks::BOXES; ++b)
+              tma_load_3d(wd + x * S::HB + b * (S::HB / Ranks::BOXES), map_w, 64 * b, row, x, bar);
+        }
       }
-      for (int e = th; e < TERMS * kRows * (R / 8); e += kNT) {
-        const int x = e / (kRows * (R / 8)), row = e / (R / 8) % kRows, ch = e % (R / 8);
-        const bool ok = ids[tile * kRows + row] == id;
-        copy16(st + S::ZB + x * S::HB + row * (R + 8) * 2 + 16 * ch,
-               ok ? p.w + (x * o.a.T + row0 + row) * R + 8 * ch : p.w, ok);
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int k = 0; k < ST - 1; ++k) {
-      if (k < count) load(k, k);
-      else cp_async_commit();
-    }
-    int slot = 0, ahead = ST - 1;
-    for (int k = 0; k < count; ++k) {
-      cp_async_wait<ST - 2>();   // this tile has landed
-      __syncthreads();           // for every thread, and the tile before it has been read
-      if (k + ST - 1 < count) load(k + ST - 1, ahead);
-      else cp_async_commit();
-      const uint8_t* st = dyn + slot * S::STAGE;
-      if (++slot == ST) slot = 0;
-      if (++ahead == ST) ahead = 0;
-      const __nv_bfloat16* zs = reinterpret_cast<const __nv_bfloat16*>(st);
-      const __nv_bfloat16* wb = reinterpret_cast<const __nv_bfloat16*>(st + S::ZB);
-#pragma unroll
-      for (int m = 0; m < RP; ++m) {
-        float acc[2 * NQ][4];
-#pragma unroll
-        for (int q = 0; q < 2 * NQ; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.0f;
-#pragma unroll
-        for (int kk = 0; kk < kRows; kk += 16) {
-          uint32_t af[TERMS][4], bf[NQ][4];
-          const int arow = kk + (lane & 7) + ((lane >> 4) << 3), acol = 16 * m + ((lane >> 3) & 1) * 8;
-#pragma unroll
-          for (int x = 0; x < TERMS; ++x) ldsm4_t(af[x], wb + x * (S::HB / 2) + arow * (R + 8) + acol);
-#pragma unroll
-          for (int q = 0; q < NQ; ++q)
-            ldsm4_t(bf[q], zs + (kk + (lane & 7) + ((lane >> 3) & 1) * 8) * (COLS + 8) + 16 * (NQ * warp + q) + (lane >> 4) * 8);
-#pragma unroll
-          for (int x = TERMS - 1; x >= 0; --x)
-#pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-              mma16(acc[2 * q], af[x], bf[q]);
-              mma16(acc[2 * q + 1], af[x], bf[q] + 2);
-            }
+      __syncwarp();
+    } else {
+      for (int k = 0; k < count; ++k) {
+        if (!ring.wait_full(abort)) break;
+        uint8_t* zs = smem + ring.slot * S::STAGE;
+        uint8_t* wb = zs + S::ZB;
+        const bool mixed = !(list[k] & 256);
+        if (mixed) {   // zeros in the place of other adapters' rows (a row's chunks are its own, whatever their order)
+          const int* row_ids = ids + (list[k] & 255) * kRowsO;
+          for (int e = th; e < S::STAGE / 16; e += 32 * kConsumers) {
+            const int at = 16 * e;
+            const int row = at < S::ZB ? at % S::ZBOX / 128 : (at - S::ZB) % (kRowsO * Ranks::ROW) / Ranks::ROW;
+            if (row_ids[row] != id) *reinterpret_cast<uint4*>(zs + at) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          consumers_sync();
         }
 #pragma unroll
-        for (int q = 0; q < 2 * NQ; ++q)
+        for (int m = 0; m < RP; ++m) {
+          float acc[2 * NQ][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sum[m][q][e] = __fadd_rn(sum[m][q][e], acc[q][e]);
+          for (int q = 0; q < 2 * NQ; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.0f;
+#pragma unroll
+          for (int kk = 0; kk < kRowsO; kk += 16) {
+            uint32_t af[TERMS][4], bf[NQ][4];
+            const int arow = kk + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+            for (int x = 0; x < TERMS; ++x)
+              ldsm4_t(af[x], Ranks::template at<kRowsO>(wb + x * S::HB, arow, 2 * m + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              const int chunk = 2 * (NQ * warp + q) + (lane >> 4);   // of eight columns
+              ldsm4_t(bf[q], chunk_at<128>(zs + (chunk >> 3) * S::ZBOX, kk + (lane & 7) + ((lane >> 3) & 1) * 8, chunk & 7));
+            }
+#pragma unroll
+            for (int x = TERMS - 1; x >= 0; --x)
+#pragma unroll
+              for (int q = 0; q < NQ; ++q) {
+                mma16(acc[2 * q], af[x], bf[q]);
+                mma16(acc[2 * q + 1], af[x], bf[q] + 2);
+              }
+          }
+#pragma unroll
+          for (int q = 0; q < 2 * NQ; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[m][q][e] = __fadd_rn(sum[m][q][e], acc[q][e]);
+        }
+        if (mixed) fence_proxy_async_smem();   // the zeros were plain stores, the next copy is not
+        release(&ring.empty[ring.slot]);
+        ring.next();
       }
     }
-    cp_async_wait<0>();
   }
+  if (warp == kConsumers) {
+    if (lane == 0 && *abort) ring.drain(issued);
+    return;
+  }
+  if (th == 0 && *abort && o.a.status) *o.a.status = kStatusTimeout;
   const bool direct = splits == 1;
   if (!direct) {
     if (th == 0) o.used[(static_cast<int64_t>(id) * splits + split) * gridDim.x + blockIdx.x] = any ? 1 : 0;
@@ -948,41 +1073,63 @@ __global__ void __launch_bounds__(256) lora_outer_sum_kernel(const OuterArgs o, 
 // ---------------------------------------------------------------------------
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// A bf16 matrix [rows, cols] with row stride ld: boxes of 64 columns (128
+// bytes, swizzled) x box_rows.
+bool map_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// n contiguous bf16 matrices [rows, cols]: boxes of box_cols (16, 32 or 64,
+// swizzled over their 32, 64 or 128 bytes) x box_rows of one matrix.  What a
+// box has outside its matrix reads as zeros.
+bool map_stack(CUtensorMap* map, const void* base, int64_t n, int64_t rows, int64_t cols, int box_cols, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(n)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(rows * cols) * 2};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1}, estr[3] = {1, 1, 1};
+  const CUtensorMapSwizzle swizzle =
+      box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : (box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+int rank_box(int rp) { return rp >= 4 ? 64 : 16 * rp; }   // ranks of a RankTile's box
+
 // Units that T tokens and n adapters (and "none") can make.
 int64_t most_units(int64_t T, int64_t n) { return std::min<int64_t>(n + 1, T) + T / 16; }
 
-// Columns per shrink split: one wave of three CTAs per SM, with few tokens
-// about eight small CTAs per SM; whole 128-column stages.
-int64_t shrink_per_split(int64_t T, int64_t C, int64_t n) {
-  const bool few = T <= kFewTokens;
-  const int64_t rows = few ? most_units(T, n) : ceil_div(T, kRows);
-  const int64_t step = 128;
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(few ? 16 : 32, (few ? 8 : 3) * sm_count() / rows));
-  return ceil_div(ceil_div(C, splits), step) * step;
+// CTAs that share a row tile's columns (a cluster): two CTAs on every SM if
+// the row tiles are too few for that, at least 256 columns each.
+int shrink_split(int64_t T, int64_t C) {
+  int s = 1;
+  while (s < 8 && ceil_div(T, kRows) * s * 2 <= 2 * sm_count() && C >= 512 * s) s *= 2;
+  return s;
 }
-int shrink_splits(int64_t T, int64_t C, int64_t n) { return static_cast<int>(ceil_div(C, shrink_per_split(T, C, n))); }
-// The backward pass shrinks with the tile kernel for any T.
-int64_t tile_per_split(int64_t T, int64_t C) {
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(32, 3 * sm_count() / ceil_div(T, kRows)));
-  return ceil_div(ceil_div(C, splits), 128) * 128;
-}
-int tile_splits(int64_t T, int64_t C) { return static_cast<int>(ceil_div(C, tile_per_split(T, C))); }
+int few_split(int64_t C) { return C >= 1024 ? 8 : (C >= 512 ? 4 : (C >= 256 ? 2 : 1)); }
 
 int outer_cols(int64_t r) { return r <= 32 ? 256 : 128; }
 // Row ranges of the outer products: at most 2048 tokens each (an adapter may
 // own all of them), unless that makes more than 8.
-int outer_splits(int64_t T) { return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, ceil_div(T, kWindow)))); }
+int outer_splits(int64_t T) { return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, ceil_div(T, 2048)))); }
 
-// Parts of the workspace, in 16-byte steps.
+// Parts of the workspace, in 16-byte steps: h where the caller keeps none, or
+// g, the terms of both and the outer products' partial sums.
 struct LoraWorkspace {
-  size_t part, g_terms, h_terms, outer_a, outer_b, used, total;
+  size_t g, g_terms, h_terms, outer_a, outer_b, used, total;
 };
 size_t up16(size_t v) { return (v + 15) & ~static_cast<size_t>(15); }
 int64_t padded_rank(int64_t r) { return r <= 16 ? 16 : (r <= 32 ? 32 : (r <= 64 ? 64 : 128)); }
 LoraWorkspace lora_workspace(int64_t T, int64_t K, int64_t N, int64_t r, int64_t n, bool backward) {
   LoraWorkspace w{};
-  w.part = 0;
-  w.total = up16(static_cast<size_t>(backward ? tile_splits(T, N) : shrink_splits(T, K, n)) * T * r * 4);
+  w.g = 0;
+  w.total = up16(static_cast<size_t>(T * r) * 4);
   if (backward) {
     const size_t terms = up16(static_cast<size_t>(3 * T) * padded_rank(r) * 2);
     w.g_terms = w.total;
@@ -1007,78 +1154,110 @@ cudaError_t allow_smem(F fn, int bytes, bool* done) {
   return e;
 }
 
+// W: [n, r, C], TRANS: [n, C, r]
 template <int RP, bool TRANS>
-cudaError_t shrink(const __nv_bfloat16* z, int64_t ldz, const __nv_bfloat16* W, const AdapterIds& a, int64_t C, int r,
-                   float* part, const float* h, __nv_bfloat16* h_terms, int n_terms, cudaStream_t st) {
+cudaError_t shrink(const __nv_bfloat16* z, int64_t ldz, const __nv_bfloat16* W, const AdapterIds& a, int64_t C, int64_t r,
+                   float* w_out, __nv_bfloat16* w_terms, const float* h, __nv_bfloat16* h_terms, int n_terms,
+                   cudaStream_t st) {
+  using S = ShrinkCfg<RP, TRANS>;
   auto fn = lora_shrink_kernel<RP, TRANS>;
-  constexpr int smem = ShrinkCfg<RP, TRANS>::BYTES;
   static bool done[64] = {false};
-  cudaError_t e = allow_smem(fn, smem, done);
+  cudaError_t e = allow_smem(fn, S::BYTES, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.T, kRows)), static_cast<unsigned>(tile_splits(a.T, C)));
-  e = launch_k(fn, grid, dim3(kNT), smem, st, 1u, z, ldz, W, a, C, r, tile_per_split(a.T, C), part, h,
-               h_terms, n_terms);
+  CUtensorMap mz, mw;
+  if (!map_rows(&mz, z, a.T, C, ldz, kRows) ||
+      !(TRANS ? map_stack(&mw, W, a.n, C, r, rank_box(RP), S::KC) : map_stack(&mw, W, a.n, r, C, 64, S::R)))
+    return cudaErrorInvalidValue;
+  const int split = shrink_split(a.T, C);
+  const int per = static_cast<int>(ceil_div(ceil_div(C, split), S::KC) * S::KC);
+  e = launch_k(fn, dim3(static_cast<unsigned>(ceil_div(a.T, kRows) * split)), dim3(kThreads), S::BYTES, st,
+               static_cast<unsigned>(split), mz, mw, a, C, static_cast<int>(r), split, per, w_out, w_terms, h, h_terms, n_terms);
   note_launch();
   return e;
 }
 
+// W: [n, C, r], TRANS: [n, r, C]
 template <int RP, bool TRANS>
-cudaError_t expand(const float* part, int splits, const __nv_bfloat16* W, const float* scaling, const AdapterIds& a,
-                   int64_t C, int r, const __nv_bfloat16* in, int64_t ldi, __nv_bfloat16* out, int64_t ldo, float* w_out,
-                   __nv_bfloat16* w_terms, int n_terms, cudaStream_t st) {
+cudaError_t expand(const float* w, const __nv_bfloat16* W, const float* scaling, const AdapterIds& a, int64_t C, int64_t r,
+                   const __nv_bfloat16* in, int64_t ldi, __nv_bfloat16* out, int64_t ldo, cudaStream_t st) {
+  using S = ExpandCfg<RP>;
   auto fn = lora_expand_kernel<RP, TRANS>;
-  constexpr int smem = ExpandCfg<RP, TRANS>::BYTES;
   static bool done[64] = {false};
-  cudaError_t e = allow_smem(fn, smem, done);
+  cudaError_t e = allow_smem(fn, S::BYTES, done);
   if (e != cudaSuccess) return e;
-  // up to eight column tiles share one sum of the partials, as long as the
-  // grid still fills the GPU a few times over
-  const int64_t rows = ceil_div(a.T, kRows), cols = ceil_div(C, kCols);
-  const int per = out ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, rows * cols / (8 * sm_count())))) : 1;
-  const int64_t groups = out ? ceil_div(cols, per) : 1;
-  e = launch_k(fn, dim3(static_cast<unsigned>(rows * groups)), dim3(kNT), smem, st, 1u, part, splits, W, scaling, a, C, r, per,
-               static_cast<int>(groups), in, ldi, out, ldo, w_out, w_terms, n_terms);
+  CUtensorMap mi, mw, mo;
+  if (!map_rows(&mo, out, a.T, C, ldo, 16) || !map_rows(&mi, in ? in : out, a.T, C, in ? ldi : ldo, kRows) ||
+      !(TRANS ? map_stack(&mw, W, a.n, r, C, 64, S::R) : map_stack(&mw, W, a.n, C, r, rank_box(RP), S::KC)))
+    return cudaErrorInvalidValue;
+  const int64_t grid = std::min<int64_t>(ceil_div(a.T, kRows) * ceil_div(C, S::KC), S::CTAS * sm_count());
+  e = launch_k(fn, dim3(static_cast<unsigned>(grid)), dim3(kThreads), S::BYTES, st, 1u, mi, mw, mo, w, scaling, a, C,
+               static_cast<int>(r), in ? 1 : 0);
   note_launch();
   return e;
 }
 
 template <int RP, int TERMS>
-cudaError_t outer(const OuterArgs& o, cudaStream_t st) {
+cudaError_t outer(const LoraArgs& l, const AdapterIds& a, uint8_t* ws, const LoraWorkspace& w, cudaStream_t st) {
+  using S = OuterCfg<RP, TERMS>;
   auto fn = lora_outer_kernel<RP, TERMS>;
-  constexpr int smem = OuterCfg<RP, TERMS>::BYTES;
   static bool done[64] = {false};
-  cudaError_t e = allow_smem(fn, smem, done);
+  cudaError_t e = allow_smem(fn, S::BYTES, done);
   if (e != cudaSuccess) return e;
-  const int splits = outer_splits(o.a.T);
-  const dim3 grid(static_cast<unsigned>(o.p[0].tiles + o.p[1].tiles), static_cast<unsigned>(o.a.n), static_cast<unsigned>(splits));
-  e = launch_k(fn, grid, dim3(kNT), smem, st, 1u, o);
+  const int64_t ka = l.dA ? ceil_div(l.K, S::COLS) : 0, kb = l.dB ? ceil_div(l.N, S::COLS) : 0;
+  OuterArgs o{};
+  o.p[0] = OuterProduct{l.K, l.dA, reinterpret_cast<float*>(ws + w.outer_a), static_cast<int>(ka), 0};
+  o.p[1] = OuterProduct{l.N, l.dB, reinterpret_cast<float*>(ws + w.outer_b), static_cast<int>(kb), 1};
+  o.scaling = l.scaling;
+  o.a = a;
+  o.r = static_cast<int>(l.r);
+  o.fp32 = l.fp32 ? 1 : 0;
+  o.used = reinterpret_cast<int32_t*>(ws + w.used);
+  CUtensorMap mz[2], mw[2];
+  const int R = S::R;
+  // a product that is not asked for has no tiles; its maps are the other's
+  const bool both = l.dA && l.dB;
+  const __nv_bfloat16* z[2] = {l.dA ? l.x : l.dy, l.dB ? l.dy : l.x};
+  const int64_t ld[2] = {l.dA ? l.ldx : l.lddy, l.dB ? l.lddy : l.ldx}, C[2] = {l.dA ? l.K : l.N, l.dB ? l.N : l.K};
+  const uint8_t* terms[2] = {ws + (l.dA ? w.g_terms : w.h_terms), ws + (l.dB ? w.h_terms : w.g_terms)};
+  for (int i = 0; i < 2; ++i) {
+    if (i == 1 && !both) {
+      mz[1] = mz[0];
+      mw[1] = mw[0];
+    } else if (!map_rows(&mz[i], z[i], a.T, C[i], ld[i], kRowsO) ||
+               !map_stack(&mw[i], terms[i], TERMS, a.T, R, rank_box(RP), kRowsO)) {
+      return cudaErrorInvalidValue;
+    }
+  }
+  const int splits = outer_splits(a.T);
+  const dim3 grid(static_cast<unsigned>(ka + kb), static_cast<unsigned>(a.n), static_cast<unsigned>(splits));
+  e = launch_k(fn, grid, dim3(kThreads), S::BYTES, st, 1u, mz[0], mw[0], mz[1], mw[1], o);
   note_launch();
   if (e != cudaSuccess || splits == 1) return e;
-  const int64_t most = static_cast<int64_t>(o.a.n) * o.r * std::max(o.p[0].tiles ? o.p[0].C : 0, o.p[1].tiles ? o.p[1].C : 0);
+  const int64_t most = l.n * l.r * std::max(l.dA ? l.K : 0, l.dB ? l.N : 0);
   const int64_t blocks = std::min<int64_t>(ceil_div(most, 1024), 8 * sm_count());
-  e = launch_k(lora_outer_sum_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, 1u, o, splits, OuterCfg<RP, TERMS>::COLS);
+  e = launch_k(lora_outer_sum_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, 1u, o, splits, S::COLS);
   note_launch();
   return e;
 }
 
 template <int RP>
-cudaError_t forward(const LoraArgs& l, float* part, cudaStream_t st) {
+cudaError_t forward(const LoraArgs& l, float* h, cudaStream_t st) {
   const AdapterIds a{l.ids, l.T, static_cast<int>(l.n), l.status};
   const int r = static_cast<int>(l.r);
   if (l.T > kFewTokens) {
-    const cudaError_t e = shrink<RP, false>(l.x, l.ldx, l.A, a, l.K, r, part, nullptr, nullptr, 0, st);
+    const cudaError_t e = shrink<RP, false>(l.x, l.ldx, l.A, a, l.K, r, h, nullptr, nullptr, nullptr, 0, st);
     if (e != cudaSuccess) return e;
-    return expand<RP, false>(part, tile_splits(l.T, l.K), l.B, l.scaling, a, l.N, r, l.in, l.ldi, l.out, l.ldo, l.h,
-                             nullptr, 0, st);
+    return expand<RP, false>(h, l.B, l.scaling, a, l.N, r, l.in, l.ldi, l.out, l.ldo, st);
   }
   const unsigned units = static_cast<unsigned>(most_units(l.T, l.n));
-  const int splits = shrink_splits(l.T, l.K, l.n);
-  cudaError_t e = launch_k(lora_shrink_few_kernel<RP>, dim3(static_cast<unsigned>(splits), units), dim3(128), 0, st, 1u,
-                           l.x, l.ldx, l.A, a, l.K, r, shrink_per_split(l.T, l.K, l.n), part);
+  const int split = few_split(l.K);
+  cudaError_t e = launch_k(lora_shrink_few_kernel<RP>, dim3(static_cast<unsigned>(split), units), dim3(128), 0, st,
+                           static_cast<unsigned>(split), l.x, l.ldx, l.A, a, l.K, r,
+                           ceil_div(ceil_div(l.K, split), 32) * 32, h);
   note_launch();
   if (e != cudaSuccess) return e;
   e = launch_k(lora_expand_few_kernel<RP>, dim3(static_cast<unsigned>(ceil_div(l.N, kFewCols)), units), dim3(128), 0, st,
-               1u, part, splits, l.B, l.scaling, a, l.N, r, l.in, l.ldi, l.out, l.ldo, l.h);
+               1u, h, l.B, l.scaling, a, l.N, r, l.in, l.ldi, l.out, l.ldo);
   note_launch();
   return e;
 }
@@ -1086,31 +1265,17 @@ cudaError_t forward(const LoraArgs& l, float* part, cudaStream_t st) {
 template <int RP>
 cudaError_t backward(const LoraArgs& l, uint8_t* ws, const LoraWorkspace& w, cudaStream_t st) {
   const AdapterIds a{l.ids, l.T, static_cast<int>(l.n), l.status};
-  const int r = static_cast<int>(l.r), n_terms = l.fp32 ? 3 : 2;
-  float* part = reinterpret_cast<float*>(ws + w.part);
+  const int n_terms = l.fp32 ? 3 : 2;
+  float* g = reinterpret_cast<float*>(ws + w.g);
   __nv_bfloat16* g_terms = reinterpret_cast<__nv_bfloat16*>(ws + w.g_terms);
   __nv_bfloat16* h_terms = reinterpret_cast<__nv_bfloat16*>(ws + w.h_terms);
   // the shrink also writes h's terms, so it runs even where dB alone is asked for
-  cudaError_t e = shrink<RP, true>(l.dy, l.lddy, l.B, a, l.N, r, part, l.h, l.dB ? h_terms : nullptr, n_terms, st);
-  if (e != cudaSuccess) return e;
-  if (l.out || l.dA) {
-    e = expand<RP, true>(part, tile_splits(l.T, l.N), l.A, l.scaling, a, l.K, r, l.in, l.ldi, l.out, l.ldo, nullptr,
-                         l.dA ? g_terms : nullptr, n_terms, st);
-    if (e != cudaSuccess) return e;
-  }
-  if (!l.dA && !l.dB) return cudaSuccess;
-  const int cols = outer_cols(l.r);
-  OuterArgs o{};
-  o.p[0] = OuterProduct{g_terms, l.x, l.ldx, l.K, l.dA, reinterpret_cast<float*>(ws + w.outer_a),
-                        l.dA ? static_cast<int>(ceil_div(l.K, cols)) : 0, 0};
-  o.p[1] = OuterProduct{h_terms, l.dy, l.lddy, l.N, l.dB, reinterpret_cast<float*>(ws + w.outer_b),
-                        l.dB ? static_cast<int>(ceil_div(l.N, cols)) : 0, 1};
-  o.scaling = l.scaling;
-  o.a = a;
-  o.r = r;
-  o.fp32 = l.fp32 ? 1 : 0;
-  o.used = reinterpret_cast<int32_t*>(ws + w.used);
-  return l.fp32 ? outer<RP, 3>(o, st) : outer<RP, 2>(o, st);
+  cudaError_t e = shrink<RP, true>(l.dy, l.lddy, l.B, a, l.N, l.r, l.out ? g : nullptr, l.dA ? g_terms : nullptr, l.h,
+                                   l.dB ? h_terms : nullptr, n_terms, st);
+  if (e == cudaSuccess && l.out)
+    e = expand<RP, true>(g, l.A, l.scaling, a, l.K, l.r, l.in, l.ldi, l.out, l.ldo, st);
+  if (e != cudaSuccess || (!l.dA && !l.dB)) return e;
+  return l.fp32 ? outer<RP, 3>(l, a, ws, w, st) : outer<RP, 2>(l, a, ws, w, st);
 }
 
 }  // namespace
@@ -1120,11 +1285,11 @@ size_t lora_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t r, int64_t 
 }
 
 cudaError_t lora_forward_launch(const LoraArgs& l, void* workspace, cudaStream_t st) {
-  float* part = static_cast<float*>(workspace);
-  if (l.r <= 16) return forward<1>(l, part, st);
-  if (l.r <= 32) return forward<2>(l, part, st);
-  if (l.r <= 64) return forward<4>(l, part, st);
-  return forward<8>(l, part, st);
+  float* h = l.h ? l.h : static_cast<float*>(workspace);
+  if (l.r <= 16) return forward<1>(l, h, st);
+  if (l.r <= 32) return forward<2>(l, h, st);
+  if (l.r <= 64) return forward<4>(l, h, st);
+  return forward<8>(l, h, st);
 }
 
 cudaError_t lora_backward_launch(const LoraArgs& l, void* workspace, cudaStream_t st) {

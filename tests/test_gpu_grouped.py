@@ -283,7 +283,7 @@ def check_gemm(api, counts, N, K, fp32, seed=21, first=0, behind=0, ldd=None):
 @pytest.mark.parametrize("counts,N,K", [
     ([1], 128, 64), ([1], 256, 256), ([3, 0, 5], 384, 320), ([256], 256, 512), ([300, 1, 0, 129], 256, 192),
     ([16, 17, 15, 31, 33], 640, 1088), ([0, 0, 2], 128, 128), ([513, 255, 257], 384, 640),
-    ([32, 33, 127, 128, 129, 0, 300], 128, 320), ([600], 256, 64), ([170, 170, 170], 128, 256),
+    ([32, 33, 127, 128, 129, 0, 300], 128, 320), ([600], 256, 64), ([79, 81, 79], 128, 256), ([81, 81, 81], 384, 256),
 ])
 def test_gemm_shapes(api, counts, N, K, fp32):
     check_gemm(api, counts, N, K, fp32)
