@@ -20,6 +20,10 @@ __device__ __forceinline__ void pdl_entry() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// A kernel that is always launched right behind another of the library may do
+// work ahead of pdl_entry() that reads only what is older than that kernel:
+// its predecessor lets it start after its own pdl_entry(), when everything
+// before the two is complete and visible.
 
 inline bool pdl_enabled() {
   static const bool on = [] {

@@ -165,13 +165,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Shared-memory tiles as TMA writes them: rows of ROW bytes (32, 64 or 128)
-// whose 16-byte chunks are swizzled by the row, so that eight rows of one
+// Shared-memory tiles as TMA writes them: rows of ROW bytes (64 or 128) whose 16-byte chunks are swizzled by the row, so that eight rows of one
 // chunk lie in different banks.  Wider tiles are several boxes, one behind
 // the other.
 template <int ROW>
 __device__ __forceinline__ const uint8_t* chunk_at(const uint8_t* tile, int row, int chunk) {
-  constexpr int kShift = ROW == 128 ? 0 : (ROW == 64 ? 1 : 2);
+  constexpr int kShift = ROW == 128 ? 0 : 1;
   return tile + row * ROW + ((chunk ^ ((row >> kShift) & (ROW / 16 - 1))) << 4);
 }
 template <int ROW>
@@ -180,6 +179,10 @@ __device__ __forceinline__ uint8_t* chunk_at(uint8_t* tile, int row, int chunk) 
 }
 
 // A tile of rank vectors: ROWS rows of R = 16 RP ranks (R = 128: two boxes).
+// Rows of 32 bytes (R = 16) are not swizzled: a tile of them is one piece of
+// memory, which a plain bulk copy brings in 128-byte lines, where a tensor copy
+// takes as long for each 32-byte row as for one of 128 (eight rows then share
+// two cycles of shared memory instead of one, which costs less).
 template <int RP>
 struct RankTile {
   static constexpr int R = 16 * RP;
@@ -187,7 +190,8 @@ struct RankTile {
   static constexpr int BOXES = RP == 8 ? 2 : 1;
   template <int ROWS>
   static __device__ __forceinline__ const uint8_t* at(const uint8_t* tile, int row, int chunk) {   // chunk: 8 ranks
-    if constexpr (BOXES == 1) return chunk_at<ROW>(tile, row, chunk);
+    if constexpr (RP == 1) return tile + row * ROW + 16 * chunk;
+    else if constexpr (BOXES == 1) return chunk_at<ROW>(tile, row, chunk);
     else return chunk_at<ROW>(tile + (chunk >> 3) * (ROWS * ROW), row, chunk & 7);
   }
 };
@@ -223,6 +227,18 @@ __device__ __forceinline__ void tile_adapters(TileAdapters& ta, int id) {
     if (lane == 0) ta.count = head + __popc(m);
   }
   __syncthreads();
+}
+
+// Rank vectors c .. c + ROWS - 1 of adapter `id` (W [n, C, r]) into a tile.
+template <int RP, int ROWS>
+__device__ __forceinline__ void load_ranks(uint32_t dst, const CUtensorMap* map, const __nv_bfloat16* W, int id, int c,
+                                           int64_t C, int r, uint32_t bar) {
+  if (RP == 1 && r == 16 && c + ROWS <= C) {
+    bulk_load(dst, W + (static_cast<int64_t>(id) * C + c) * 16, ROWS * 32, bar);
+    return;
+  }
+  tma_load_3d(dst, map, 0, c, id, bar);   // rows past the last one read as zeros
+  if constexpr (RP == 8) tma_load_3d(dst + ROWS * 128, map, 64, c, id, bar);
 }
 
 // The bf16 numbers that make up w [T, r] (n_terms of them), rows padded to R
@@ -267,7 +283,7 @@ struct ShrinkCfg {
 template <int RP, bool TRANS>
 __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap tmap_z, const __grid_constant__ CUtensorMap tmap_w,
-                       const AdapterIds a, int64_t C, int r, int split, int per_split, float* __restrict__ w_out,
+                       const __nv_bfloat16* __restrict__ W, const AdapterIds a, int64_t C, int r, int split, float* __restrict__ w_out,
                        __nv_bfloat16* __restrict__ w_terms, const float* __restrict__ h,
                        __nv_bfloat16* __restrict__ h_terms, int n_terms) {
   pdl_entry();
@@ -285,9 +301,10 @@ __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
   const int th = threadIdx.x, lane = th & 31, warp = th >> 5;
   const int rank = static_cast<int>(blockIdx.x) % split;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / split) * kRows;
-  const int64_t c_begin = static_cast<int64_t>(rank) * per_split;
-  const int64_t c_end = c_begin + per_split < C ? c_begin + per_split : C;
-  const int steps = c_end > c_begin ? static_cast<int>((c_end - c_begin + KC - 1) / KC) : 0;
+  // stages rank, rank + split, ..: the cluster reads neighbouring columns at a
+  // time, which DRAM answers faster than distant ones
+  const int stages = static_cast<int>((C + KC - 1) / KC);
+  const int steps = (stages - rank + split - 1) / split;
   if (th == 0) {
     ring.init();
     *abort = 0;
@@ -304,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
           if (!ring.wait_empty(abort)) break;
           const uint32_t bar = smem_u32(&ring.full[ring.slot]);
           const uint32_t zd = smem_u32(zs + ring.slot * S::ZB), wd = smem_u32(wsm + ring.slot * S::WB);
-          const int c = static_cast<int>(c_begin) + s * KC;
+          const int c = (s * split + rank) * KC;
           mbar_expect_tx(bar, S::ZB + S::WB);
           tma_load_2d(zd, &tmap_z, c, static_cast<int>(row0), bar);
           tma_load_2d(zd + S::ZB / 2, &tmap_z, c + 64, static_cast<int>(row0), bar);
@@ -312,8 +329,7 @@ __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
             tma_load_3d(wd, &tmap_w, c, 0, ta.list[u], bar);
             tma_load_3d(wd + S::WB / 2, &tmap_w, c + 64, 0, ta.list[u], bar);
           } else {
-            tma_load_3d(wd, &tmap_w, 0, c, ta.list[u], bar);
-            if constexpr (RP == 8) tma_load_3d(wd + S::WB / 2, &tmap_w, 64, c, ta.list[u], bar);
+            load_ranks<RP, KC>(wd, &tmap_w, W, ta.list[u], c, C, r, bar);
           }
         }
       }
@@ -414,10 +430,11 @@ __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
 // ---------------------------------------------------------------------------
 // expand: out[t, c] = base[t, c] + s_a sum_j w[t, j] W[c, j].
 // TRANS: W is stored [r, C], else [C, r].
-// Persistent CTAs walk runs of 64 x 128 tiles, columns fastest.  One ring
-// holds base tiles (TMA in, changed in place, TMA out), another the weights
-// of the tile's adapters, one slot each; w stays in registers while the row
-// tile does, its scale folded in.  Warp w: rows 16 (w % 4), columns 64 (w / 4).
+// A CTA takes 64 rows and every groups-th tile of 128 columns, so that the
+// CTAs at work read and write neighbouring columns at a time.  One ring holds
+// base tiles (TMA in, changed in place, TMA out), another the weights of the
+// rows' adapters, one slot each; w stays in registers, its scale folded in.
+// Warp w: rows 16 (w % 4), columns 64 (w / 4) of a tile.
 // ---------------------------------------------------------------------------
 template <int RP>
 struct ExpandCfg {
@@ -434,9 +451,11 @@ struct ExpandCfg {
 template <int RP, bool TRANS>
 __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
     lora_expand_kernel(const __grid_constant__ CUtensorMap tmap_in, const __grid_constant__ CUtensorMap tmap_w,
-                       const __grid_constant__ CUtensorMap tmap_out, const float* __restrict__ w,
-                       const float* __restrict__ scaling, const AdapterIds a, int64_t C, int r, int has_in) {
-  pdl_entry();
+                       const __grid_constant__ CUtensorMap tmap_out, const __nv_bfloat16* __restrict__ W,
+                       const float* __restrict__ w,
+                       const float* __restrict__ scaling, const AdapterIds a, int64_t C, int r, int has_in, int groups) {
+  // launched right behind the shrink kernel: all but w is older than that, so
+  // the producer and the adapters need not wait for it (see pdl_entry below)
   using S = ExpandCfg<RP>;
   [[maybe_unused]] constexpr int R = S::R, KC = S::KC;
   extern __shared__ uint8_t dyn[];
@@ -449,151 +468,141 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
   volatile int* abort = reinterpret_cast<volatile int*>(bars + 2 * (S::YSLOTS + S::WSLOTS));
   __shared__ TileAdapters ta;
   const int th = threadIdx.x, lane = th & 31, warp = th >> 5;
-  const int64_t col_tiles = (C + KC - 1) / KC, total = (a.T + kRows - 1) / kRows * col_tiles;
-  const int64_t begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+  const int group = static_cast<int>(blockIdx.x) % groups;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / groups) * kRows;
   if (th == 0) {
     yr.init();
     wr.init();
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  __syncthreads();
-  // Row tile by row tile: all threads agree on its adapters, then the producer
-  // and the consumers walk its column tiles at their own pace.
-  int64_t tile = begin;
-  int y_issued = 0, w_issued = 0;
-  int held = -1;   // base slot whose store may still be reading it
-  while (tile < end) {
-    const int64_t row_tile = tile / col_tiles, row0 = row_tile * kRows;
-    const int64_t stop = min(end, (row_tile + 1) * col_tiles);
-    // the previous row tile's adapters have been read; after an abort all leave
-    if (__syncthreads_or(*abort != 0)) break;
-    tile_adapters(ta, th < kRows ? adapter_of(a, row0 + th, false) : -1);
-    if (warp == kConsumers) {
-      if (lane == 0) {
-        for (int64_t k = tile; k < stop && !*abort; ++k) {
-          const int c = static_cast<int>(k - row_tile * col_tiles) * KC;
-          if (!yr.wait_empty(abort)) break;
-          const uint32_t yb = smem_u32(&yr.full[yr.slot]), yd = smem_u32(ys + yr.slot * S::YB);
-          if (has_in) {
-            mbar_expect_tx(yb, S::YB);
-            tma_load_2d(yd, &tmap_in, c, static_cast<int>(row0), yb);
-            tma_load_2d(yd + S::YB / 2, &tmap_in, c + 64, static_cast<int>(row0), yb);
+  tile_adapters(ta, th < kRows ? adapter_of(a, row0 + th, false) : -1);   // ends with a barrier
+  const int stride = groups * KC;   // between this CTA's columns
+  if (warp == kConsumers) {
+    if (lane == 0) {
+      int y_issued = 0, w_issued = 0;
+      for (int c = group * KC; c < C && !*abort; c += stride) {
+        if (!yr.wait_empty(abort)) break;
+        const uint32_t yb = smem_u32(&yr.full[yr.slot]), yd = smem_u32(ys + yr.slot * S::YB);
+        if (has_in) {
+          mbar_expect_tx(yb, S::YB);
+          tma_load_2d(yd, &tmap_in, c, static_cast<int>(row0), yb);
+          tma_load_2d(yd + S::YB / 2, &tmap_in, c + 64, static_cast<int>(row0), yb);
+        } else {
+          mbar_expect_tx(yb, 0);
+        }
+        yr.next();
+        ++y_issued;
+        for (int u = 0; u < ta.count; ++u) {
+          if (!wr.wait_empty(abort)) break;
+          const uint32_t wb = smem_u32(&wr.full[wr.slot]), wd = smem_u32(wsm + wr.slot * S::WB);
+          mbar_expect_tx(wb, S::WB);
+          if constexpr (!TRANS) {
+            load_ranks<RP, KC>(wd, &tmap_w, W, ta.list[u], c, C, r, wb);
           } else {
-            mbar_expect_tx(yb, 0);
+            tma_load_3d(wd, &tmap_w, c, 0, ta.list[u], wb);
+            tma_load_3d(wd + S::WB / 2, &tmap_w, c + 64, 0, ta.list[u], wb);
           }
-          yr.next();
-          ++y_issued;
-          for (int u = 0; u < ta.count; ++u) {
-            if (!wr.wait_empty(abort)) break;
-            const uint32_t wb = smem_u32(&wr.full[wr.slot]), wd = smem_u32(wsm + wr.slot * S::WB);
-            mbar_expect_tx(wb, S::WB);
-            if constexpr (!TRANS) {
-              tma_load_3d(wd, &tmap_w, 0, c, ta.list[u], wb);
-              if constexpr (RP == 8) tma_load_3d(wd + S::WB / 2, &tmap_w, 64, c, ta.list[u], wb);
-            } else {
-              tma_load_3d(wd, &tmap_w, c, 0, ta.list[u], wb);
-              tma_load_3d(wd + S::WB / 2, &tmap_w, c + 64, 0, ta.list[u], wb);
-            }
-            wr.next();
-            ++w_issued;
-          }
+          wr.next();
+          ++w_issued;
         }
       }
-      __syncwarp();
-    } else {
-      const int rg = warp & 3, ch = warp >> 2;
-      const int my_row = 16 * rg + (lane >> 2);   // this thread's rows of the tile: my_row and my_row + 8
-      const int id_lo = ta.ids[my_row], id_hi = ta.ids[my_row + 8];
-      // w of this warp's rows as MMA operands: hi and lo parts of s_a w
-      uint32_t ah[RP][4], al[RP][4];
-      const float s_lo = id_lo >= 0 ? __ldg(scaling + id_lo) : 0.0f, s_hi = id_hi >= 0 ? __ldg(scaling + id_hi) : 0.0f;
+      if (*abort) {
+        yr.drain(y_issued);
+        wr.drain(w_issued);
+      }
+    }
+    __syncwarp();
+    pdl_entry();
+  } else {
+    const int rg = warp & 3, ch = warp >> 2;
+    const int my_row = 16 * rg + (lane >> 2);   // this thread's rows of the tile: my_row and my_row + 8
+    const int id_lo = ta.ids[my_row], id_hi = ta.ids[my_row + 8];
+    pdl_entry();
+    // w of this warp's rows as MMA operands: hi and lo parts of s_a w
+    uint32_t ah[RP][4], al[RP][4];
+    const float s_lo = id_lo >= 0 ? __ldg(scaling + id_lo) : 0.0f, s_hi = id_hi >= 0 ? __ldg(scaling + id_hi) : 0.0f;
 #pragma unroll
-      for (int p = 0; p < RP; ++p)
+    for (int p = 0; p < RP; ++p)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {   // row + 8 (e % 2), ranks 16 p + 2 (lane % 4) + 8 (e / 2), + 1
-          const int id = e & 1 ? id_hi : id_lo, j = 16 * p + 2 * (lane & 3) + 8 * (e >> 1);
-          float2 v = make_float2(0.0f, 0.0f);
-          if (id >= 0 && j < r) v = __ldcg(reinterpret_cast<const float2*>(w + (row0 + my_row + 8 * (e & 1)) * r + j));
-          const float s = e & 1 ? s_hi : s_lo;
-          __nv_bfloat16 h0, l0, h1, l1;
-          split_bf16(id >= 0 ? __fmul_rn(s, v.x) : 0.0f, h0, l0);
-          split_bf16(id >= 0 ? __fmul_rn(s, v.y) : 0.0f, h1, l1);
-          ah[p][e] = pack_bf16(h0, h1);
-          al[p][e] = pack_bf16(l0, l1);
-        }
-      for (int64_t k = tile; k < stop; ++k) {
-        const int c0 = static_cast<int>(k - row_tile * col_tiles) * KC;
-        if (held >= 0) {   // the previous tile's store has read its slot
-          if (lane == 0) bulk_wait_read<0>();
-          release(&yr.empty[held]);
-          held = -1;
-        }
-        if (!yr.wait_full(abort)) break;
-        uint8_t* yt = ys + yr.slot * S::YB + ch * (S::YB / 2);   // this half's box of 64 columns
-        if (!has_in) {
+      for (int e = 0; e < 4; ++e) {   // row + 8 (e % 2), ranks 16 p + 2 (lane % 4) + 8 (e / 2), + 1
+        const int id = e & 1 ? id_hi : id_lo, j = 16 * p + 2 * (lane & 3) + 8 * (e >> 1);
+        float2 v = make_float2(0.0f, 0.0f);
+        if (id >= 0 && j < r) v = __ldcg(reinterpret_cast<const float2*>(w + (row0 + my_row + 8 * (e & 1)) * r + j));
+        const float s = e & 1 ? s_hi : s_lo;
+        __nv_bfloat16 h0, l0, h1, l1;
+        split_bf16(id >= 0 ? __fmul_rn(s, v.x) : 0.0f, h0, l0);
+        split_bf16(id >= 0 ? __fmul_rn(s, v.y) : 0.0f, h1, l1);
+        ah[p][e] = pack_bf16(h0, h1);
+        al[p][e] = pack_bf16(l0, l1);
+      }
+    int held = -1;   // base slot whose store may still be reading it
+    for (int c0 = group * KC; c0 < C; c0 += stride) {
+      if (!yr.wait_full(abort)) break;
+      uint8_t* yt = ys + yr.slot * S::YB + ch * (S::YB / 2);   // this half's box of 64 columns
+      if (!has_in) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(yt + (16 * rg) * 128 + 16 * (lane + 32 * i)) = make_uint4(0u, 0u, 0u, 0u);
-          __syncwarp();
-        }
-        bool ok = true;
-        for (int u = 0; u < ta.count && ok; ++u) {
-          ok = wr.wait_full(abort);
-          if (!ok) break;
-          const int id = ta.list[u];
-          const uint8_t* wt = wsm + wr.slot * S::WB;
-          const bool lo_mine = id_lo == id, hi_mine = id_hi == id;
-          if (__any_sync(0xFFFFFFFFu, lo_mine || hi_mine)) {
-#pragma unroll
-            for (int n = 0; n < 64; n += 16) {   // columns of this half
-              float acc[2][4] = {};
-#pragma unroll
-              for (int p = 0; p < RP; ++p) {
-                uint32_t bf[4];
-                if constexpr (!TRANS)
-                  ldsm4(bf, RankTile<RP>::template at<KC>(wt, 64 * ch + n + (lane & 7) + ((lane >> 4) << 3), 2 * p + ((lane >> 3) & 1)));
-                else
-                  ldsm4_t(bf, chunk_at<128>(wt + ch * (S::WB / 2), 16 * p + (lane & 7) + ((lane >> 3) & 1) * 8, n / 8 + (lane >> 4)));
-                mma16(acc[0], al[p], bf);
-                mma16(acc[1], al[p], bf + 2);
-                mma16(acc[0], ah[p], bf);
-                mma16(acc[1], ah[p], bf + 2);
-              }
-              // a token without an adapter keeps the base's bits (a NaN's payload, a zero's sign)
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-                  if (half ? hi_mine : lo_mine) {
-                    uint32_t* at = reinterpret_cast<uint32_t*>(chunk_at<128>(yt, my_row + 8 * half, n / 8 + q)) + (lane & 3);
-                    *at = add_round(*at, acc[q][2 * half], acc[q][2 * half + 1]);
-                  }
-            }
-          }
-          release(&wr.empty[wr.slot]);
-          wr.next();
-        }
-        if (!ok) break;
-        fence_proxy_async_smem();
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(yt + (16 * rg) * 128 + 16 * (lane + 32 * i)) = make_uint4(0u, 0u, 0u, 0u);
         __syncwarp();
-        if (lane == 0 && c0 + 64 * ch < C && row0 + 16 * rg < a.T) {
+      }
+      bool ok = true;
+      for (int u = 0; u < ta.count && ok; ++u) {
+        ok = wr.wait_full(abort);
+        if (!ok) break;
+        const int id = ta.list[u];
+        const uint8_t* wt = wsm + wr.slot * S::WB;
+        const bool lo_mine = id_lo == id, hi_mine = id_hi == id;
+        if (__any_sync(0xFFFFFFFFu, lo_mine || hi_mine)) {
+#pragma unroll
+          for (int n = 0; n < 64; n += 16) {   // columns of this half
+            float acc[2][4] = {};
+#pragma unroll
+            for (int p = 0; p < RP; ++p) {
+              uint32_t bf[4];
+              if constexpr (!TRANS)
+                ldsm4(bf, RankTile<RP>::template at<KC>(wt, 64 * ch + n + (lane & 7) + ((lane >> 4) << 3), 2 * p + ((lane >> 3) & 1)));
+              else
+                ldsm4_t(bf, chunk_at<128>(wt + ch * (S::WB / 2), 16 * p + (lane & 7) + ((lane >> 3) & 1) * 8, n / 8 + (lane >> 4)));
+              mma16(acc[0], al[p], bf);
+              mma16(acc[1], al[p], bf + 2);
+              mma16(acc[0], ah[p], bf);
+              mma16(acc[1], ah[p], bf + 2);
+            }
+            // a token without an adapter keeps the base's bits (a NaN's payload, a zero's sign)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int half = 0; half < 2; ++half)
+                if (half ? hi_mine : lo_mine) {
+                  uint32_t* at = reinterpret_cast<uint32_t*>(chunk_at<128>(yt, my_row + 8 * half, n / 8 + q)) + (lane & 3);
+                  *at = add_round(*at, acc[q][2 * half], acc[q][2 * half + 1]);
+                }
+          }
+        }
+        release(&wr.empty[wr.slot]);
+        wr.next();
+      }
+      if (!ok) break;
+      fence_proxy_async_smem();
+      __syncwarp();
+      // store this warp's part; the previous tile's store has read its slot by
+      // now (a part that lies outside makes no store, so all are waited for)
+      const bool inside = c0 + 64 * ch < C && row0 + 16 * rg < a.T;
+      if (lane == 0) {
+        if (inside) {
           tma_store_2d(&tmap_out, smem_u32(yt + 16 * rg * 128), c0 + 64 * ch, static_cast<int>(row0) + 16 * rg);
           bulk_commit();
+          bulk_wait_read<1>();
+        } else {
+          bulk_wait_read<0>();
         }
-        held = yr.slot;
-        yr.next();
       }
+      if (held >= 0) release(&yr.empty[held]);
+      held = yr.slot;
+      yr.next();
     }
-    tile = stop;
-  }
-  if (warp == kConsumers) {
-    if (lane == 0 && *abort) {
-      yr.drain(y_issued);
-      wr.drain(w_issued);
-    }
-  } else if (lane == 0) {
-    bulk_wait_all();
+    if (lane == 0) bulk_wait_all();
   }
   if (th == 0 && *abort && a.status) *a.status = kStatusTimeout;
 }
@@ -697,22 +706,31 @@ __global__ void __launch_bounds__(128) lora_shrink_few_kernel(const __nv_bfloat1
   const int t0 = un.member[g], t1 = un.member[g + 8];
   const int64_t c_begin = blockIdx.x * per_split, c_end = min(c_begin + per_split, C);
   float acc[2 * RP][4] = {};
-  for (int64_t c0 = c_begin + 32 * warp; c0 < c_end; c0 += 128) {
-    const int64_t cc = c0 + 8 * c;
-    const bool ok = cc < c_end;
-    const uint4 a0 = load16(z + t0 * ldz + cc, ok && t0 >= 0), a1 = load16(z + t1 * ldz + cc, ok && t1 >= 0);
-    uint4 b[2 * RP];
+  // the loads of kBlocks blocks are in flight together
+  constexpr int kBlocks = RP == 1 ? 4 : (RP == 2 ? 2 : 1);
+  for (int64_t c0 = c_begin + 32 * warp; c0 < c_end; c0 += 128 * kBlocks) {
+    uint4 a0[kBlocks], a1[kBlocks], b[kBlocks][2 * RP];
 #pragma unroll
-    for (int i = 0; i < 2 * RP; ++i) b[i] = load16(w + (8 * i + g) * C + cc, ok && 8 * i + g < r);
-    const uint32_t f0[4] = {a0.x, a1.x, a0.y, a1.y}, f1[4] = {a0.z, a1.z, a0.w, a1.w};
-    float run[2 * RP][4] = {};   // short runs on the tensor core, fp32 sums outside
+    for (int x = 0; x < kBlocks; ++x) {
+      const int64_t cc = c0 + 128 * x + 8 * c;
+      const bool ok = cc < c_end;
+      a0[x] = load16(z + t0 * ldz + cc, ok && t0 >= 0);
+      a1[x] = load16(z + t1 * ldz + cc, ok && t1 >= 0);
 #pragma unroll
-    for (int i = 0; i < 2 * RP; ++i) {
-      const uint32_t b0[2] = {b[i].x, b[i].y}, b1[2] = {b[i].z, b[i].w};
-      mma16(run[i], f0, b0);
-      mma16(run[i], f1, b1);
+      for (int i = 0; i < 2 * RP; ++i) b[x][i] = load16(w + (8 * i + g) * C + cc, ok && 8 * i + g < r);
+    }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = __fadd_rn(acc[i][e], run[i][e]);
+    for (int x = 0; x < kBlocks; ++x) {
+      const uint32_t f0[4] = {a0[x].x, a1[x].x, a0[x].y, a1[x].y}, f1[4] = {a0[x].z, a1[x].z, a0[x].w, a1[x].w};
+#pragma unroll
+      for (int i = 0; i < 2 * RP; ++i) {
+        float run[4] = {};   // short runs on the tensor core, fp32 sums outside
+        const uint32_t b0[2] = {b[x][i].x, b[x][i].y}, b1[2] = {b[x][i].z, b[x][i].w};
+        mma16(run, f0, b0);
+        mma16(run, f1, b1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] = __fadd_rn(acc[i][e], run[e]);
+      }
     }
   }
 #pragma unroll
@@ -746,12 +764,15 @@ __global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __res
                                                               const float* __restrict__ scaling, const AdapterIds a,
                                                               int64_t C, int r, const __nv_bfloat16* in, int64_t ldi,
                                                               __nv_bfloat16* out, int64_t ldo) {
-  pdl_entry();
+  // launched right behind the shrink kernel: all but h is older than that
   constexpr int R = 16 * RP;
   __shared__ __align__(16) Unit un;
   __shared__ __align__(16) float hs[16][R + 4];   // read as float4
   const int th = threadIdx.x, lane = th & 31, warp = th >> 5, g = lane >> 2, c = lane & 3;
-  if (!find_unit(un, a, blockIdx.y, false)) return;
+  if (!find_unit(un, a, blockIdx.y, false)) {
+    pdl_entry();
+    return;
+  }
   const int64_t c_warp = static_cast<int64_t>(blockIdx.x) * kFewCols + 128 * warp;
   const int t0 = un.member[g], t1 = un.member[g + 8];
   uint4 y[4][2];
@@ -764,6 +785,7 @@ __global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __res
       y[q][half] = make_uint4(0u, 0u, 0u, 0u);
       if (in && t >= 0 && col < C) y[q][half] = __ldcg(reinterpret_cast<const uint4*>(in + t * ldi + col));
     }
+  pdl_entry();
   for (int k = th; k < 16 * R; k += 128) {
     const int row = k / R, j = k % R, t = un.member[row];
     const float v = (t >= 0 && j < r) ? __ldcg(h + static_cast<int64_t>(t) * r + j) : 0.0f;
@@ -1085,8 +1107,8 @@ bool map_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, in
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// n contiguous bf16 matrices [rows, cols]: boxes of box_cols (16, 32 or 64,
-// swizzled over their 32, 64 or 128 bytes) x box_rows of one matrix.  What a
+// n contiguous bf16 matrices [rows, cols]: boxes of box_cols (16, or 32 or 64
+// swizzled over their 64 or 128 bytes) x box_rows of one matrix.  What a
 // box has outside its matrix reads as zeros.
 bool map_stack(CUtensorMap* map, const void* base, int64_t n, int64_t rows, int64_t cols, int box_cols, int box_rows) {
   auto fn = encode_fn();
@@ -1095,7 +1117,7 @@ bool map_stack(CUtensorMap* map, const void* base, int64_t n, int64_t rows, int6
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(rows * cols) * 2};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1}, estr[3] = {1, 1, 1};
   const CUtensorMapSwizzle swizzle =
-      box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : (box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+      box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : (box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE);
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1105,19 +1127,24 @@ int rank_box(int rp) { return rp >= 4 ? 64 : 16 * rp; }   // ranks of a RankTile
 // Units that T tokens and n adapters (and "none") can make.
 int64_t most_units(int64_t T, int64_t n) { return std::min<int64_t>(n + 1, T) + T / 16; }
 
-// CTAs that share a row tile's columns (a cluster): two CTAs on every SM if
-// the row tiles are too few for that, at least 256 columns each.
+// CTAs that share a row tile's columns (a cluster): enough for one on every
+// SM, and beyond that 32 stages each (a CTA's start and the cluster's meeting
+// cost a few stages): backward of 8192 tokens, 14336 columns, with 8, 16, 32
+// stages: r = 16 223, 214, 207 us, r = 64 465, 430, 418 us.
+constexpr int kShrinkStages = 32;
 int shrink_split(int64_t T, int64_t C) {
+  const int64_t rows = ceil_div(T, kRows), stages = ceil_div(C, 128);
   int s = 1;
-  while (s < 8 && ceil_div(T, kRows) * s * 2 <= 2 * sm_count() && C >= 512 * s) s *= 2;
+  while (s < 8 && stages >= 2 * s && (rows * s < sm_count() || stages >= kShrinkStages * 2 * s)) s *= 2;
   return s;
 }
 int few_split(int64_t C) { return C >= 1024 ? 8 : (C >= 512 ? 4 : (C >= 256 ? 2 : 1)); }
 
 int outer_cols(int64_t r) { return r <= 32 ? 256 : 128; }
-// Row ranges of the outer products: at most 2048 tokens each (an adapter may
-// own all of them), unless that makes more than 8.
-int outer_splits(int64_t T) { return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, ceil_div(T, 2048)))); }
+// Row ranges of the outer products, for an adapter that owns most tokens: at
+// most 4096 tokens each, unless that makes more than 8.  (Backward of 8192
+// tokens, r = 16, ranges of 1024, 2048, 4096: 209, 214, 186 us.)
+int outer_splits(int64_t T) { return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, ceil_div(T, 4096)))); }
 
 // Parts of the workspace, in 16-byte steps: h where the caller keeps none, or
 // g, the terms of both and the outer products' partial sums.
@@ -1169,12 +1196,16 @@ cudaError_t shrink(const __nv_bfloat16* z, int64_t ldz, const __nv_bfloat16* W, 
       !(TRANS ? map_stack(&mw, W, a.n, C, r, rank_box(RP), S::KC) : map_stack(&mw, W, a.n, r, C, 64, S::R)))
     return cudaErrorInvalidValue;
   const int split = shrink_split(a.T, C);
-  const int per = static_cast<int>(ceil_div(ceil_div(C, split), S::KC) * S::KC);
   e = launch_k(fn, dim3(static_cast<unsigned>(ceil_div(a.T, kRows) * split)), dim3(kThreads), S::BYTES, st,
-               static_cast<unsigned>(split), mz, mw, a, C, static_cast<int>(r), split, per, w_out, w_terms, h, h_terms, n_terms);
+               static_cast<unsigned>(split), mz, mw, W, a, C, static_cast<int>(r), split, w_out, w_terms, h, h_terms, n_terms);
   note_launch();
   return e;
 }
+
+// Column tiles of a CTA, where that leaves enough CTAs: forward of 8192 tokens
+// 4096 -> 14336 with 2, 4, 7, 14: r = 16 163, 136, 124, 120 us, r = 64 275,
+// 222, 191, 175 us.
+constexpr int64_t kExpandTiles = 14;
 
 // W: [n, C, r], TRANS: [n, r, C]
 template <int RP, bool TRANS>
@@ -1189,9 +1220,10 @@ cudaError_t expand(const float* w, const __nv_bfloat16* W, const float* scaling,
   if (!map_rows(&mo, out, a.T, C, ldo, 16) || !map_rows(&mi, in ? in : out, a.T, C, in ? ldi : ldo, kRows) ||
       !(TRANS ? map_stack(&mw, W, a.n, r, C, 64, S::R) : map_stack(&mw, W, a.n, C, r, rank_box(RP), S::KC)))
     return cudaErrorInvalidValue;
-  const int64_t grid = std::min<int64_t>(ceil_div(a.T, kRows) * ceil_div(C, S::KC), S::CTAS * sm_count());
-  e = launch_k(fn, dim3(static_cast<unsigned>(grid)), dim3(kThreads), S::BYTES, st, 1u, mi, mw, mo, w, scaling, a, C,
-               static_cast<int>(r), in ? 1 : 0);
+  const int64_t rows = ceil_div(a.T, kRows), cols = ceil_div(C, S::KC);
+  const int groups = static_cast<int>(ceil_div(cols, std::max<int64_t>(1, std::min<int64_t>(kExpandTiles, rows * cols / (S::CTAS * sm_count())))));
+  e = launch_k(fn, dim3(static_cast<unsigned>(rows * groups)), dim3(kThreads), S::BYTES, st, 1u, mi, mw, mo, W, w, scaling, a, C,
+               static_cast<int>(r), in ? 1 : 0, groups);
   note_launch();
   return e;
 }
