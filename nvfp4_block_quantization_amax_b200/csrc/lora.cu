@@ -443,7 +443,7 @@ struct ExpandCfg {
   static constexpr int YB = kRows * KC * 2;       // two boxes of 64 columns
   static constexpr int WB = R * KC * 2;
   static constexpr int CTAS = RP <= 4 ? 2 : 1;    // per SM
-  static constexpr int WSLOTS = RP <= 2 ? 3 : 2;
+  static constexpr int WSLOTS = RP <= 2 ? 3 : (RP == 4 ? 2 : 4);
   static constexpr int YSLOTS = ((CTAS == 2 ? 110 : 224) * 1024 - WSLOTS * WB) / YB;
   static constexpr int BYTES = 1024 + YSLOTS * YB + WSLOTS * WB + 512;
 };
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
         if (__any_sync(0xFFFFFFFFu, lo_mine || hi_mine)) {
 #pragma unroll
           for (int n = 0; n < 64; n += 16) {   // columns of this half
-            float acc[2][4] = {};
+            float acc[2][4] = {}, low[2][4] = {};   // hi and lo parts apart: two shorter chains
 #pragma unroll
             for (int p = 0; p < RP; ++p) {
               uint32_t bf[4];
@@ -564,11 +564,15 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
                 ldsm4(bf, RankTile<RP>::template at<KC>(wt, 64 * ch + n + (lane & 7) + ((lane >> 4) << 3), 2 * p + ((lane >> 3) & 1)));
               else
                 ldsm4_t(bf, chunk_at<128>(wt + ch * (S::WB / 2), 16 * p + (lane & 7) + ((lane >> 3) & 1) * 8, n / 8 + (lane >> 4)));
-              mma16(acc[0], al[p], bf);
-              mma16(acc[1], al[p], bf + 2);
+              mma16(low[0], al[p], bf);
+              mma16(low[1], al[p], bf + 2);
               mma16(acc[0], ah[p], bf);
               mma16(acc[1], ah[p], bf + 2);
             }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[q][e] = __fadd_rn(acc[q][e], low[q][e]);
             // a token without an adapter keeps the base's bits (a NaN's payload, a zero's sign)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
@@ -875,7 +879,7 @@ struct OuterArgs {
 };
 
 constexpr int kRowsO = 32;                   // rows of a tile
-constexpr int kWindow = 32 * kRowsO;         // rows whose ids a CTA looks at together
+constexpr int kWindow = 64 * kRowsO;         // rows whose ids a CTA looks at together
 
 template <int RP, int TERMS>
 struct OuterCfg {
@@ -886,8 +890,8 @@ struct OuterCfg {
   static constexpr int ZB = COLS / 64 * ZBOX;
   static constexpr int HB = kRowsO * R * 2;
   static constexpr int STAGE = ZB + TERMS * HB;
-  static constexpr int CTAS = RP <= 2 ? 2 : 1;        // per SM
-  static constexpr int STAGES = (CTAS == 2 ? 104 : 200) * 1024 / STAGE;
+  static constexpr int CTAS = RP <= 4 ? 2 : 1;        // per SM
+  static constexpr int STAGES = (CTAS == 2 ? 100 : 200) * 1024 / STAGE;
   static constexpr int BYTES = 1024 + STAGES * STAGE + 256;
 };
 
@@ -945,17 +949,22 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
     for (int k = th; k < n_tiles * kRowsO; k += kThreads) ids[k] = adapter_of(o.a, row_base + k, false);
     __syncthreads();
     if (warp == 0) {
-      bool some = false, all = true;
-      if (lane < n_tiles)
-        for (int k = 0; k < kRowsO / 4; ++k) {
-          // lanes start at different places: fewer bank conflicts
-          const int4 v = *reinterpret_cast<const int4*>(&ids[lane * kRowsO + 4 * ((k + lane) % (kRowsO / 4))]);
-          some |= v.x == id || v.y == id || v.z == id || v.w == id;
-          all &= v.x == id && v.y == id && v.z == id && v.w == id;
-        }
-      const uint32_t m = __ballot_sync(0xFFFFFFFFu, some);
-      if (some) list[__popc(m & ((1u << lane) - 1u))] = lane | (all ? 256 : 0);
-      if (lane == 0) listed = __popc(m);
+      int n = 0;
+      for (int first_tile = 0; first_tile < n_tiles; first_tile += 32) {
+        const int tile = first_tile + lane;
+        bool some = false, all = true;
+        if (tile < n_tiles)
+          for (int k = 0; k < kRowsO / 4; ++k) {
+            // lanes start at different places: fewer bank conflicts
+            const int4 v = *reinterpret_cast<const int4*>(&ids[tile * kRowsO + 4 * ((k + lane) % (kRowsO / 4))]);
+            some |= v.x == id || v.y == id || v.z == id || v.w == id;
+            all &= v.x == id && v.y == id && v.z == id && v.w == id;
+          }
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, some);
+        if (some) list[n + __popc(m & ((1u << lane) - 1u))] = tile | (all ? 256 : 0);
+        n += __popc(m);
+      }
+      if (lane == 0) listed = n;
     }
     __syncthreads();
     const int count = listed;
@@ -993,35 +1002,45 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
           }
           consumers_sync();
         }
+        // kPair groups of 16 ranks at a time: their chains of products overlap
+        constexpr int kPair = RP >= 2 ? 2 : 1;
 #pragma unroll
-        for (int m = 0; m < RP; ++m) {
-          float acc[2 * NQ][4];
+        for (int m0 = 0; m0 < RP; m0 += kPair) {
+          float acc[kPair][2 * NQ][4];
 #pragma unroll
-          for (int q = 0; q < 2 * NQ; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.0f;
+          for (int m = 0; m < kPair; ++m)
+#pragma unroll
+            for (int q = 0; q < 2 * NQ; ++q) acc[m][q][0] = acc[m][q][1] = acc[m][q][2] = acc[m][q][3] = 0.0f;
 #pragma unroll
           for (int kk = 0; kk < kRowsO; kk += 16) {
-            uint32_t af[TERMS][4], bf[NQ][4];
+            uint32_t af[kPair][TERMS][4], bf[NQ][4];
             const int arow = kk + (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-            for (int x = 0; x < TERMS; ++x)
-              ldsm4_t(af[x], Ranks::template at<kRowsO>(wb + x * S::HB, arow, 2 * m + ((lane >> 3) & 1)));
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
               const int chunk = 2 * (NQ * warp + q) + (lane >> 4);   // of eight columns
               ldsm4_t(bf[q], chunk_at<128>(zs + (chunk >> 3) * S::ZBOX, kk + (lane & 7) + ((lane >> 3) & 1) * 8, chunk & 7));
             }
 #pragma unroll
+            for (int m = 0; m < kPair; ++m)
+#pragma unroll
+              for (int x = 0; x < TERMS; ++x)
+                ldsm4_t(af[m][x], Ranks::template at<kRowsO>(wb + x * S::HB, arow, 2 * (m0 + m) + ((lane >> 3) & 1)));
+#pragma unroll
             for (int x = TERMS - 1; x >= 0; --x)
 #pragma unroll
-              for (int q = 0; q < NQ; ++q) {
-                mma16(acc[2 * q], af[x], bf[q]);
-                mma16(acc[2 * q + 1], af[x], bf[q] + 2);
-              }
+              for (int m = 0; m < kPair; ++m)
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                  mma16(acc[m][2 * q], af[m][x], bf[q]);
+                  mma16(acc[m][2 * q + 1], af[m][x], bf[q] + 2);
+                }
           }
 #pragma unroll
-          for (int q = 0; q < 2 * NQ; ++q)
+          for (int m = 0; m < kPair; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[m][q][e] = __fadd_rn(sum[m][q][e], acc[q][e]);
+            for (int q = 0; q < 2 * NQ; ++q)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sum[m0 + m][q][e] = __fadd_rn(sum[m0 + m][q][e], acc[m][q][e]);
         }
         if (mixed) fence_proxy_async_smem();   // the zeros were plain stores, the next copy is not
         release(&ring.empty[ring.slot]);
