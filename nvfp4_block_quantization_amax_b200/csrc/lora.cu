@@ -909,6 +909,7 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
   using S = OuterCfg<RP, TERMS>;
   using Ranks = RankTile<RP>;
   [[maybe_unused]] constexpr int R = S::R, COLS = S::COLS, NQ = S::NQ;
+  constexpr int kRankBox = kRowsO * Ranks::ROW;   // one term's rows in a box
   extern __shared__ uint8_t dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::STAGES * S::STAGE);
@@ -979,11 +980,9 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
           mbar_expect_tx(bar, S::STAGE);
 #pragma unroll
           for (int b = 0; b < COLS / 64; ++b) tma_load_2d(zd + b * S::ZBOX, map_z, c0 + 64 * b, row, bar);
+          // all terms in one copy (a tensor copy costs some 100 ns, however small)
 #pragma unroll
-          for (int x = 0; x < TERMS; ++x)
-#pragma unroll
-            for (int b = 0; b < Ranks::BOXES; ++b)
-              tma_load_3d(wd + x * S::HB + b * (S::HB / Ranks::BOXES), map_w, 64 * b, row, x, bar);
+          for (int b = 0; b < Ranks::BOXES; ++b) tma_load_3d(wd + b * TERMS * kRankBox, map_w, 64 * b, row, 0, bar);
         }
       }
       __syncwarp();
@@ -1024,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
             for (int m = 0; m < kPair; ++m)
 #pragma unroll
               for (int x = 0; x < TERMS; ++x)
-                ldsm4_t(af[m][x], Ranks::template at<kRowsO>(wb + x * S::HB, arow, 2 * (m0 + m) + ((lane >> 3) & 1)));
+                ldsm4_t(af[m][x], Ranks::template at<TERMS * kRowsO>(wb, x * kRowsO + arow, 2 * (m0 + m) + ((lane >> 3) & 1)));
 #pragma unroll
             for (int x = TERMS - 1; x >= 0; --x)
 #pragma unroll
@@ -1127,14 +1126,17 @@ bool map_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, in
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // n contiguous bf16 matrices [rows, cols]: boxes of box_cols (16, or 32 or 64
-// swizzled over their 64 or 128 bytes) x box_rows of one matrix.  What a
-// box has outside its matrix reads as zeros.
-bool map_stack(CUtensorMap* map, const void* base, int64_t n, int64_t rows, int64_t cols, int box_cols, int box_rows) {
+// swizzled over their 64 or 128 bytes) x box_rows of box_n matrices.  What a
+// box has outside a matrix reads as zeros.
+bool map_stack(CUtensorMap* map, const void* base, int64_t n, int64_t rows, int64_t cols, int box_cols, int box_rows,
+               int box_n = 1) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(n)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(rows * cols) * 2};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1}, estr[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows),
+                             static_cast<cuuint32_t>(box_n)};
+  const cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapSwizzle swizzle =
       box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : (box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE);
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
@@ -1275,7 +1277,7 @@ cudaError_t outer(const LoraArgs& l, const AdapterIds& a, uint8_t* ws, const Lor
       mz[1] = mz[0];
       mw[1] = mw[0];
     } else if (!map_rows(&mz[i], z[i], a.T, C[i], ld[i], kRowsO) ||
-               !map_stack(&mw[i], terms[i], TERMS, a.T, R, rank_box(RP), kRowsO)) {
+               !map_stack(&mw[i], terms[i], TERMS, a.T, R, rank_box(RP), kRowsO, TERMS)) {
       return cudaErrorInvalidValue;
     }
   }
