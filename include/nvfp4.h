@@ -415,7 +415,8 @@ NVFP4_API size_t nvfp4_grouped_workspace_size(int64_t E);
  *     NVFP4_HEADROOM; scales are always written in the GEMM layout
  *     (NVFP4_GEMM_SCALE_LAYOUT is accepted and changes nothing).
  *   out: codes and scales as above; alpha_row, alpha_col: E floats; amax_out:
- *     optional, 2 E floats (rows' maxima, then columns'), may be the
+ *     optional, 2 E floats (rows' maxima, then columns'; those of an
+ *     orientation that is not asked for are unspecified), may be the
  *     workspace; status: optional.
  * C % 64 == 0, with NVFP4_COLWISE C % 128 == 0; ld % 8 == 0; x, codes, scales
  * and the workspace 16-byte aligned; stream_id + E <= 2^31; a NaN or Inf in
@@ -471,8 +472,8 @@ NVFP4_API nvfp4_status_t nvfp4_gemm_grouped_wgrad(const uint8_t* A, const uint8_
  * r % 8 == 0, 8 <= r <= 128; K % 8 == 0, N % 8 == 0, at most 2^22; n <= 65535.
  * Rows x, y, out, dy, dx: bf16, 16-byte aligned, row strides (ld, elements) a
  * multiple of 8; A, B, h, dA, dB and the workspace 16-byte aligned.
- * Sums are held in fp32, in an order that depends on the sizes alone: the
- * same call gives the same bits.
+ * Sums are held in fp32 and added in a fixed order: the same call on the same
+ * device gives the same bits.
  * ------------------------------------------------------------------------ */
 
 /* Bytes of device workspace of nvfp4_lora_apply (backward = 0) or

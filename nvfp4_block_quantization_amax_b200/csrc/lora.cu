@@ -253,11 +253,20 @@ __device__ __forceinline__ void write_terms(__nv_bfloat16* terms, int n_terms, i
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-// The float at this shared-memory address in CTA `rank` of the cluster.
-__device__ __forceinline__ float load_cluster(const float* p, int rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to_rank(smem_u32(p), static_cast<uint32_t>(rank))) : "memory");
-  return v;
+// Sum over the cluster's `split` <= 8 CTAs, in rank order, of the float at this
+// shared-memory address in each (the loads go out together).
+__device__ __forceinline__ float sum_cluster(const float* p, int split) {
+  float v[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    v[q] = 0.0f;
+    if (q < split)
+      asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                   : "=f"(v[q]) : "r"(map_to_rank(smem_u32(p), static_cast<uint32_t>(q))) : "memory");
+  }
+#pragma unroll
+  for (int q = 1; q < 8; ++q) v[0] = __fadd_rn(v[0], v[q]);
+  return v[0];
 }
 
 // ---------------------------------------------------------------------------
@@ -415,10 +424,7 @@ __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
     const int row = first + k / R, j = k % R;
     const int64_t t = row0 + row;
     if (t >= a.T) continue;
-    float v = 0.0f;
-    if (split == 1) v = sums[row * R + j];
-    else
-      for (int q = 0; q < split; ++q) v = __fadd_rn(v, load_cluster(sums + row * R + j, q));
+    const float v = split == 1 ? sums[row * R + j] : sum_cluster(sums + row * R + j, split);
     if (w_out && j < r) w_out[t * r + j] = v;
     if (w_terms) write_terms(w_terms, n_terms, a.T, R, t, j, v);
     if (h_terms) write_terms(h_terms, n_terms, a.T, R, t, j, j < r ? __ldg(h + t * r + j) : 0.0f);
@@ -752,9 +758,7 @@ __global__ void __launch_bounds__(128) lora_shrink_few_kernel(const __nv_bfloat1
   for (int k = begin + th; k < end; k += 128) {
     const int row = k / R, j = k % R, t = un.member[row];
     if (t < 0 || j >= r) continue;
-    float v = 0.0f;
-    for (int q = 0; q < split; ++q) v = __fadd_rn(v, load_cluster(&total[row][j], q));
-    h[static_cast<int64_t>(t) * r + j] = v;
+    h[static_cast<int64_t>(t) * r + j] = sum_cluster(&total[row][j], split);
   }
   cluster_barrier();   // no CTA leaves while another may still read its sums
 }

@@ -198,6 +198,74 @@ def test_an_infinite_h_gives_infinities_where_the_formula_does(api):
     assert h[0, 0] == float("inf") and bool((out == float("inf")).all())
 
 
+def test_many_tokens_in_place_strided_and_with_a_bad_token(api):
+    """The forward pass of more tokens than are gathered: out is y, rows are
+    slices of wider ones, and a NaN token stays alone."""
+    T, K, N, r, n = 333, 264, 200, 24, 4
+    p = problem(T, K, N, r, n, "random", seed=21)
+    want, h = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"], y=p["y"])
+    f, e = reference(p, h)
+    within(want, f["out"], e["out"], "out")
+    wide_x = torch.full((T, K + 24), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide_y = torch.full((T, N + 40), 3.0, dtype=torch.bfloat16, device="cuda")
+    x, y = wide_x[:, 8:8 + K], wide_y[:, 16:16 + N]
+    x.copy_(p["x"])
+    y.copy_(p["y"])
+    got, h2 = api.nvfp4_lora_apply(x, p["A"], p["B"], p["scaling"], p["ids"], y=y, out=y)
+    assert torch.equal(got, want) and torch.equal(h2, h)
+    assert bool((wide_y[:, :16] == 3).all()) and bool((wide_y[:, 16 + N:] == 3).all())
+    alone, _ = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"])
+    zero, _ = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"], y=torch.zeros_like(p["y"]))
+    assert torch.equal(alone, zero)
+    p["x"][100] = float("nan")
+    bad, _ = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"], y=p["y"])
+    keep = torch.arange(T, device="cuda") != 100
+    assert torch.equal(bad[keep], want[keep])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T", [130, 300])
+def test_a_bad_adapter_reaches_no_other_token(api, bad, T):
+    p = problem(T, 72, 72, 16, 3, "random", seed=22)
+    args = lambda q: (q["x"], q["A"], q["B"], q["scaling"], q["ids"])   # noqa: E731
+    want, h = api.nvfp4_lora_apply(*args(p), y=p["y"])
+    dx, dA, dB = api.nvfp4_lora_backward(p["dy"], p["x"], h, *args(p)[1:], dx=p["dx"])
+    q = dict(p, A=p["A"].clone(), B=p["B"].clone())
+    q["A"][1] = bad
+    q["B"][1] = bad
+    others = p["ids"] != 1
+    got, h2 = api.nvfp4_lora_apply(*args(q), y=p["y"])
+    gx, gA, gB = api.nvfp4_lora_backward(p["dy"], p["x"], h2, *args(q)[1:], dx=p["dx"])
+    assert torch.equal(got[others], want[others]) and torch.equal(gx[others], dx[others])
+    assert torch.equal(gA[[0, 2]], dA[[0, 2]]) and torch.equal(gB[[0, 2]], dB[[0, 2]])
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_parts_of_the_results_through_the_c_abi(api, T):
+    """h may stay in the workspace; dx, dA and dB are each optional."""
+    L = api.L
+    K, N, r, n = 136, 200, 24, 3
+    p = problem(T, K, N, r, n, "random", seed=23)
+    out, h = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"], y=p["y"])
+    dx, dA, dB = api.nvfp4_lora_backward(p["dy"], p["x"], h, p["A"], p["B"], p["scaling"], p["ids"], dx=p["dx"], out_dtype=FP32)
+    d = {k: v.data_ptr() for k, v in p.items()}
+    stream = torch.cuda.current_stream().cuda_stream
+    ws = torch.empty(L.nvfp4_lora_workspace_size(T, K, N, r, n, 1), dtype=torch.uint8, device="cuda")
+    got = torch.empty_like(out)
+    assert L.nvfp4_lora_apply(d["x"], K, d["A"], d["B"], d["scaling"], d["ids"], T, K, N, r, n, d["y"], N, got.data_ptr(), N,
+                              None, ws.data_ptr(), L.nvfp4_lora_workspace_size(T, K, N, r, n, 0), None, stream) == 0
+    assert torch.equal(got, out)
+    for want in ("x", "A", "B", "xA", "AB", "xB"):
+        gx, gA, gB = torch.empty_like(dx), torch.empty_like(dA), torch.empty_like(dB)
+        ws.fill_(0xFF)
+        assert L.nvfp4_lora_backward(d["dy"], N, d["x"], K, h.data_ptr(), d["A"], d["B"], d["scaling"], d["ids"], T, K, N, r, n,
+                                     d["dx"], K, gx.data_ptr() if "x" in want else None, K,
+                                     gA.data_ptr() if "A" in want else None, gB.data_ptr() if "B" in want else None, FP32,
+                                     ws.data_ptr(), ws.numel(), None, stream) == 0
+        for k, a, b in (("x", gx, dx), ("A", gA, dA), ("B", gB, dB)):
+            assert k not in want or torch.equal(a, b), (want, k)
+
+
 def test_bad_ids_set_the_status(api):
     p = problem(80, 128, 128, 16, 3, "one", seed=9)
     for bad in (3, -2, 1 << 30):
