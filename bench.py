@@ -313,13 +313,14 @@ def gemm_traffic_record():
     if not os.path.exists(p):
         return None
     d = json.load(open(p))
-    src = os.path.join(ROOT, "nvfp4_block_quantization_amax_b200", "csrc", "gemm.cu")
-    h = hashlib.sha256(open(src, "rb").read()).hexdigest()[:16]
+    csrc = os.path.join(ROOT, "nvfp4_block_quantization_amax_b200", "csrc")
+    h = hashlib.sha256(b"".join(open(os.path.join(csrc, f), "rb").read() for f in GEMM_SOURCES)).hexdigest()[:16]
     g = d.get("gemm", {})
     return g.get("dram_bytes_per_launch") if g.get("source_sha256_16") == h else None
 
 
-QUANT_SOURCES = ("quantize.cu", "nvfp4_device.cuh", "tile.cuh", "launch.cuh")
+GEMM_SOURCES = ("gemm.cu", "gemm_ptx.cuh")
+QUANT_SOURCES = ("quantize.cu", "block_modes.cuh", "nvfp4_device.cuh", "tile.cuh", "launch.cuh")
 
 
 def quantizer_issue_record():
