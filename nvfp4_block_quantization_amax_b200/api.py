@@ -377,6 +377,8 @@ def _stream_of(device):
 
 def _guard(device):
     """Context in which `device` is current."""
+    if device.type != "cuda":
+        raise TypeError(f"the tensors must be CUDA tensors, not on {device}")
     if _current_device is not None and _current_device() == device.index:
         return _HERE
     return torch.cuda.device(device)

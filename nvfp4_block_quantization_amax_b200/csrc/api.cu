@@ -444,6 +444,7 @@ nvfp4_status_t nvfp4_lora_backward(const void* dy, int64_t lddy, const void* x, 
   if (!aligned(h, 16) || !aligned(dA, 16) || !aligned(dB, 16)) return NVFP4_ERR_ALIGN;
   if (T && (!workspace || workspace_bytes < nvfp4::lora_workspace_bytes(T, K, N, r, n, true) || !aligned(workspace, 16)))
     return NVFP4_ERR_WORKSPACE;
+  if (T && dx && (dA || dB) && (dx == x || dx == dy)) return NVFP4_ERR_ARG;   // written before dA and dB read them
   nvfp4::LoraArgs l{};
   l.dy = static_cast<const __nv_bfloat16*>(dy);
   l.lddy = lddy;

@@ -474,3 +474,94 @@ def test_two_streams_at_once(api):
                 got.append(pass_(t))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ---------------------------------------------------------------------------
+# buffers as they come, and sizes past 32 bits
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("counts", [[37, 0, 1, 64, 65], [300, 0, 129, 200]])
+def test_bytes_of_no_group_do_not_matter(api, counts):
+    """Outputs full of 0xFF (codes of -6, scales and alphas of NaN) before the
+    call: the products and the decoded rows are those of zeroed outputs."""
+    T, C, N, E = sum(counts), 256, 384, len(counts)
+    x, g = rows_of(T, C, 41).cuda(), rows_of(T, N, 42).cuda()
+    off, B = offsets_of(counts), weights(api, E, N, C, 43)
+    got = []
+    for fill in (0xFF, 0):
+        qs = []
+        for t in (x, g):
+            q = api.grouped_alloc_outputs(T, t.shape[1], E, ROW | COL, t.device)
+            for b in (q.codes_row, q.scales_row, q.codes_col, q.scales_col, q.alpha_row, q.alpha_col, q.amax):
+                b.view(torch.uint8).fill_(fill)
+            qs.append(api.nvfp4_quantize_grouped(t, off, 1, ROW | COL, out=q))
+        qx, qg = qs
+        got.append((api.nvfp4_gemm_grouped(qx.codes_row, qx.scales_row, qx.alpha_row, *B, off),
+                    api.nvfp4_gemm_grouped_wgrad(qg.codes_col, qg.scales_col, qg.alpha_col, qx.codes_col, qx.scales_col,
+                                                 qx.alpha_col, off, T),
+                    api.nvfp4_dequantize_grouped(qx.codes_row, qx.scales_row, qx.alpha_row, off, T, C, ROW),
+                    api.nvfp4_dequantize_grouped(qx.codes_col, qx.scales_col, qx.alpha_col, off, T, C, COL)))
+    for a, b in zip(*got):
+        assert bool(torch.isfinite(a).all()) and torch.equal(a, b)
+
+
+def test_offsets_past_32_bits_quantize(api):
+    """More than 2^31 elements: the last group is that of a call of its own."""
+    T, C, last = 139000, 16384, 1000
+    x = torch.empty((T, C), dtype=torch.bfloat16, device="cuda")
+    x[:] = rows_of(1000, C, 51).cuda().repeat(139, 1)
+    off = torch.tensor([0, 70001, T - last, T], dtype=torch.int32, device="cuda")
+    tail = torch.tensor([0, last], dtype=torch.int32, device="cuda")
+    q = api.nvfp4_quantize_grouped(x, off, 1, ROW | COL, stream_id=0)
+    own = api.nvfp4_quantize_grouped(x[T - last:].clone(), tail, 1, ROW | COL, stream_id=2)
+    assert float(q.alpha_row[2]) == float(own.alpha_row[0]) and float(q.alpha_col[2]) == float(own.alpha_col[0])
+    assert torch.equal(q.codes_row[T - last:], own.codes_row)
+    at = -(-70001 // 64) * 32 + -(-(T - last - 70001) // 64) * 32
+    assert torch.equal(q.codes_col[:, at:at + own.codes_col.shape[1]], own.codes_col)
+    for side, bit in (("row", ROW), ("col", COL)):
+        y = api.nvfp4_dequantize_grouped(*(getattr(q, f"{k}_{side}") for k in ("codes", "scales", "alpha")), off, T, C,
+                                         bit | BF)
+        z = api.nvfp4_dequantize_grouped(*(getattr(own, f"{k}_{side}") for k in ("codes", "scales", "alpha")), tail, last, C,
+                                         bit | BF)
+        assert torch.equal(y[T - last:], z)
+        del y
+
+
+def test_offsets_past_32_bits_products(api):
+    """Results and weights of more than 2^31 elements or bytes: the last group
+    against its own product, which has one group and the same tiles."""
+    T, N, K, last = 139000, 16384, 64, 1000
+    x = rows_of(1000, K, 52).cuda().repeat(139, 1)
+    off = torch.tensor([0, T - last, T], dtype=torch.int32, device="cuda")
+    tail = torch.tensor([0, last], dtype=torch.int32, device="cuda")
+    q = api.nvfp4_quantize_grouped(x, off, 0, ROW)
+    own = api.nvfp4_quantize_grouped(x[T - last:], tail, 0, ROW)
+    B, sB, aB = weights(api, 2, N, K, 53)
+    D = api.nvfp4_gemm_grouped(q.codes_row, q.scales_row, q.alpha_row, B, sB, aB, off, out_dtype=FP32)
+    want = api.nvfp4_gemm_grouped(own.codes_row, own.scales_row, own.alpha_row, B[1:].contiguous(), sB[N * K // 16:],
+                                  aB[1:], tail, out_dtype=FP32)
+    assert torch.equal(D[T - last:], want)
+    del D, x
+    # a column of D per expert row: E M N elements, few tokens
+    E, M = 33, 8192
+    counts = [3] * E
+    g = rows_of(sum(counts), M, 54).cuda()
+    qc = api.nvfp4_quantize_grouped(g, offsets_of(counts), 0, COL)
+    one = api.nvfp4_quantize_grouped(g[-3:].clone(), offsets_of([3]), 0, COL)
+    W = api.nvfp4_gemm_grouped_wgrad(*(t for _ in range(2) for t in (qc.codes_col, qc.scales_col, qc.alpha_col)),
+                                     offsets_of(counts), sum(counts))
+    assert torch.equal(W[-1], api.nvfp4_gemm_grouped_wgrad(
+        *(t for _ in range(2) for t in (one.codes_col, one.scales_col, one.alpha_col)), offsets_of([3]), 3)[0])
+    del W
+    # weights of more than 2^31 bytes of codes, few tokens each
+    E, N, K = 40, 8192, 16384
+    w = synthetic.weight(N, K, seed=55).cuda()
+    qw = api.nvfp4_quantize(w, 0, ROW | GEMM)
+    B = qw.codes_row[None].repeat(E, 1, 1)
+    sB, aB = qw.scales_row.repeat(E), qw.alpha_row.repeat(E)
+    xs = rows_of(2 * E, K, 56).cuda()
+    q = api.nvfp4_quantize_grouped(xs, offsets_of([2] * E), 0, ROW)
+    own = api.nvfp4_quantize_grouped(xs[-2:].clone(), offsets_of([2]), 0, ROW)
+    D = api.nvfp4_gemm_grouped(q.codes_row, q.scales_row, q.alpha_row, B, sB, aB, offsets_of([2] * E))
+    want = api.nvfp4_gemm_grouped(own.codes_row, own.scales_row, own.alpha_row, B[:1], qw.scales_row, qw.alpha_row,
+                                  offsets_of([2]))
+    assert torch.equal(D[-2:], want)

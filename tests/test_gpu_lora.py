@@ -378,3 +378,44 @@ def test_captured_and_on_two_streams(api):
                 res.append(step(q))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for u, v in zip(res, want) for a, b in zip(u, v))
+
+
+def test_offsets_past_32_bits(api):
+    """Rows past 2^31 elements: only the last tokens have an adapter, and their
+    results are those of a call on them alone (bounds of both calls)."""
+    T, K, N, r, n, last = 150016, 128, 14400, 16, 2, 320
+    p = problem(last, K, N, r, n, "random", seed=61)
+    first = T - last
+    long = dict(p)
+    for k, v in (("x", p["x"]), ("y", p["y"]), ("dy", p["dy"]), ("dx", p["dx"])):
+        long[k] = torch.zeros((T, v.shape[1]), dtype=torch.bfloat16, device="cuda")
+        long[k][first:] = v
+    long["ids"] = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    long["ids"][first:] = p["ids"]
+    out, h = api.nvfp4_lora_apply(long["x"], p["A"], p["B"], p["scaling"], long["ids"], y=long["y"], out=long["y"])
+    f, e = reference(p, h[first:])
+    within(h[first:], f["h"], e["h"], "h")
+    within(out[first:], f["out"], e["out"], "out")
+    assert not bool(h[:first].any()) and not bool(out[:first].any())
+    dx, dA, dB = api.nvfp4_lora_backward(long["dy"], long["x"], h, p["A"], p["B"], p["scaling"], long["ids"], dx=long["dx"],
+                                         out_dtype=FP32)
+    within(dx[first:], f["dx"], e["dx"], "dx")
+    assert not bool(dx[:first].any())
+    for got, k in ((dA, "dA"), (dB, "dB")):
+        within(got, f[k], e[k] + 2.0 ** -24 * (f[k].abs() + e[k]), k)
+
+
+def test_on_a_side_stream(api):
+    """Calls on a side stream, inputs made on the default one, results read
+    after a wait; the workspace of each call is its own."""
+    p = problem(300, 256, 512, 24, 3, "random", seed=62)
+    want = check(api, p)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out, h = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"], y=p["y"])
+        got = (out, h) + tuple(api.nvfp4_lora_backward(p["dy"], p["x"], h, p["A"], p["B"], p["scaling"], p["ids"], dx=p["dx"],
+                                                       out_dtype=FP32))
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

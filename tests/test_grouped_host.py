@@ -124,3 +124,18 @@ def test_binding_refuses_wrong_tensors():
     q.scales_col = q.scales_col[:-1]
     with pytest.raises(ValueError, match="scales_col"):
         api.grouped_check_outputs(q, 5, 128, 2, ROW | COL, torch.device("cpu"))
+
+
+def test_binding_refuses_host_tensors():
+    """Tensors that pass every other check but are not on a GPU."""
+    off = torch.tensor([0, 3, 5], dtype=torch.int32)
+    u8 = dict(dtype=torch.uint8)
+    A, B, f = torch.zeros((5, 64), **u8), torch.zeros((2, 128, 64), **u8), torch.zeros(2)
+    sA, sB = torch.zeros(256 * 8, **u8), torch.zeros(2 * 128 * 8, **u8)
+    with pytest.raises(TypeError, match="CUDA"):
+        api.nvfp4_gemm_grouped(A, sA, f, B, sB, f, off)
+    with pytest.raises(TypeError, match="CUDA"):
+        api.nvfp4_dequantize_grouped(A, sA, f, off, 5, 128, ROW)
+    W, sW = torch.zeros((128, 64), **u8), torch.zeros(128 * 8, **u8)   # 5 rows of 2 groups: 128 padded rows
+    with pytest.raises(TypeError, match="CUDA"):
+        api.nvfp4_gemm_grouped_wgrad(W, sW, f, W, sW, f, off, 5)

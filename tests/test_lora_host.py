@@ -75,3 +75,12 @@ def test_binding_refuses_wrong_tensors():
         api._rows(torch.zeros((64, 5), **bf).t(), 5, 64, "x", dev)
     with pytest.raises(ValueError, match="row-major"):
         api._rows(torch.zeros((4, 64), **bf), 5, 64, "x", dev)
+
+
+@pytest.mark.parametrize("name", ["x", "dy"])
+def test_backward_refuses_dx_over_an_input_of_the_weight_gradients(name):
+    a = dict(dy=FAKE, x=2 * FAKE)
+    call = lambda dA, dB: L.nvfp4_lora_backward(   # noqa: E731
+        a["dy"], 128, a["x"], 128, FAKE, FAKE, FAKE, FAKE, FAKE, 64, 128, 128, 16, 2, None, 128, a[name], 128, dA, dB, 1,
+        FAKE, 1 << 30, None, None)
+    assert call(FAKE, None) == -1 and call(None, FAKE) == -1 and call(FAKE, FAKE) == -1
