@@ -65,12 +65,21 @@ __device__ __forceinline__ void load_group_tile(uint4 (*buf)[TC / 8], const uint
   const int64_t c0 = static_cast<int64_t>(tc) * TC + 8 * cc;
   const int left = rows - tr * TR;
   const uint16_t* src = x + (static_cast<int64_t>(tr) * TR + row0) * ld + c0;
-  const bool col_ok = c0 < C;
+  if (left >= TR && static_cast<int64_t>(tc + 1) * TC <= C) {
+    const int64_t step = kRowStep * ld;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int row = row0 + kRowStep * i;
-    const bool ok = col_ok && row < left;
-    cp_async16_or_zero(&buf[row][tile_chunk(row, cc)], ok ? src + static_cast<int64_t>(kRowStep * i) * ld : x, ok);
+    for (int i = 0; i < kPasses; ++i) {
+      const int row = row0 + kRowStep * i;
+      cp_async16(&buf[row][tile_chunk(row, cc)], src + i * step);
+    }
+  } else {
+    const bool col_ok = c0 < C;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int row = row0 + kRowStep * i;
+      const bool ok = col_ok && row < left;
+      cp_async16_or_zero(&buf[row][tile_chunk(row, cc)], ok ? src + static_cast<int64_t>(kRowStep * i) * ld : x, ok);
+    }
   }
   cp_async_commit();
 }
@@ -90,7 +99,7 @@ struct TileRun {
 // its columns: four 32-byte pieces of a column's codes and, two columns on,
 // two 64-byte pieces of a row's complete 128-byte lines within a few tiles of
 // one CTA.  (Row by row, columns first, each column piece was a partial line
-// of its own: decoding 16301 x 14336 column codes took 202 us.)
+// of its own, and decoding 16301 x 14336 column codes took a third longer.)
 constexpr int kBand = 4;
 struct GroupTile {
   int e, tr;
@@ -118,6 +127,14 @@ __device__ __forceinline__ void next_tile(const GroupTable& g, GroupTile& t, uin
   }
 }
 
+// The two halves of pdl_entry().  The kernels that walk many tiles let the next
+// kernel launch at their last tile: CTAs of the next kernel that were resident
+// (waiting) from the start kept the SM in this kernel's split of L1 and shared
+// memory, and ran in it to their end (decoding the columns right behind the
+// encoding of 16301 x 14336 took 240 us instead of 150).
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // All threads of the cluster; what they wrote to shared memory before is
 // visible to the others after.
 __device__ __forceinline__ void cluster_barrier() {
@@ -132,7 +149,9 @@ __device__ __forceinline__ uint32_t load_cluster_u32(const uint32_t* p, int rank
 }
 
 // ---------------------------------------------------------------------------
-// amax per group
+// amax per group.  Plain: memory bounds it (16384 x 4096 25 us, 5.4 TB/s).
+// Rotated: instruction issue (a butterfly per orientation; 16301 x 14336, both,
+// 143 us, 3.3 TB/s).
 // ---------------------------------------------------------------------------
 // Fold the CTA's running maximum (float bits) into a group's word.
 template <int NT>
@@ -147,7 +166,7 @@ __device__ __forceinline__ void flush_max(uint32_t m, uint32_t* dst, uint32_t* r
 constexpr int kPlainNT = 256;
 
 __global__ void __launch_bounds__(kPlainNT) grouped_amax_plain_kernel(const GroupedArgs a) {
-  pdl_entry();
+  pdl_wait();
   extern __shared__ int table_mem[];
   __shared__ uint32_t red[kPlainNT / 32];
   const GroupTable g = build_group_table<kPlainNT>(a.offsets, a.E, a.T, TR, 128, table_mem, a.status, blockIdx.x == 0);
@@ -162,6 +181,7 @@ __global__ void __launch_bounds__(kPlainNT) grouped_amax_plain_kernel(const Grou
     hm = 0;
   };
   for (; run.tile < run.end; ++run.tile, next_tile(g, t, a.tiles_c)) {
+    if (run.tile + 1 == run.end) pdl_release();
     if (t.e != e) {   // uniform over the CTA
       flush();
       e = t.e;
@@ -190,19 +210,20 @@ __global__ void __launch_bounds__(kPlainNT) grouped_amax_plain_kernel(const Grou
 
 // Rotated maxima, rows and / or columns.  The transform's final 1/4 commutes
 // with the maximum and is applied at the end.
+constexpr int kRotNT = 128;
 template <bool ROW, bool COL>
-__global__ void __launch_bounds__(TNT) grouped_amax_rot_kernel(const GroupedArgs a) {
-  pdl_entry();
+__global__ void __launch_bounds__(kRotNT) grouped_amax_rot_kernel(const GroupedArgs a) {
+  pdl_wait();
   extern __shared__ int table_mem[];
   __shared__ __align__(16) uint4 tiles[2][TR][TC / 8];
-  __shared__ uint32_t red[TNT / 32];
-  const GroupTable g = build_group_table<TNT>(a.offsets, a.E, a.T, TR, 128, table_mem, a.status, blockIdx.x == 0);
+  __shared__ uint32_t red[kRotNT / 32];
+  const GroupTable g = build_group_table<kRotNT>(a.offsets, a.E, a.T, TR, 128, table_mem, a.status, blockIdx.x == 0);
   TileRun run(static_cast<uint32_t>(g.pa[a.E]) * a.tiles_c, blockIdx.x, gridDim.x);
   if (run.tile >= run.end) return;
   const SignMasks sm = sign_masks(sign_bits(philox_keys(a.seed)));
   GroupTile t = group_tile(g, run.tile, a.tiles_c), ahead = t;
   auto load = [&](int b) {
-    load_group_tile<TNT>(tiles[b], a.x + static_cast<int64_t>(g.off[ahead.e]) * a.ld, g.rows(ahead.e), a.C, a.ld,
+    load_group_tile<kRotNT>(tiles[b], a.x + static_cast<int64_t>(g.off[ahead.e]) * a.ld, g.rows(ahead.e), a.C, a.ld,
                          ahead.tr, ahead.tc);
     next_tile(g, ahead, a.tiles_c);
   };
@@ -213,14 +234,16 @@ __global__ void __launch_bounds__(TNT) grouped_amax_rot_kernel(const GroupedArgs
   auto flush = [&]() {
     const bool inf = max(hm & 0xFFFFu, hm >> 16) >= 0x7F80u;
     if constexpr (ROW)
-      flush_max<TNT>(inf ? kNonFinite : __float_as_uint(__fmul_rn(mr, 0.25f)), a.amax_r + e, red, a.status);
+      flush_max<kRotNT>(inf ? kNonFinite : __float_as_uint(__fmul_rn(mr, 0.25f)), a.amax_r + e, red, a.status);
     if constexpr (COL)
-      flush_max<TNT>(inf ? kNonFinite : __float_as_uint(__fmul_rn(mc, 0.25f)), a.amax_c + e, red, a.status);
+      flush_max<kRotNT>(inf ? kNonFinite : __float_as_uint(__fmul_rn(mc, 0.25f)), a.amax_c + e, red, a.status);
     mr = mc = 0.0f;
     hm = 0;
   };
   const int th = threadIdx.x;
+  constexpr int kReps = 256 / kRotNT;   // row pairs and column units per thread and tile
   for (; run.tile < run.end; ++run.tile, next_tile(g, t, a.tiles_c), buf ^= 1) {
+    if (run.tile + 1 == run.end) pdl_release();
     if (t.e != e) {
       flush();
       e = t.e;
@@ -230,8 +253,12 @@ __global__ void __launch_bounds__(TNT) grouped_amax_rot_kernel(const GroupedArgs
     cp_async_wait<1>();
     __syncthreads();
     const uint4 (*s)[TC / 8] = tiles[buf];
+    const int left = g.rows(t.e) - t.tr * TR;   // blocks of padding rows alone have nothing to add
     if constexpr (ROW) {
-      const int row = th >> 3, cb = th & 7;
+#pragma unroll
+      for (int k = 0; k < kReps; ++k) {
+      const int row = (th >> 3) + (kRotNT / 8) * k, cb = th & 7;
+      if (row >= left) continue;
       const uint4 a0 = s[row][tile_chunk(row, 2 * cb)], a1 = s[row][tile_chunk(row, 2 * cb + 1)];
       const uint4 b0 = s[row + 32][tile_chunk(row + 32, 2 * cb)], b1 = s[row + 32][tile_chunk(row + 32, 2 * cb + 1)];
       const uint32_t w[16] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w,
@@ -244,9 +271,13 @@ __global__ void __launch_bounds__(TNT) grouped_amax_rot_kernel(const GroupedArgs
       float ma, mb;
       max_abs16x2(v, ma, mb);
       mr = max3(mr, ma, mb);
+      }
     }
     if constexpr (COL) {
-      const int cp = th >> 2, rb = th & 3;
+#pragma unroll
+      for (int k = 0; k < kReps; ++k) {
+      const int cp = th & 63, rb = (th >> 6) + (kRotNT / 64) * k;
+      if (16 * rb >= left) continue;
       const uint32_t* base = reinterpret_cast<const uint32_t*>(&s[16 * rb][0]);
       const int wofs = tile_word(16 * rb, cp);
       float2 v[16];
@@ -260,6 +291,7 @@ __global__ void __launch_bounds__(TNT) grouped_amax_rot_kernel(const GroupedArgs
       float ma, mb;
       max_abs16x2(v, ma, mb);
       mc = max3(mc, ma, mb);
+      }
     }
     __syncthreads();   // the buffer is refilled two iterations on
   }
@@ -268,12 +300,14 @@ __global__ void __launch_bounds__(TNT) grouped_amax_rot_kernel(const GroupedArgs
 }
 
 // ---------------------------------------------------------------------------
-// encode
+// encode.  Instruction issue bounds it (16384 x 4096 rows and columns, 4/6: 26
+// thread instructions per value, 67% of the issue slots): 144 us with 4/6,
+// 55 us to nearest; 16301 x 14336 to nearest, rotated: 240 us.
 // ---------------------------------------------------------------------------
 struct GroupStaging {
   uint8_t colcodes[TC][48];        // transposed codes of one tile (32 bytes used per column)
   uint8_t colscale[TC][TR / 16];
-  uint4 words[TNT / 32][32];       // scale-SR words shared by a warp (MS-EDEN)
+  uint4 words[TNT / 32][32];       // scale-SR words shared by a warp (MS-EDEN, 256 threads)
   float2 tab_r[kScaleTab];
   float2 tab_c[kScaleTab];
 };
@@ -283,17 +317,31 @@ __device__ __forceinline__ float group_alpha(const GroupedArgs& a, const uint32_
   return __fdiv_rn(m == kNonFinite ? 0.0f : __uint_as_float(m), (a.flags & kHeadroom) ? 1792.0f : 2688.0f);
 }
 
+// Threads of a CTA (128: two row pairs and two column pairs of a tile each) and
+// CTAs per SM.  Times of amax and encoding, 16301 x 14336 in 64 groups, rows
+// and columns: to nearest, rotated, 256 threads x 3 482 us, 128 x 5 446,
+// 128 x 4 410; MS-EDEN, whose draws want 256, x 3 630, x 2 612; software
+// stochastic rounding 256 x 2 971, 128 x 4 1298 (registers).  16384 x 4096 in
+// 8 groups, 4/6 rows alone: 256 x 2 120, 128 x 4 109; one orientation alone of
+// the 256-thread modes keeps three (2048 x 4096 in 64 groups, MS-EDEN columns:
+// x 2 53 us, x 3 43).
+template <int MODE>
+constexpr int encode_threads() { return (MODE == kModeMsEden || MODE == kModeRhtSR) ? 256 : 128; }
+template <int MODE, bool ROW, bool COL>
+constexpr int encode_ctas() { return encode_threads<MODE>() == 128 ? 4 : ROW && COL ? 2 : 3; }
+
 template <int MODE, bool ROT, bool ROW, bool COL>
-__global__ void __launch_bounds__(TNT, 3) grouped_quantize_kernel(const GroupedArgs a) {
-  pdl_entry();
+__global__ void __launch_bounds__(encode_threads<MODE>(), encode_ctas<MODE, ROW, COL>()) grouped_quantize_kernel(const GroupedArgs a) {
+  constexpr int NT = encode_threads<MODE>(), kReps = 256 / NT;   // row pairs and column units per thread and tile
+  pdl_wait();
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ __align__(16) GroupStaging stg;
   auto tiles = reinterpret_cast<uint4(*)[TR][TC / 8]>(dyn);
   int* table_mem = reinterpret_cast<int*>(dyn + 2 * TR * TC * 2);
-  const GroupTable g = build_group_table<TNT>(a.offsets, a.E, a.T, TR, 128, table_mem, a.status, blockIdx.x == 0);
+  const GroupTable g = build_group_table<NT>(a.offsets, a.E, a.T, TR, 128, table_mem, a.status, blockIdx.x == 0);
   const int th = threadIdx.x;
   if (blockIdx.x == 0) {
-    for (int e = th; e < a.E; e += TNT) {
+    for (int e = th; e < a.E; e += NT) {
       if constexpr (ROW) a.alpha_row[e] = group_alpha(a, a.amax_r, e);
       if constexpr (COL) a.alpha_col[e] = group_alpha(a, a.amax_c, e);
       if (a.amax_out) {
@@ -319,7 +367,7 @@ __global__ void __launch_bounds__(TNT, 3) grouped_quantize_kernel(const GroupedA
 
   GroupTile t = group_tile(g, run.tile, a.tiles_c), ahead = t;
   auto load = [&](int b) {
-    load_group_tile<TNT>(tiles[b], a.x + static_cast<int64_t>(g.off[ahead.e]) * a.ld, g.rows(ahead.e), a.C, a.ld,
+    load_group_tile<NT>(tiles[b], a.x + static_cast<int64_t>(g.off[ahead.e]) * a.ld, g.rows(ahead.e), a.C, a.ld,
                          ahead.tr, ahead.tc);
     next_tile(g, ahead, a.tiles_c);
   };
@@ -327,18 +375,19 @@ __global__ void __launch_bounds__(TNT, 3) grouped_quantize_kernel(const GroupedA
   int e = -1, buf = 0;
   TabScales scr{}, scc{};
   for (; run.tile < run.end; ++run.tile, next_tile(g, t, a.tiles_c), buf ^= 1) {
+    if (run.tile + 1 == run.end) pdl_release();
     if (run.tile + 1 < run.end) load(buf ^ 1);
     else cp_async_commit();
     if (t.e != e) {   // the scale tables of this group; the barrier below publishes them
       e = t.e;
       if constexpr (ROW) {
         const float al = group_alpha(a, a.amax_r, e);
-        build_scale_tab<TNT>(stg.tab_r, al);
+        build_scale_tab<NT>(stg.tab_r, al);
         scr = make_scale_ctx(stg.tab_r, al);
       }
       if constexpr (COL) {
         const float al = group_alpha(a, a.amax_c, e);
-        build_scale_tab<TNT>(stg.tab_c, al);
+        build_scale_tab<NT>(stg.tab_c, al);
         scc = make_scale_ctx(stg.tab_c, al);
       }
     }
@@ -375,7 +424,9 @@ __global__ void __launch_bounds__(TNT, 3) grouped_quantize_kernel(const GroupedA
     }
 
     if constexpr (ROW) {
-      const int row = trow, cb = tcb;
+#pragma unroll
+      for (int k = 0; k < kReps; ++k) {
+      const int row = trow + (NT / 8) * k, cb = tcb;
       const bool va = row < rows && 16 * cb < cols, vb = row + 32 < rows && 16 * cb < cols;
       if (va || vb) {
         const uint4 a0 = s[row][tile_chunk(row, 2 * cb)], a1 = s[row][tile_chunk(row, 2 * cb + 1)];
@@ -386,7 +437,8 @@ __global__ void __launch_bounds__(TNT, 3) grouped_quantize_kernel(const GroupedA
         if constexpr (ROT) rht16x2_presigned(v);
         Packed16 pa, pb;
         uint32_t sa, sb;
-        quantize_pair<MODE>(v, scr, K, c2r, static_cast<uint64_t>(rblk), static_cast<uint64_t>(rblk + 32 * nbr), pa, pb,
+        const int64_t blk = rblk + (NT / 8) * k * nbr;
+        quantize_pair<MODE>(v, scr, K, c2r, static_cast<uint64_t>(blk), static_cast<uint64_t>(blk + 32 * nbr), pa, pb,
                             sa, sb, MODE == kModeMsEden, w_ra, w_rb);
         uint8_t* crow = a.codes_row + (static_cast<int64_t>(g.off[e]) + t.tr * TR + row) * (a.C / 2) + c0 / 2 + 8 * cb;
         if (va) *reinterpret_cast<uint2*>(crow) = make_uint2(pa.lo, pa.hi);
@@ -396,11 +448,15 @@ __global__ void __launch_bounds__(TNT, 3) grouped_quantize_kernel(const GroupedA
         if (va) srow[0] = static_cast<uint8_t>(sa);
         if (vb) srow[4] = static_cast<uint8_t>(sb);
       }
+      }
     }
     if constexpr (COL) {
-      {
+#pragma unroll
+      for (int k = 0; k < kReps; ++k) {
+        const int cp = tcp + (NT / 4) * k;
+        const int64_t blk = cblk + 2 * (NT / 4) * k * nbc;
         const uint32_t* base = reinterpret_cast<const uint32_t*>(&s[16 * trb][0]);
-        const int wofs = tile_word(16 * trb, tcp);
+        const int wofs = tile_word(16 * trb, cp);
         float2 v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -410,20 +466,23 @@ __global__ void __launch_bounds__(TNT, 3) grouped_quantize_kernel(const GroupedA
         if constexpr (ROT) rht16x2_presigned(v);
         Packed16 qa, qb;
         uint32_t sa, sb;
-        quantize_pair<MODE>(v, scc, K, c2c, static_cast<uint64_t>(cblk), static_cast<uint64_t>(cblk + nbc), qa, qb, sa,
+        quantize_pair<MODE>(v, scc, K, c2c, static_cast<uint64_t>(blk), static_cast<uint64_t>(blk + nbc), qa, qb, sa,
                             sb, MODE == kModeMsEden, w_ca, w_cb);
-        *reinterpret_cast<uint2*>(&stg.colcodes[2 * tcp][8 * trb]) = make_uint2(qa.lo, qa.hi);
-        *reinterpret_cast<uint2*>(&stg.colcodes[2 * tcp + 1][8 * trb]) = make_uint2(qb.lo, qb.hi);
-        stg.colscale[2 * tcp][trb] = static_cast<uint8_t>(sa);
-        stg.colscale[2 * tcp + 1][trb] = static_cast<uint8_t>(sb);
+        *reinterpret_cast<uint2*>(&stg.colcodes[2 * cp][8 * trb]) = make_uint2(qa.lo, qa.hi);
+        *reinterpret_cast<uint2*>(&stg.colcodes[2 * cp + 1][8 * trb]) = make_uint2(qb.lo, qb.hi);
+        stg.colscale[2 * cp][trb] = static_cast<uint8_t>(sa);
+        stg.colscale[2 * cp + 1][trb] = static_cast<uint8_t>(sb);
       }
       __syncthreads();
       // 16 code bytes of column th / 2 and column th's four scales: whole
       // tiles of the padded frame (C % 128 == 0 with columns)
       const int64_t kt = g.pa[e] + t.tr;   // 64-row tile of the padded frame
-      const int c = th >> 1, h = th & 1;
-      *reinterpret_cast<uint4*>(a.codes_col + (c0 + c) * (a.kcap / 2) + 32 * kt + 16 * h) =
-          *reinterpret_cast<const uint4*>(&stg.colcodes[c][16 * h]);
+#pragma unroll
+      for (int k = 0; k < kReps; ++k) {
+        const int c = (th >> 1) + (NT / 2) * k, h = th & 1;
+        *reinterpret_cast<uint4*>(a.codes_col + (c0 + c) * (a.kcap / 2) + 32 * kt + 16 * h) =
+            *reinterpret_cast<const uint4*>(&stg.colcodes[c][16 * h]);
+      }
       if (th < TC)
         *reinterpret_cast<uint32_t*>(a.scales_col + gemm_scale_tile_col(kt, t.tc, a.kcap / 16) +
                                      gemm_scale_thread_col(th)) = *reinterpret_cast<const uint32_t*>(&stg.colscale[th][0]);
@@ -561,7 +620,8 @@ __global__ void __launch_bounds__(kFewNT) grouped_quantize_few_kernel(const Grou
 
 // ---------------------------------------------------------------------------
 // decode.  Memory bounds it (0.5625 bytes in, 2 or 4 out per element); what
-// counts is that every warp store is whole and contiguous.
+// counts is that every warp store is whole and contiguous.  To bf16, 16301 x
+// 14336: rows 115 us (5.2 TB/s), columns 124 us (4.8); 16384 x 4096 37 and 39.
 // ---------------------------------------------------------------------------
 template <bool BF16>
 __device__ __forceinline__ void store8(void* y, int64_t at, const float* v) {   // eight values of a row
@@ -580,9 +640,30 @@ __device__ __forceinline__ void store8(void* y, int64_t at, const float* v) {   
   }
 }
 
+__device__ __forceinline__ void scale8(float* v, float s) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float2 p = mul2(make_float2(v[j], v[j + 1]), make_float2(s, s));
+    v[j] = p.x;
+    v[j + 1] = p.y;
+  }
+}
+
+// The inverse rotation of two lane-paired blocks, as irht16 does it for one:
+// its final (1/4 and the sign) is one exact product.  q: +-1/4 per element.
+__device__ __forceinline__ void inverse_factors(uint32_t signs, float* q) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) q[i] = __uint_as_float(0x3E800000u ^ (((signs >> i) & 1u) << 31));
+}
+__device__ __forceinline__ void irht16x2(float2* v, const float* q) {
+  hadamard16x2(v);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = mul2(v[i], make_float2(q[i], q[i]));
+}
+
 // Row operands: 64 x 256 tiles, a warp takes one row at a time, lane l the
-// elements 8 l .. 8 l + 7 (a 16-byte bf16 store).  With INV a lane takes two
-// rows' worth of one 16-element block instead, since the rotation mixes it.
+// elements 8 l .. 8 l + 7 (a 16-byte bf16 store).  With INV a lane takes
+// one 16-element block of two rows instead, since the rotation mixes it.
 template <bool INV, bool BF16>
 __global__ void __launch_bounds__(256) grouped_dequantize_rows_kernel(const uint8_t* __restrict__ codes,
                                                                       const uint8_t* __restrict__ scales,
@@ -590,18 +671,19 @@ __global__ void __launch_bounds__(256) grouped_dequantize_rows_kernel(const uint
                                                                       int64_t C, const int32_t* __restrict__ offsets,
                                                                       int E, uint64_t seed, void* __restrict__ y,
                                                                       int32_t* status) {
-  pdl_entry();
+  pdl_wait();
   extern __shared__ int table_mem[];
   const GroupTable g = build_group_table<256>(offsets, E, T, TR, 128, table_mem, status, blockIdx.x == 0);
   const uint32_t tiles_c = static_cast<uint32_t>((C + 255) / 256);
   TileRun run(static_cast<uint32_t>(g.pa[E]) * tiles_c, blockIdx.x, gridDim.x);
   if (run.tile >= run.end) return;
-  uint32_t signs = 0;
-  if constexpr (INV) signs = sign_bits(philox_keys(seed));
+  [[maybe_unused]] float q[16];
+  if constexpr (INV) inverse_factors(sign_bits(philox_keys(seed)), q);
   GroupTile t = group_tile(g, run.tile, tiles_c);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t katoms = C / 64;
   for (; run.tile < run.end; ++run.tile, next_tile(g, t, tiles_c)) {
+    if (run.tile + 1 == run.end) pdl_release();
     const int left = g.rows(t.e) - t.tr * TR;
     const int rows = left < TR ? left : TR;
     const float al = __ldg(alpha + t.e);
@@ -628,25 +710,37 @@ __global__ void __launch_bounds__(256) grouped_dequantize_rows_kernel(const uint
         const float s = __fmul_rn(al, e4m3_value((sw[i] >> (8 * ((lane >> 1) & 3))) & 0xFFu));
         float v[8];
         e2m1x8_values(w[i], v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], s);
+        scale8(v, s);
         if (col_ok && r < rows) store8<BF16>(y, (row0 + r) * C + c, v);
       }
     } else {
       const int64_t c = static_cast<int64_t>(t.tc) * 256 + 16 * (lane & 15);
       if (c < C) {
-#pragma unroll 2
-        for (int r = 2 * warp + (lane >> 4); r < rows; r += 16) {
-          const uint2 p = __ldg(reinterpret_cast<const uint2*>(codes + (row0 + r) * (C / 2) + c / 2));
-          const float s = __fmul_rn(al, e4m3_value(__ldg(sbase + (c >> 6) * 512 + (r & 31) * 16 + (r >> 5) * 4 + ((c >> 4) & 3))));
-          float v[16];
-          e2m1x8_values(p.x, v);
-          e2m1x8_values(p.y, v + 8);
+        for (int r0 = 2 * warp + (lane >> 4); r0 < rows; r0 += 32) {   // rows r0 and r0 + 16
+          float v[2][16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], s);
-          irht16(v, signs);
-          store8<BF16>(y, (row0 + r) * C + c, v);
-          store8<BF16>(y, (row0 + r) * C + c + 8, v + 8);
+          for (int k = 0; k < 2; ++k) {
+            const int r = min(r0 + 16 * k, rows - 1);
+            const uint2 p = __ldg(reinterpret_cast<const uint2*>(codes + (row0 + r) * (C / 2) + c / 2));
+            const float s = __fmul_rn(al, e4m3_value(__ldg(sbase + (c >> 6) * 512 + (r & 31) * 16 + (r >> 5) * 4 + ((c >> 4) & 3))));
+            e2m1x8_values(p.x, v[k]);
+            e2m1x8_values(p.y, v[k] + 8);
+            // scalar: a packed product could be merged into the first addition
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[k][j] = __fmul_rn(v[k][j], s);
+          }
+          float2 u[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) u[j] = make_float2(v[0][j], v[1][j]);
+          irht16x2(u, q);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if (r0 + 16 * k >= rows) continue;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[k][j] = k ? u[j].y : u[j].x;
+            store8<BF16>(y, (row0 + r0 + 16 * k) * C + c, v[k]);
+            store8<BF16>(y, (row0 + r0 + 16 * k) * C + c + 8, v[k] + 8);
+          }
         }
       }
     }
@@ -654,9 +748,14 @@ __global__ void __launch_bounds__(256) grouped_dequantize_rows_kernel(const uint
 }
 
 // Column operands: 64 x 128 tiles of the rows' frame.  A thread decodes one
-// 16-row block of two neighbouring columns and leaves them in shared memory
-// pairwise (a warp's stores cover 32 neighbouring pairs of one row), from
-// where rows are written whole.
+// 16-row block of two neighbouring columns, four lanes the 32 bytes (one
+// sector) that a tile holds of a column, and leaves the values in shared
+// memory pairwise, from where rows are written whole.  (With a block per warp
+// instead, four warps shared each sector through L1, and 16301 x 14336
+// columns took 150 us, or 240 where a quantizer's shared memory had left
+// little of L1.)
+// Pair p of the rows of block b is stored at p ^ (kSwap b): the pairs of the
+// four blocks that a store writes at once are in different banks.
 template <bool INV, bool BF16>
 __global__ void __launch_bounds__(256) grouped_dequantize_cols_kernel(const uint8_t* __restrict__ codes,
                                                                       const uint8_t* __restrict__ scales,
@@ -665,19 +764,19 @@ __global__ void __launch_bounds__(256) grouped_dequantize_cols_kernel(const uint
                                                                       int E, int64_t kcap, uint64_t seed,
                                                                       void* __restrict__ y, int32_t* status) {
   using Pair = typename std::conditional<BF16, uint32_t, float2>::type;
-  constexpr int kPitch = TC / 2 + (BF16 ? 4 : 2);   // pairs: rows stay 16-byte aligned, and shift by a few banks
-  pdl_entry();
+  constexpr int kSwap = BF16 ? 8 : 4;
+  pdl_wait();
   extern __shared__ int table_mem[];
-  __shared__ __align__(16) Pair vals[TR][kPitch];
+  __shared__ __align__(16) Pair vals[TR][TC / 2];
   const GroupTable g = build_group_table<256>(offsets, E, T, TR, 128, table_mem, status, blockIdx.x == 0);
   const uint32_t tiles_c = static_cast<uint32_t>(C / TC);
   TileRun run(static_cast<uint32_t>(g.pa[E]) * tiles_c, blockIdx.x, gridDim.x);
   if (run.tile >= run.end) return;
-  uint32_t signs = 0;
-  if constexpr (INV) signs = sign_bits(philox_keys(seed));
+  [[maybe_unused]] float q[16];
+  if constexpr (INV) inverse_factors(sign_bits(philox_keys(seed)), q);
   GroupTile t = group_tile(g, run.tile, tiles_c);
-  const int th = threadIdx.x, warp = th >> 5, lane = th & 31;
-  const int pair = 32 * (warp >> 2) + lane, b = warp & 3;   // column pair and 16-row block
+  const int th = threadIdx.x;
+  const int pair = th >> 2, b = th & 3;   // column pair and 16-row block
   // the next tile's codes and scales are on their way while this one is
   // written (8 bytes per column and thread leave little in flight otherwise)
   struct Column {
@@ -696,6 +795,7 @@ __global__ void __launch_bounds__(256) grouped_dequantize_cols_kernel(const uint
   fetch(t);
   GroupTile ahead = t;
   for (; run.tile < run.end; ++run.tile, t = ahead) {
+    if (run.tile + 1 == run.end) pdl_release();
     const int left = g.rows(t.e) - t.tr * TR;
     const int rows = left < TR ? left : TR;
     const int64_t c0 = static_cast<int64_t>(t.tc) * TC;
@@ -709,22 +809,20 @@ __global__ void __launch_bounds__(256) grouped_dequantize_cols_kernel(const uint
     e2m1x8_values(pa.y, va + 8);
     e2m1x8_values(pb.x, vb);
     e2m1x8_values(pb.y, vb + 8);
+    float2 u[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      va[j] = __fmul_rn(va[j], sa);
-      vb[j] = __fmul_rn(vb[j], sb);
+      // with INV scalar: a packed product could be merged into the first addition
+      u[j] = INV ? make_float2(__fmul_rn(va[j], sa), __fmul_rn(vb[j], sb)) : mul2(make_float2(va[j], vb[j]), make_float2(sa, sb));
     }
-    if constexpr (INV) {
-      irht16(va, signs);
-      irht16(vb, signs);
-    }
+    if constexpr (INV) irht16x2(u, q);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       if constexpr (BF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(va[j], vb[j]);
-        vals[16 * b + j][pair] = *reinterpret_cast<const uint32_t*>(&h);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(u[j].x, u[j].y);
+        vals[16 * b + j][pair ^ (kSwap * b)] = *reinterpret_cast<const uint32_t*>(&h);
       } else {
-        vals[16 * b + j][pair] = make_float2(va[j], vb[j]);
+        vals[16 * b + j][pair ^ (kSwap * b)] = u[j];
       }
     }
     __syncthreads();
@@ -738,7 +836,7 @@ __global__ void __launch_bounds__(256) grouped_dequantize_cols_kernel(const uint
         const int64_t at = (row0 + r) * C + c0 + kEach * piece;
         uint4* dst = BF16 ? reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + at)
                           : reinterpret_cast<uint4*>(static_cast<float*>(y) + at);
-        *dst = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(&vals[r][0]) + 16 * piece);
+        *dst = *reinterpret_cast<const uint4*>(&vals[r][(kEach / 2 * piece) ^ (kSwap * (r >> 4))]);
       }
     }
     __syncthreads();
@@ -748,11 +846,20 @@ __global__ void __launch_bounds__(256) grouped_dequantize_cols_kernel(const uint
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// Persistent grid: enough CTAs for every tile that T rows in E groups can
-// make, at most `per_sm` on each SM.
-int grid_for(int64_t T, int64_t E, int64_t tiles_c, int per_sm) {
-  const int64_t most = grouped_capacity(T, E, TR) / TR * tiles_c;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, static_cast<int64_t>(sm_count()) * per_sm)));
+// CTAs for the tiles that T rows in E groups can make: `per_sm` on each SM
+// where there are as many tiles, and up to `most` times as many while each
+// keeps a run of six (whole multiples: 3.6 times as many took 182 us where
+// 4 times took 172).  Shorter runs keep the CTAs of a moment closer together
+// in memory; below six the group table of each CTA costs more.  16301 x
+// 14336 in 64 groups, per_sm alone / this / runs of two: column decode 148 /
+// 124 / 142 us, row decode 123 / 115 / 130; rotated amax and encoding (both
+// orientations, to nearest) 411 us with per_sm CTAs, 391 with 4 times as many
+// for the encoding, 403 with 8 times.  16384 x 4096 in 8 groups: column decode
+// 38.6 us, with runs of one or two 50.
+int grid_for(int64_t T, int64_t E, int64_t tiles_c, int per_sm, int most) {
+  const int64_t tiles = grouped_capacity(T, E, TR) / TR * tiles_c, one = static_cast<int64_t>(sm_count()) * per_sm;
+  const int64_t times = std::max<int64_t>(1, std::min<int64_t>(most, tiles / (6 * one)));
+  return static_cast<int>(std::max<int64_t>(1, std::min(tiles, times * one)));
 }
 
 // Once per kernel and device: raise the dynamic shared memory limit.
@@ -773,7 +880,7 @@ cudaError_t launch_encode(const GroupedArgs& a, cudaStream_t st) {
   constexpr int ring = 2 * TR * TC * 2;
   cudaError_t e = allow_smem(fn, ring + static_cast<int>(group_table_bytes(kMaxGroups)), done);
   if (e != cudaSuccess) return e;
-  e = launch_k(fn, dim3(grid_for(a.T, a.E, a.tiles_c, 3)), dim3(TNT), ring + group_table_bytes(a.E), st, 1u, a);
+  e = launch_k(fn, dim3(grid_for(a.T, a.E, a.tiles_c, encode_ctas<MODE, ROW, COL>(), 4)), dim3(encode_threads<MODE>()), ring + group_table_bytes(a.E), st, 1u, a);
   note_launch();
   return e;
 }
@@ -787,12 +894,12 @@ cudaError_t dispatch_encode(const GroupedArgs& a, bool row, bool col, cudaStream
 cudaError_t launch_group_amax(const GroupedArgs& a, bool row, bool col, bool rot, cudaStream_t st) {
   const size_t tab = group_table_bytes(a.E);
   cudaError_t e;
-  if (!rot) e = launch_k(grouped_amax_plain_kernel, dim3(grid_for(a.T, a.E, a.tiles_c, 8)), dim3(kPlainNT), tab, st, 1u, a);
+  if (!rot) e = launch_k(grouped_amax_plain_kernel, dim3(grid_for(a.T, a.E, a.tiles_c, 6, 1)), dim3(kPlainNT), tab, st, 1u, a);
   else {
-    const dim3 grid(grid_for(a.T, a.E, a.tiles_c, 4));
-    if (row && col) e = launch_k(grouped_amax_rot_kernel<true, true>, grid, dim3(TNT), tab, st, 1u, a);
-    else if (row) e = launch_k(grouped_amax_rot_kernel<true, false>, grid, dim3(TNT), tab, st, 1u, a);
-    else e = launch_k(grouped_amax_rot_kernel<false, true>, grid, dim3(TNT), tab, st, 1u, a);
+    const dim3 grid(grid_for(a.T, a.E, a.tiles_c, 6, 1));
+    if (row && col) e = launch_k(grouped_amax_rot_kernel<true, true>, grid, dim3(kRotNT), tab, st, 1u, a);
+    else if (row) e = launch_k(grouped_amax_rot_kernel<true, false>, grid, dim3(kRotNT), tab, st, 1u, a);
+    else e = launch_k(grouped_amax_rot_kernel<false, true>, grid, dim3(kRotNT), tab, st, 1u, a);
   }
   note_launch();
   return e;
@@ -816,10 +923,10 @@ cudaError_t launch_decode(const uint8_t* codes, const uint8_t* scales, const flo
     static bool done[64] = {false};
     auto fn = grouped_dequantize_cols_kernel<INV, BF16>;
     if ((e = allow_smem(fn, static_cast<int>(group_table_bytes(kMaxGroups)), done)) != cudaSuccess) return e;
-    e = launch_k(fn, dim3(grid_for(T, E, C / TC, 8)), dim3(256), tab, st, 1u, codes, scales, alpha, T, C, offsets, E,
+    e = launch_k(fn, dim3(grid_for(T, E, C / TC, 8, 3)), dim3(256), tab, st, 1u, codes, scales, alpha, T, C, offsets, E,
                  grouped_capacity(T, E, 64), seed, y, status);
   } else {
-    e = launch_k(grouped_dequantize_rows_kernel<INV, BF16>, dim3(grid_for(T, E, (C + 255) / 256, 8)), dim3(256), tab, st, 1u,
+    e = launch_k(grouped_dequantize_rows_kernel<INV, BF16>, dim3(grid_for(T, E, (C + 255) / 256, 8, 3)), dim3(256), tab, st, 1u,
                  codes, scales, alpha, T, C, offsets, E, seed, y, status);
   }
   note_launch();
