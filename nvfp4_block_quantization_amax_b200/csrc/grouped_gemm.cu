@@ -15,6 +15,10 @@
 //     stored.  A's scales sit in 128-row atoms, each group starting a new one.
 //   * contraction grouped: a group's tokens are padded with zero codes to 64
 //     (one MMA's K), and only its own K blocks are multiplied.
+// What bounds it is the operands' way from L2 into the SMs (each 256 x 256
+// tile loads 2 x 256 rows of its K): at about 12.7 TB/s, 16384 tokens of 8
+// groups x 14336 x 4096 take 374 us alone (5.1 PFLOP/s, bf16 results) and the
+// fp32 weight gradient of the same sizes 615 us, 1.9 GB of results among them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -406,6 +410,9 @@ __global__ void __launch_bounds__(G_THREADS, 1)
 // start while the epilogue drains this one.
 // D^T comes out of the MMA: lane n of the accumulator is a weight row, column
 // j a token; a warp stores 64 (bf16) or 128 (fp32) contiguous bytes per token.
+// 16 tokens, 6 of 8 groups, 14336 x 4096: 38 us, the weights at 5.2 TB/s; 5003
+// tokens of 64 groups, 1408 x 2112: 39 us, five rounds of tiles of 128 weight
+// rows over 148 SMs, the last one half empty.
 // ===========================================================================
 constexpr int F_STAGE_W = 128 * BK_BYTES, F_STAGE_X = 128 * BK_BYTES;   // weight rows, token rows
 constexpr int F_STAGE = F_STAGE_W + F_STAGE_X + 2 * G_SF;

@@ -276,6 +276,8 @@ __device__ __forceinline__ float sum_cluster(const float* p, int split) {
 // of 128 (16 KB of z, 4 to 32 KB of weights).  Warp w multiplies rows
 // 16 (w % 4) over half w / 4 of a stage.  Sums of the cluster are added in
 // rank order.  In the backward pass the terms of w and of h are written here.
+// Memory bounds it: 8192 x 4096, r = 16 21 us (3.2 TB/s), 8192 x 14336 63 us
+// (3.7 TB/s): 256 CTAs on 148 SMs leave 40 SMs with half the work of the rest.
 // ---------------------------------------------------------------------------
 template <int RP, bool TRANS>
 struct ShrinkCfg {
@@ -441,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
 // base tiles (TMA in, changed in place, TMA out), another the weights of the
 // rows' adapters, one slot each; w stays in registers, its scale folded in.
 // Warp w: rows 16 (w % 4), columns 64 (w / 4) of a tile.
+// Memory bounds it: 8192 x 14336, r = 16 92 us (5.1 TB/s read and written).
 // ---------------------------------------------------------------------------
 template <int RP>
 struct ExpandCfg {
@@ -693,7 +696,9 @@ __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p, bool ok) {
 
 // grid: split (a cluster), unit.  Warp w takes the 32-column blocks w, w + 4,
 // .. of the split; thread c of a quad holds columns 8c .. 8c + 7 of a block.
-// The cluster's sums are added in rank order.
+// The cluster's sums are added in rank order.  Latency bounds it, as it does
+// the expand of few tokens: 64 tokens of 32 adapters, 4096 -> 14336, r = 16:
+// 10 us each, 20 us in all.
 template <int RP>
 __global__ void __launch_bounds__(128) lora_shrink_few_kernel(const __nv_bfloat16* __restrict__ z, int64_t ldz,
                                                               const __nv_bfloat16* __restrict__ W, const AdapterIds a,
@@ -866,6 +871,8 @@ __global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __res
 // grid: column tiles of both products, adapter, split of the rows.
 // TERMS: bf16 numbers that w enters as: 3 (all of fp32) for fp32 gradients,
 // 2 (2^-17) for bf16 ones, as the shrink kernel wrote them.
+// Memory bounds it: x 8192 x 4096 and dy 8192 x 14336, r = 16, fp32: 82 us
+// (3.7 TB/s; tensor pipe 40% busy with the three terms).
 // ---------------------------------------------------------------------------
 struct OuterProduct {
   int64_t C;
@@ -1079,7 +1086,8 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
 }
 
 // Sum of the splits' partials, in their order, those that saw a token; four
-// elements per thread.
+// elements per thread.  Latency of dependent loads: 9 us for 2 x 4 x 16 x
+// 18432 elements.
 __global__ void __launch_bounds__(256) lora_outer_sum_kernel(const OuterArgs o, int splits, int cols) {
   pdl_entry();
   const int all_tiles = o.p[0].tiles + o.p[1].tiles;
