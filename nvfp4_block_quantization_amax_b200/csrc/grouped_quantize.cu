@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kRotNT) grouped_amax_rot_kernel(const GroupedA
 
 // ---------------------------------------------------------------------------
 // encode.  Instruction issue bounds it (16384 x 4096 rows and columns, 4/6: 26
-// thread instructions per value, 67% of the issue slots): 144 us with 4/6,
+// thread instructions per value, about 70% of the issue slots): 133 us with 4/6,
 // 55 us to nearest; 16301 x 14336 to nearest, rotated: 240 us.
 // ---------------------------------------------------------------------------
 struct GroupStaging {
@@ -333,6 +333,10 @@ constexpr int encode_ctas() { return encode_threads<MODE>() == 128 ? 4 : ROW && 
 template <int MODE, bool ROT, bool ROW, bool COL>
 __global__ void __launch_bounds__(encode_threads<MODE>(), encode_ctas<MODE, ROW, COL>()) grouped_quantize_kernel(const GroupedArgs a) {
   constexpr int NT = encode_threads<MODE>(), kReps = 256 / NT;   // row pairs and column units per thread and tile
+  // Both orientations of the longer modes: the row pairs share their code,
+  // which otherwise outgrows the instruction cache (4/6, 16384 x 4096, amax
+  // and encoding 174 -> 158 us; to nearest, short, 391 -> 397 for 16301 x 14336).
+  constexpr int kUnroll = ROW && COL && MODE != kModeRTN ? 1 : kReps;
   pdl_wait();
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ __align__(16) GroupStaging stg;
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(encode_threads<MODE>(), encode_ctas<MODE, ROW,
     }
 
     if constexpr (ROW) {
-#pragma unroll
+#pragma unroll(kUnroll)
       for (int k = 0; k < kReps; ++k) {
       const int row = trow + (NT / 8) * k, cb = tcb;
       const bool va = row < rows && 16 * cb < cols, vb = row + 32 < rows && 16 * cb < cols;
