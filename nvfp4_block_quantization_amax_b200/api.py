@@ -561,21 +561,23 @@ def _rows(t: torch.Tensor, T: int, cols: int, what: str, device):
         raise TypeError(f"{what}: dtype {t.dtype}, expected {torch.bfloat16}")
     if t.device != device:
         raise ValueError(f"{what}: on {t.device}, expected {device}")
-    if tuple(t.shape) != (T, cols) or (t.numel() and t.stride(1) != 1):
-        raise ValueError(f"{what}: shape {tuple(t.shape)} / strides {t.stride()}, need a row-major [{T}, {cols}] matrix")
-    return t.stride(0) if T > 1 else cols
+    st = t.stride()
+    if t.shape != (T, cols) or (T and st[1] != 1):
+        raise ValueError(f"{what}: shape {tuple(t.shape)} / strides {st}, need a row-major [{T}, {cols}] matrix")
+    return st[0] if T > 1 else cols
 
 
 def _check_lora(A, B, scaling, ids, T, device):
     """(K, N, r, n) of adapters A [n, r, K], B [n, N, r] and the tokens' ids [T]."""
-    if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
+    sa, sb = A.shape, B.shape
+    if len(sa) != 3 or len(sb) != 3 or sa[0] != sb[0] or sa[1] != sb[2]:
         raise ValueError("A must be [n, r, K] and B [n, N, r]")
-    n, r, K = A.shape
-    N = B.shape[1]
+    n, r, K = sa
+    N = sb[1]
     _need(A, n * r * K, torch.bfloat16, "A", device)
     _need(B, n * N * r, torch.bfloat16, "B", device)
     _need(scaling, n, torch.float32, "scaling", device)
-    if ids.dim() != 1 or ids.numel() != T:
+    if ids.shape != (T,):
         raise ValueError(f"ids: shape {tuple(ids.shape)}, need [{T}]")
     _need(ids, T, torch.int32, "ids", device)
     return K, N, r, n
