@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int ti = 0;
     for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++ti) {
       const int tile_m = tile % m_tiles, tile_n = tile / m_tiles;
-      if (!mbar_wait(smem_u32(acc_full), ti & 1, abort_flag)) break;
+      if (!mbar_wait_warp(smem_u32(acc_full), ti & 1, abort_flag)) break;
       fence_after();
       const int row0 = tile_m * BM + 32 * q;
       const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16);
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     for (int tile = pair; tile < num_tiles; tile += num_pairs, ++ti) {
       int tile_m, tile_n;
       pair_tile_coords(tile, m_tiles, N / 256, group_m, tile_m, tile_n);
-      if (!mbar_wait(smem_u32(acc_full), ti & 1, abort_flag)) break;
+      if (!mbar_wait_warp(smem_u32(acc_full), ti & 1, abort_flag)) break;
       fence_after();
       const int row0 = tile_m * 256 + 128 * static_cast<int>(rank) + 32 * q;
       const int col0 = tile_n * 256 + 128 * h;

@@ -76,6 +76,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// mbar_wait by all lanes of a warp, with one answer for all of them.  Near the
+// time limit one lane may give up where another still sees the phase complete;
+// instructions that the whole warp executes together (ldmatrix, tcgen05.ld,
+// __syncwarp) must not follow on such a split.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
+}
+
 // Bounded wait for the first phase of `bar` (used only after an abort, where
 // the abort flag is already up).
 __device__ __forceinline__ void mbar_wait_bounded(uint32_t bar, uint32_t parity) {

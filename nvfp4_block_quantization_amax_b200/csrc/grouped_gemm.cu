@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
       const TileAt t = locate<WGRAD>(g, p, tile, n_tiles);
       const bool zero = t.kblocks == 0;
       if (!zero) {
-        if (!mbar_wait(smem_u32(acc_full), acc_ph, abort_flag)) break;
+        if (!mbar_wait_warp(smem_u32(acc_full), acc_ph, abort_flag)) break;
         acc_ph ^= 1;
         fence_after();
       }
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
       const FewAt t = locate_few(g, p, tile, n_tiles);
       const float ab = __fmul_rn(__ldg(p.alpha_a + t.e), __ldg(p.alpha_b + t.e));
-      if (!mbar_wait(smem_u32(&acc_full[buf]), acc_ph, abort_flag)) break;
+      if (!mbar_wait_warp(smem_u32(&acc_full[buf]), acc_ph, abort_flag)) break;
       fence_after();
       const uint32_t taddr = tmem + buf * F_ACC + (static_cast<uint32_t>(32 * q) << 16);
       const int64_t n = 128 * static_cast<int64_t>(t.tn) + 32 * q + lane;   // this lane's output column

@@ -142,7 +142,9 @@ struct Ring {
       phase ^= 1;
     }
   }
-  __device__ __forceinline__ bool wait_full(volatile int* abort) const { return mbar_wait(smem_u32(&full[slot]), phase, abort); }
+  // by all lanes of a consumer warp
+  __device__ __forceinline__ bool wait_full(volatile int* abort) const { return mbar_wait_warp(smem_u32(&full[slot]), phase, abort); }
+  // by the producer's lane
   __device__ __forceinline__ bool wait_empty(volatile int* abort) const { return mbar_wait(smem_u32(&empty[slot]), phase ^ 1, abort); }
   // After an abort the producer lets the copies it has issued land before its
   // CTA goes: `issued` slots in all.

@@ -1,0 +1,33 @@
+"""The bounded waits of the kernels that stream through shared memory (GEMMs,
+adapters), as far as their sources show it (CPU).
+
+A wait that gives up must leave the CTA in a state from which every role still
+ends.  The time limit is seconds away from what a copy takes, so ordinary runs
+never come there."""
+import os
+import re
+
+import pytest
+
+from nvfp4_block_quantization_amax_b200 import build
+
+FILES = ("gemm.cu", "grouped_gemm.cu", "lora.cu")
+
+
+def source(name):
+    text = open(os.path.join(build.CSRC, name)).read()
+    return re.sub(r"//[^\n]*", "", text)
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_whole_warps_wait_with_one_answer(name):
+    """What a whole warp waits for (an accumulator, a filled slot) is asked for
+    with mbar_wait_warp: lanes that disagreed about the time limit would part
+    in front of warp-wide instructions.  mbar_wait itself is left to single
+    lanes: producers (empty slots) and MMA issuers (full slots, drained
+    accumulators)."""
+    text = source(name)
+    for args in re.findall(r"\bmbar_wait\(([^;]*?), abort(?:_flag)?\)", text):
+        assert re.search(r"empty|&full\[s\]", args), args
+    whole = re.findall(r"\bmbar_wait_warp\(([^;]*?), abort(?:_flag)?\)", text)
+    assert whole and all("acc_full" in a or "&full[slot]" in a for a in whole)
