@@ -153,13 +153,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                       nk * 512, fb);
         }
       }
-      if (*abort_flag) {
-        // A wait gave up somewhere: let the copies already issued land before
-        // the CTA exits (each wait again bounded).
-        for (int i = (it > STAGES ? it - STAGES : 0); i < it; ++i) {
-          const uint32_t bar = smem_u32(&full[i % STAGES]), ph = (i / STAGES) & 1;
-          mbar_wait_bounded(bar, ph);
-        }
+      // the copies issued land before the CTA exits
+      for (int i = (it > STAGES ? it - STAGES : 0); i < it; ++i) {
+        const uint32_t bar = smem_u32(&full[i % STAGES]), ph = (i / STAGES) & 1;
+        mbar_wait_bounded(bar, ph);
       }
     }
   } else if (warp == 1) {
@@ -200,12 +197,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         umma_commit(smem_u32(&empty[s]));
         if (kt == kstages - 1) umma_commit(smem_u32(acc_full));
       }
-      if (*abort_flag) {
-        // a wait gave up: the copies and MMAs already issued may still run;
-        // let them finish (bounded) before TMEM is freed
-        umma_commit(smem_u32(drain));
-        mbar_wait_bounded(smem_u32(drain), 0);
-      }
+      // the copies and MMAs issued finish before TMEM is freed
+      umma_commit(smem_u32(drain));
+      mbar_wait_bounded(smem_u32(drain), 0);
     }
   } else {
     // ---------------- epilogue (warps 2..5) ----------------
@@ -461,9 +455,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           tma_load_2d_pair(dSB + PC::SFA, &tmap_sfb, 0, ysb + 2 * katoms, fb_leader);
         }
       }
-      if (*abort_flag && leader) {
-        // a wait gave up somewhere: let the copies already issued land
-        // before the CTA exits (each wait again bounded)
+      if (leader) {
+        // the copies issued, the peer's among them, land before the pair exits
         for (int i = (it > PC::STAGES ? it - PC::STAGES : 0); i < it; ++i) {
           const uint32_t bar = smem_u32(&full[i % PC::STAGES]), ph = (i / PC::STAGES) & 1;
           mbar_wait_bounded(bar, ph);
@@ -542,13 +535,10 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         }
         if (++kt == kstages) kt = 0;
       }
-      if (*abort_flag) {
-        // a wait gave up: the copies and MMAs already issued (into both
-        // CTAs' TMEM) may still run; let them finish (bounded) before the
-        // pair frees TMEM
-        umma_commit_pair(smem_u32(drain));
-        mbar_wait_bounded(smem_u32(drain), 0);
-      }
+      // the copies and MMAs issued (into both CTAs' TMEM) finish before the
+      // pair frees TMEM
+      umma_commit_pair_own(smem_u32(drain));
+      mbar_wait_bounded(smem_u32(drain), 0);
     }
   } else {
     // ---------------- epilogue (warps 2..9 of both CTAs) ----------------

@@ -84,8 +84,11 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
 }
 
-// Bounded wait for the first phase of `bar` (used only after an abort, where
-// the abort flag is already up).
+// Bounded wait that raises nothing: a role's last wait, for what it has itself
+// issued.  Every role ends with it, whether or not a wait has given up: another
+// role may give up after this one has finished, and the CTA must not leave (or
+// free TMEM) under copies or MMAs in flight.  On ordinary runs the roles behind
+// wait for the same things.
 __device__ __forceinline__ void mbar_wait_bounded(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
   while (!mbar_try_wait(bar, parity) && globaltimer() - t0 < kTimeoutNs) {
@@ -255,6 +258,12 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
       "h"(static_cast<uint16_t>(0x3))
       : "memory");
+}
+
+// Arrive on this CTA's mbarrier alone, once every tcgen05 operation of the pair
+// that this thread has issued has completed.
+__device__ __forceinline__ void umma_commit_pair_own(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Tile order of the CTA-pair kernel: groups of `gm` M-tiles (the whole N

@@ -211,9 +211,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
           }
         }
       }
-      if (*abort_flag && leader) {
-        // a wait gave up somewhere: let the copies already issued land
-        // before the CTA exits (each wait again bounded)
+      if (leader) {
+        // the copies issued, the peer's among them, land before the pair exits
         for (int i = (it > G_STAGES ? it - G_STAGES : 0); i < it; ++i)
           mbar_wait_bounded(smem_u32(&full[i % G_STAGES]), (i / G_STAGES) & 1);
       }
@@ -259,12 +258,9 @@ __global__ void __launch_bounds__(G_THREADS, 1)
           }
         }
       }
-      if (*abort_flag) {
-        // MMAs already issued may still run: let them finish (bounded) before
-        // TMEM is freed
-        umma_commit_pair(smem_u32(drain));
-        mbar_wait_bounded(smem_u32(drain), 0);
-      }
+      // the MMAs issued finish before TMEM is freed
+      umma_commit_pair_own(smem_u32(drain));
+      mbar_wait_bounded(smem_u32(drain), 0);
     }
   } else {
     // ---------------- epilogue (warps 2..9 of both CTAs) ----------------
@@ -523,12 +519,9 @@ __global__ void __launch_bounds__(F_THREADS, 1)
           }
         }
       }
-      if (*abort_flag) {
-        // a wait gave up somewhere: let the copies already issued land before
-        // the CTA exits (each wait again bounded)
-        for (int i = (it > F_STAGES ? it - F_STAGES : 0); i < it; ++i)
-          mbar_wait_bounded(smem_u32(&full[i % F_STAGES]), (i / F_STAGES) & 1);
-      }
+      // the copies issued land before the CTA exits
+      for (int i = (it > F_STAGES ? it - F_STAGES : 0); i < it; ++i)
+        mbar_wait_bounded(smem_u32(&full[i % F_STAGES]), (i / F_STAGES) & 1);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
@@ -570,12 +563,9 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         buf ^= 1;
         if (buf == 0) acc_ph ^= 1;
       }
-      if (*abort_flag) {
-        // MMAs already issued may still run: let them finish (bounded) before
-        // TMEM is freed
-        umma_commit(smem_u32(drain));
-        mbar_wait_bounded(smem_u32(drain), 0);
-      }
+      // the MMAs issued finish before TMEM is freed
+      umma_commit(smem_u32(drain));
+      mbar_wait_bounded(smem_u32(drain), 0);
     }
   } else {
     // ---------------- epilogue (warps 2..5) ----------------

@@ -146,8 +146,8 @@ struct Ring {
   __device__ __forceinline__ bool wait_full(volatile int* abort) const { return mbar_wait_warp(smem_u32(&full[slot]), phase, abort); }
   // by the producer's lane
   __device__ __forceinline__ bool wait_empty(volatile int* abort) const { return mbar_wait(smem_u32(&empty[slot]), phase ^ 1, abort); }
-  // After an abort the producer lets the copies it has issued land before its
-  // CTA goes: `issued` slots in all.
+  // The producer lets the copies it has issued (`issued` slots in all) land
+  // before its CTA goes.
   __device__ __forceinline__ void drain(int issued) const {
     for (int i = issued > slots ? issued - slots : 0; i < issued; ++i)
       mbar_wait_bounded(smem_u32(&full[i % slots]), (i / slots) & 1);
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
           }
         }
       }
-      if (*abort) ring.drain(issued);
+      ring.drain(issued);
     }
     __syncwarp();
   } else {
@@ -490,8 +490,8 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
   tile_adapters(ta, th < kRows ? adapter_of(a, row0 + th, false) : -1);   // ends with a barrier
   const int stride = groups * KC;   // between this CTA's columns
   if (warp == kConsumers) {
+    int y_issued = 0, w_issued = 0;
     if (lane == 0) {
-      int y_issued = 0, w_issued = 0;
       for (int c = group * KC; c < C && !*abort; c += stride) {
         if (!yr.wait_empty(abort)) break;
         const uint32_t yb = smem_u32(&yr.full[yr.slot]), yd = smem_u32(ys + yr.slot * S::YB);
@@ -518,13 +518,13 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
           ++w_issued;
         }
       }
-      if (*abort) {
-        yr.drain(y_issued);
-        wr.drain(w_issued);
-      }
     }
     __syncwarp();
     pdl_entry();
+    if (lane == 0) {
+      yr.drain(y_issued);
+      wr.drain(w_issued);
+    }
   } else {
     const int rg = warp & 3, ch = warp >> 2;
     const int my_row = 16 * rg + (lane >> 2);   // this thread's rows of the tile: my_row and my_row + 8
@@ -1061,7 +1061,7 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
     }
   }
   if (warp == kConsumers) {
-    if (lane == 0 && *abort) ring.drain(issued);
+    if (lane == 0) ring.drain(issued);
     return;
   }
   if (th == 0 && *abort && o.a.status) *o.a.status = kStatusTimeout;

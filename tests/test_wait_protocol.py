@@ -31,3 +31,18 @@ def test_whole_warps_wait_with_one_answer(name):
         assert re.search(r"empty|&full\[s\]", args), args
     whole = re.findall(r"\bmbar_wait_warp\(([^;]*?), abort(?:_flag)?\)", text)
     assert whole and all("acc_full" in a or "&full[slot]" in a for a in whole)
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_roles_wait_for_what_they_have_issued(name):
+    """A role may finish before another one gives up, so a role's last wait,
+    for the copies or products it has itself issued, cannot depend on the
+    abort flag as it stands when the role finishes."""
+    text = source(name)
+    for cond in re.findall(r"if \(([^()]*abort[^()]*)\)", text):
+        assert "status" in cond, cond                        # reporting alone
+    if name == "lora.cu":
+        assert len(re.findall(r"\.drain\(", text)) == 4      # shrink, expand (two rings), outer
+    else:
+        kernels = text.count("full[i %")
+        assert kernels == 2 and len(re.findall(r"mbar_wait_bounded\(smem_u32\(drain\), 0\)", text)) == kernels
