@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 
 #include "gemm_ptx.cuh"
 #include "launch.cuh"
@@ -51,6 +52,7 @@ struct AdapterIds {
   int64_t T;
   int n;
   int32_t* status;
+  uint64_t wait_ns;   // time limit of a ring's wait
 };
 
 // Adapter of token t: -1 for none, for rows past the last token, and for an
@@ -120,7 +122,8 @@ __device__ __forceinline__ int slot_col(int slot) {
 // ---- rings of shared memory, filled by TMA --------------------------------
 // A ring's barriers: full[s] completes when a slot's bytes have landed,
 // empty[s] when every consumer warp has arrived.  All waits are bounded (see
-// mbar_wait): one that gives up raises `abort`, every role leaves its loop,
+// mbar_wait): one that gives up raises `abort`, every role runs to its end
+// without the data (a barrier that others may stand at is met all the same),
 // and the kernel reports NVFP4_ERR_TIMEOUT.
 constexpr int kConsumers = 8;                      // warps
 constexpr int kThreads = 32 * (kConsumers + 1);    // and the producer warp
@@ -128,8 +131,10 @@ constexpr int kThreads = 32 * (kConsumers + 1);    // and the producer warp
 struct Ring {
   uint64_t* full;
   uint64_t* empty;
-  int slots, slot;
-  uint32_t phase;   // of the current pass over the slots
+  int slots;
+  uint64_t limit_ns;   // of a wait
+  int slot = 0;
+  uint32_t phase = 0;   // of the current pass over the slots
   __device__ __forceinline__ void init() const {   // one thread
     for (int i = 0; i < slots; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
@@ -143,9 +148,9 @@ struct Ring {
     }
   }
   // by all lanes of a consumer warp
-  __device__ __forceinline__ bool wait_full(volatile int* abort) const { return mbar_wait_warp(smem_u32(&full[slot]), phase, abort); }
+  __device__ __forceinline__ bool wait_full(volatile int* abort) const { return mbar_wait_warp(smem_u32(&full[slot]), phase, abort, limit_ns); }
   // by the producer's lane
-  __device__ __forceinline__ bool wait_empty(volatile int* abort) const { return mbar_wait(smem_u32(&empty[slot]), phase ^ 1, abort); }
+  __device__ __forceinline__ bool wait_empty(volatile int* abort) const { return mbar_wait(smem_u32(&empty[slot]), phase ^ 1, abort, limit_ns); }
   // The producer lets the copies it has issued (`issued` slots in all) land
   // before its CTA goes.
   __device__ __forceinline__ void drain(int issued) const {
@@ -308,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
   uint8_t* wsm = zs + S::STAGES * S::ZB;
   float* sums = reinterpret_cast<float*>(wsm + S::STAGES * S::WB);   // [64][R]
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sums) + S::SUM);
-  Ring ring{bars, bars + S::STAGES, S::STAGES, 0, 0u};
+  Ring ring{bars, bars + S::STAGES, S::STAGES, a.wait_ns};
   volatile int* abort = reinterpret_cast<volatile int*>(bars + 2 * S::STAGES);
   __shared__ TileAdapters ta;
   const int th = threadIdx.x, lane = th & 31, warp = th >> 5;
@@ -474,8 +479,8 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
   uint8_t* ys = smem;
   uint8_t* wsm = ys + S::YSLOTS * S::YB;
   uint64_t* bars = reinterpret_cast<uint64_t*>(wsm + S::WSLOTS * S::WB);
-  Ring yr{bars, bars + S::YSLOTS, S::YSLOTS, 0, 0u};
-  Ring wr{bars + 2 * S::YSLOTS, bars + 2 * S::YSLOTS + S::WSLOTS, S::WSLOTS, 0, 0u};
+  Ring yr{bars, bars + S::YSLOTS, S::YSLOTS, a.wait_ns};
+  Ring wr{bars + 2 * S::YSLOTS, bars + 2 * S::YSLOTS + S::WSLOTS, S::WSLOTS, a.wait_ns};
   volatile int* abort = reinterpret_cast<volatile int*>(bars + 2 * (S::YSLOTS + S::WSLOTS));
   __shared__ TileAdapters ta;
   const int th = threadIdx.x, lane = th & 31, warp = th >> 5;
@@ -926,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
   extern __shared__ uint8_t dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::STAGES * S::STAGE);
-  Ring ring{bars, bars + S::STAGES, S::STAGES, 0, 0u};
+  Ring ring{bars, bars + S::STAGES, S::STAGES, o.a.wait_ns};
   volatile int* abort = reinterpret_cast<volatile int*>(bars + 2 * S::STAGES);
   __shared__ __align__(16) int ids[kWindow];
   __shared__ int list[kWindow / kRowsO];   // tiles with a token of this adapter; bit 8: all tokens are its
@@ -952,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
   for (int m = 0; m < RP; ++m)
 #pragma unroll
     for (int q = 0; q < 2 * NQ; ++q) sum[m][q][0] = sum[m][q][1] = sum[m][q][2] = sum[m][q][3] = 0.0f;
-  bool any = false;
+  bool any = false, ok = true;
   int issued = 0;
 
   for (int64_t base = first; base < last; base += kWindow / kRowsO) {
@@ -1001,19 +1006,20 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
       __syncwarp();
     } else {
       for (int k = 0; k < count; ++k) {
-        if (!ring.wait_full(abort)) break;
+        ok = ok && ring.wait_full(abort);   // once a wait has given up the warp only meets the others
         uint8_t* zs = smem + ring.slot * S::STAGE;
         uint8_t* wb = zs + S::ZB;
         const bool mixed = !(list[k] & 256);
         if (mixed) {   // zeros in the place of other adapters' rows (a row's chunks are its own, whatever their order)
           const int* row_ids = ids + (list[k] & 255) * kRowsO;
-          for (int e = th; e < S::STAGE / 16; e += 32 * kConsumers) {
+          for (int e = th; ok && e < S::STAGE / 16; e += 32 * kConsumers) {
             const int at = 16 * e;
             const int row = at < S::ZB ? at % S::ZBOX / 128 : (at - S::ZB) % (kRowsO * Ranks::ROW) / Ranks::ROW;
             if (row_ids[row] != id) *reinterpret_cast<uint4*>(zs + at) = make_uint4(0u, 0u, 0u, 0u);
           }
-          consumers_sync();
+          consumers_sync();   // of all consumer warps, whatever their waits said
         }
+        if (!ok) continue;
         // kPair groups of 16 ranks at a time: their chains of products overlap
         constexpr int kPair = RP >= 2 ? 2 : 1;
 #pragma unroll
@@ -1126,6 +1132,18 @@ __global__ void __launch_bounds__(256) lora_outer_sum_kernel(const OuterArgs o, 
 // host side
 // ---------------------------------------------------------------------------
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Time limit of the rings' waits: the GEMMs' 2 s, or the nanoseconds in the
+// environment variable NVFP4_WAIT_TIMEOUT_NS, read at every call (tests let
+// the waits run out with it).
+uint64_t wait_limit_ns() {
+  if (const char* env = std::getenv("NVFP4_WAIT_TIMEOUT_NS")) {
+    char* end = nullptr;
+    const unsigned long long v = std::strtoull(env, &end, 10);
+    if (end != env && *end == '\0') return v;
+  }
+  return kTimeoutNs;
+}
 
 // A bf16 matrix [rows, cols] with row stride ld: boxes of 64 columns (128
 // bytes, swizzled) x box_rows.
@@ -1309,7 +1327,7 @@ cudaError_t outer(const LoraArgs& l, const AdapterIds& a, uint8_t* ws, const Lor
 
 template <int RP>
 cudaError_t forward(const LoraArgs& l, float* h, cudaStream_t st) {
-  const AdapterIds a{l.ids, l.T, static_cast<int>(l.n), l.status};
+  const AdapterIds a{l.ids, l.T, static_cast<int>(l.n), l.status, l.T > kFewTokens ? wait_limit_ns() : 0};
   const int r = static_cast<int>(l.r);
   if (l.T > kFewTokens) {
     const cudaError_t e = shrink<RP, false>(l.x, l.ldx, l.A, a, l.K, r, h, nullptr, nullptr, nullptr, 0, st);
@@ -1331,7 +1349,7 @@ cudaError_t forward(const LoraArgs& l, float* h, cudaStream_t st) {
 
 template <int RP>
 cudaError_t backward(const LoraArgs& l, uint8_t* ws, const LoraWorkspace& w, cudaStream_t st) {
-  const AdapterIds a{l.ids, l.T, static_cast<int>(l.n), l.status};
+  const AdapterIds a{l.ids, l.T, static_cast<int>(l.n), l.status, wait_limit_ns()};
   const int n_terms = l.fp32 ? 3 : 2;
   float* g = reinterpret_cast<float*>(ws + w.g);
   __nv_bfloat16* g_terms = reinterpret_cast<__nv_bfloat16*>(ws + w.g_terms);

@@ -419,3 +419,40 @@ def test_on_a_side_stream(api):
     torch.cuda.current_stream().wait_stream(side)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def cut_short(api, call, want, monkeypatch, limit):
+    """`call` with the kernels' waits limited to `limit` ns returns, and the next
+    one with the usual limit gives `want` again."""
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    monkeypatch.setenv("NVFP4_WAIT_TIMEOUT_NS", str(limit))
+    call(st)
+    torch.cuda.synchronize()
+    monkeypatch.delenv("NVFP4_WAIT_TIMEOUT_NS")
+    assert st.item() in (0, api.L.NVFP4_ERR_TIMEOUT)
+    st.zero_()
+    assert all(torch.equal(a, b) for a, b in zip(call(st), want)) and st.item() == 0
+
+
+@pytest.mark.parametrize("limit", [0, 2500])
+@pytest.mark.parametrize("r,kind", [(16, "random"), (16, "runs"), (40, "random"), (128, "random")])
+def test_waits_that_give_up_end_the_backward_pass(api, monkeypatch, limit, r, kind):
+    """Ring waits cut short on purpose, in tiles of several adapters and of
+    one: every kernel ends, and the context stays usable."""
+    p = problem(5000, 520, 776, r, 3, kind, seed=24)
+    _, h = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"])
+    call = lambda st: api.nvfp4_lora_backward(p["dy"], p["x"], h, p["A"], p["B"], p["scaling"], p["ids"], dx=p["dx"],   # noqa: E731
+                                              out_dtype=FP32, status=st)
+    want = call(None)
+    for _ in range(3):
+        cut_short(api, call, want, monkeypatch, limit)
+
+
+@pytest.mark.parametrize("limit", [0, 2500])
+@pytest.mark.parametrize("r,kind", [(16, "random"), (40, "runs"), (128, "random")])
+def test_waits_that_give_up_end_the_forward_pass(api, monkeypatch, limit, r, kind):
+    p = problem(5000, 1160, 776, r, 3, kind, seed=25)
+    call = lambda st: api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"], y=p["y"], status=st)   # noqa: E731
+    want = call(None)
+    for _ in range(3):
+        cut_short(api, call, want, monkeypatch, limit)

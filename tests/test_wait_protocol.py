@@ -27,9 +27,9 @@ def test_whole_warps_wait_with_one_answer(name):
     lanes: producers (empty slots) and MMA issuers (full slots, drained
     accumulators)."""
     text = source(name)
-    for args in re.findall(r"\bmbar_wait\(([^;]*?), abort(?:_flag)?\)", text):
+    for args in re.findall(r"\bmbar_wait\(([^;]*?), abort(?:_flag)?[,)]", text):
         assert re.search(r"empty|&full\[s\]", args), args
-    whole = re.findall(r"\bmbar_wait_warp\(([^;]*?), abort(?:_flag)?\)", text)
+    whole = re.findall(r"\bmbar_wait_warp\(([^;]*?), abort(?:_flag)?[,)]", text)
     assert whole and all("acc_full" in a or "&full[slot]" in a for a in whole)
 
 
@@ -46,3 +46,15 @@ def test_roles_wait_for_what_they_have_issued(name):
     else:
         kernels = text.count("full[i %")
         assert kernels == 2 and len(re.findall(r"mbar_wait_bounded\(smem_u32\(drain\), 0\)", text)) == kernels
+
+
+def test_adapters_outer_consumers_all_meet_at_their_barrier():
+    """The consumer warps of the outer products meet at a named barrier in
+    tiles of several adapters.  A warp whose wait has given up must come there
+    too: another one may still have seen its data and be waiting."""
+    text = source("lora.cu")
+    kernel = text[text.index("lora_outer_kernel(const"):]
+    loop = kernel[kernel.index("for (int k = 0; k < count; ++k) {"):kernel.index("release(&ring.empty[ring.slot]);")]
+    before, after = loop.split("consumers_sync();")
+    assert "wait_full(abort)" in before and "break" not in before and "continue" not in before
+    assert "if (!ok) continue;" in after
