@@ -553,8 +553,10 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
         al[p][e] = pack_bf16(l0, l1);
       }
     int held = -1;   // base slot whose store may still be reading it
+    bool ok = true;
     for (int c0 = group * KC; c0 < C; c0 += stride) {
-      if (!yr.wait_full(abort)) break;
+      ok = yr.wait_full(abort);
+      if (!ok) break;
       uint8_t* yt = ys + yr.slot * S::YB + ch * (S::YB / 2);   // this half's box of 64 columns
       if (!has_in) {
 #pragma unroll
@@ -562,8 +564,7 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
           *reinterpret_cast<uint4*>(yt + (16 * rg) * 128 + 16 * (lane + 32 * i)) = make_uint4(0u, 0u, 0u, 0u);
         __syncwarp();
       }
-      bool ok = true;
-      for (int u = 0; u < ta.count && ok; ++u) {
+      for (int u = 0; u < ta.count; ++u) {
         ok = wr.wait_full(abort);
         if (!ok) break;
         const int id = ta.list[u];
@@ -623,8 +624,8 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
       yr.next();
     }
     if (lane == 0) bulk_wait_all();
+    if (!ok && lane == 0 && a.status) *a.status = kStatusTimeout;   // by each warp that gave up: the others may have left
   }
-  if (th == 0 && *abort && a.status) *a.status = kStatusTimeout;
 }
 
 // ---------------------------------------------------------------------------
@@ -1070,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
     if (lane == 0) ring.drain(issued);
     return;
   }
-  if (th == 0 && *abort && o.a.status) *o.a.status = kStatusTimeout;
+  if (!ok && lane == 0 && o.a.status) *o.a.status = kStatusTimeout;   // by each warp that gave up: the others may have left
   const bool direct = splits == 1;
   if (!direct) {
     if (th == 0) o.used[(static_cast<int64_t>(id) * splits + split) * gridDim.x + blockIdx.x] = any ? 1 : 0;

@@ -58,3 +58,14 @@ def test_adapters_outer_consumers_all_meet_at_their_barrier():
     before, after = loop.split("consumers_sync();")
     assert "wait_full(abort)" in before and "break" not in before and "continue" not in before
     assert "if (!ok) continue;" in after
+
+
+def test_adapters_a_warp_that_gives_up_reports_it_itself():
+    """Without a barrier behind the waits one thread cannot report for the
+    others: it may have left before they give up."""
+    text = source("lora.cu")
+    for kernel in text.split("__global__")[1:]:
+        for at in re.finditer(r"\*(?:o\.)?a\.status = kStatusTimeout", kernel):
+            line = kernel[kernel.rindex("\n", 0, at.start()):at.start()]
+            meets = kernel.rfind("__syncthreads();", 0, at.start()) > kernel.rfind("wait_full", 0, at.start())
+            assert "!ok && lane == 0" in line or ("*abort" in line and meets), line
