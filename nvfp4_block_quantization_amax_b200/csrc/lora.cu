@@ -52,7 +52,7 @@ struct AdapterIds {
   int64_t T;
   int n;
   int32_t* status;
-  uint64_t wait_ns;   // time limit of a ring's wait
+  uint32_t wait_ns;   // time limit of a ring's wait
 };
 
 // Adapter of token t: -1 for none, for rows past the last token, and for an
@@ -121,18 +121,35 @@ __device__ __forceinline__ int slot_col(int slot) {
 
 // ---- rings of shared memory, filled by TMA --------------------------------
 // A ring's barriers: full[s] completes when a slot's bytes have landed,
-// empty[s] when every consumer warp has arrived.  All waits are bounded (see
-// mbar_wait): one that gives up raises `abort`, every role runs to its end
-// without the data (a barrier that others may stand at is met all the same),
-// and the kernel reports NVFP4_ERR_TIMEOUT.
+// empty[s] when every consumer warp has arrived.  All waits are bounded: one
+// that gives up raises the abort flag and reports NVFP4_ERR_TIMEOUT, and the
+// kernel runs to its end.  The producer then issues nothing more.  The
+// consumers' lanes may disagree about a wait near its limit (one gives up,
+// another still sees the data), so none of them leaves its loop: the warps go
+// on in step through whatever the slots hold and meet at every barrier.
 constexpr int kConsumers = 8;                      // warps
 constexpr int kThreads = 32 * (kConsumers + 1);    // and the producer warp
+
+// The abort flag and the time limit of a wait (shared memory; the limit is
+// looked at only by a wait that did not succeed at once).
+struct Abort {
+  volatile int flag;
+  volatile uint32_t limit_ns;
+};
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, Abort* abort) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (!abort->flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (globaltimer() - t0 > abort->limit_ns) abort->flag = 1;
+  }
+  return false;
+}
 
 struct Ring {
   uint64_t* full;
   uint64_t* empty;
   int slots;
-  uint64_t limit_ns;   // of a wait
   int slot = 0;
   uint32_t phase = 0;   // of the current pass over the slots
   __device__ __forceinline__ void init() const {   // one thread
@@ -147,10 +164,17 @@ struct Ring {
       phase ^= 1;
     }
   }
-  // by all lanes of a consumer warp
-  __device__ __forceinline__ bool wait_full(volatile int* abort) const { return mbar_wait_warp(smem_u32(&full[slot]), phase, abort, limit_ns); }
-  // by the producer's lane
-  __device__ __forceinline__ bool wait_empty(volatile int* abort) const { return mbar_wait(smem_u32(&empty[slot]), phase ^ 1, abort, limit_ns); }
+  // By every lane of a consumer warp, which goes on together.
+  __device__ __forceinline__ void wait_full(Abort* abort, int32_t* status) const {
+    if (!ring_wait(smem_u32(&full[slot]), phase, abort) && status) *status = kStatusTimeout;
+    __syncwarp();
+  }
+  // By the producer's lane; false: nothing more is to be issued (a consumer
+  // that gave up raised the flag before it gave the slot back, in which a copy
+  // may still be landing).
+  __device__ __forceinline__ bool wait_empty(Abort* abort) const {
+    return ring_wait(smem_u32(&empty[slot]), phase ^ 1, abort) && !abort->flag;
+  }
   // The producer lets the copies it has issued (`issued` slots in all) land
   // before its CTA goes.
   __device__ __forceinline__ void drain(int issued) const {
@@ -313,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
   uint8_t* wsm = zs + S::STAGES * S::ZB;
   float* sums = reinterpret_cast<float*>(wsm + S::STAGES * S::WB);   // [64][R]
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sums) + S::SUM);
-  Ring ring{bars, bars + S::STAGES, S::STAGES, a.wait_ns};
-  volatile int* abort = reinterpret_cast<volatile int*>(bars + 2 * S::STAGES);
+  Ring ring{bars, bars + S::STAGES, S::STAGES};
+  Abort* abort = reinterpret_cast<Abort*>(bars + 2 * S::STAGES);
   __shared__ TileAdapters ta;
   const int th = threadIdx.x, lane = th & 31, warp = th >> 5;
   const int rank = static_cast<int>(blockIdx.x) % split;
@@ -325,7 +349,8 @@ __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
   const int steps = (stages - rank + split - 1) / split;
   if (th == 0) {
     ring.init();
-    *abort = 0;
+    abort->flag = 0;
+    abort->limit_ns = a.wait_ns;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   for (int k = th; k < kRows * R; k += kThreads) sums[k] = 0.0f;
@@ -334,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
   if (warp == kConsumers) {
     if (lane == 0) {
       int issued = 0;
-      for (int u = 0; u < ta.count && !*abort; ++u) {
+      for (int u = 0; u < ta.count && !abort->flag; ++u) {
         for (int s = 0; s < steps; ++s, ++issued, ring.next()) {
           if (!ring.wait_empty(abort)) break;
           const uint32_t bar = smem_u32(&ring.full[ring.slot]);
@@ -362,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
 #pragma unroll
       for (int i = 0; i < 2 * RP; ++i) sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.0f;
       for (int s = 0; s < steps; ++s) {
-        if (!ring.wait_full(abort)) break;
+        ring.wait_full(abort, a.status);
         const uint8_t* zt = zs + ring.slot * S::ZB + kh * (S::ZB / 2);   // this half's box of 64 columns
         const uint8_t* wt = wsm + ring.slot * S::WB;
         // this stage's sums start from zero and are added to the running ones:
@@ -438,7 +463,6 @@ __global__ void __launch_bounds__(kThreads, ShrinkCfg<RP, TRANS>::CTAS)
     if (w_terms) write_terms(w_terms, n_terms, a.T, R, t, j, v);
     if (h_terms) write_terms(h_terms, n_terms, a.T, R, t, j, j < r ? __ldg(h + t * r + j) : 0.0f);
   }
-  if (th == 0 && *abort && a.status) *a.status = kStatusTimeout;
   if (split > 1) cluster_barrier();   // no CTA leaves while another may still read its sums
 }
 
@@ -479,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
   uint8_t* ys = smem;
   uint8_t* wsm = ys + S::YSLOTS * S::YB;
   uint64_t* bars = reinterpret_cast<uint64_t*>(wsm + S::WSLOTS * S::WB);
-  Ring yr{bars, bars + S::YSLOTS, S::YSLOTS, a.wait_ns};
-  Ring wr{bars + 2 * S::YSLOTS, bars + 2 * S::YSLOTS + S::WSLOTS, S::WSLOTS, a.wait_ns};
-  volatile int* abort = reinterpret_cast<volatile int*>(bars + 2 * (S::YSLOTS + S::WSLOTS));
+  Ring yr{bars, bars + S::YSLOTS, S::YSLOTS};
+  Ring wr{bars + 2 * S::YSLOTS, bars + 2 * S::YSLOTS + S::WSLOTS, S::WSLOTS};
+  Abort* abort = reinterpret_cast<Abort*>(bars + 2 * (S::YSLOTS + S::WSLOTS));
   __shared__ TileAdapters ta;
   const int th = threadIdx.x, lane = th & 31, warp = th >> 5;
   const int group = static_cast<int>(blockIdx.x) % groups;
@@ -489,7 +513,8 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
   if (th == 0) {
     yr.init();
     wr.init();
-    *abort = 0;
+    abort->flag = 0;
+    abort->limit_ns = a.wait_ns;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tile_adapters(ta, th < kRows ? adapter_of(a, row0 + th, false) : -1);   // ends with a barrier
@@ -497,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
   if (warp == kConsumers) {
     int y_issued = 0, w_issued = 0;
     if (lane == 0) {
-      for (int c = group * KC; c < C && !*abort; c += stride) {
+      for (int c = group * KC; c < C && !abort->flag; c += stride) {
         if (!yr.wait_empty(abort)) break;
         const uint32_t yb = smem_u32(&yr.full[yr.slot]), yd = smem_u32(ys + yr.slot * S::YB);
         if (has_in) {
@@ -553,10 +578,8 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
         al[p][e] = pack_bf16(l0, l1);
       }
     int held = -1;   // base slot whose store may still be reading it
-    bool ok = true;
     for (int c0 = group * KC; c0 < C; c0 += stride) {
-      ok = yr.wait_full(abort);
-      if (!ok) break;
+      yr.wait_full(abort, a.status);
       uint8_t* yt = ys + yr.slot * S::YB + ch * (S::YB / 2);   // this half's box of 64 columns
       if (!has_in) {
 #pragma unroll
@@ -565,8 +588,7 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
         __syncwarp();
       }
       for (int u = 0; u < ta.count; ++u) {
-        ok = wr.wait_full(abort);
-        if (!ok) break;
+        wr.wait_full(abort, a.status);
         const int id = ta.list[u];
         const uint8_t* wt = wsm + wr.slot * S::WB;
         const bool lo_mine = id_lo == id, hi_mine = id_hi == id;
@@ -604,7 +626,6 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
         release(&wr.empty[wr.slot]);
         wr.next();
       }
-      if (!ok) break;
       fence_proxy_async_smem();
       __syncwarp();
       // store this warp's part; the previous tile's store has read its slot by
@@ -624,7 +645,6 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
       yr.next();
     }
     if (lane == 0) bulk_wait_all();
-    if (!ok && lane == 0 && a.status) *a.status = kStatusTimeout;   // by each warp that gave up: the others may have left
   }
 }
 
@@ -932,8 +952,8 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
   extern __shared__ uint8_t dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::STAGES * S::STAGE);
-  Ring ring{bars, bars + S::STAGES, S::STAGES, o.a.wait_ns};
-  volatile int* abort = reinterpret_cast<volatile int*>(bars + 2 * S::STAGES);
+  Ring ring{bars, bars + S::STAGES, S::STAGES};
+  Abort* abort = reinterpret_cast<Abort*>(bars + 2 * S::STAGES);
   __shared__ __align__(16) int ids[kWindow];
   __shared__ int list[kWindow / kRowsO];   // tiles with a token of this adapter; bit 8: all tokens are its
   __shared__ int listed;
@@ -948,7 +968,8 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
   const int64_t first = tiles * split / splits, last = tiles * (split + 1) / splits;
   if (th == 0) {
     ring.init();
-    *abort = 0;
+    abort->flag = 0;
+    abort->limit_ns = o.a.wait_ns;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -958,14 +979,14 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
   for (int m = 0; m < RP; ++m)
 #pragma unroll
     for (int q = 0; q < 2 * NQ; ++q) sum[m][q][0] = sum[m][q][1] = sum[m][q][2] = sum[m][q][3] = 0.0f;
-  bool any = false, ok = true;
+  bool any = false;
   int issued = 0;
 
   for (int64_t base = first; base < last; base += kWindow / kRowsO) {
     const int n_tiles = static_cast<int>(last - base < kWindow / kRowsO ? last - base : kWindow / kRowsO);
     const int64_t row_base = base * kRowsO;
     // the previous window's ids and list have been read; after an abort all leave
-    if (__syncthreads_or(*abort != 0)) break;
+    if (__syncthreads_or(abort->flag != 0)) break;
     for (int k = th; k < n_tiles * kRowsO; k += kThreads) ids[k] = adapter_of(o.a, row_base + k, false);
     __syncthreads();
     if (warp == 0) {
@@ -1007,20 +1028,19 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
       __syncwarp();
     } else {
       for (int k = 0; k < count; ++k) {
-        ok = ok && ring.wait_full(abort);   // once a wait has given up the warp only meets the others
+        ring.wait_full(abort, o.a.status);
         uint8_t* zs = smem + ring.slot * S::STAGE;
         uint8_t* wb = zs + S::ZB;
         const bool mixed = !(list[k] & 256);
         if (mixed) {   // zeros in the place of other adapters' rows (a row's chunks are its own, whatever their order)
           const int* row_ids = ids + (list[k] & 255) * kRowsO;
-          for (int e = th; ok && e < S::STAGE / 16; e += 32 * kConsumers) {
+          for (int e = th; e < S::STAGE / 16; e += 32 * kConsumers) {
             const int at = 16 * e;
             const int row = at < S::ZB ? at % S::ZBOX / 128 : (at - S::ZB) % (kRowsO * Ranks::ROW) / Ranks::ROW;
             if (row_ids[row] != id) *reinterpret_cast<uint4*>(zs + at) = make_uint4(0u, 0u, 0u, 0u);
           }
-          consumers_sync();   // of all consumer warps, whatever their waits said
+          consumers_sync();
         }
-        if (!ok) continue;
         // kPair groups of 16 ranks at a time: their chains of products overlap
         constexpr int kPair = RP >= 2 ? 2 : 1;
 #pragma unroll
@@ -1071,7 +1091,6 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
     if (lane == 0) ring.drain(issued);
     return;
   }
-  if (!ok && lane == 0 && o.a.status) *o.a.status = kStatusTimeout;   // by each warp that gave up: the others may have left
   const bool direct = splits == 1;
   if (!direct) {
     if (th == 0) o.used[(static_cast<int64_t>(id) * splits + split) * gridDim.x + blockIdx.x] = any ? 1 : 0;
@@ -1137,13 +1156,13 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Time limit of the rings' waits: the GEMMs' 2 s, or the nanoseconds in the
 // environment variable NVFP4_WAIT_TIMEOUT_NS, read at every call (tests let
 // the waits run out with it).
-uint64_t wait_limit_ns() {
+uint32_t wait_limit_ns() {
   if (const char* env = std::getenv("NVFP4_WAIT_TIMEOUT_NS")) {
     char* end = nullptr;
     const unsigned long long v = std::strtoull(env, &end, 10);
-    if (end != env && *end == '\0') return v;
+    if (end != env && *end == '\0') return static_cast<uint32_t>(std::min<unsigned long long>(v, kTimeoutNs));
   }
-  return kTimeoutNs;
+  return static_cast<uint32_t>(kTimeoutNs);
 }
 
 // A bf16 matrix [rows, cols] with row stride ld: boxes of 64 columns (128
@@ -1328,7 +1347,7 @@ cudaError_t outer(const LoraArgs& l, const AdapterIds& a, uint8_t* ws, const Lor
 
 template <int RP>
 cudaError_t forward(const LoraArgs& l, float* h, cudaStream_t st) {
-  const AdapterIds a{l.ids, l.T, static_cast<int>(l.n), l.status, l.T > kFewTokens ? wait_limit_ns() : 0};
+  const AdapterIds a{l.ids, l.T, static_cast<int>(l.n), l.status, l.T > kFewTokens ? wait_limit_ns() : 0u};
   const int r = static_cast<int>(l.r);
   if (l.T > kFewTokens) {
     const cudaError_t e = shrink<RP, false>(l.x, l.ldx, l.A, a, l.K, r, h, nullptr, nullptr, nullptr, 0, st);
