@@ -83,6 +83,24 @@ __device__ __forceinline__ void mma16(float* d, const uint32_t* a, const uint32_
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+// The leading bf16 part of v.  Where v is neither zero nor infinite, nor is it
+// (the first and the last half steps of the range would round to those), so
+// that its product with an infinity, or with zero, is v's.
+__device__ __forceinline__ __nv_bfloat16 lead_bf16(float v) {
+  uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  if ((__float_as_uint(v) & 0x7FFFFFFFu) - 1u < 0x7F7FFFFFu) h = (h & 0x8000u) | min(max(h & 0x7FFFu, 1u), 0x7F7Fu);
+  return __ushort_as_bfloat16(static_cast<unsigned short>(h));
+}
+// A sum of the lower parts' products made finite (NaN: the largest number).
+// Next to an infinite factor such sums are infinities of any sign, or
+// 0 inf = NaN; the leading parts' sum is infinite or NaN there as the formula
+// is, and a number added to it changes nothing.
+__device__ __forceinline__ float clamp(float low) {
+  float v;   // the sign of low, the smaller magnitude
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(v) : "f"(low), "f"(3.402823466e38f));
+  return v;
+}
+
 // v = hi + lo up to 2^-17 |v| (an infinity or NaN is all in hi: its lo would
 // be a NaN of its own)
 __device__ __forceinline__ float rest_of(float v, float hi) {
@@ -90,12 +108,12 @@ __device__ __forceinline__ float rest_of(float v, float hi) {
   return fabsf(rest) <= 3.402823466e38f ? rest : 0.0f;
 }
 __device__ __forceinline__ void split_bf16(float v, __nv_bfloat16& hi, __nv_bfloat16& lo) {
-  hi = __float2bfloat16_rn(v);
+  hi = lead_bf16(v);
   lo = __float2bfloat16_rn(rest_of(v, __bfloat162float(hi)));
 }
 // v = hi + mid + lo, all 24 bits
 __device__ __forceinline__ void split_bf16(float v, __nv_bfloat16& hi, __nv_bfloat16& mid, __nv_bfloat16& lo) {
-  hi = __float2bfloat16_rn(v);
+  hi = lead_bf16(v);
   const float r1 = rest_of(v, __bfloat162float(hi));
   mid = __float2bfloat16_rn(r1);
   lo = __float2bfloat16_rn(__fsub_rn(r1, __bfloat162float(mid)));
@@ -593,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
         const uint8_t* wt = wsm + wr.slot * S::WB;
         const bool lo_mine = id_lo == id, hi_mine = id_hi == id;
         if (__any_sync(0xFFFFFFFFu, lo_mine || hi_mine)) {
-#pragma unroll
+#pragma unroll(RP == 4 ? 2 : 4)   // registers (forward, r = 64: 196 us with 4)
           for (int n = 0; n < 64; n += 16) {   // columns of this half
             float acc[2][4] = {}, low[2][4] = {};   // hi and lo parts apart: two shorter chains
 #pragma unroll
@@ -608,19 +626,18 @@ __global__ void __launch_bounds__(kThreads, ExpandCfg<RP>::CTAS)
               mma16(acc[0], ah[p], bf);
               mma16(acc[1], ah[p], bf + 2);
             }
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[q][e] = __fadd_rn(acc[q][e], low[q][e]);
             // a token without an adapter keeps the base's bits (a NaN's payload, a zero's sign)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
-              for (int half = 0; half < 2; ++half)
+              for (int half = 0; half < 2; ++half) {
+                const float2 d = __fadd2_rn(make_float2(acc[q][2 * half], acc[q][2 * half + 1]),
+                                            make_float2(clamp(low[q][2 * half]), clamp(low[q][2 * half + 1])));
                 if (half ? hi_mine : lo_mine) {
                   uint32_t* at = reinterpret_cast<uint32_t*>(chunk_at<128>(yt, my_row + 8 * half, n / 8 + q)) + (lane & 3);
-                  *at = add_round(*at, acc[q][2 * half], acc[q][2 * half + 1]);
+                  *at = add_round(*at, d.x, d.y);
                 }
+              }
           }
         }
         release(&wr.empty[wr.slot]);
@@ -867,6 +884,12 @@ __global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __res
         for (int p = 0; p < RP; ++p) {
           const uint32_t bb[2] = {b[p].x, b[p].y};
           mma16(acc[m], al[p], bb);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[m][e] = clamp(acc[m][e]);
+#pragma unroll
+        for (int p = 0; p < RP; ++p) {
+          const uint32_t bb[2] = {b[p].x, b[p].y};
           mma16(acc[m], ah[p], bb);
         }
       }
@@ -899,6 +922,9 @@ __global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __res
 // grid: column tiles of both products, adapter, split of the rows.
 // TERMS: bf16 numbers that w enters as: 3 (all of fp32) for fp32 gradients,
 // 2 (2^-17) for bf16 ones, as the shrink kernel wrote them.
+// Where a sum is NaN, an infinite z may have met lower terms of the other sign
+// or of zero: a second walk over the rows, with the leading terms alone, gives
+// those elements what the formula does.
 // Memory bounds it: x 8192 x 4096 and dy 8192 x 14336, r = 16, fp32: 82 us
 // (3.7 TB/s; tensor pipe 40% busy with the three terms).
 // ---------------------------------------------------------------------------
@@ -939,55 +965,44 @@ __device__ __forceinline__ void store_out(void* dst, int64_t at, float v, bool f
   else static_cast<__nv_bfloat16*>(dst)[at] = __float2bfloat16_rn(v);
 }
 
-template <int RP, int TERMS>
-__global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
-    lora_outer_kernel(const __grid_constant__ CUtensorMap tmap_z0, const __grid_constant__ CUtensorMap tmap_w0,
-                      const __grid_constant__ CUtensorMap tmap_z1, const __grid_constant__ CUtensorMap tmap_w1,
-                      const OuterArgs o) {
-  pdl_entry();
+__device__ __forceinline__ bool is_nan(const void* src, int64_t at, bool fp32) {
+  return fp32 ? isnan(static_cast<const float*>(src)[at]) : __hisnan(static_cast<const __nv_bfloat16*>(src)[at]);
+}
+
+// A CTA's walk over its rows: where it reads and writes, and how far its ring is.
+struct OuterWalk {
+  uint8_t* smem;
+  int *ids, *list, *listed;   // of a window: its rows' adapters; its tiles with a token of this adapter (bit 8: all are), how many
+  Abort* abort;
+  const CUtensorMap *map_z, *map_w;
+  int c0, id, split, splits;
+  int64_t first, last;        // tiles
+  Ring ring;
+  int issued;
+  bool any;                   // a token of this adapter was seen
+};
+
+// Sums over the rows, and their store.  Returns whether a sum is NaN.  LEAD: with
+// the leading terms alone, storing where the memory holds a NaN.
+template <int RP, int TERMS, bool LEAD>
+__device__ __forceinline__ bool outer_walk(OuterWalk& v, const OuterArgs& o, const OuterProduct& p) {
   using S = OuterCfg<RP, TERMS>;
   using Ranks = RankTile<RP>;
   [[maybe_unused]] constexpr int R = S::R, COLS = S::COLS, NQ = S::NQ;
   constexpr int kRankBox = kRowsO * Ranks::ROW;   // one term's rows in a box
-  extern __shared__ uint8_t dyn[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::STAGES * S::STAGE);
-  Ring ring{bars, bars + S::STAGES, S::STAGES};
-  Abort* abort = reinterpret_cast<Abort*>(bars + 2 * S::STAGES);
-  __shared__ __align__(16) int ids[kWindow];
-  __shared__ int list[kWindow / kRowsO];   // tiles with a token of this adapter; bit 8: all tokens are its
-  __shared__ int listed;
-  const int th = threadIdx.x, lane = th & 31, warp = th >> 5;
-  const bool second = static_cast<int>(blockIdx.x) >= o.p[0].tiles;
-  const OuterProduct& p = o.p[second ? 1 : 0];
-  const CUtensorMap* map_z = second ? &tmap_z1 : &tmap_z0;
-  const CUtensorMap* map_w = second ? &tmap_w1 : &tmap_w0;
-  const int c0 = (static_cast<int>(blockIdx.x) - (second ? o.p[0].tiles : 0)) * COLS;
-  const int id = blockIdx.y, splits = gridDim.z, split = blockIdx.z, r = o.r;
-  const int64_t tiles = (o.a.T + kRowsO - 1) / kRowsO;
-  const int64_t first = tiles * split / splits, last = tiles * (split + 1) / splits;
-  if (th == 0) {
-    ring.init();
-    abort->flag = 0;
-    abort->limit_ns = o.a.wait_ns;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncthreads();
-
+  const int th = threadIdx.x, lane = th & 31, warp = th >> 5, id = v.id, r = o.r;
   float sum[RP][2 * NQ][4];
 #pragma unroll
   for (int m = 0; m < RP; ++m)
 #pragma unroll
     for (int q = 0; q < 2 * NQ; ++q) sum[m][q][0] = sum[m][q][1] = sum[m][q][2] = sum[m][q][3] = 0.0f;
-  bool any = false;
-  int issued = 0;
 
-  for (int64_t base = first; base < last; base += kWindow / kRowsO) {
-    const int n_tiles = static_cast<int>(last - base < kWindow / kRowsO ? last - base : kWindow / kRowsO);
+  for (int64_t base = v.first; base < v.last; base += kWindow / kRowsO) {
+    const int n_tiles = static_cast<int>(v.last - base < kWindow / kRowsO ? v.last - base : kWindow / kRowsO);
     const int64_t row_base = base * kRowsO;
     // the previous window's ids and list have been read; after an abort all leave
-    if (__syncthreads_or(abort->flag != 0)) break;
-    for (int k = th; k < n_tiles * kRowsO; k += kThreads) ids[k] = adapter_of(o.a, row_base + k, false);
+    if (__syncthreads_or(v.abort->flag != 0)) break;
+    for (int k = th; k < n_tiles * kRowsO; k += kThreads) v.ids[k] = adapter_of(o.a, row_base + k, false);
     __syncthreads();
     if (warp == 0) {
       int n = 0;
@@ -997,43 +1012,43 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
         if (tile < n_tiles)
           for (int k = 0; k < kRowsO / 4; ++k) {
             // lanes start at different places: fewer bank conflicts
-            const int4 v = *reinterpret_cast<const int4*>(&ids[tile * kRowsO + 4 * ((k + lane) % (kRowsO / 4))]);
-            some |= v.x == id || v.y == id || v.z == id || v.w == id;
-            all &= v.x == id && v.y == id && v.z == id && v.w == id;
+            const int4 four = *reinterpret_cast<const int4*>(&v.ids[tile * kRowsO + 4 * ((k + lane) % (kRowsO / 4))]);
+            some |= four.x == id || four.y == id || four.z == id || four.w == id;
+            all &= four.x == id && four.y == id && four.z == id && four.w == id;
           }
         const uint32_t m = __ballot_sync(0xFFFFFFFFu, some);
-        if (some) list[n + __popc(m & ((1u << lane) - 1u))] = tile | (all ? 256 : 0);
+        if (some) v.list[n + __popc(m & ((1u << lane) - 1u))] = tile | (all ? 256 : 0);
         n += __popc(m);
       }
-      if (lane == 0) listed = n;
+      if (lane == 0) *v.listed = n;
     }
     __syncthreads();
-    const int count = listed;
-    any |= count > 0;
+    const int count = *v.listed;
+    v.any |= count > 0;
 
     if (warp == kConsumers) {
       if (lane == 0) {
-        for (int k = 0; k < count; ++k, ++issued, ring.next()) {
-          if (!ring.wait_empty(abort)) break;
-          const uint32_t bar = smem_u32(&ring.full[ring.slot]), zd = smem_u32(smem + ring.slot * S::STAGE), wd = zd + S::ZB;
-          const int row = static_cast<int>(row_base) + (list[k] & 255) * kRowsO;
+        for (int k = 0; k < count; ++k, ++v.issued, v.ring.next()) {
+          if (!v.ring.wait_empty(v.abort)) break;
+          const uint32_t bar = smem_u32(&v.ring.full[v.ring.slot]), zd = smem_u32(v.smem + v.ring.slot * S::STAGE), wd = zd + S::ZB;
+          const int row = static_cast<int>(row_base) + (v.list[k] & 255) * kRowsO;
           mbar_expect_tx(bar, S::STAGE);
 #pragma unroll
-          for (int b = 0; b < COLS / 64; ++b) tma_load_2d(zd + b * S::ZBOX, map_z, c0 + 64 * b, row, bar);
+          for (int b = 0; b < COLS / 64; ++b) tma_load_2d(zd + b * S::ZBOX, v.map_z, v.c0 + 64 * b, row, bar);
           // all terms in one copy (a tensor copy costs some 100 ns, however small)
 #pragma unroll
-          for (int b = 0; b < Ranks::BOXES; ++b) tma_load_3d(wd + b * TERMS * kRankBox, map_w, 64 * b, row, 0, bar);
+          for (int b = 0; b < Ranks::BOXES; ++b) tma_load_3d(wd + b * TERMS * kRankBox, v.map_w, 64 * b, row, 0, bar);
         }
       }
       __syncwarp();
     } else {
       for (int k = 0; k < count; ++k) {
-        ring.wait_full(abort, o.a.status);
-        uint8_t* zs = smem + ring.slot * S::STAGE;
+        v.ring.wait_full(v.abort, o.a.status);
+        uint8_t* zs = v.smem + v.ring.slot * S::STAGE;
         uint8_t* wb = zs + S::ZB;
-        const bool mixed = !(list[k] & 256);
+        const bool mixed = !(v.list[k] & 256);
         if (mixed) {   // zeros in the place of other adapters' rows (a row's chunks are its own, whatever their order)
-          const int* row_ids = ids + (list[k] & 255) * kRowsO;
+          const int* row_ids = v.ids + (v.list[k] & 255) * kRowsO;
           for (int e = th; e < S::STAGE / 16; e += 32 * kConsumers) {
             const int at = 16 * e;
             const int row = at < S::ZB ? at % S::ZBOX / 128 : (at - S::ZB) % (kRowsO * Ranks::ROW) / Ranks::ROW;
@@ -1062,10 +1077,10 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
 #pragma unroll
             for (int m = 0; m < kPair; ++m)
 #pragma unroll
-              for (int x = 0; x < TERMS; ++x)
+              for (int x = 0; x < (LEAD ? 1 : TERMS); ++x)
                 ldsm4_t(af[m][x], Ranks::template at<TERMS * kRowsO>(wb, x * kRowsO + arow, 2 * (m0 + m) + ((lane >> 3) & 1)));
 #pragma unroll
-            for (int x = TERMS - 1; x >= 0; --x)
+            for (int x = LEAD ? 0 : TERMS - 1; x >= 0; --x)
 #pragma unroll
               for (int m = 0; m < kPair; ++m)
 #pragma unroll
@@ -1082,20 +1097,14 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
               for (int e = 0; e < 4; ++e) sum[m0 + m][q][e] = __fadd_rn(sum[m0 + m][q][e], acc[m][q][e]);
         }
         if (mixed) fence_proxy_async_smem();   // the zeros were plain stores, the next copy is not
-        release(&ring.empty[ring.slot]);
-        ring.next();
+        release(&v.ring.empty[v.ring.slot]);
+        v.ring.next();
       }
     }
   }
-  if (warp == kConsumers) {
-    if (lane == 0) ring.drain(issued);
-    return;
-  }
-  const bool direct = splits == 1;
-  if (!direct) {
-    if (th == 0) o.used[(static_cast<int64_t>(id) * splits + split) * gridDim.x + blockIdx.x] = any ? 1 : 0;
-    if (!any) return;
-  }
+  bool nan = false;
+  const bool direct = v.splits == 1;
+  if (warp == kConsumers || (!direct && !v.any)) return nan;
   const float s = direct ? __ldg(o.scaling + id) : 1.0f;   // with splits the sum is scaled once, at the end
 #pragma unroll
   for (int m = 0; m < RP; ++m)
@@ -1104,13 +1113,64 @@ __global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int j = 16 * m + (lane >> 2) + 8 * (e >> 1);
-        const int64_t c = c0 + 16 * NQ * warp + 8 * q + 2 * (lane & 3) + (e & 1);
+        const int64_t c = v.c0 + 16 * NQ * warp + 8 * q + 2 * (lane & 3) + (e & 1);
         if (j < r && c < p.C) {
           const int64_t at = p.cols_first ? (static_cast<int64_t>(id) * p.C + c) * r + j : (static_cast<int64_t>(id) * r + j) * p.C + c;
+          float* part = p.part + static_cast<int64_t>(v.split) * o.a.n * r * p.C + at;
+          if constexpr (LEAD) {
+            if (!(direct ? is_nan(p.dst, at, o.fp32) : isnan(*part))) continue;
+          } else {
+            nan |= isnan(sum[m][q][e]);
+          }
           if (direct) store_out(p.dst, at, __fmul_rn(s, sum[m][q][e]), o.fp32);
-          else p.part[static_cast<int64_t>(split) * o.a.n * r * p.C + at] = sum[m][q][e];
+          else *part = sum[m][q][e];
         }
       }
+  return nan;
+}
+
+// Apart, so that the first walk keeps its registers; returns the slots issued.
+template <int RP, int TERMS>
+__device__ __noinline__ int outer_again(OuterWalk v, const OuterArgs& o, const OuterProduct& p) {
+  outer_walk<RP, TERMS, true>(v, o, p);
+  return v.issued;
+}
+
+template <int RP, int TERMS>
+__global__ void __launch_bounds__(kThreads, OuterCfg<RP, TERMS>::CTAS)
+    lora_outer_kernel(const __grid_constant__ CUtensorMap tmap_z0, const __grid_constant__ CUtensorMap tmap_w0,
+                      const __grid_constant__ CUtensorMap tmap_z1, const __grid_constant__ CUtensorMap tmap_w1,
+                      const __grid_constant__ OuterArgs o) {
+  pdl_entry();
+  using S = OuterCfg<RP, TERMS>;
+  extern __shared__ uint8_t dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::STAGES * S::STAGE);
+  Ring ring{bars, bars + S::STAGES, S::STAGES};
+  Abort* abort = reinterpret_cast<Abort*>(bars + 2 * S::STAGES);
+  __shared__ __align__(16) int ids[kWindow];
+  __shared__ int list[kWindow / kRowsO];
+  __shared__ int listed;
+  const int th = threadIdx.x;
+  const bool second = static_cast<int>(blockIdx.x) >= o.p[0].tiles;
+  const OuterProduct& p = o.p[second ? 1 : 0];
+  const int splits = gridDim.z, split = blockIdx.z;
+  const int64_t tiles = (o.a.T + kRowsO - 1) / kRowsO;
+  if (th == 0) {
+    ring.init();
+    abort->flag = 0;
+    abort->limit_ns = o.a.wait_ns;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+
+  OuterWalk v{smem, ids, list, &listed, abort, second ? &tmap_z1 : &tmap_z0, second ? &tmap_w1 : &tmap_w0,
+              (static_cast<int>(blockIdx.x) - (second ? o.p[0].tiles : 0)) * S::COLS, static_cast<int>(blockIdx.y), split, splits,
+              tiles * split / splits, tiles * (split + 1) / splits, ring, 0, false};
+  const bool nan = outer_walk<RP, TERMS, false>(v, o, p);
+  if (__syncthreads_or(nan)) v.issued = outer_again<RP, TERMS>(v, o, p);
+  if (th == 32 * kConsumers) v.ring.drain(v.issued);
+  if (splits > 1 && th == 0) o.used[(static_cast<int64_t>(v.id) * splits + split) * gridDim.x + blockIdx.x] = v.any ? 1 : 0;
 }
 
 // Sum of the splits' partials, in their order, those that saw a token; four

@@ -458,3 +458,70 @@ def test_waits_that_give_up_end_the_forward_pass(api, monkeypatch, limit, r, kin
     want = call(None)
     for _ in range(3):
         cut_short(api, call, want, monkeypatch, limit)
+
+
+def same_kind(got, ref, bound, what):
+    """NaN where the formula gives NaN, its infinities where it gives those,
+    and within the bound elsewhere (where the bound itself is a number)."""
+    got = got.double()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)), what
+    inf = torch.isinf(ref)
+    assert torch.equal(got[inf], ref[inf]), what
+    at = torch.isfinite(ref) & torch.isfinite(bound)
+    within(got[at], ref[at], bound[at], what)
+
+
+@pytest.mark.parametrize("T", [30, 300, 4200])
+@pytest.mark.parametrize("r,kind", [(16, "random"), (24, "runs"), (64, "random"), (128, "runs")])
+@pytest.mark.parametrize("where", ["A", "B", "x", "dy"])
+@pytest.mark.parametrize("out_dtype", [FP32, BF16])
+def test_infinities_stay_infinities(api, T, r, kind, where, out_dtype):
+    """An infinite weight, input or gradient of a token's own: the results are
+    the formula's in 64 bits, infinities with their signs and NaN only where
+    infinities of both signs (or an infinity and a zero) meet."""
+    p = problem(T, 72, 136, r, 3, kind, seed=26)
+    t = int(torch.nonzero(p["ids"] >= 0)[T // 3])
+    a = int(p["ids"][t])
+    inf = float("inf")
+    if where == "A":
+        p["A"][a, 3, 10], p["A"][a, 5, 11] = inf, -inf
+    elif where == "B":
+        p["B"][a, 20, 1], p["B"][a, 21, 7] = -inf, inf
+    elif where == "x":
+        p["x"][t, 17] = -inf
+    else:
+        p["dy"][t, 100] = inf
+    out, h = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"], y=p["y"])
+    dx, dA, dB = api.nvfp4_lora_backward(p["dy"], p["x"], h, p["A"], p["B"], p["scaling"], p["ids"], dx=p["dx"],
+                                         out_dtype=out_dtype)
+    f, e = reference(p, h)
+    step = HALF if out_dtype == BF16 else 2.0 ** -24
+    for got, k in ((h, "h"), (out, "out"), (dx, "dx")):
+        same_kind(got, f[k], e[k], k)
+    for got, k in ((dA, "dA"), (dB, "dB")):
+        same_kind(got, f[k], e[k] + step * (f[k].abs() + e[k]), k)
+    assert any(bool(torch.isinf(f[k]).any()) for k in ("out", "dx", "dA", "dB"))
+
+
+@pytest.mark.parametrize("T", [30, 300])
+def test_products_at_the_ends_of_the_range(api, T):
+    """h next to the largest and the smallest fp32 numbers: its leading bf16
+    part is neither an infinity nor zero."""
+    p = problem(T, 64, 64, 16, 1, "one", seed=27)
+    p["A"].zero_()
+    p["A"][0, 0, 0] = p["A"][0, 1, 1] = p["A"][0, 2, 2] = 1.0
+    p["x"].zero_()
+    p["x"][:, 0] = 3.3895e38                     # the largest bf16 number, and half of its last step on top
+    p["A"][0, 0, 3], p["x"][:, 3] = 1.0, 2.0 ** 119
+    p["x"][:, 1] = 2.0 ** -133
+    p["A"][0, 1, 1] = 2.0 ** -2                  # h[1] = 2^-135
+    p["B"].zero_()
+    p["B"][0, :, 0] = 2.0 ** -10
+    p["B"][0, 5, 1] = float("inf")
+    p["scaling"].fill_(1.0)
+    out, h = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"])
+    assert bool(torch.isfinite(h).all()) and float(h[0, 0]) > 3.3961e38 and float(h[0, 1]) == 2.0 ** -135
+    ref = h.double() @ p["B"][0].double().t()
+    assert bool((out[:, 5] == float("inf")).all())
+    keep = torch.arange(64, device="cuda") != 5
+    within(out[:, keep], ref[:, keep], (2.0 ** -17 + 35 * U + HALF) * 1.01 * ref[:, keep].abs(), "out")
