@@ -504,7 +504,7 @@ NVFP4_API nvfp4_status_t nvfp4_lora_apply(const void* x, int64_t ldx, const void
  * optional, one at least.  dx_in (the shared projection's input gradient) may
  * be NULL and may be dx itself.  The outputs overlap nothing else; dx == x or
  * dx == dy next to dA or dB, which read both after dx is written, is refused.
- * An adapter without tokens gets zeros. */
+ * An adapter without tokens gets zeros, whatever its weights and scaling. */
 NVFP4_API nvfp4_status_t nvfp4_lora_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* h,
                                              const void* A, const void* B, const float* scaling, const int32_t* ids,
                                              int64_t T, int64_t K, int64_t N, int64_t r, int64_t n, const void* dx_in,

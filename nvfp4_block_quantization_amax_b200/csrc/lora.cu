@@ -1105,7 +1105,9 @@ __device__ __forceinline__ bool outer_walk(OuterWalk& v, const OuterArgs& o, con
   bool nan = false;
   const bool direct = v.splits == 1;
   if (warp == kConsumers || (!direct && !v.any)) return nan;
-  const float s = direct ? __ldg(o.scaling + id) : 1.0f;   // with splits the sum is scaled once, at the end
+  // with splits the sum is scaled once, at the end; the scale of an adapter
+  // without tokens says nothing
+  const float s = !direct ? 1.0f : v.any ? __ldg(o.scaling + id) : 0.0f;
 #pragma unroll
   for (int m = 0; m < RP; ++m)
 #pragma unroll
@@ -1190,12 +1192,14 @@ __global__ void __launch_bounds__(256) lora_outer_sum_kernel(const OuterArgs o, 
       const int64_t in = k - id * per, c = p.cols_first ? in / o.r : in % p.C;
       const int32_t* used = o.used + static_cast<int64_t>(id) * splits * all_tiles + (which ? o.p[0].tiles : 0) + c / cols;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      bool any = false;
       for (int s = 0; s < splits; ++s)
         if (__ldcg(used + s * all_tiles)) {
+          any = true;
           const float4 q = __ldcg(reinterpret_cast<const float4*>(p.part + s * total + k));
           v = make_float4(__fadd_rn(v.x, q.x), __fadd_rn(v.y, q.y), __fadd_rn(v.z, q.z), __fadd_rn(v.w, q.w));
         }
-      const float sc = __ldg(o.scaling + id);
+      const float sc = any ? __ldg(o.scaling + id) : 0.0f;
       v = make_float4(__fmul_rn(sc, v.x), __fmul_rn(sc, v.y), __fmul_rn(sc, v.z), __fmul_rn(sc, v.w));
       if (o.fp32) {
         *reinterpret_cast<float4*>(static_cast<float*>(p.dst) + k) = v;

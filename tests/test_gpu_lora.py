@@ -525,3 +525,19 @@ def test_products_at_the_ends_of_the_range(api, T):
     assert bool((out[:, 5] == float("inf")).all())
     keep = torch.arange(64, device="cuda") != 5
     within(out[:, keep], ref[:, keep], (2.0 ** -17 + 35 * U + HALF) * 1.01 * ref[:, keep].abs(), "out")
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -1.0])
+@pytest.mark.parametrize("T", [64, 5000])
+@pytest.mark.parametrize("out_dtype", [FP32, BF16])
+def test_an_adapter_without_tokens_gets_zeros_whatever_its_scale(api, value, T, out_dtype):
+    """Slots of a pool that no request uses: their scaling says nothing."""
+    p = problem(T, 136, 264, 16, 4, "random", seed=28)
+    p["ids"][p["ids"] == 2] = 1
+    p["scaling"][2] = value
+    p["A"][2], p["B"][2] = value, value
+    _, h = api.nvfp4_lora_apply(p["x"], p["A"], p["B"], p["scaling"], p["ids"])
+    _, dA, dB = api.nvfp4_lora_backward(p["dy"], p["x"], h, p["A"], p["B"], p["scaling"], p["ids"], out_dtype=out_dtype)
+    for d in (dA, dB):
+        assert bool((d[2] == 0).all()) and not bool(torch.signbit(d[2]).any())
+        assert bool(torch.isfinite(d).all()) and bool(d[1].any())
