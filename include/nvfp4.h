@@ -384,6 +384,7 @@ NVFP4_API nvfp4_status_t mxfp4_dequantize(const uint8_t* codes, const uint8_t* s
  * before offsets[0] and from offsets[E] on are neither read nor written.
  * Offsets that break the rule set NVFP4_ERR_ARG in *status (device, sticky)
  * and every group is then treated as empty.  1 <= E <= 1024.
+ * offsets, the alphas, amax_out and status are 4-byte aligned in every call.
  *
  * Operand layouts.  With ceil(r / s) s written "r padded to s" and
  * P_s(e) = the sum of the rows of groups 0 .. e-1, each padded to s:
@@ -471,7 +472,8 @@ NVFP4_API nvfp4_status_t nvfp4_gemm_grouped_wgrad(const uint8_t* A, const uint8_
  * sets NVFP4_ERR_ARG in *status and counts as -1.
  * r % 8 == 0, 8 <= r <= 128; K % 8 == 0, N % 8 == 0, at most 2^22; n <= 65535.
  * Rows x, y, out, dy, dx: bf16, 16-byte aligned, row strides (ld, elements) a
- * multiple of 8; A, B, h, dA, dB and the workspace 16-byte aligned.
+ * multiple of 8; A, B, h, dA, dB and the workspace 16-byte aligned, scaling,
+ * ids and status 4-byte.
  * Sums are held in fp32 and added in a fixed order: the same call on the same
  * device gives the same bits.
  * Waits inside the kernels give up after 2 s, or after the nanoseconds in the

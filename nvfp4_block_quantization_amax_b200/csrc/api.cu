@@ -318,6 +318,9 @@ nvfp4_status_t nvfp4_quantize_grouped(const void* x, int64_t T, int64_t C, int64
   if (!aligned(x, 16) || ld % 8) return NVFP4_ERR_ALIGN;
   if (row && (!aligned(out->codes_row, 16) || !aligned(out->scales_row, 16))) return NVFP4_ERR_ALIGN;
   if (col && (!aligned(out->codes_col, 16) || !aligned(out->scales_col, 16))) return NVFP4_ERR_ALIGN;
+  if ((row && !aligned(out->alpha_row, 4)) || (col && !aligned(out->alpha_col, 4)) || !aligned(out->amax_out, 4) ||
+      !aligned(out->status, 4))
+    return NVFP4_ERR_ALIGN;
   if (!workspace || workspace_bytes < nvfp4::grouped_workspace_bytes(E) || !aligned(workspace, 16))
     return NVFP4_ERR_WORKSPACE;
   const nvfp4::QuantOutputs o{out->codes_row, out->scales_row, out->alpha_row, out->codes_col,
@@ -339,7 +342,8 @@ nvfp4_status_t nvfp4_dequantize_grouped(const uint8_t* codes, const uint8_t* sca
   if (nvfp4::grouped_capacity(T, E, 128) * (C / 16) >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
   if (T == 0) return NVFP4_OK;
   if (!codes || !scales || !alpha || !y) return NVFP4_ERR_ARG;
-  if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(y, 16)) return NVFP4_ERR_ALIGN;
+  if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(y, 16) || !aligned(alpha, 4) || !aligned(status, 4))
+    return NVFP4_ERR_ALIGN;
   return launch_status(nvfp4::grouped_dequantize_launch(codes, scales, alpha, T, C, offsets, E, flags, seed, y, status,
                                                         static_cast<cudaStream_t>(stream)));
 }
@@ -361,7 +365,7 @@ nvfp4_status_t nvfp4_gemm_grouped(const uint8_t* A, const uint8_t* sA, const flo
   if (T == 0) return NVFP4_OK;
   if (!A || !sA || !alphaA || !B || !sB || !alphaB || !D) return NVFP4_ERR_ARG;
   if (!aligned(A, 16) || !aligned(B, 16) || !aligned(sA, 16) || !aligned(sB, 16) || !aligned(D, 16) ||
-      !aligned(alphaA, 4) || !aligned(alphaB, 4) || (ldd * (out_dtype == NVFP4_OUT_DTYPE_BF16 ? 2 : 4)) % 16)
+      !aligned(alphaA, 4) || !aligned(alphaB, 4) || !aligned(status, 4) || (ldd * (out_dtype == NVFP4_OUT_DTYPE_BF16 ? 2 : 4)) % 16)
     return NVFP4_ERR_ALIGN;
   return launch_status(nvfp4::grouped_gemm_launch(A, sA, alphaA, B, sB, alphaB, offsets, E, T, N, K, D, out_dtype, ldd,
                                                   status, static_cast<cudaStream_t>(stream)));
@@ -382,7 +386,7 @@ nvfp4_status_t nvfp4_gemm_grouped_wgrad(const uint8_t* A, const uint8_t* sA, con
     return NVFP4_ERR_SHAPE;
   if (!D || (T && (!A || !sA || !alphaA || !B || !sB || !alphaB))) return NVFP4_ERR_ARG;
   if (!aligned(A, 16) || !aligned(B, 16) || !aligned(sA, 16) || !aligned(sB, 16) || !aligned(D, 16) ||
-      !aligned(alphaA, 4) || !aligned(alphaB, 4))
+      !aligned(alphaA, 4) || !aligned(alphaB, 4) || !aligned(status, 4))
     return NVFP4_ERR_ALIGN;
   return launch_status(nvfp4::grouped_wgrad_launch(A, sA, alphaA, B, sB, alphaB, offsets, E, T, M, N, D, out_dtype,
                                                    status, static_cast<cudaStream_t>(stream)));
@@ -401,7 +405,7 @@ nvfp4_status_t nvfp4_lora_apply(const void* x, int64_t ldx, const void* A, const
   if (T == 0) return NVFP4_OK;
   if ((chk = check_rows(x, ldx, K)) != NVFP4_OK || (chk = check_rows(out, ldo, N)) != NVFP4_OK) return chk;
   if (y && (chk = check_rows(y, ldy, N)) != NVFP4_OK) return chk;
-  if (!aligned(h, 16)) return NVFP4_ERR_ALIGN;
+  if (!aligned(h, 16) || !aligned(status, 4)) return NVFP4_ERR_ALIGN;
   if (!workspace || workspace_bytes < nvfp4::lora_workspace_bytes(T, K, N, r, n, false) || !aligned(workspace, 16))
     return NVFP4_ERR_WORKSPACE;
   nvfp4::LoraArgs l{};
@@ -441,7 +445,7 @@ nvfp4_status_t nvfp4_lora_backward(const void* dy, int64_t lddy, const void* x, 
     if (dA && (chk = check_rows(x, ldx, K)) != NVFP4_OK) return chk;
     if (dB && !h) return NVFP4_ERR_ARG;
   }
-  if (!aligned(h, 16) || !aligned(dA, 16) || !aligned(dB, 16)) return NVFP4_ERR_ALIGN;
+  if (!aligned(h, 16) || !aligned(dA, 16) || !aligned(dB, 16) || !aligned(status, 4)) return NVFP4_ERR_ALIGN;
   if (T && (!workspace || workspace_bytes < nvfp4::lora_workspace_bytes(T, K, N, r, n, true) || !aligned(workspace, 16)))
     return NVFP4_ERR_WORKSPACE;
   if (T && dx && (dA || dB) && (dx == x || dx == dy)) return NVFP4_ERR_ARG;   // written before dA and dB read them

@@ -139,3 +139,31 @@ def test_binding_refuses_host_tensors():
     W, sW = torch.zeros((128, 64), **u8), torch.zeros(128 * 8, **u8)   # 5 rows of 2 groups: 128 padded rows
     with pytest.raises(TypeError, match="CUDA"):
         api.nvfp4_gemm_grouped_wgrad(W, sW, f, W, sW, f, off, 5)
+
+
+def qt(**kw):
+    f = dict(codes_row=FAKE, scales_row=FAKE, alpha_row=FAKE, codes_col=FAKE, scales_col=FAKE, alpha_col=FAKE,
+             amax_out=FAKE, status=FAKE)
+    f.update(kw)
+    return L.nvfp4_qtensor_t(*f.values())
+
+
+@pytest.mark.parametrize("name", ["alpha_row", "alpha_col", "amax_out", "status"])
+@pytest.mark.parametrize("T", [0, 16, 200])
+def test_quantize_refuses_misaligned_words(name, T):
+    assert quantize(T=T, flags=ROW | COL, out=qt(**{name: FAKE + 2})) == -3
+
+
+def test_words_of_the_other_orientation_are_not_looked_at():
+    assert quantize(flags=ROW, ws=None, out=qt(alpha_col=FAKE + 2)) == -8
+    assert quantize(flags=COL, ws=None, out=qt(alpha_row=FAKE + 2)) == -8
+
+
+@pytest.mark.parametrize("alpha,status", [(FAKE + 2, None), (FAKE, FAKE + 1)])
+def test_dequantize_refuses_misaligned_words(alpha, status):
+    assert L.nvfp4_dequantize_grouped(FAKE, FAKE, alpha, 64, 128, FAKE, 2, ROW, 0, FAKE, status, None) == -3
+
+
+def test_products_refuse_misaligned_words():
+    assert L.nvfp4_gemm_grouped(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 2, 64, 128, 128, FAKE, 0, 128, FAKE + 2, None) == -3
+    assert L.nvfp4_gemm_grouped_wgrad(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 2, 64, 128, 128, FAKE, 1, FAKE + 2, None) == -3

@@ -84,3 +84,10 @@ def test_backward_refuses_dx_over_an_input_of_the_weight_gradients(name):
         a["dy"], 128, a["x"], 128, FAKE, FAKE, FAKE, FAKE, FAKE, 64, 128, 128, 16, 2, None, 128, a[name], 128, dA, dB, 1,
         FAKE, 1 << 30, None, None)
     assert call(FAKE, None) == -1 and call(None, FAKE) == -1 and call(FAKE, FAKE) == -1
+
+
+def test_a_misaligned_status_word_is_refused():
+    assert L.nvfp4_lora_apply(FAKE, 128, FAKE, FAKE, FAKE, FAKE, 64, 128, 256, 16, 2, None, 256, FAKE, 256, FAKE, FAKE, 1 << 30,
+                              FAKE + 2, None) == -3
+    assert L.nvfp4_lora_backward(FAKE, 256, 2 * FAKE, 128, FAKE, FAKE, FAKE, FAKE, FAKE, 64, 128, 256, 16, 2, None, 128, 3 * FAKE,
+                                 128, FAKE, FAKE, 1, FAKE, 1 << 30, FAKE + 2, None) == -3
