@@ -476,8 +476,8 @@ NVFP4_API nvfp4_status_t nvfp4_gemm_grouped_wgrad(const uint8_t* A, const uint8_
  * ids and status 4-byte.
  * Sums are held in fp32 and added in a fixed order: the same call on the same
  * device gives the same bits.
- * Waits inside the kernels give up after 2 s, or after the nanoseconds in the
- * environment variable NVFP4_WAIT_TIMEOUT_NS (read at each call), with
+ * Waits inside the kernels give up after 2 s, or sooner, after the nanoseconds
+ * in the environment variable NVFP4_WAIT_TIMEOUT_NS (read at each call), with
  * NVFP4_ERR_TIMEOUT in *status.
  * ------------------------------------------------------------------------ */
 

@@ -565,3 +565,61 @@ def test_offsets_past_32_bits_products(api):
     want = api.nvfp4_gemm_grouped(own.codes_row, own.scales_row, own.alpha_row, B[:1], qw.scales_row, qw.alpha_row,
                                   offsets_of([2]))
     assert torch.equal(D[-2:], want)
+
+
+@pytest.mark.parametrize("T", [40, 64, 300])
+@pytest.mark.parametrize("flags", [ROW, COL, ROW | COL, ROW | RHT, ROW | COL | RHT])
+def test_bad_offsets_leave_everything_empty(api, T, flags):
+    """Bad offsets count as no group at all: alphas 0, no code or scale byte
+    written, decoded rows left alone, weight gradients zeros - in the kernels of
+    few rows as in the others."""
+    C, E = 128, 2
+    x = rows_of(T, C, 44).cuda()
+    good = api.nvfp4_quantize_grouped(x, offsets_of([T - 9, 9]), 0, ROW | COL)
+    for bad in ([0, T, T - 1], [0, T // 2, T + 1], [-1, T // 2, T], [T + 6] * 3):
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        q = api.grouped_alloc_outputs(T, C, E, flags, x.device)
+        sides = [s for s, bit in (("row", ROW), ("col", COL)) if flags & bit]
+        for s in sides:
+            for k in ("codes", "scales"):
+                getattr(q, f"{k}_{s}").fill_(0xA5)
+            getattr(q, f"alpha_{s}").fill_(7.0)
+        api.nvfp4_quantize_grouped(x, off, 1, flags, out=q, status=st)
+        assert st.item() == -1
+        for s in sides:
+            assert getattr(q, f"alpha_{s}").tolist() == [0.0, 0.0]
+            assert all(bool((getattr(q, f"{k}_{s}") == 0xA5).all()) for k in ("codes", "scales"))
+            for extra in (0, INV | BF):
+                st.zero_()
+                y = torch.full((T, C), 3.0, dtype=torch.bfloat16 if extra & BF else torch.float32, device="cuda")
+                api.nvfp4_dequantize_grouped(getattr(good, f"codes_{s}"), getattr(good, f"scales_{s}"), getattr(good, f"alpha_{s}"),
+                                             off, T, C, (ROW if s == "row" else COL) | extra, out=y, status=st)
+                assert st.item() == -1 and bool((y == 3).all())
+        for dt, out in ((FP32, torch.float32), (BF16, torch.bfloat16)):
+            st.zero_()
+            D = torch.full((E, C, C), 5.0, dtype=out, device="cuda")
+            api.nvfp4_gemm_grouped_wgrad(*(t for _ in range(2) for t in (good.codes_col, good.scales_col, good.alpha_col)), off, T,
+                                         out_dtype=dt, out=D, status=st)
+            assert st.item() == -1 and not bool(D.any())
+
+
+@pytest.mark.parametrize("counts", [[(5 * i) % 4 for i in range(1024)], [0] * 1000 + [1] * 24])
+def test_as_many_groups_as_there_may_be(api, counts):
+    check_quantize(api, rows_of(sum(counts), 128, 45), counts, 1, ROW | COL)
+    check_gemm(api, counts, 128, 64, True, seed=46)
+    check_wgrad(api, counts, 128, 128, False, seed=48)
+
+
+@pytest.mark.parametrize("flags", [ROW, ROW | COL, ROW | RHT, COL | RHT])
+@pytest.mark.parametrize("T", [48, 100])
+def test_values_at_the_ends_of_the_range(api, T, flags):
+    """Groups of the largest, of the smallest and of mixed numbers: as the
+    oracle does each by itself."""
+    x = rows_of(T, 128, 47).float().sign()
+    x[: T // 3] *= 2.0 ** 123
+    x[T // 3: T // 2] *= 2.0 ** -133
+    x[T // 2:, ::3] *= 2.0 ** 100
+    x[T // 2:, 1::3] *= 2.0 ** -120
+    check_quantize(api, x.bfloat16(), [T // 3, T // 2 - T // 3, T - T // 2], 0, flags)
+    check_quantize(api, x.bfloat16(), [T // 3, T // 2 - T // 3, T - T // 2], 1, flags)

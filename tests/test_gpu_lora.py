@@ -541,3 +541,12 @@ def test_an_adapter_without_tokens_gets_zeros_whatever_its_scale(api, value, T, 
     for d in (dA, dB):
         assert bool((d[2] == 0).all()) and not bool(torch.signbit(d[2]).any())
         assert bool(torch.isfinite(d).all()) and bool(d[1].any())
+
+
+@pytest.mark.parametrize("r", [8, 24, 32, 56, 64, 96, 128])
+@pytest.mark.parametrize("T,kind", [(300, "random"), (4200, "runs"), (8300, "random")])
+@pytest.mark.parametrize("out_dtype", [FP32, BF16])
+def test_every_rank_class_and_gradient_type(api, r, T, kind, out_dtype):
+    """Gradients in both types for every padded rank, with the rows in one
+    range and in several (whose sums are added by a kernel of their own)."""
+    check(api, problem(T, 136, 264, r, 3, kind, seed=29), out_dtype=out_dtype)
