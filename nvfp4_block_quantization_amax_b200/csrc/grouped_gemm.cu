@@ -15,10 +15,16 @@
 //     stored.  A's scales sit in 128-row atoms, each group starting a new one.
 //   * contraction grouped: a group's tokens are padded with zero codes to 64
 //     (one MMA's K), and only its own K blocks are multiplied.
-// What bounds it is the operands' way from L2 into the SMs (each 256 x 256
-// tile loads 2 x 256 rows of its K): at about 12.7 TB/s, 16384 tokens of 8
-// groups x 14336 x 4096 take 374 us alone (5.1 PFLOP/s, bf16 results) and the
-// fp32 weight gradient of the same sizes 615 us, 1.9 GB of results among them.
+// 16384 tokens of 8 groups x 14336 x 4096 take 374 us in a short run (5.1
+// PFLOP/s, bf16 results) and about 465 in long ones, under the power cap; the
+// tensor pipe is busy 67% of the time (the plain GEMM's 70%), the operands
+// come from L2 at 11 TB/s, a third of what that way carries.  The fp32 weight
+// gradient of the same sizes takes 595 to 615 us, 705 to 715 in long runs: the
+// tensor pipe is busy 40% of the time (54% with bf16 results), operands come at
+// 7 TB/s, DRAM is at 37%.  None of them is at its limit; it is the results'
+// way out that costs: a tile has eight stages of products (2048 tokens of a
+// group), then 256 KB of results leave the one accumulator through one small
+// box per warp (GroupedCfg).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>

@@ -150,8 +150,8 @@ __device__ __forceinline__ uint32_t load_cluster_u32(const uint32_t* p, int rank
 
 // ---------------------------------------------------------------------------
 // amax per group.  Plain: memory bounds it (16384 x 4096 25 us, 5.4 TB/s).
-// Rotated: instruction issue (a butterfly per orientation; 16301 x 14336, both,
-// 143 us, 3.3 TB/s).
+// Rotated: its instructions (a butterfly per orientation, 13 thread instructions
+// per value, 61% of the issue slots used; 16301 x 14336, both, 143 us, 3.3 TB/s).
 // ---------------------------------------------------------------------------
 // Fold the CTA's running maximum (float bits) into a group's word.
 template <int NT>
@@ -300,9 +300,11 @@ __global__ void __launch_bounds__(kRotNT) grouped_amax_rot_kernel(const GroupedA
 }
 
 // ---------------------------------------------------------------------------
-// encode.  Instruction issue bounds it (16384 x 4096 rows and columns, 4/6: 26
-// thread instructions per value, about 70% of the issue slots): 133 us with 4/6,
-// 55 us to nearest; 16301 x 14336 to nearest, rotated: 240 us.
+// encode.  Its instructions bound it.  Rows and columns, thread instructions per
+// value and issue slots used: 4/6 26, 71% (16384 x 4096 133 us; to nearest 55);
+// rotated, to nearest 21, 58% (16301 x 14336 240 us), MS-EDEN 40, 60%, software
+// stochastic rounding 76, 64% with the ALU pipe 62% busy.  Registers keep 16
+// warps or fewer on an SM, which leave the rest of the slots to latencies.
 // ---------------------------------------------------------------------------
 struct GroupStaging {
   uint8_t colcodes[TC][48];        // transposed codes of one tile (32 bytes used per column)

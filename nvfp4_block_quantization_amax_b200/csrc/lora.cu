@@ -26,7 +26,7 @@
 // through memory, so they run on mma.sync with bf16 operands and fp32 sums.
 // h and g are kept in fp32; where they are an operand of a product they enter
 // as the sum of two bf16 numbers (16 bits of mantissa, error 2^-17), which
-// costs one more product of the rank's size instead of bf16's 2^-9.
+// costs one more product of the rank's size instead of bf16's 2^-8.
 // Adapters are found tile by tile: a tile of 64 tokens loops over the
 // adapters that occur in it, so tokens of one request (in a row) share one
 // pass and any order is right.  The forward pass of few tokens gathers them by
@@ -45,7 +45,15 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kRows = 64;      // tokens of a tile
-constexpr int kFewTokens = 256;   // up to here the tokens are gathered by adapter
+// Up to here the tokens are gathered by adapter.  4096 -> 14336, gathered /
+// tiles of 64 tokens, us: 256 tokens of 32 adapters in random order r = 16
+// 30 / 92, r = 64 71 / 163; one adapter's after the other r = 16 30 / 36,
+// r = 64 70 / 66; of one adapter r = 16 20 / 20, r = 64 45 / 25 (64 tokens
+// 21 / 20).  The host does not know the ids, so the size alone decides, for
+// the order that costs most.  Beyond, tiles of many adapters take their time:
+// 32 adapters in random order / in runs, r = 16, 257 tokens 93 / 37, 512
+// 141 / 35, 1024 246 / 39, 2048 450 / 57.
+constexpr int kFewTokens = 256;
 
 struct AdapterIds {
   const int32_t* ids;
@@ -214,9 +222,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Shared-memory tiles as TMA writes them: rows of ROW bytes (64 or 128) whose 16-byte chunks are swizzled by the row, so that eight rows of one
-// chunk lie in different banks.  Wider tiles are several boxes, one behind
-// the other.
+// Shared-memory tiles as TMA writes them: rows of ROW bytes (64 or 128) whose
+// 16-byte chunks are swizzled by the row, so that eight rows of one chunk lie
+// in different banks.  Wider tiles are several boxes, one behind the other.
 template <int ROW>
 __device__ __forceinline__ const uint8_t* chunk_at(const uint8_t* tile, int row, int chunk) {
   constexpr int kShift = ROW == 128 ? 0 : 1;
@@ -925,8 +933,9 @@ __global__ void __launch_bounds__(128) lora_expand_few_kernel(const float* __res
 // Where a sum is NaN, an infinite z may have met lower terms of the other sign
 // or of zero: a second walk over the rows, with the leading terms alone, gives
 // those elements what the formula does.
-// Memory bounds it: x 8192 x 4096 and dy 8192 x 14336, r = 16, fp32: 82 us
-// (3.7 TB/s; tensor pipe 40% busy with the three terms).
+// x 8192 x 4096 and dy 8192 x 14336, r = 16, fp32: 81 us (3.8 TB/s; tensor pipe
+// 43% busy with the three terms).  Neither is at its limit: a CTA takes one
+// adapter's tokens of a range of rows, and the longest run sets the time.
 // ---------------------------------------------------------------------------
 struct OuterProduct {
   int64_t C;
