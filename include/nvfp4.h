@@ -520,6 +520,105 @@ NVFP4_API nvfp4_status_t nvfp4_lora_backward(const void* dy, int64_t lddy, const
                                              int64_t ld_in, void* dx, int64_t lddx, void* dA, void* dB, int out_dtype,
                                              void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Around the experts' products (no page defines them): which experts a token
+ * goes to, its row next to the others of each expert (the ragged groups
+ * above), products of a few unquantized rows, and the way back.
+ *
+ * Common to these calls: ids, rows, offsets int32, weights, dweights, bias,
+ * alphaW fp32, all 4-byte aligned and contiguous; token rows bf16, 16-byte
+ * aligned with row strides that are multiples of 8; status: optional.  A token
+ * has k choices, 1 <= k <= 32; "pair" t k + j is choice j of token t, and
+ * T k < 2^31.  Sums are fp32 and added in a fixed order.  Outputs overlap
+ * nothing else unless a call says so.  No workspace.
+ * ------------------------------------------------------------------------ */
+
+/* A router's scores s of the logits z. */
+#define NVFP4_ROUTE_SOFTMAX 0
+#define NVFP4_ROUTE_SIGMOID 1
+/* nvfp4_route flags */
+#define NVFP4_ROUTE_RENORM 0x1u     /* weights are s / (sum of the chosen s)     */
+#define NVFP4_ROUTE_GROUP_PAIR 0x2u /* a group's value is the sum of its two
+                                     * largest values (of its only open one),
+                                     * instead of its largest                    */
+
+/* Choose k of E experts for each token, best first.
+ *     s = softmax(z) or sigmoid(z);   value = s + bias   (bias: optional, [E])
+ * The experts form `groups` runs of E / groups; only those of the groups_kept
+ * groups with the largest value take part.  Equal values go by the lowest
+ * index.  ids [T, k], weights [T, k]: s of the chosen expert, without the
+ * bias, or its share of the chosen ones' sum (NVFP4_ROUTE_RENORM), times scale.
+ *   The order is that of the values in 64 bits; with neither bias nor groups
+ * it is the order of z.  An expert whose logit or bias is -inf or the lowest
+ * number of its type is never chosen; where fewer than k are left the rest of
+ * the row is -1 with weight 0 (every choice of a padding token, say).  A row
+ * with a NaN or +inf, or any NaN or +inf in bias, sets NVFP4_ERR_NONFINITE and
+ * gets -1 and 0 throughout.
+ * logits: bf16 (dtype NVFP4_OUT_DTYPE_BF16) or fp32, row stride ldl >= E,
+ * aligned to their type.  1 <= E <= 1024, 1 <= groups <= 32, groups divides E,
+ * k <= groups_kept (E / groups). */
+NVFP4_API nvfp4_status_t nvfp4_route(const void* logits, int64_t ldl, int dtype, const float* bias, int64_t T, int64_t E,
+                                     int64_t k, int64_t groups, int64_t groups_kept, int score, uint32_t flags,
+                                     float scale, int32_t* ids, float* weights, int32_t* status, void* stream);
+
+/* Gradient of the weights of nvfp4_route with respect to the logits: dlogits
+ * [T, E] of the logits' type, row stride ldd.  ids, score, scale and flags
+ * (NVFP4_ROUTE_RENORM; NVFP4_ROUTE_GROUP_PAIR changes nothing) as there; the
+ * choice itself has no gradient.  Choices of -1 add nothing, rows without any
+ * get zeros; an id outside -1 .. E - 1 sets NVFP4_ERR_ARG and counts as -1.
+ * dlogits may be the logits. */
+NVFP4_API nvfp4_status_t nvfp4_route_backward(const float* dweights, const int32_t* ids, const void* logits, int64_t ldl,
+                                              int dtype, int64_t T, int64_t E, int64_t k, int score, uint32_t flags,
+                                              float scale, void* dlogits, int64_t ldd, int32_t* status, void* stream);
+
+/* Sort token rows by expert: the operand of nvfp4_quantize_grouped.
+ *   offsets [E + 1]: where each expert's rows begin (offsets[E]: all of them)
+ *   rows [T, k]: the place of each pair, equal experts in the order of the
+ *     pairs; -1 for a choice of -1
+ *   xs [T k, C]: xs[rows[t, j]] = x[t]; rows from offsets[E] on are left as
+ *     they are
+ * x and xs may both be NULL: then only the places are computed.  An id outside
+ * -1 .. E - 1 sets NVFP4_ERR_ARG and counts as -1.  1 <= E <= 1024, C % 8 == 0.
+ * (The gradient with respect to x is nvfp4_combine of dxs without weights.) */
+NVFP4_API nvfp4_status_t nvfp4_dispatch(const void* x, int64_t ldx, const int32_t* ids, int64_t T, int64_t k, int64_t E,
+                                        int64_t C, void* xs, int64_t ldxs, int32_t* offsets, int32_t* rows,
+                                        int32_t* status, void* stream);
+
+/*     out[t] = residual[t] + sum_j weights[t, j] y[rows[t, j]]
+ * y [R, C], rows [T, k] as nvfp4_dispatch wrote them (a place may occur any
+ * number of times), or NULL: pair p has row p, as nvfp4_gemv writes them, and
+ * R >= T k.  out is rounded once, to bf16.  weights NULL: all 1.
+ * residual (optional) may be out itself.  A row of -1 adds nothing; one outside
+ * -1 .. R - 1 sets NVFP4_ERR_ARG and counts as -1.  C % 8 == 0. */
+NVFP4_API nvfp4_status_t nvfp4_combine(const void* y, int64_t ldy, int64_t R, const int32_t* rows, const float* weights,
+                                       int64_t T, int64_t k, int64_t C, const void* residual, int64_t ldr, void* out,
+                                       int64_t ldo, int32_t* status, void* stream);
+
+/* Gradients of nvfp4_combine for the output gradient dout [T, C]:
+ *     dy[rows[t, j]] = weights[t, j] dout[t],   dweights[t, j] = sum_c dout[t, c] y[rows[t, j], c]
+ * dy [R, C] and dweights [T, k] are each optional, one at least; y is needed
+ * for dweights.  No place may occur twice in rows; rows of dy that do not occur
+ * are left as they are; dweights of a row of -1 is 0. */
+NVFP4_API nvfp4_status_t nvfp4_combine_backward(const void* dout, int64_t lddo, const void* y, int64_t ldy, int64_t R,
+                                                const int32_t* rows, const float* weights, int64_t T, int64_t k,
+                                                int64_t C, void* dy, int64_t lddy, float* dweights, int32_t* status,
+                                                void* stream);
+
+/* Products of a few bf16 rows with NVFP4 weights, the rows not quantized:
+ *     out[p, n] = alphaW[e] * sum_k x[p / rep, k] (q Delta)[e, n, k],   e = ids[p]
+ * for P pairs, with x [ceil(P / rep), K]: rep = k where a token's k choices
+ * read its row, 1 where each pair has its own.  ids NULL: E = 1 and every row
+ * takes the one weight.  W: codes [E, N, K/2] and sW: scales in the GEMM layout
+ * of E N rows, alphaW: E floats, as nvfp4_gemm_grouped takes them (E = 1: as
+ * nvfp4_gemm does).  Products are exact and summed in fp32; out is bf16 or
+ * fp32 with row stride ldo.  A pair of -1 gets zeros, an id outside -1 .. E - 1
+ * sets NVFP4_ERR_ARG and does too.  0 <= P <= 1024 (more rows: nvfp4_gemm,
+ * nvfp4_gemm_grouped), N % 128 == 0, K % 64 == 0, 1 <= E <= 1024; W and sW
+ * 16-byte aligned, out aligned to its type. */
+NVFP4_API nvfp4_status_t nvfp4_gemv(const void* x, int64_t ldx, const int32_t* ids, int64_t P, int64_t rep,
+                                    const uint8_t* W, const uint8_t* sW, const float* alphaW, int64_t E, int64_t N,
+                                    int64_t K, void* out, int out_dtype, int64_t ldo, int32_t* status, void* stream);
+
 /* Number of kernels this library has launched in the calling process since
  * it was loaded (all devices, all streams).  Instrumentation for callers that
  * account for their launches; not a page-defined operation. */

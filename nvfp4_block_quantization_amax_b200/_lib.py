@@ -32,11 +32,17 @@ NVFP4_OUT_BF16 = 0x100
 NVFP4_OUT_DTYPE_BF16 = 0
 NVFP4_OUT_DTYPE_FP32 = 1
 
+NVFP4_ROUTE_SOFTMAX, NVFP4_ROUTE_SIGMOID = 0, 1
+NVFP4_ROUTE_RENORM = 0x1
+NVFP4_ROUTE_GROUP_PAIR = 0x2
+
 EXPORTED = ("nvfp4_workspace_size", "nvfp4_quantize", "nvfp4_quantize_noalloc", "nvfp4_amax", "nvfp4_dequantize",
             "nvfp4_gemm", "nvfp4_gemm_vector_scales", "nvfp4_gemm_quantize", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm",
             "nvfp4_grouped_capacity", "nvfp4_grouped_workspace_size", "nvfp4_quantize_grouped",
             "nvfp4_dequantize_grouped", "nvfp4_gemm_grouped", "nvfp4_gemm_grouped_wgrad",
-            "nvfp4_lora_workspace_size", "nvfp4_lora_apply", "nvfp4_lora_backward", "nvfp4_launch_count",
+            "nvfp4_lora_workspace_size", "nvfp4_lora_apply", "nvfp4_lora_backward",
+            "nvfp4_route", "nvfp4_route_backward", "nvfp4_dispatch", "nvfp4_combine", "nvfp4_combine_backward", "nvfp4_gemv",
+            "nvfp4_launch_count",
             "nvfp4_status_string", "nvfp4_version")
 
 
@@ -105,6 +111,19 @@ def load(path=LIB_PATH):
     L.nvfp4_lora_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, i64, vp, i64,
                                       vp, vp, ctypes.c_int, vp, sz, vp, vp]
     L.nvfp4_lora_backward.restype = ctypes.c_int
+    ci, f32 = ctypes.c_int, ctypes.c_float
+    L.nvfp4_route.argtypes = [vp, i64, ci, vp, i64, i64, i64, i64, i64, ci, u32, f32, vp, vp, vp, vp]
+    L.nvfp4_route.restype = ci
+    L.nvfp4_route_backward.argtypes = [vp, vp, vp, i64, ci, i64, i64, i64, ci, u32, f32, vp, i64, vp, vp]
+    L.nvfp4_route_backward.restype = ci
+    L.nvfp4_dispatch.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, i64, vp, vp, vp, vp]
+    L.nvfp4_dispatch.restype = ci
+    L.nvfp4_combine.argtypes = [vp, i64, i64, vp, vp, i64, i64, i64, vp, i64, vp, i64, vp, vp]
+    L.nvfp4_combine.restype = ci
+    L.nvfp4_combine_backward.argtypes = [vp, i64, vp, i64, i64, vp, vp, i64, i64, i64, vp, i64, vp, vp, vp]
+    L.nvfp4_combine_backward.restype = ci
+    L.nvfp4_gemv.argtypes = [vp, i64, vp, i64, i64, vp, vp, vp, i64, i64, i64, vp, ci, i64, vp, vp]
+    L.nvfp4_gemv.restype = ci
     L.nvfp4_status_string.argtypes = [ctypes.c_int]
     L.nvfp4_status_string.restype = ctypes.c_char_p
     L.nvfp4_version.argtypes = []
@@ -215,6 +234,32 @@ def nvfp4_lora_backward(dy, lddy, x, ldx, h, A, B, scaling, ids, T, K, N, r, n, 
                         out_dtype, workspace, workspace_bytes, status, stream):
     return int(load().nvfp4_lora_backward(dy, lddy, x, ldx, h, A, B, scaling, ids, T, K, N, r, n, dx_in, ld_in, dx, lddx,
                                           dA, dB, out_dtype, workspace, workspace_bytes, status, stream))
+
+
+def nvfp4_route(logits, ldl, dtype, bias, T, E, k, groups, groups_kept, score, flags, scale, ids, weights, status, stream):
+    return load().nvfp4_route(logits, ldl, dtype, bias, T, E, k, groups, groups_kept, score, flags, scale, ids, weights,
+                              status, stream)
+
+
+def nvfp4_route_backward(dweights, ids, logits, ldl, dtype, T, E, k, score, flags, scale, dlogits, ldd, status, stream):
+    return load().nvfp4_route_backward(dweights, ids, logits, ldl, dtype, T, E, k, score, flags, scale, dlogits, ldd, status,
+                                       stream)
+
+
+def nvfp4_dispatch(x, ldx, ids, T, k, E, C, xs, ldxs, offsets, rows, status, stream):
+    return load().nvfp4_dispatch(x, ldx, ids, T, k, E, C, xs, ldxs, offsets, rows, status, stream)
+
+
+def nvfp4_combine(y, ldy, R, rows, weights, T, k, C, residual, ldr, out, ldo, status, stream):
+    return load().nvfp4_combine(y, ldy, R, rows, weights, T, k, C, residual, ldr, out, ldo, status, stream)
+
+
+def nvfp4_combine_backward(dout, lddo, y, ldy, R, rows, weights, T, k, C, dy, lddy, dweights, status, stream):
+    return load().nvfp4_combine_backward(dout, lddo, y, ldy, R, rows, weights, T, k, C, dy, lddy, dweights, status, stream)
+
+
+def nvfp4_gemv(x, ldx, ids, P, rep, W, sW, alphaW, E, N, K, out, out_dtype, ldo, status, stream):
+    return load().nvfp4_gemv(x, ldx, ids, P, rep, W, sW, alphaW, E, N, K, out, out_dtype, ldo, status, stream)
 
 
 def nvfp4_status_string(status):

@@ -13,7 +13,7 @@ from . import _lib as L
 from ._lib import (NVFP4_ALPHA_PROVIDED, NVFP4_AMAX_PROVIDED, NVFP4_BLOCK2D, NVFP4_COLWISE, NVFP4_FOUR_SIX,  # noqa: F401
                    NVFP4_GEMM_SCALE_LAYOUT, NVFP4_HEADROOM, NVFP4_INVERSE_RHT, NVFP4_MS_EDEN, NVFP4_OUT_BF16,
                    NVFP4_OUT_DTYPE_BF16, NVFP4_OUT_DTYPE_FP32, NVFP4_RHT, NVFP4_RHT_SR, NVFP4_RHT_SR_HW,
-                   NVFP4_ROWWISE, NVFP4_RTN, NVFP4_SINGLE_PASS, NVFP4_VECTOR_SCALES)
+                   NVFP4_ROUTE_GROUP_PAIR, NVFP4_ROUTE_RENORM, NVFP4_ROUTE_SIGMOID, NVFP4_ROUTE_SOFTMAX, NVFP4_ROWWISE, NVFP4_RTN, NVFP4_SINGLE_PASS, NVFP4_VECTOR_SCALES)
 
 
 class NVFP4Error(RuntimeError):
@@ -652,3 +652,247 @@ def nvfp4_lora_backward(dy: torch.Tensor, x: torch.Tensor, h: torch.Tensor, A: t
                                    ws.numel(), _p(status), _stream_of(dev))
     _check(st, "nvfp4_lora_backward")
     return dx_out, dA, dB
+
+
+# ---------------------------------------------------------------------------
+# Around the experts' products: routing, sorting rows by expert, the way back,
+# and products of a few unquantized rows.
+# ---------------------------------------------------------------------------
+def _pairs(t: torch.Tensor, dtype, what: str, device):
+    """Shape (T, k) of a contiguous tensor of one value per token and choice."""
+    if t.dim() != 2:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, need [T, k]")
+    _need(t, t.shape[0] * t.shape[1], dtype, what, device)
+    return t.shape
+
+
+def _like_pairs(t: torch.Tensor, shape, dtype, what: str, device):
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, need {tuple(shape)}")
+    _need(t, shape[0] * shape[1], dtype, what, device)
+
+
+def _logits(t: torch.Tensor, what: str):
+    """(row stride, dtype flag) of router logits, fp32 or bf16."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise TypeError(f"{what} must be a 2D CUDA tensor")
+    if t.dtype == torch.float32:
+        kind = NVFP4_OUT_DTYPE_FP32
+    elif t.dtype == torch.bfloat16:
+        kind = NVFP4_OUT_DTYPE_BF16
+    else:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {torch.float32} or {torch.bfloat16}")
+    T, E = t.shape
+    if T and E > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have unit column stride")
+    return t.stride(0) if T > 1 else E, kind
+
+
+def nvfp4_route(logits: torch.Tensor, k: int, score: int = NVFP4_ROUTE_SOFTMAX, flags: int = 0,
+                bias: Optional[torch.Tensor] = None, groups: int = 1, groups_kept: int = 1, scale: float = 1.0,
+                ids: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
+                status: Optional[torch.Tensor] = None):
+    """Choose k experts of each token from router logits [T, E] (fp32 or
+    bf16): returns (ids [T, k] int32, weights [T, k] fp32), best first.
+    score: NVFP4_ROUTE_SOFTMAX or NVFP4_ROUTE_SIGMOID; bias [E] fp32 is added
+    for the choice alone; groups / groups_kept restrict it to the best groups
+    of experts; flags: NVFP4_ROUTE_RENORM, NVFP4_ROUTE_GROUP_PAIR.  Experts
+    with a logit of -inf are never chosen; -1 stands where none is left."""
+    ldl, kind = _logits(logits, "logits")
+    dev = logits.device
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, E, torch.float32, "bias", dev)
+    if ids is not None:
+        _like_pairs(ids, (T, k), torch.int32, "ids", dev)
+    if weights is not None:
+        _like_pairs(weights, (T, k), torch.float32, "weights", dev)
+    _check_status(status, dev)
+    with _guard(dev):
+        if ids is None:
+            ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        if weights is None:
+            weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        st = L.nvfp4_route(_p(logits), ldl, kind, _p(bias), T, E, k, groups, groups_kept, score, flags, scale, _p(ids),
+                           _p(weights), _p(status), _stream_of(dev))
+    _check(st, "nvfp4_route")
+    return ids, weights
+
+
+def nvfp4_route_backward(dweights: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor, score: int = NVFP4_ROUTE_SOFTMAX,
+                         flags: int = 0, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                         status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of nvfp4_route's weights with respect to the logits ([T, E],
+    the logits' type) for dweights [T, k]; ids, score, flags and scale as in
+    the forward call.  out may be the logits."""
+    ldl, kind = _logits(logits, "logits")
+    dev = logits.device
+    T, E = logits.shape
+    shape = _pairs(ids, torch.int32, "ids", dev)
+    if shape[0] != T:
+        raise ValueError(f"ids: {shape[0]} tokens, logits {T}")
+    _like_pairs(dweights, shape, torch.float32, "dweights", dev)
+    ldd = E
+    if out is not None:
+        if out.dtype != logits.dtype or out.device != dev or out.shape != logits.shape:
+            raise ValueError("out must have the logits' type, device and shape")
+        ldd = _logits(out, "out")[0]
+    _check_status(status, dev)
+    with _guard(dev):
+        if out is None:
+            out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        st = L.nvfp4_route_backward(_p(dweights), _p(ids), _p(logits), ldl, kind, T, E, shape[1], score, flags, scale,
+                                    _p(out), ldd, _p(status), _stream_of(dev))
+    _check(st, "nvfp4_route_backward")
+    return out
+
+
+def nvfp4_dispatch(x: Optional[torch.Tensor], ids: torch.Tensor, E: int, out: Optional[torch.Tensor] = None,
+                   rows: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None):
+    """Sort token rows x [T, C] (bf16) by the experts ids [T, k]: returns (xs
+    [T k, C], rows [T, k], offsets [E + 1]); xs and offsets are the operands of
+    nvfp4_quantize_grouped, rows those of nvfp4_combine.  Rows of xs from
+    offsets[E] on are left as they are (unspecified in a new tensor).  Without
+    x only rows and offsets are computed (xs is None)."""
+    if not ids.is_cuda:
+        raise TypeError("ids must be a 2D int32 CUDA tensor")
+    dev = ids.device
+    T, k = _pairs(ids, torch.int32, "ids", dev)
+    C = ldx = ldo = 8
+    if x is not None:
+        if x.dim() != 2:
+            raise ValueError("x must be [T, C]")
+        C = x.shape[1]
+        ldx, ldo = _rows(x, T, C, "x", dev), C
+        if out is not None:
+            ldo = _rows(out, T * k, C, "out", dev)
+    elif out is not None:
+        raise ValueError("out without x")
+    if rows is not None:
+        _like_pairs(rows, (T, k), torch.int32, "rows", dev)
+    if offsets is not None:
+        _need(offsets, E + 1, torch.int32, "offsets", dev)
+    _check_status(status, dev)
+    with _guard(dev):
+        if rows is None:
+            rows = torch.empty((T, k), dtype=torch.int32, device=dev)
+        if offsets is None:
+            offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        if x is not None and out is None:
+            out = torch.empty((T * k, C), dtype=torch.bfloat16, device=dev)
+        st = L.nvfp4_dispatch(_p(x), ldx, _p(ids), T, k, E, C, _p(out), ldo, _p(offsets), _p(rows), _p(status),
+                              _stream_of(dev))
+    _check(st, "nvfp4_dispatch")
+    return out, rows, offsets
+
+
+def _places(rows, weights, device):
+    """Shape (T, k) of the pairs: that of rows, or of weights without rows."""
+    if rows is not None:
+        shape = _pairs(rows, torch.int32, "rows", device)
+    elif weights is None:
+        raise ValueError("rows or weights are needed")
+    else:
+        return _pairs(weights, torch.float32, "weights", device)
+    if weights is not None:
+        _like_pairs(weights, shape, torch.float32, "weights", device)
+    return shape
+
+
+def nvfp4_combine(y: torch.Tensor, rows: Optional[torch.Tensor], weights: Optional[torch.Tensor] = None,
+                  residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[t] = residual[t] + sum_j weights[t, j] y[rows[t, j]] (bf16 [T, C]):
+    the experts' rows y [R, C] back to their tokens.  rows as nvfp4_dispatch
+    returned them (-1: nothing), or None: y's rows are those of the pairs in
+    order, as nvfp4_gemv returns them; weights [T, k] fp32, or all 1; residual
+    optional, may be out.  Without weights it is nvfp4_dispatch's gradient."""
+    if y.dtype != torch.bfloat16 or y.dim() != 2 or not y.is_cuda:
+        raise TypeError("y must be a 2D bfloat16 CUDA tensor")
+    dev = y.device
+    R, C = y.shape
+    T, k = _places(rows, weights, dev)
+    ldy = _rows(y, R, C, "y", dev)
+    ldr = 0 if residual is None else _rows(residual, T, C, "residual", dev)
+    ldo = C if out is None else _rows(out, T, C, "out", dev)
+    _check_status(status, dev)
+    with _guard(dev):
+        if out is None:
+            out = torch.empty((T, C), dtype=torch.bfloat16, device=dev)
+        st = L.nvfp4_combine(_p(y), ldy, R, _p(rows), _p(weights), T, k, C, _p(residual), ldr, _p(out), ldo, _p(status),
+                             _stream_of(dev))
+    _check(st, "nvfp4_combine")
+    return out
+
+
+def nvfp4_combine_backward(dout: torch.Tensor, rows: Optional[torch.Tensor], weights: Optional[torch.Tensor], y: torch.Tensor,
+                           need_dy: bool = True, need_dweights: bool = True, out: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None):
+    """Gradients of nvfp4_combine for dout [T, C]: returns (dy [R, C], dweights
+    [T, k]), None in the place of one that is not needed.  rows, weights and y
+    as in the forward call; no place may occur twice in rows.  Rows of dy that
+    do not occur are left as they are in `out` (unspecified in a new tensor)."""
+    if dout.dtype != torch.bfloat16 or dout.dim() != 2 or not dout.is_cuda:
+        raise TypeError("dout must be a 2D bfloat16 CUDA tensor")
+    dev = dout.device
+    T, C = dout.shape
+    shape = _places(rows, weights, dev)
+    if shape[0] != T:
+        raise ValueError(f"rows: {shape[0]} tokens, dout {T}")
+    if y.dim() != 2:
+        raise ValueError("y must be [R, C]")
+    R = y.shape[0]
+    lddo, ldy = _rows(dout, T, C, "dout", dev), _rows(y, R, C, "y", dev)
+    if out is not None and not need_dy:
+        raise ValueError("out without need_dy")
+    lddy = C if out is None else _rows(out, R, C, "out", dev)
+    _check_status(status, dev)
+    with _guard(dev):
+        if need_dy and out is None:
+            out = torch.empty((R, C), dtype=torch.bfloat16, device=dev)
+        dw = torch.empty(shape, dtype=torch.float32, device=dev) if need_dweights else None
+        st = L.nvfp4_combine_backward(_p(dout), lddo, _p(y), ldy, R, _p(rows), _p(weights), T, shape[1], C, _p(out), lddy,
+                                      _p(dw), _p(status), _stream_of(dev))
+    _check(st, "nvfp4_combine_backward")
+    return out, dw
+
+
+def nvfp4_gemv(x: torch.Tensor, W: torch.Tensor, sW: torch.Tensor, alphaW: torch.Tensor, ids: Optional[torch.Tensor] = None,
+               out_dtype: int = NVFP4_OUT_DTYPE_BF16, out: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Products of a few bf16 rows with NVFP4 weights, the rows not quantized
+    (at most 1024 results).  Without ids: x [P, K], W codes [N, K/2] -> [P, N].
+    With ids [T, k]: W codes [E, N, K/2], and x [T, K] (a token's choices share
+    its row) or [T k, K] (a row each) -> [T k, N], zeros for a choice of -1.
+    Scales in the GEMM layout, alphaW one float per weight."""
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_cuda:
+        raise TypeError("x must be a 2D bfloat16 CUDA tensor")
+    dev = x.device
+    X, K = x.shape
+    if W.dim() != (2 if ids is None else 3) or 2 * W.shape[-1] != K:
+        raise ValueError(f"W must be codes [{'' if ids is None else 'E, '}N, {K // 2}], not {tuple(W.shape)}")
+    N = W.shape[-2]
+    E = 1 if ids is None else W.shape[0]
+    P, rep = X, 1
+    if ids is not None:
+        T, k = _pairs(ids, torch.int32, "ids", dev)
+        P = T * k
+        if X == T:
+            rep = k
+        elif X != P:
+            raise ValueError(f"x: {X} rows, need {T} or {P}")
+    ldx = _rows(x, X, K, "x", dev)
+    _need(W, E * N * (K // 2), torch.uint8, "W", dev)
+    _need(sW, E * N * (K // 16), torch.uint8, "sW", dev)
+    _need(alphaW, E, torch.float32, "alphaW", dev)
+    _check_status(status, dev)
+    dt = torch.bfloat16 if out_dtype == NVFP4_OUT_DTYPE_BF16 else torch.float32
+    if out is not None:
+        _need_matrix(out, P, N, dt, "out", dev)
+    with _guard(dev):
+        y = out if out is not None else torch.empty((P, N), dtype=dt, device=dev)
+        st = L.nvfp4_gemv(_p(x), ldx, _p(ids), P, max(rep, 1), _p(W), _p(sW), _p(alphaW), E, N, K, _p(y), out_dtype,
+                          y.stride(0) if P > 1 else N, _p(status), _stream_of(dev))
+    _check(st, "nvfp4_gemv")
+    return y

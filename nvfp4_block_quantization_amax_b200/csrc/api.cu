@@ -53,6 +53,30 @@ nvfp4_status_t check_rows(const void* p, int64_t ld, int64_t cols) {
   return aligned(p, 16) && ld % 8 == 0 ? NVFP4_OK : NVFP4_ERR_ALIGN;
 }
 
+constexpr int64_t kMost = int64_t(1) << 31;
+
+// Tokens and their choices: T k pairs are counted in 32 bits.
+bool bad_pairs(int64_t T, int64_t k) { return T < 0 || T >= kMost || k < 1 || k > 32 || T * k >= kMost; }
+
+// Checks shared by the routing calls.
+nvfp4_status_t check_route(const void* logits, int64_t ldl, int dtype, int64_t T, int64_t E, int64_t k, int score,
+                           uint32_t flags) {
+  if (dtype != NVFP4_OUT_DTYPE_BF16 && dtype != NVFP4_OUT_DTYPE_FP32) return NVFP4_ERR_ARG;
+  if (score != NVFP4_ROUTE_SOFTMAX && score != NVFP4_ROUTE_SIGMOID) return NVFP4_ERR_ARG;
+  if (flags & ~(NVFP4_ROUTE_RENORM | NVFP4_ROUTE_GROUP_PAIR)) return NVFP4_ERR_ARG;
+  if (bad_pairs(T, k) || E < 1 || E > nvfp4::kMaxGroups || k > E || ldl < E) return NVFP4_ERR_SHAPE;
+  if (T && !logits) return NVFP4_ERR_ARG;
+  return aligned(logits, dtype == NVFP4_OUT_DTYPE_BF16 ? 2 : 4) ? NVFP4_OK : NVFP4_ERR_ALIGN;
+}
+
+// Checks shared by the calls that move rows between tokens and pairs.
+nvfp4_status_t check_pairs(const int32_t* rows, const float* weights, int64_t T, int64_t k, int64_t C, int64_t R,
+                           const int32_t* status) {
+  if (bad_pairs(T, k) || R < 0 || R >= kMost || C < 8 || C % 8 || C >= kMost) return NVFP4_ERR_SHAPE;
+  if (!rows && T * k > R) return NVFP4_ERR_SHAPE;   // pair p has row p
+  return aligned(rows, 4) && aligned(weights, 4) && aligned(status, 4) ? NVFP4_OK : NVFP4_ERR_ALIGN;
+}
+
 }  // namespace
 
 namespace nvfp4 {
@@ -473,6 +497,138 @@ nvfp4_status_t nvfp4_lora_backward(const void* dy, int64_t lddy, const void* x, 
   l.fp32 = out_dtype == NVFP4_OUT_DTYPE_FP32;
   l.status = status;
   return launch_status(nvfp4::lora_backward_launch(l, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status_t nvfp4_route(const void* logits, int64_t ldl, int dtype, const float* bias, int64_t T, int64_t E, int64_t k,
+                           int64_t groups, int64_t groups_kept, int score, uint32_t flags, float scale, int32_t* ids,
+                           float* weights, int32_t* status, void* stream) {
+  const nvfp4_status_t chk = check_route(logits, ldl, dtype, T, E, k, score, flags);
+  if (chk != NVFP4_OK) return chk;
+  if (groups < 1 || groups > 32 || E % groups || groups_kept < 1 || groups_kept > groups || k > groups_kept * (E / groups))
+    return NVFP4_ERR_SHAPE;
+  if (T == 0) return NVFP4_OK;
+  if (!ids || !weights) return NVFP4_ERR_ARG;
+  if (!aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(status, 4)) return NVFP4_ERR_ALIGN;
+  const nvfp4::RouteArgs a{logits, ldl, bias, T, E, k, groups, groups_kept, score, flags, scale,
+                           dtype == NVFP4_OUT_DTYPE_FP32, ids, weights, status};
+  return launch_status(nvfp4::route_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status_t nvfp4_route_backward(const float* dweights, const int32_t* ids, const void* logits, int64_t ldl, int dtype,
+                                    int64_t T, int64_t E, int64_t k, int score, uint32_t flags, float scale, void* dlogits,
+                                    int64_t ldd, int32_t* status, void* stream) {
+  const nvfp4_status_t chk = check_route(logits, ldl, dtype, T, E, k, score, flags);
+  if (chk != NVFP4_OK) return chk;
+  if (ldd < E) return NVFP4_ERR_SHAPE;
+  if (T == 0) return NVFP4_OK;
+  if (!dweights || !ids || !dlogits) return NVFP4_ERR_ARG;
+  if (dlogits == logits && ldd != ldl) return NVFP4_ERR_ARG;   // in place only row by row
+  if (!aligned(dweights, 4) || !aligned(ids, 4) || !aligned(dlogits, dtype == NVFP4_OUT_DTYPE_BF16 ? 2 : 4) ||
+      !aligned(status, 4))
+    return NVFP4_ERR_ALIGN;
+  const nvfp4::RouteArgs a{logits, ldl, nullptr, T, E, k, 1, 1, score, flags, scale,
+                           dtype == NVFP4_OUT_DTYPE_FP32, const_cast<int32_t*>(ids), nullptr, status};
+  return launch_status(nvfp4::route_backward_launch(a, dweights, dlogits, ldd, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status_t nvfp4_dispatch(const void* x, int64_t ldx, const int32_t* ids, int64_t T, int64_t k, int64_t E, int64_t C,
+                              void* xs, int64_t ldxs, int32_t* offsets, int32_t* rows, int32_t* status, void* stream) {
+  if (E < 1 || E > nvfp4::kMaxGroups) return NVFP4_ERR_SHAPE;
+  nvfp4_status_t chk = check_pairs(rows, nullptr, T, k, x || xs ? C : 8, T * k, status);
+  if (chk != NVFP4_OK) return chk;
+  if (!offsets || (T && (!ids || !rows || !x != !xs))) return NVFP4_ERR_ARG;
+  if (!aligned(offsets, 4) || !aligned(ids, 4)) return NVFP4_ERR_ALIGN;
+  if (T && x && ((chk = check_rows(x, ldx, C)) != NVFP4_OK || (chk = check_rows(xs, ldxs, C)) != NVFP4_OK)) return chk;
+  if (x && x == xs) return NVFP4_ERR_ARG;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  chk = launch_status(nvfp4::sort_launch(ids, T * k, E, offsets, rows, status, st));
+  if (chk != NVFP4_OK || T == 0 || !x) return chk;
+  nvfp4::RowArgs a{};
+  a.in = static_cast<const __nv_bfloat16*>(x);
+  a.ldi = ldx;
+  a.rows = rows;
+  a.T = T;
+  a.k = k;
+  a.C = C;
+  a.R = T * k;
+  a.out = static_cast<__nv_bfloat16*>(xs);
+  a.ldo = ldxs;
+  return launch_status(nvfp4::dispatch_rows_launch(a, st));
+}
+
+nvfp4_status_t nvfp4_combine(const void* y, int64_t ldy, int64_t R, const int32_t* rows, const float* weights, int64_t T,
+                             int64_t k, int64_t C, const void* residual, int64_t ldr, void* out, int64_t ldo,
+                             int32_t* status, void* stream) {
+  nvfp4_status_t chk = check_pairs(rows, weights, T, k, C, R, status);
+  if (chk != NVFP4_OK) return chk;
+  if (T == 0) return NVFP4_OK;
+  if (R && (chk = check_rows(y, ldy, C)) != NVFP4_OK) return chk;
+  if ((chk = check_rows(out, ldo, C)) != NVFP4_OK) return chk;
+  if (residual && (chk = check_rows(residual, ldr, C)) != NVFP4_OK) return chk;
+  if (out == y || (out == residual && ldr != ldo)) return NVFP4_ERR_ARG;
+  nvfp4::RowArgs a{};
+  a.in = static_cast<const __nv_bfloat16*>(residual);
+  a.ldi = ldr;
+  a.y = static_cast<const __nv_bfloat16*>(y);
+  a.ldy = ldy;
+  a.rows = rows;
+  a.weights = weights;
+  a.T = T;
+  a.k = k;
+  a.C = C;
+  a.R = R;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.ldo = ldo;
+  a.status = status;
+  return launch_status(nvfp4::combine_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status_t nvfp4_combine_backward(const void* dout, int64_t lddo, const void* y, int64_t ldy, int64_t R,
+                                      const int32_t* rows, const float* weights, int64_t T, int64_t k, int64_t C, void* dy,
+                                      int64_t lddy, float* dweights, int32_t* status, void* stream) {
+  nvfp4_status_t chk = check_pairs(rows, weights, T, k, C, R, status);
+  if (chk != NVFP4_OK) return chk;
+  if (!dy && !dweights) return NVFP4_ERR_ARG;
+  if (T == 0) return NVFP4_OK;
+  if ((chk = check_rows(dout, lddo, C)) != NVFP4_OK) return chk;
+  if (R && dweights && (chk = check_rows(y, ldy, C)) != NVFP4_OK) return chk;
+  if (R && dy && (chk = check_rows(dy, lddy, C)) != NVFP4_OK) return chk;
+  if (!aligned(dweights, 4)) return NVFP4_ERR_ALIGN;
+  if (dy && (dy == dout || (dweights && dy == y))) return NVFP4_ERR_ARG;
+  nvfp4::RowArgs a{};
+  a.in = static_cast<const __nv_bfloat16*>(dout);
+  a.ldi = lddo;
+  a.y = static_cast<const __nv_bfloat16*>(y);
+  a.ldy = ldy;
+  a.rows = rows;
+  a.weights = weights;
+  a.T = T;
+  a.k = k;
+  a.C = C;
+  a.R = R;
+  a.out = static_cast<__nv_bfloat16*>(dy);
+  a.ldo = lddy;
+  a.dweights = dweights;
+  a.status = status;
+  return launch_status(nvfp4::combine_backward_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status_t nvfp4_gemv(const void* x, int64_t ldx, const int32_t* ids, int64_t P, int64_t rep, const uint8_t* W,
+                          const uint8_t* sW, const float* alphaW, int64_t E, int64_t N, int64_t K, void* out, int out_dtype,
+                          int64_t ldo, int32_t* status, void* stream) {
+  if (out_dtype != NVFP4_OUT_DTYPE_BF16 && out_dtype != NVFP4_OUT_DTYPE_FP32) return NVFP4_ERR_ARG;
+  if (P < 0 || P > 1024 || rep < 1 || rep > 1024 || E < 1 || E > nvfp4::kMaxGroups || (!ids && E != 1)) return NVFP4_ERR_SHAPE;
+  if (N <= 0 || K <= 0 || N % 128 || K % 64 || ldo < N || N >= kMost || K >= kMost) return NVFP4_ERR_SHAPE;
+  if (P == 0) return NVFP4_OK;
+  if (!W || !sW || !alphaW || !out) return NVFP4_ERR_ARG;
+  const nvfp4_status_t chk = check_rows(x, ldx, K);
+  if (chk != NVFP4_OK) return chk;
+  if (!aligned(W, 16) || !aligned(sW, 16) || !aligned(alphaW, 4) || !aligned(ids, 4) || !aligned(status, 4) ||
+      !aligned(out, out_dtype == NVFP4_OUT_DTYPE_BF16 ? 2 : 4))
+    return NVFP4_ERR_ALIGN;
+  const nvfp4::GemvArgs a{static_cast<const __nv_bfloat16*>(x), ldx, ids, P, rep, W, sW, alphaW, E, N, K, out, ldo,
+                          out_dtype == NVFP4_OUT_DTYPE_FP32, status};
+  return launch_status(nvfp4::gemv_launch(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

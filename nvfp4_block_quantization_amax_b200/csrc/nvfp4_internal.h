@@ -140,4 +140,61 @@ size_t lora_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t r, int64_t 
 cudaError_t lora_forward_launch(const LoraArgs& l, void* workspace, cudaStream_t st);
 cudaError_t lora_backward_launch(const LoraArgs& l, void* workspace, cudaStream_t st);
 
+// Routing (route.cu): logits [T, E] fp32 or bf16 -> ids, weights [T, k], and
+// back.
+struct RouteArgs {
+  const void* logits;
+  int64_t ldl;
+  const float* bias;
+  int64_t T, E, k, groups, kept;
+  int score;
+  uint32_t flags;
+  float scale;
+  bool fp32;
+  int32_t* ids;
+  float* weights;
+  int32_t* status;
+};
+cudaError_t route_launch(const RouteArgs& a, cudaStream_t st);
+cudaError_t route_backward_launch(const RouteArgs& a, const float* dweights, void* dlogits, int64_t ldd, cudaStream_t st);
+
+// Rows of tokens and of pairs (dispatch.cu).  Dispatch: in (x) -> out (xs).
+// Combine: in (residual) + y -> out.  Backward: in (dout), y -> out (dy),
+// dweights.  R: rows of y, xs, dy.  Members not used are null.
+struct RowArgs {
+  const __nv_bfloat16* in;
+  int64_t ldi;
+  const __nv_bfloat16* y;
+  int64_t ldy;
+  const int32_t* rows;
+  const float* weights;
+  int64_t T, k, C, R;
+  __nv_bfloat16* out;
+  int64_t ldo;
+  float* dweights;
+  int32_t* status;
+};
+cudaError_t sort_launch(const int32_t* ids, int64_t P, int64_t E, int32_t* offsets, int32_t* rows, int32_t* status,
+                        cudaStream_t st);
+cudaError_t dispatch_rows_launch(const RowArgs& a, cudaStream_t st);
+cudaError_t combine_launch(const RowArgs& a, cudaStream_t st);
+cudaError_t combine_backward_launch(const RowArgs& a, cudaStream_t st);
+
+// Few bf16 rows times NVFP4 weights (gemv.cu); ids null: one weight.
+struct GemvArgs {
+  const __nv_bfloat16* x;
+  int64_t ldx;
+  const int32_t* ids;
+  int64_t P, rep;
+  const uint8_t* W;
+  const uint8_t* sW;
+  const float* alphaW;
+  int64_t E, N, K;
+  void* out;
+  int64_t ldo;
+  bool fp32;
+  int32_t* status;
+};
+cudaError_t gemv_launch(const GemvArgs& a, cudaStream_t st);
+
 }  // namespace nvfp4
