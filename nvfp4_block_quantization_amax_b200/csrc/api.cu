@@ -618,7 +618,7 @@ nvfp4_status_t nvfp4_gemv(const void* x, int64_t ldx, const int32_t* ids, int64_
                           int64_t ldo, int32_t* status, void* stream) {
   if (out_dtype != NVFP4_OUT_DTYPE_BF16 && out_dtype != NVFP4_OUT_DTYPE_FP32) return NVFP4_ERR_ARG;
   if (P < 0 || P > 1024 || rep < 1 || rep > 1024 || E < 1 || E > nvfp4::kMaxGroups || (!ids && E != 1)) return NVFP4_ERR_SHAPE;
-  if (N <= 0 || K <= 0 || N % 128 || K % 64 || ldo < N || N >= kMost || K >= kMost) return NVFP4_ERR_SHAPE;
+  if (N <= 0 || K <= 0 || N % 128 || K % 64 || ldo < N || N > (int64_t(1) << 25) || K >= kMost) return NVFP4_ERR_SHAPE;
   if (P == 0) return NVFP4_OK;
   if (!W || !sW || !alphaW || !out) return NVFP4_ERR_ARG;
   const nvfp4_status_t chk = check_rows(x, ldx, K);

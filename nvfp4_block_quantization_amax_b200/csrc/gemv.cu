@@ -19,15 +19,19 @@
 // A CTA takes 32 weight rows, 8 b + g and 32, 64, 96 further of a 128-row
 // atom: with that choice 16 bytes of the scale layout hold the scales of a
 // lane's four rows.  Its 8 warps share out K; their sums are added in order.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "launch.cuh"
 #include "nvfp4_internal.h"
+
+namespace cg = cooperative_groups;
 
 namespace nvfp4 {
 namespace {
@@ -49,15 +53,14 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Two E4M3 bytes as bf16 pairs (each in both halves), times 2^118.
-__device__ __forceinline__ void scale_pairs(uint32_t two, uint32_t* s) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(two)));
-  const __half2 v = *reinterpret_cast<const __half2*>(&h);
-  const __nv_bfloat162 lo = __float2bfloat162_rn(__low2float(v) * 0x1p118f);
-  const __nv_bfloat162 hi = __float2bfloat162_rn(__high2float(v) * 0x1p118f);
-  s[0] = *reinterpret_cast<const uint32_t*>(&lo);
-  s[1] = *reinterpret_cast<const uint32_t*>(&hi);
+// Two E4M3 bytes of a word, picked by a byte selector, as bf16 pairs (each in
+// both halves) times 2^118: a byte's bits e e e e, m m m at a bf16's bits 10 .. 7,
+// 6 .. 4 are Delta 2^-120, denormals included.
+__device__ __forceinline__ void scale_pairs(uint32_t word, uint32_t pick, uint32_t* s) {
+  constexpr uint32_t up = 0x7B007B00u;   // 2^119 twice
+  const uint32_t v = mul2(mul2(__byte_perm(word, 0u, pick) << 4, up), up);
+  s[0] = __byte_perm(v, v, 0x1010);
+  s[1] = __byte_perm(v, v, 0x3232);
 }
 
 // The eight codes of a word times their scale: pairs (0, 4), (1, 5), (2, 6), (3, 7).
@@ -69,149 +72,265 @@ __device__ __forceinline__ void decode(uint32_t w, uint32_t s, uint32_t* q) {
   q[3] = mul2(((v & 0x00F000F0u) * 0x0104u) & 0x81C081C0u, s);
 }
 
-struct Weights {   // of one lane and 128 values of K
-  uint4 code[4];   // rows 32 i + 8 b + g
-  uint4 scale;
+__device__ const uint4 kNothing[4] = {};
+
+// Codes and scales of one lane and 128 values of K: four rows' 16 bytes and
+// the 16 bytes with their scales.
+constexpr int kPieces = 5;
+
+__device__ __forceinline__ void copy16(uint4* to, const uint8_t* from, bool real) {
+  const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(real ? 16 : 0) : "memory");
+}
+
+// Pairs sorted by expert and cut into slots of at most kGroup pairs of one expert.
+struct Slots {
+  short pairs[1024];            // in the order of their experts
+  short begin[1026];            // where an expert's begin
+  short expert[1024], pass[1024];   // of a slot
+  int counts[1024];
+  int scan[2][kWarps];
+  int number;
 };
 
-// NT: groups of eight x rows at a time.
-template <int NT, typename Out>
-__global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvArgs a) {
-  __shared__ float part[kWarps][NT * 8][kTileRows + 1];
-  __shared__ int list[1024];            // pairs of this CTA's expert
-  __shared__ uint32_t used[32];         // experts that occur
-  __shared__ int counts[kWarps], found;
-  pdl_entry();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  const int P = static_cast<int>(a.P);
-  const int64_t N = a.N, K = a.K;
-  const int64_t atom = blockIdx.x >> 2, quarter = blockIdx.x & 3;
-  Out* const out = static_cast<Out*>(a.out);
-  int expert = 0, members = P;
-  if (a.ids) {
-    // the blockIdx.y-th expert that occurs, and its pairs in order
-    if (tid < 32) used[tid] = 0u;
-    if (tid == 0) found = -1;
-    __syncthreads();
-    for (int p = tid; p < P; p += kThreads) {
-      const int id = __ldg(a.ids + p);
-      if (id >= 0 && id < a.E) atomicOr(&used[id >> 5], 1u << (id & 31));
-      else if (id != -1 && a.status) *a.status = kStatusArg;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      const uint32_t bits = used[lane];
-      int upto = __popc(bits);
+// Fill the tables, with all threads; ends with a barrier.  The number of slots.
+template <int kGroup>
+__device__ __forceinline__ int find_slots(const GemvArgs& a, Slots& t, bool report) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = static_cast<int>(a.P), E = static_cast<int>(a.E);
+  for (int e = tid; e < E; e += kThreads) t.counts[e] = 0;
+  __syncthreads();
+  for (int p = tid; p < P; p += kThreads) {
+    const int id = __ldg(a.ids + p);
+    if (id >= 0 && id < E) atomicAdd(&t.counts[id], 1);
+    else if (id != -1 && report && a.status) *a.status = kStatusArg;
+  }
+  __syncthreads();
+  // where an expert's pairs and slots begin: four experts a thread
+  int n[4], pairs = 0, passes = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      const int skip = static_cast<int>(blockIdx.y) - (upto - __popc(bits));
-      if (skip >= 0 && skip < __popc(bits)) {
-        uint32_t rest = bits;
-        for (int i = 0; i < skip; ++i) rest &= rest - 1u;
-        found = lane * 32 + __ffs(rest) - 1;
-      }
-    }
-    __syncthreads();
-    expert = found;
-    // rows of pairs without an expert are zeros
-    if (blockIdx.y == 0)
-      for (int p = warp; p < P; p += kWarps) {
-        const int id = __ldg(a.ids + p);
-        if (id < 0 || id >= a.E) out[p * a.ldo + atom * 128 + (lane >> 3) * 32 + quarter * 8 + (lane & 7)] = Out(0.0f);
-      }
-    if (expert < 0) return;
-    members = 0;
-    for (int p0 = 0; p0 < P; p0 += kThreads) {
-      const int p = p0 + tid;
-      const bool is = p < P && __ldg(a.ids + p) == expert;
-      const unsigned vote = __ballot_sync(0xFFFFFFFFu, is);
-      if (lane == 0) counts[warp] = __popc(vote);
-      __syncthreads();
-      int at = members;
-      for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) at += counts[i];
-        members += counts[i];
-      }
-      if (is) list[at + __popc(vote & ((1u << lane) - 1u))] = p;
-      __syncthreads();
+  for (int i = 0; i < 4; ++i) {
+    const int e = tid * 4 + i;
+    n[i] = e < E ? t.counts[e] : 0;
+    pairs += n[i];
+    passes += (n[i] + kGroup - 1) / kGroup;
+  }
+  int up = pairs, us = passes;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int vp = __shfl_up_sync(0xFFFFFFFFu, up, o), vs = __shfl_up_sync(0xFFFFFFFFu, us, o);
+    if (lane >= o) {
+      up += vp;
+      us += vs;
     }
   }
-
-  const int64_t row0 = atom * 128 + quarter * 8 + g;
-  const uint8_t* const codes = a.W + (expert * N + row0) * (K / 2) + c * 16;
-  const uint8_t* const scales = a.sW + (expert * N * (K / 16)) + (atom * (K / 64) + (c >> 1)) * 512 + (quarter * 8 + g) * 16;
-  const float alpha = __ldg(a.alphaW + expert);
-  const int chunks = static_cast<int>((K + 127) / 128);
-
-  auto fetch = [&](int kc, Weights& w) {
-    if (kc < chunks && kc * 128 + c * 32 < K) {
+  if (lane == 31) {
+    t.scan[0][warp] = up;
+    t.scan[1][warp] = us;
+  }
+  __syncthreads();
+  int p0 = up - pairs, s0 = us - passes;
+  for (int i = 0; i < warp; ++i) {
+    p0 += t.scan[0][i];
+    s0 += t.scan[1][i];
+  }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w.code[i] = __ldg(reinterpret_cast<const uint4*>(codes + i * 32 * (K / 2) + kc * 64));
-      w.scale = __ldg(reinterpret_cast<const uint4*>(scales + static_cast<int64_t>(kc) * 1024));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w.code[i] = make_uint4(0u, 0u, 0u, 0u);
-      w.scale = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < 4; ++i) {
+    const int e = tid * 4 + i;
+    if (e >= E) break;
+    t.begin[e] = static_cast<short>(p0);
+    t.counts[e] = p0;   // where its next pair goes
+    p0 += n[i];
+    for (int m = 0; m * kGroup < n[i]; ++m, ++s0) {
+      t.expert[s0] = static_cast<short>(e);
+      t.pass[s0] = static_cast<short>(m);
     }
-  };
+    if (e == E - 1) {
+      t.begin[E] = static_cast<short>(p0);
+      t.number = s0;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // an expert's pairs in order: every CTA cuts them into the same slots
+    for (int p = lane; p < (P + 31) / 32 * 32; p += 32) {
+      const int id = p < P ? __ldg(a.ids + p) : -1;
+      const bool is = id >= 0 && id < E;
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, is ? id : -1);
+      if (is) t.pairs[t.counts[id] + __popc(same & ((1u << lane) - 1u))] = static_cast<short>(p);
+      __syncwarp();
+      if (is && lane == __ffs(same) - 1) t.counts[id] += __popc(same);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  return t.number;
+}
 
-  for (int m0 = 0; m0 < members; m0 += NT * 8) {
+// Zeros in the rows of pairs without an expert; CTA `me` of `crowd` takes its
+// share of the tiles of `rows` columns.
+template <int rows, typename Out>
+__device__ __forceinline__ void clear_rows(const GemvArgs& a, Out* out, int me, int crowd) {
+  const int lane = threadIdx.x & 31, P = static_cast<int>(a.P);
+  for (int p = threadIdx.x >> 5; p < P; p += kWarps) {
+    const int id = __ldg(a.ids + p);
+    if (id >= 0 && id < a.E) continue;
+    for (int64_t tile = me; tile < a.N / rows; tile += crowd)
+      for (int i = lane; i < rows; i += 32) out[p * a.ldo + tile * rows + i] = Out(0.0f);
+  }
+}
+
+template <int NT>
+struct GemvCfg {
+  static constexpr int kDepth = NT == 1 ? 2 : NT == 2 ? 3 : 6;      // chunks of a lane on their way and in use
+  static constexpr int kCtas = NT == 1 ? 3 : NT == 2 ? 2 : 1;       // per SM
+  static constexpr int kParts = NT <= 2 ? 2 : 1;      // copies of the warps' sums
+  struct Smem {
+    uint4 ring[kDepth][kPieces][kThreads];            // every thread copies and reads its own pieces
+    float part[kParts][kWarps][NT * 8][kTileRows + 1];
+    float share[2][NT * 8][kTileRows];                // this CTA's sums, read by its cluster
+    Slots slots;
+  };
+};
+
+// A CTA (a cluster of `ranks` CTAs that share out K) takes a run of items: an
+// item is 32 weight rows for up to 8 NT pairs of one expert, a slot.  Weights
+// stream through a ring of shared memory that every thread fills for itself,
+// across the items' borders.
+template <int NT, typename Out>
+__global__ void __launch_bounds__(kThreads, GemvCfg<NT>::kCtas) gemv_kernel(const __grid_constant__ GemvArgs a) {
+  using Cfg = GemvCfg<NT>;
+  constexpr int kDepth = Cfg::kDepth, kGroup = NT * 8;
+  extern __shared__ __align__(16) uint8_t gemv_smem[];
+  typename Cfg::Smem& sm = *reinterpret_cast<typename Cfg::Smem*>(gemv_smem);
+  pdl_entry();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int P = static_cast<int>(a.P);
+  const int64_t N = a.N, K = a.K;
+  const int tiles = static_cast<int>(N / kTileRows);
+  Out* const out = static_cast<Out*>(a.out);
+  int slots = (P + kGroup - 1) / kGroup;
+  if (a.ids) {
+    slots = find_slots<kGroup>(a, sm.slots, rank == 0);
+    if (rank == 0) clear_rows<kTileRows>(a, out, blockIdx.x / ranks, gridDim.x / ranks);
+  }
+
+  // items are counted in 32 bits: at most 1024 slots and 2^20 tiles
+  const uint32_t crowd = gridDim.x / ranks, me = blockIdx.x / ranks, items = static_cast<uint32_t>(slots) * tiles;
+  const uint32_t each = items / crowd, more = items % crowd;
+  const uint32_t first = me * each + min(me, more);
+  uint32_t left = each + (me < more);
+  const int chunks = static_cast<int>((K + 127) / 128);
+  const int stride = kWarps * ranks, start = rank * kWarps + warp;
+  const int mine = chunks > start ? (chunks - start + stride - 1) / stride : 0;   // chunks of this warp and an item
+  const uint32_t pick = c & 1 ? 0x4342u : 0x4140u;                                // this lane's two scales of four
+  const bool tail = c * 32 + (chunks - 1) * 128 < K;                              // this lane has values in the last chunk
+
+  // the ring's filling end; an item is (slot, tile)
+  uint32_t f_left = left;
+  int f_slot = static_cast<int>(first / tiles), f_tile = static_cast<int>(first) - f_slot * tiles;
+  int tile = f_tile, slot = f_slot;
+  int f_chunk = 0, f_stage = 0;
+  const uint8_t *f_codes = nullptr, *f_scales = nullptr;
+  auto aim = [&]() {
+    const int64_t e = a.ids ? sm.slots.expert[f_slot] : 0;
+    const int64_t row = (f_tile >> 2) * 128ll + (f_tile & 3) * 8 + g;
+    f_codes = a.W + (e * N + row) * (K / 2) + start * 64 + c * 16;
+    f_scales = a.sW + e * N * (K / 16) + ((f_tile >> 2) * (K / 64) + start * 2 + (c >> 1)) * 512 + ((f_tile & 3) * 8 + g) * 16;
+  };
+  auto fill = [&]() {
+    if (f_left && mine) {
+      const bool real = tail || f_chunk + 1 < mine || start + f_chunk * stride + 1 < chunks;
+      const uint8_t* const codes = real ? f_codes : a.W;
+      const int64_t apart = real ? 16 * K : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) copy16(&sm.ring[f_stage][i][tid], codes + i * apart, real);
+      copy16(&sm.ring[f_stage][4][tid], real ? f_scales : a.sW, real);
+      f_codes += stride * 64;
+      f_scales += stride * 1024;
+      if (++f_chunk == mine) {
+        f_chunk = 0;
+        if (++f_tile == tiles) {
+          f_tile = 0;
+          ++f_slot;
+        }
+        if (--f_left) aim();
+      }
+      f_stage = f_stage + 1 == kDepth ? 0 : f_stage + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (left) aim();
+#pragma unroll
+  for (int s = 0; s < kDepth - 1; ++s) fill();
+
+  int use = 0, turn = 0;
+  for (; left; --left, turn ^= 1) {
+    const int e = a.ids ? sm.slots.expert[slot] : 0;
+    const int m0 = a.ids ? sm.slots.begin[e] + sm.slots.pass[slot] * kGroup : slot * kGroup;
+    const int members = min((a.ids ? sm.slots.begin[e + 1] : P) - m0, kGroup);
+    // columns without a pair read the first one's row; their sums are dropped
     const __nv_bfloat16* x[NT];
-    bool has[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int m = m0 + i * 8 + g;
-      has[i] = m < members;
-      const int64_t p = !has[i] ? 0 : a.ids ? list[m] : m;
-      x[i] = a.x + p / a.rep * a.ldx + c * 32;
+      const int m = m0 + (i * 8 + g < members ? i * 8 + g : 0);
+      const uint32_t p = a.ids ? sm.slots.pairs[m] : m;
+      x[i] = a.x + static_cast<int64_t>(p / static_cast<uint32_t>(a.rep)) * a.ldx + start * 128 + c * 32;
     }
     float acc[NT][2][4] = {};
-    constexpr int kDepth = 3;
-    Weights w[kDepth];
+    for (int j = 0, kc = start; j < mine; ++j, kc += stride) {
+      if (!tail && kc + 1 == chunks) {   // nothing here: no number in x's place may meet the zero weights
 #pragma unroll
-    for (int s = 0; s < kDepth - 1; ++s) fetch(warp + s * kWarps, w[s]);
-    for (int kc0 = warp; kc0 < chunks; kc0 += kWarps * kDepth) {
+        for (int i = 0; i < NT; ++i) x[i] = reinterpret_cast<const __nv_bfloat16*>(kNothing);
+      }
+      fill();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+      uint32_t u[4][4];
 #pragma unroll
-      for (int s = 0; s < kDepth; ++s) {
-        const int kc = kc0 + s * kWarps;
-        fetch(kc + (kDepth - 1) * kWarps, w[(s + kDepth - 1) % kDepth]);
-        if (kc >= chunks) continue;
-        const bool inside = kc * 128 + c * 32 < K;
-        uint32_t sc[4][2];
-        const uint32_t sw[4] = {w[s].scale.x, w[s].scale.y, w[s].scale.z, w[s].scale.w};
+      for (int i = 0; i < 4; ++i) {
+        const uint4 w = sm.ring[use][i][tid];
+        u[i][0] = w.x;
+        u[i][1] = w.y;
+        u[i][2] = w.z;
+        u[i][3] = w.w;
+      }
+      const uint4 sw = sm.ring[use][4][tid];
+      use = use + 1 == kDepth ? 0 : use + 1;
+      uint32_t sc[4][2];
+      scale_pairs(sw.x, pick, sc[0]);
+      scale_pairs(sw.y, pick, sc[1]);
+      scale_pairs(sw.z, pick, sc[2]);
+      scale_pairs(sw.w, pick, sc[3]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) scale_pairs(c & 1 ? sw[i] >> 16 : sw[i] & 0xFFFFu, sc[i]);
+      for (int word = 0; word < 4; ++word) {
+        uint32_t b[NT][4];
 #pragma unroll
-        for (int word = 0; word < 4; ++word) {
-          uint32_t q[4][4];
+        for (int i = 0; i < NT; ++i) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(x[i]) + word);
+          b[i][0] = __byte_perm(v.x, v.z, 0x5410);
+          b[i][1] = __byte_perm(v.x, v.z, 0x7632);
+          b[i][2] = __byte_perm(v.y, v.w, 0x5410);
+          b[i][3] = __byte_perm(v.y, v.w, 0x7632);
+        }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t u[4] = {w[s].code[i].x, w[s].code[i].y, w[s].code[i].z, w[s].code[i].w};
-            decode(u[word], sc[i][word >> 1], q[i]);
-          }
+        for (int m = 0; m < 2; ++m) {
+          uint32_t lo[4], hi[4];
+          decode(u[2 * m][word], sc[2 * m][word >> 1], lo);
+          decode(u[2 * m + 1][word], sc[2 * m + 1][word >> 1], hi);
+          const uint32_t op0[4] = {lo[0], hi[0], lo[1], hi[1]}, op1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (inside && has[i]) v = __ldg(reinterpret_cast<const uint4*>(x[i] + kc * 128 + word * 8));
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint32_t lo = half ? v.y : v.x, hi = half ? v.w : v.z;
-              const uint32_t b0 = __byte_perm(lo, hi, 0x5410), b1 = __byte_perm(lo, hi, 0x7632);
-#pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                const uint32_t op[4] = {q[2 * m][2 * half], q[2 * m + 1][2 * half], q[2 * m][2 * half + 1],
-                                        q[2 * m + 1][2 * half + 1]};
-                mma16(acc[i][m], op, b0, b1);
-              }
-            }
+            mma16(acc[i][m], op0, b[i][0], b[i][1]);
+            mma16(acc[i][m], op1, b[i][2], b[i][3]);
           }
         }
       }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) x[i] += stride * 128;
     }
-    __syncthreads();   // part is read until here in the round before
+    auto& part = sm.part[Cfg::kParts == 2 ? turn : 0];
+    if (Cfg::kParts == 1) __syncthreads();   // read until here in the item before
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -221,30 +340,257 @@ __global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvArgs a) {
           // weight row: 32 (2 m + h / 2) + g; x row 2 c + h % 2 of the group
           part[warp][i * 8 + 2 * c + (h & 1)][(2 * m + (h >> 1)) * 8 + g] = acc[i][m][h];
     __syncthreads();
-    for (int v = tid; v < NT * 8 * kTileRows; v += kThreads) {
+    const float alpha = __ldg(a.alphaW + e);
+    const int64_t n0 = (tile >> 2) * 128ll + (tile & 3) * 8;
+    for (int v = tid; v < members * kTileRows; v += kThreads) {
       const int m = v / kTileRows, r = v % kTileRows;
-      if (m0 + m >= members) break;
       float s = 0.0f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) s += part[i][m][r];
-      const int64_t p = a.ids ? list[m0 + m] : m0 + m;
-      out[p * a.ldo + atom * 128 + (r >> 3) * 32 + quarter * 8 + (r & 7)] = Out(s * 256.0f * alpha);
+      if (ranks > 1) {
+        sm.share[turn][m][r] = s;
+      } else {
+        const int64_t p = a.ids ? sm.slots.pairs[m0 + m] : m0 + m;
+        out[p * a.ldo + n0 + (r >> 3) * 32 + (r & 7)] = Out(s * 256.0f * alpha);
+      }
+    }
+    if (ranks > 1) {
+      cluster.sync();   // share is complete; the other copy has been read by all
+      for (int v = rank * kThreads + tid; v < members * kTileRows; v += ranks * kThreads) {
+        const int m = v / kTileRows, r = v % kTileRows;
+        float s = 0.0f;
+        for (int i = 0; i < ranks; ++i) s += cluster.map_shared_rank(&sm.share[turn][m][r], i)[0];
+        const int64_t p = a.ids ? sm.slots.pairs[m0 + m] : m0 + m;
+        out[p * a.ldo + n0 + (r >> 3) * 32 + (r & 7)] = Out(s * 256.0f * alpha);
+      }
+    }
+    if (++tile == tiles) {
+      tile = 0;
+      ++slot;
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (ranks > 1) cluster.sync();   // no CTA leaves while its share is read
 }
 
+// ---------------------------------------------------------------------------
+// More rows.  x is as large as the weight's rows that share it, so a CTA takes a
+// whole 128-row atom: warp w its quarter w % 4 and, of each 256 values of K, half
+// w / 4; x comes once per CTA, through shared memory.  One item per cluster of
+// `ranks` CTAs, which share out K.
+// ---------------------------------------------------------------------------
 template <int NT>
-cudaError_t launch_nt(const GemvArgs& a, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(a.N / kTileRows), static_cast<unsigned>(a.ids ? std::min(a.P, a.E) : 1));
+struct WideCfg {
+  static constexpr int kDepth = 3;   // stages of 256 values of K
+  struct Stage {
+    uint4 w[kPieces][kThreads];      // every thread copies and reads its own
+    uint4 x[2][NT * 8][16];          // half, row: 16 bytes of word v of lane c at 4 c + (v + c + row) % 4
+  };
+  struct Smem {
+    union {
+      Stage ring[kDepth];
+      float share[2][NT * 8][129];   // sums of the halves, read by the cluster
+    };
+    Slots slots;
+  };
+};
+
+template <int NT, typename Out>
+__global__ void __launch_bounds__(kThreads, 2) gemv_wide_kernel(const __grid_constant__ GemvArgs a) {
+  using Cfg = WideCfg<NT>;
+  constexpr int kDepth = Cfg::kDepth, kGroup = NT * 8;
+  extern __shared__ __align__(16) uint8_t gemv_smem[];
+  typename Cfg::Smem& sm = *reinterpret_cast<typename Cfg::Smem*>(gemv_smem);
+  pdl_entry();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3, part = warp >> 2;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int64_t N = a.N, K = a.K;
+  const int atoms = static_cast<int>(N / 128);
+  const int item = blockIdx.x / ranks, slot = item / atoms, atom = item - slot * atoms;
+  Out* const out = static_cast<Out*>(a.out);
+  int slots = (static_cast<int>(a.P) + kGroup - 1) / kGroup;
+  if (a.ids) {
+    slots = find_slots<kGroup>(a, sm.slots, rank == 0);
+    if (rank == 0 && slot == 0) clear_rows<128>(a, out, atom, atoms);
+  }
+  if (slot >= slots) return;   // the whole cluster
+  const int64_t e = a.ids ? sm.slots.expert[slot] : 0;
+  const int m0 = a.ids ? sm.slots.begin[e] + sm.slots.pass[slot] * kGroup : slot * kGroup;
+  const int members = min((a.ids ? sm.slots.begin[e + 1] : static_cast<int>(a.P)) - m0, kGroup);
+  const int stages = static_cast<int>((K + 255) / 256);
+  const int from = static_cast<int>(static_cast<int64_t>(stages) * rank / ranks), to = static_cast<int>(static_cast<int64_t>(stages) * (rank + 1) / ranks);
+
+  const int row0 = (warp & 3) * 8 + g;   // of the atom; its others 32, 64, 96 further
+  const uint8_t* codes = a.W + (e * N + atom * 128ll + row0) * (K / 2) + (from * 2ll + part) * 64 + c * 16;
+  const uint8_t* scales = a.sW + e * N * (K / 16) + (atom * (K / 64) + (from * 2ll + part) * 2 + (c >> 1)) * 512 + row0 * 16;
+  // copied by this thread: piece `lane` of rows warp, warp + 8, ..; rows behind
+  // the last pair's are copies of the first, and their sums are dropped
+  const __nv_bfloat16* x[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int m = m0 + (i * 8 + warp < members ? i * 8 + warp : 0);
+    const uint32_t p = a.ids ? sm.slots.pairs[m] : m;
+    x[i] = a.x + static_cast<int64_t>(p / static_cast<uint32_t>(a.rep)) * a.ldx + from * 256ll + lane * 8;
+  }
+  const int x_at = ((lane & 15) & ~3) + ((lane + ((lane & 15) >> 2) + warp) & 3);   // rows i * 8 + warp: (row) % 4 = warp % 4
+
+  int fill = from, f_stage = 0;
+  auto copy = [&]() {
+    if (fill < to) {
+      typename Cfg::Stage& st = sm.ring[f_stage];
+      const bool real = fill * 256ll + part * 128 + c * 32 < K, x_real = fill * 256ll + lane * 8 < K;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) copy16(&st.w[i][tid], real ? codes + i * 16 * K : a.W, real);
+      copy16(&st.w[4][tid], real ? scales : a.sW, real);
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        copy16(&st.x[lane >> 4][i * 8 + warp][x_at], reinterpret_cast<const uint8_t*>(x_real ? x[i] : a.x), x_real);
+      codes += 128;
+      scales += 2048;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) x[i] += 256;
+      ++fill;
+      f_stage = f_stage + 1 == kDepth ? 0 : f_stage + 1;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < kDepth - 1; ++s) copy();
+
+  const uint32_t pick = c & 1 ? 0x4342u : 0x4140u;
+  float acc[NT][2][4] = {};
+  int use = 0;
+  for (int s = from; s < to; ++s) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+    __syncthreads();   // everyone's copies are here; the stage before is free
+    copy();
+    const typename Cfg::Stage& st = sm.ring[use];
+    use = use + 1 == kDepth ? 0 : use + 1;
+    uint32_t u[4][4], sc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 w = st.w[i][tid];
+      u[i][0] = w.x;
+      u[i][1] = w.y;
+      u[i][2] = w.z;
+      u[i][3] = w.w;
+    }
+    const uint4 sw = st.w[4][tid];
+    scale_pairs(sw.x, pick, sc[0]);
+    scale_pairs(sw.y, pick, sc[1]);
+    scale_pairs(sw.z, pick, sc[2]);
+    scale_pairs(sw.w, pick, sc[3]);
+#pragma unroll
+    for (int word = 0; word < 4; ++word) {
+      uint32_t b[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const uint4 v = st.x[part][i * 8 + g][4 * c + ((word + c + g) & 3)];
+        b[i][0] = __byte_perm(v.x, v.z, 0x5410);
+        b[i][1] = __byte_perm(v.x, v.z, 0x7632);
+        b[i][2] = __byte_perm(v.y, v.w, 0x5410);
+        b[i][3] = __byte_perm(v.y, v.w, 0x7632);
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        uint32_t lo[4], hi[4];
+        decode(u[2 * m][word], sc[2 * m][word >> 1], lo);
+        decode(u[2 * m + 1][word], sc[2 * m + 1][word >> 1], hi);
+        const uint32_t op0[4] = {lo[0], hi[0], lo[1], hi[1]}, op1[4] = {lo[2], hi[2], lo[3], hi[3]};
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          mma16(acc[i][m], op0, b[i][0], b[i][1]);
+          mma16(acc[i][m], op1, b[i][2], b[i][3]);
+        }
+      }
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();   // the ring becomes share
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        sm.share[part][i * 8 + 2 * c + (h & 1)][(2 * m + (h >> 1)) * 32 + row0] = acc[i][m][h];
+  if (ranks > 1) cluster.sync();
+  else __syncthreads();
+  const float alpha = __ldg(a.alphaW + e);
+  for (int v = rank * kThreads + tid; v < members * 128; v += ranks * kThreads) {
+    const int m = v >> 7, r = v & 127;
+    float sum = 0.0f;
+    for (int i = 0; i < ranks; ++i) {
+      const float* const from_rank = ranks > 1 ? cluster.map_shared_rank(&sm.share[0][m][r], i) : &sm.share[0][m][r];
+      sum += from_rank[0];
+      sum += from_rank[NT * 8 * 129];
+    }
+    const int64_t p = a.ids ? sm.slots.pairs[m0 + m] : m0 + m;
+    out[p * a.ldo + atom * 128ll + r] = Out(sum * 256.0f * alpha);
+  }
+  if (ranks > 1) cluster.sync();   // no CTA leaves while its share is read
+}
+
+// The dynamic shared memory of a kernel, asked for once per device.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done.load(std::memory_order_relaxed) >> dev & 1)) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  return e;
+}
+
+template <typename Out>
+cudaError_t launch_narrow(const GemvArgs& a, cudaStream_t st) {
+  using Cfg = GemvCfg<1>;
+  constexpr size_t smem = sizeof(typename Cfg::Smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(gemv_kernel<1, Out>, smem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t slots = a.ids ? std::min(a.P, a.E) : (a.P + 7) / 8;
+  const int64_t items = slots * (a.N / kTileRows), chunks = (a.K + 127) / 128;
+  const int64_t room = static_cast<int64_t>(sm_count()) * Cfg::kCtas;
+  int ranks = 1;
+  while (ranks < 8 && items * ranks * 2 <= room && chunks >= 2 * ranks * kWarps) ranks *= 2;
+  const int64_t crowd = std::max<int64_t>(1, std::min(items, room / ranks));
   note_launch();
-  return a.fp32 ? launch_k(gemv_kernel<NT, float>, grid, dim3(kThreads), 0, st, 1, a)
-                : launch_k(gemv_kernel<NT, __nv_bfloat16>, grid, dim3(kThreads), 0, st, 1, a);
+  return launch_k(gemv_kernel<1, Out>, dim3(static_cast<unsigned>(crowd * ranks)), dim3(kThreads), smem, st,
+                  static_cast<unsigned>(ranks), a);
+}
+
+template <int NT, typename Out>
+cudaError_t launch_wide(const GemvArgs& a, cudaStream_t st) {
+  constexpr size_t smem = sizeof(typename WideCfg<NT>::Smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(gemv_wide_kernel<NT, Out>, smem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t full = (a.P + NT * 8 - 1) / (NT * 8);
+  const int64_t slots = a.ids ? std::min(a.P, full + std::min(a.P, a.E) - 1) : full;
+  const int64_t items = slots * (a.N / 128), stages = (a.K + 255) / 256;
+  const int64_t room = static_cast<int64_t>(sm_count()) * 2;
+  int ranks = 1;
+  while (ranks < 8 && items * ranks * 2 <= room && stages >= 4 * ranks) ranks *= 2;
+  note_launch();
+  return launch_k(gemv_wide_kernel<NT, Out>, dim3(static_cast<unsigned>(items * ranks)), dim3(kThreads), smem, st,
+                  static_cast<unsigned>(ranks), a);
+}
+
+template <typename Out>
+cudaError_t launch_out(const GemvArgs& a, cudaStream_t st) {
+  const int64_t rows = a.ids ? std::max<int64_t>(1, a.P / std::min(a.P, a.E) * 2) : a.P;   // likely ones of a weight
+  return rows <= 8    ? launch_narrow<Out>(a, st)
+         : rows <= 16 ? launch_wide<2, Out>(a, st)
+         : rows <= 24 ? launch_wide<3, Out>(a, st)
+                      : launch_wide<4, Out>(a, st);
 }
 
 }  // namespace
 
 cudaError_t gemv_launch(const GemvArgs& a, cudaStream_t st) {
-  return a.P <= 8 ? launch_nt<1>(a, st) : a.P <= 16 ? launch_nt<2>(a, st) : launch_nt<4>(a, st);
+  return a.fp32 ? launch_out<float>(a, st) : launch_out<__nv_bfloat16>(a, st);
 }
 
 }  // namespace nvfp4

@@ -87,7 +87,7 @@ def test_combine_backward_refusals(kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dt=2), -1), (dict(P=-1), -2), (dict(P=1025), -2), (dict(rep=0), -2), (dict(E=0), -2), (dict(E=1025), -2),
-    (dict(ids=None), -2), (dict(N=64, ldo=64), -2), (dict(N=0), -2), (dict(K=96), -2), (dict(K=0), -2), (dict(ldo=64), -2),
+    (dict(ids=None), -2), (dict(N=64, ldo=64), -2), (dict(N=0), -2), (dict(N=(1 << 25) + 128, ldo=1 << 26), -2), (dict(K=96), -2), (dict(K=0), -2), (dict(ldo=64), -2),
     (dict(x=None), -1), (dict(W=None), -1), (dict(sW=None), -1), (dict(alpha=None), -1), (dict(out=None), -1),
     (dict(x=FAKE + 8), -3), (dict(ldx=64), -2), (dict(ldx=132), -3), (dict(W=FAKE + 8), -3), (dict(sW=FAKE + 4), -3),
     (dict(alpha=FAKE + 2), -3), (dict(ids=FAKE + 2), -3), (dict(status=FAKE + 2), -3), (dict(out=FAKE + 2), -3),
