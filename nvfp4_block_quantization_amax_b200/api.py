@@ -656,8 +656,23 @@ def nvfp4_lora_backward(dy: torch.Tensor, x: torch.Tensor, h: torch.Tensor, A: t
 
 # ---------------------------------------------------------------------------
 # Around the experts' products: routing, sorting rows by expert, the way back,
-# and products of a few unquantized rows.
+# and products of a few unquantized rows.  Their small calls are as long as
+# their host path: new tensors come from empty_strided (1.5 us, torch.empty
+# 2.3 us), tensors on another device than the current one take a second call
+# under that device instead of a context around the first, and the library's
+# functions are called without the names in _lib between.
 # ---------------------------------------------------------------------------
+def _elsewhere(device) -> bool:
+    """Whether `device`, which must be a GPU, is not the current one."""
+    if device.type != "cuda":
+        raise TypeError(f"the tensors must be CUDA tensors, not on {device}")
+    return _current_device is None or _current_device() != device.index
+
+
+def _new(rows: int, cols: int, dtype, device) -> torch.Tensor:
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
 def _pairs(t: torch.Tensor, dtype, what: str, device):
     """Shape (T, k) of a contiguous tensor of one value per token and choice."""
     if t.dim() != 2:
@@ -700,6 +715,9 @@ def nvfp4_route(logits: torch.Tensor, k: int, score: int = NVFP4_ROUTE_SOFTMAX, 
     with a logit of -inf are never chosen; -1 stands where none is left."""
     ldl, kind = _logits(logits, "logits")
     dev = logits.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_route(logits, k, score, flags, bias, groups, groups_kept, scale, ids, weights, status)
     T, E = logits.shape
     if bias is not None:
         _need(bias, E, torch.float32, "bias", dev)
@@ -707,15 +725,16 @@ def nvfp4_route(logits: torch.Tensor, k: int, score: int = NVFP4_ROUTE_SOFTMAX, 
         _like_pairs(ids, (T, k), torch.int32, "ids", dev)
     if weights is not None:
         _like_pairs(weights, (T, k), torch.float32, "weights", dev)
-    _check_status(status, dev)
-    with _guard(dev):
-        if ids is None:
-            ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-        if weights is None:
-            weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-        st = L.nvfp4_route(_p(logits), ldl, kind, _p(bias), T, E, k, groups, groups_kept, score, flags, scale, _p(ids),
-                           _p(weights), _p(status), _stream_of(dev))
-    _check(st, "nvfp4_route")
+    if status is not None:
+        _check_status(status, dev)
+    if ids is None:
+        ids = _new(T, k, torch.int32, dev)
+    if weights is None:
+        weights = _new(T, k, torch.float32, dev)
+    st = L.load().nvfp4_route(logits.data_ptr(), ldl, kind, _p(bias), T, E, k, groups, groups_kept, score, flags, scale,
+                              ids.data_ptr(), weights.data_ptr(), _p(status), _stream_of(dev))
+    if st:
+        _check(st, "nvfp4_route")
     return ids, weights
 
 
@@ -727,6 +746,9 @@ def nvfp4_route_backward(dweights: torch.Tensor, ids: torch.Tensor, logits: torc
     the forward call.  out may be the logits."""
     ldl, kind = _logits(logits, "logits")
     dev = logits.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_route_backward(dweights, ids, logits, score, flags, scale, out, status)
     T, E = logits.shape
     shape = _pairs(ids, torch.int32, "ids", dev)
     if shape[0] != T:
@@ -737,13 +759,14 @@ def nvfp4_route_backward(dweights: torch.Tensor, ids: torch.Tensor, logits: torc
         if out.dtype != logits.dtype or out.device != dev or out.shape != logits.shape:
             raise ValueError("out must have the logits' type, device and shape")
         ldd = _logits(out, "out")[0]
-    _check_status(status, dev)
-    with _guard(dev):
-        if out is None:
-            out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-        st = L.nvfp4_route_backward(_p(dweights), _p(ids), _p(logits), ldl, kind, T, E, shape[1], score, flags, scale,
-                                    _p(out), ldd, _p(status), _stream_of(dev))
-    _check(st, "nvfp4_route_backward")
+    if status is not None:
+        _check_status(status, dev)
+    if out is None:
+        out = _new(T, E, logits.dtype, dev)
+    st = L.load().nvfp4_route_backward(dweights.data_ptr(), ids.data_ptr(), logits.data_ptr(), ldl, kind, T, E, shape[1],
+                                       score, flags, scale, out.data_ptr(), ldd, _p(status), _stream_of(dev))
+    if st:
+        _check(st, "nvfp4_route_backward")
     return out
 
 
@@ -758,6 +781,9 @@ def nvfp4_dispatch(x: Optional[torch.Tensor], ids: torch.Tensor, E: int, out: Op
     if not ids.is_cuda:
         raise TypeError("ids must be a 2D int32 CUDA tensor")
     dev = ids.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_dispatch(x, ids, E, out, rows, offsets, status)
     T, k = _pairs(ids, torch.int32, "ids", dev)
     C = ldx = ldo = 8
     if x is not None:
@@ -773,17 +799,18 @@ def nvfp4_dispatch(x: Optional[torch.Tensor], ids: torch.Tensor, E: int, out: Op
         _like_pairs(rows, (T, k), torch.int32, "rows", dev)
     if offsets is not None:
         _need(offsets, E + 1, torch.int32, "offsets", dev)
-    _check_status(status, dev)
-    with _guard(dev):
-        if rows is None:
-            rows = torch.empty((T, k), dtype=torch.int32, device=dev)
-        if offsets is None:
-            offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        if x is not None and out is None:
-            out = torch.empty((T * k, C), dtype=torch.bfloat16, device=dev)
-        st = L.nvfp4_dispatch(_p(x), ldx, _p(ids), T, k, E, C, _p(out), ldo, _p(offsets), _p(rows), _p(status),
-                              _stream_of(dev))
-    _check(st, "nvfp4_dispatch")
+    if status is not None:
+        _check_status(status, dev)
+    if rows is None:
+        rows = _new(T, k, torch.int32, dev)
+    if offsets is None:
+        offsets = torch.empty_strided((max(E, 0) + 1,), (1,), dtype=torch.int32, device=dev)
+    if x is not None and out is None:
+        out = _new(T * k, C, torch.bfloat16, dev)
+    st = L.load().nvfp4_dispatch(_p(x), ldx, ids.data_ptr(), T, k, E, C, _p(out), ldo, offsets.data_ptr(), rows.data_ptr(),
+                                 _p(status), _stream_of(dev))
+    if st:
+        _check(st, "nvfp4_dispatch")
     return out, rows, offsets
 
 
@@ -811,18 +838,22 @@ def nvfp4_combine(y: torch.Tensor, rows: Optional[torch.Tensor], weights: Option
     if y.dtype != torch.bfloat16 or y.dim() != 2 or not y.is_cuda:
         raise TypeError("y must be a 2D bfloat16 CUDA tensor")
     dev = y.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_combine(y, rows, weights, residual, out, status)
     R, C = y.shape
     T, k = _places(rows, weights, dev)
     ldy = _rows(y, R, C, "y", dev)
     ldr = 0 if residual is None else _rows(residual, T, C, "residual", dev)
     ldo = C if out is None else _rows(out, T, C, "out", dev)
-    _check_status(status, dev)
-    with _guard(dev):
-        if out is None:
-            out = torch.empty((T, C), dtype=torch.bfloat16, device=dev)
-        st = L.nvfp4_combine(_p(y), ldy, R, _p(rows), _p(weights), T, k, C, _p(residual), ldr, _p(out), ldo, _p(status),
-                             _stream_of(dev))
-    _check(st, "nvfp4_combine")
+    if status is not None:
+        _check_status(status, dev)
+    if out is None:
+        out = _new(T, C, torch.bfloat16, dev)
+    st = L.load().nvfp4_combine(y.data_ptr(), ldy, R, _p(rows), _p(weights), T, k, C, _p(residual), ldr, out.data_ptr(), ldo,
+                                _p(status), _stream_of(dev))
+    if st:
+        _check(st, "nvfp4_combine")
     return out
 
 
@@ -836,6 +867,9 @@ def nvfp4_combine_backward(dout: torch.Tensor, rows: Optional[torch.Tensor], wei
     if dout.dtype != torch.bfloat16 or dout.dim() != 2 or not dout.is_cuda:
         raise TypeError("dout must be a 2D bfloat16 CUDA tensor")
     dev = dout.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_combine_backward(dout, rows, weights, y, need_dy, need_dweights, out, status)
     T, C = dout.shape
     shape = _places(rows, weights, dev)
     if shape[0] != T:
@@ -847,14 +881,15 @@ def nvfp4_combine_backward(dout: torch.Tensor, rows: Optional[torch.Tensor], wei
     if out is not None and not need_dy:
         raise ValueError("out without need_dy")
     lddy = C if out is None else _rows(out, R, C, "out", dev)
-    _check_status(status, dev)
-    with _guard(dev):
-        if need_dy and out is None:
-            out = torch.empty((R, C), dtype=torch.bfloat16, device=dev)
-        dw = torch.empty(shape, dtype=torch.float32, device=dev) if need_dweights else None
-        st = L.nvfp4_combine_backward(_p(dout), lddo, _p(y), ldy, R, _p(rows), _p(weights), T, shape[1], C, _p(out), lddy,
-                                      _p(dw), _p(status), _stream_of(dev))
-    _check(st, "nvfp4_combine_backward")
+    if status is not None:
+        _check_status(status, dev)
+    if need_dy and out is None:
+        out = _new(R, C, torch.bfloat16, dev)
+    dw = _new(shape[0], shape[1], torch.float32, dev) if need_dweights else None
+    st = L.load().nvfp4_combine_backward(dout.data_ptr(), lddo, y.data_ptr(), ldy, R, _p(rows), _p(weights), T, shape[1], C,
+                                         _p(out), lddy, _p(dw), _p(status), _stream_of(dev))
+    if st:
+        _check(st, "nvfp4_combine_backward")
     return out, dw
 
 
@@ -869,6 +904,9 @@ def nvfp4_gemv(x: torch.Tensor, W: torch.Tensor, sW: torch.Tensor, alphaW: torch
     if x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_cuda:
         raise TypeError("x must be a 2D bfloat16 CUDA tensor")
     dev = x.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return nvfp4_gemv(x, W, sW, alphaW, ids, out_dtype, out, status)
     X, K = x.shape
     if W.dim() != (2 if ids is None else 3) or 2 * W.shape[-1] != K:
         raise ValueError(f"W must be codes [{'' if ids is None else 'E, '}N, {K // 2}], not {tuple(W.shape)}")
@@ -886,13 +924,18 @@ def nvfp4_gemv(x: torch.Tensor, W: torch.Tensor, sW: torch.Tensor, alphaW: torch
     _need(W, E * N * (K // 2), torch.uint8, "W", dev)
     _need(sW, E * N * (K // 16), torch.uint8, "sW", dev)
     _need(alphaW, E, torch.float32, "alphaW", dev)
-    _check_status(status, dev)
+    if status is not None:
+        _check_status(status, dev)
     dt = torch.bfloat16 if out_dtype == NVFP4_OUT_DTYPE_BF16 else torch.float32
-    if out is not None:
+    ldo = N
+    if out is None:
+        out = _new(P, N, dt, dev)
+    else:
         _need_matrix(out, P, N, dt, "out", dev)
-    with _guard(dev):
-        y = out if out is not None else torch.empty((P, N), dtype=dt, device=dev)
-        st = L.nvfp4_gemv(_p(x), ldx, _p(ids), P, max(rep, 1), _p(W), _p(sW), _p(alphaW), E, N, K, _p(y), out_dtype,
-                          y.stride(0) if P > 1 else N, _p(status), _stream_of(dev))
-    _check(st, "nvfp4_gemv")
-    return y
+        if P > 1:
+            ldo = out.stride(0)
+    st = L.load().nvfp4_gemv(x.data_ptr(), ldx, _p(ids), P, rep or 1, W.data_ptr(), sW.data_ptr(), alphaW.data_ptr(), E, N, K,
+                             out.data_ptr(), out_dtype, ldo, _p(status), _stream_of(dev))
+    if st:
+        _check(st, "nvfp4_gemv")
+    return out

@@ -540,11 +540,8 @@ nvfp4_status_t nvfp4_dispatch(const void* x, int64_t ldx, const int32_t* ids, in
   if (!aligned(offsets, 4) || !aligned(ids, 4)) return NVFP4_ERR_ALIGN;
   if (T && x && ((chk = check_rows(x, ldx, C)) != NVFP4_OK || (chk = check_rows(xs, ldxs, C)) != NVFP4_OK)) return chk;
   if (x && x == xs) return NVFP4_ERR_ARG;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  chk = launch_status(nvfp4::sort_launch(ids, T * k, E, offsets, rows, status, st));
-  if (chk != NVFP4_OK || T == 0 || !x) return chk;
   nvfp4::RowArgs a{};
-  a.in = static_cast<const __nv_bfloat16*>(x);
+  a.in = T ? static_cast<const __nv_bfloat16*>(x) : nullptr;
   a.ldi = ldx;
   a.rows = rows;
   a.T = T;
@@ -553,7 +550,8 @@ nvfp4_status_t nvfp4_dispatch(const void* x, int64_t ldx, const int32_t* ids, in
   a.R = T * k;
   a.out = static_cast<__nv_bfloat16*>(xs);
   a.ldo = ldxs;
-  return launch_status(nvfp4::dispatch_rows_launch(a, st));
+  a.status = status;
+  return launch_status(nvfp4::dispatch_launch(a, ids, E, offsets, rows, static_cast<cudaStream_t>(stream)));
 }
 
 nvfp4_status_t nvfp4_combine(const void* y, int64_t ldy, int64_t R, const int32_t* rows, const float* weights, int64_t T,

@@ -30,7 +30,8 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 // ---------------------------------------------------------------------------
-// sort: one cluster; each warp takes a run of consecutive pairs
+// sort: one cluster; each warp takes a run of consecutive pairs, and counts
+// them while it notes each one's rank among its run's
 // ---------------------------------------------------------------------------
 constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
@@ -46,13 +47,27 @@ __device__ __forceinline__ int expert_of(const int32_t* __restrict__ ids, int64_
   return -1;
 }
 
+// Lanes with the same e, found bit by bit (match.any takes several times as long).
+template <int kBits>
+__device__ __forceinline__ unsigned same_as(int e) {
+  unsigned same = kAll;
+#pragma unroll
+  for (int b = 0; b < kBits; ++b) {
+    const bool one = e >> b & 1;
+    const unsigned v = __ballot_sync(kAll, one);
+    same &= one ? v : ~v;
+  }
+  return same;
+}
+
+template <int kBits>   // of E - 1
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(const int32_t* __restrict__ ids, int64_t P, int E,
-                                                            int32_t* __restrict__ offsets, int32_t* __restrict__ rows,
-                                                            int32_t* status) {
+                                                            int32_t* __restrict__ offsets, int32_t* rows, int32_t* status) {
   extern __shared__ int sort_smem[];
   pdl_entry();
-  int* const hist = sort_smem;                      // [warps][E]: counts, then where the warp's next pair goes
+  int* const hist = sort_smem;                      // [warps][E]: counts, then those of the warps before
   int* const total = sort_smem + kSortWarps * E;    // [E]: this CTA's counts, read by the cluster
+  int* const start = total + E;                     // [E]: where this CTA's pairs of an expert go
   __shared__ int warp_sum[kSortWarps];
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, rank = static_cast<int>(cluster.block_rank());
@@ -62,15 +77,31 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const int32_t* __res
   int* const mine = hist + w * E;
   for (int e = lane; e < E; e += 32) mine[e] = 0;
   __syncwarp();
-  for (int64_t p = from; p < to; p += 32) {
-    const int e = expert_of(ids, p + lane, P, E, status);
-    const unsigned same = __match_any_sync(kAll, e);
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
+  constexpr int kAhead = 4;
+  for (int64_t p0 = from; p0 < to; p0 += 32 * kAhead) {
+    int id[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t p = p0 + i * 32 + lane;
+      id[i] = expert_of(ids, p, to, E, status);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t p = p0 + i * 32 + lane;
+      const int e = id[i];
+      const unsigned same = same_as<kBits>(e) & __ballot_sync(kAll, e >= 0);
+      const unsigned before = same & ((1u << lane) - 1u);
+      const int at = e >= 0 ? mine[e] + __popc(before) : -1;
+      __syncwarp();
+      if (e >= 0 && !before) mine[e] += __popc(same);
+      __syncwarp();
+      if (p < to) rows[p] = at;
+    }
   }
   __syncthreads();
   if (tid < E) {
     int sum = 0;
+#pragma unroll 8
     for (int i = 0; i < kSortWarps; ++i) {
       const int v = hist[i * E + tid];
       hist[i * E + tid] = sum;
@@ -80,12 +111,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const int32_t* __res
   }
   cluster.sync();
   int all = 0, before = 0;
-  if (tid < E)
+  if (tid < E) {
+#pragma unroll
     for (int r = 0; r < kSortCtas; ++r) {
       const int v = cluster.map_shared_rank(total, r)[tid];
       before += r < rank ? v : 0;
       all += v;
     }
+  }
   int incl = all;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -101,17 +134,20 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const int32_t* __res
       offsets[tid] = base;
       if (tid == E - 1) offsets[E] = base + all;
     }
-    for (int i = 0; i < kSortWarps; ++i) hist[i * E + tid] += base + before;
+    start[tid] = base + before;
   }
-  cluster.sync();   // the others have read total; hist is complete
-  for (int64_t p = from; p < to; p += 32) {
-    const int e = expert_of(ids, p + lane, P, E, nullptr);
-    const unsigned same = __match_any_sync(kAll, e);
-    const int at = e >= 0 ? mine[e] + __popc(same & ((1u << lane) - 1u)) : -1;
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
-    if (p + lane < P) rows[p + lane] = at;
+  cluster.sync();   // the others have read total; start is complete
+  for (int64_t p0 = from; p0 < to; p0 += 32 * kAhead) {
+    int id[kAhead], at[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t p = p0 + i * 32 + lane;
+      at[i] = p < to ? rows[p] : -1;
+      id[i] = at[i] >= 0 ? __ldg(ids + p) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (at[i] >= 0) rows[p0 + i * 32 + lane] = at[i] + mine[id[i]] + start[id[i]];
   }
 }
 
@@ -138,6 +174,7 @@ __device__ __forceinline__ uint32_t narrow(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ uint4 load16_once(const __nv_bfloat16* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
 __device__ __forceinline__ void store16(__nv_bfloat16* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
 
 // s += w v of eight values
@@ -168,7 +205,56 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowArgs a, 
   }
 }
 
+// Few pairs: every CTA counts for itself where its tokens' rows go (the pairs
+// with a lower expert and the earlier ones with the same), one warp per pair,
+// and copies them; the experts' offsets are shared out over all warps.
+constexpr int kFewPairs = 4096;
+constexpr int kFewThreads = 256;
+
+__global__ void __launch_bounds__(kFewThreads) dispatch_few_kernel(const RowArgs a, const int32_t* __restrict__ ids, int E,
+                                                                   int32_t* __restrict__ offsets, int32_t* __restrict__ rows) {
+  __shared__ int id[kFewPairs];
+  __shared__ int place[kFewThreads];
+  pdl_entry();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = static_cast<int>(a.k), P = static_cast<int>(a.T) * k;
+  for (int p = tid; p < P; p += kFewThreads) {
+    const int e = __ldg(ids + p);
+    const bool is = e >= 0 && e < E;
+    if (!is && e != -1 && a.status) *a.status = kStatusArg;
+    id[p] = is ? e : E;   // behind all others
+  }
+  __syncthreads();
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    for (int j = warp; j < k; j += kFewThreads / 32) {
+      const int p = t * k + j, e = id[p];
+      int n = 0;
+      for (int q = lane; q < P; q += 32) n += id[q] < e + (q < p);
+      n = __reduce_add_sync(kAll, n);
+      if (lane == 0) {
+        n = e < E ? n : -1;
+        place[j] = n;
+        rows[p] = n;
+      }
+    }
+    __syncthreads();
+    if (a.in)
+      for (int64_t c = tid * 8; c < a.C; c += kFewThreads * 8) {
+        const uint4 v = load16(a.in + t * a.ldi + c);
+        for (int j = 0; j < k; ++j)
+          if (place[j] >= 0) store16(a.out + place[j] * a.ldo + c, v);
+      }
+    __syncthreads();
+  }
+  for (int e = blockIdx.x * (kFewThreads / 32) + warp; e <= E; e += gridDim.x * (kFewThreads / 32)) {
+    int n = 0;
+    for (int q = lane; q < P; q += 32) n += id[q] < e;
+    n = __reduce_add_sync(kAll, n);
+    if (lane == 0) offsets[e] = n;
+  }
+}
+
 constexpr int kTogether = 8;   // rows of a token on their way at the same time
+constexpr int kBack = 4;       // the same in the backward pass
 
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a, int per_token) {
   pdl_entry();
@@ -185,7 +271,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a, i
       for (int j = 0; j < kTogether; ++j) {
         const int64_t r = j0 + j < k ? place_of(a, t * k + j0 + j) : -1;
         got[j] = r >= 0;
-        if (got[j]) v[j] = load16(a.y + r * a.ldy + c);
+        if (got[j]) v[j] = load16_once(a.y + r * a.ldy + c);
       }
 #pragma unroll
       for (int j = 0; j < kTogether; ++j)
@@ -197,33 +283,33 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a, i
 
 // per_token threads of one token; the sums of dw go through shared memory when
 // they are more than a warp's.
-__global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const RowArgs a, int per_token) {
-  __shared__ float part[kRowThreads / 32][kTogether];
+__global__ void __launch_bounds__(kRowThreads, 4) combine_backward_kernel(const RowArgs a, int per_token) {
+  __shared__ float part[kRowThreads / 32][kBack];
   pdl_entry();
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRowThreads / per_token) + threadIdx.x / per_token;
   const int k = static_cast<int>(a.k), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool live = t < a.T;
-  for (int j0 = 0; j0 < k; j0 += kTogether) {
-    float dot[kTogether] = {};
+  for (int j0 = 0; j0 < k; j0 += kBack) {
+    float dot[kBack] = {};
     if (live) {
-      int64_t r[kTogether];
-      float w[kTogether];
+      int64_t r[kBack];
+      float w[kBack];
 #pragma unroll
-      for (int j = 0; j < kTogether; ++j) {
+      for (int j = 0; j < kBack; ++j) {
         r[j] = j0 + j < k ? place_of(a, t * k + j0 + j) : -1;
         w[j] = a.weights && r[j] >= 0 ? __ldg(a.weights + t * k + j0 + j) : 1.0f;
       }
       for (int64_t c = (threadIdx.x % per_token) * 8; c < a.C; c += per_token * 8) {
         float d[8] = {};
         add_scaled(d, 1.0f, load16(a.in + t * a.ldi + c));
-        uint4 v[kTogether];
+        uint4 v[kBack];
         if (a.dweights) {
 #pragma unroll
-          for (int j = 0; j < kTogether; ++j)
+          for (int j = 0; j < kBack; ++j)
             if (r[j] >= 0) v[j] = load16(a.y + r[j] * a.ldy + c);
         }
 #pragma unroll
-        for (int j = 0; j < kTogether; ++j) {
+        for (int j = 0; j < kBack; ++j) {
           if (r[j] < 0) continue;
           if (a.dweights) {
             const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
@@ -246,23 +332,23 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const Row
     if (!a.dweights) continue;
     const int width = per_token < 32 ? per_token : 32;
 #pragma unroll
-    for (int j = 0; j < kTogether; ++j)
+    for (int j = 0; j < kBack; ++j)
       for (int o = width >> 1; o; o >>= 1) dot[j] += __shfl_xor_sync(kAll, dot[j], o);
     const int own = threadIdx.x % per_token;
     if (per_token > 32) {
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kTogether; ++j)
+      for (int j = 0; j < kBack; ++j)
         if (lane == 0) part[warp][j] = dot[j];
       __syncthreads();
-      if (live && own < kTogether && j0 + own < k) {
+      if (live && own < kBack && j0 + own < k) {
         float s = 0.0f;
         for (int i = 0; i < per_token / 32; ++i) s += part[warp + i][own];
         a.dweights[t * k + j0 + own] = s;
       }
     } else if (live && own == 0) {
 #pragma unroll
-      for (int j = 0; j < kTogether; ++j)
+      for (int j = 0; j < kBack; ++j)
         if (j0 + j < k) a.dweights[t * k + j0 + j] = dot[j];
     }
   }
@@ -275,28 +361,54 @@ int threads_per_token(int64_t C) {
 }
 
 template <typename Kernel>
-cudaError_t rows_launch(Kernel kernel, const RowArgs& a, cudaStream_t st) {
-  const int per_token = threads_per_token(a.C), tokens = kRowThreads / per_token;
+cudaError_t rows_launch(Kernel kernel, const RowArgs& a, cudaStream_t st, int per_token) {
+  const int tokens = kRowThreads / per_token;
   note_launch();
   return launch_k(kernel, dim3(static_cast<unsigned>((a.T + tokens - 1) / tokens)), dim3(kRowThreads), 0, st, 1, a, per_token);
 }
 
-}  // namespace
-
-cudaError_t sort_launch(const int32_t* ids, int64_t P, int64_t E, int32_t* offsets, int32_t* rows, int32_t* status,
+template <int kBits>
+cudaError_t sort_launch(const RowArgs& a, const int32_t* ids, int64_t P, int64_t E, int32_t* offsets, int32_t* rows,
                         cudaStream_t st) {
-  const size_t smem = static_cast<size_t>(kSortWarps + 1) * E * sizeof(int);
+  const size_t smem = static_cast<size_t>(kSortWarps + 2) * E * sizeof(int);
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e =
+        cudaFuncSetAttribute(sort_kernel<kBits>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
   note_launch();
-  return launch_k(sort_kernel, dim3(kSortCtas), dim3(kSortThreads), smem, st, kSortCtas, ids, P, static_cast<int>(E), offsets,
-                  rows, status);
+  return launch_k(sort_kernel<kBits>, dim3(kSortCtas), dim3(kSortThreads), smem, st, kSortCtas, ids, P, static_cast<int>(E),
+                  offsets, rows, a.status);
 }
 
-cudaError_t dispatch_rows_launch(const RowArgs& a, cudaStream_t st) { return rows_launch(dispatch_kernel, a, st); }
-cudaError_t combine_launch(const RowArgs& a, cudaStream_t st) { return rows_launch(combine_kernel, a, st); }
-cudaError_t combine_backward_launch(const RowArgs& a, cudaStream_t st) { return rows_launch(combine_backward_kernel, a, st); }
+}  // namespace
+
+// Without rows to copy (in null) only the places and offsets.
+cudaError_t dispatch_launch(const RowArgs& a, const int32_t* ids, int64_t E, int32_t* offsets, int32_t* rows, cudaStream_t st) {
+  const int64_t P = a.T * a.k;
+  if (P <= kFewPairs) {
+    note_launch();
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(a.T, 32), 2 * sm_count()));
+    return launch_k(dispatch_few_kernel, dim3(grid), dim3(kFewThreads), 0, st, 1, a, ids, static_cast<int>(E), offsets, rows);
+  }
+  const cudaError_t e = E <= 64    ? sort_launch<6>(a, ids, P, E, offsets, rows, st)
+                        : E <= 256 ? sort_launch<8>(a, ids, P, E, offsets, rows, st)
+                                   : sort_launch<10>(a, ids, P, E, offsets, rows, st);
+  if (e != cudaSuccess || !a.in) return e;
+  RowArgs copy = a;
+  copy.status = nullptr;   // what is wrong has been said
+  return rows_launch(dispatch_kernel, copy, st, threads_per_token(a.C));
+}
+
+cudaError_t combine_launch(const RowArgs& a, cudaStream_t st) {
+  return rows_launch(combine_kernel, a, st, threads_per_token(a.C));
+}
+
+cudaError_t combine_backward_launch(const RowArgs& a, cudaStream_t st) {
+  // a warp per token where that fills the GPU: no barrier between its rows
+  int per_token = threads_per_token(a.C);
+  while (per_token > 32 && a.T * per_token > static_cast<int64_t>(sm_count()) * 2048) per_token /= 2;
+  return rows_launch(combine_backward_kernel, a, st, per_token);
+}
 
 }  // namespace nvfp4

@@ -174,9 +174,7 @@ struct RowArgs {
   float* dweights;
   int32_t* status;
 };
-cudaError_t sort_launch(const int32_t* ids, int64_t P, int64_t E, int32_t* offsets, int32_t* rows, int32_t* status,
-                        cudaStream_t st);
-cudaError_t dispatch_rows_launch(const RowArgs& a, cudaStream_t st);
+cudaError_t dispatch_launch(const RowArgs& a, const int32_t* ids, int64_t E, int32_t* offsets, int32_t* rows, cudaStream_t st);
 cudaError_t combine_launch(const RowArgs& a, cudaStream_t st);
 cudaError_t combine_backward_launch(const RowArgs& a, cudaStream_t st);
 
