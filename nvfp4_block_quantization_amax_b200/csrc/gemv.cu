@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, GemvCfg<NT>::kCtas) gemv_kernel(cons
         sm.share[turn][m][r] = s;
       } else {
         const int64_t p = a.ids ? sm.slots.pairs[m0 + m] : m0 + m;
-        out[p * a.ldo + n0 + (r >> 3) * 32 + (r & 7)] = Out(s * 256.0f * alpha);
+        out[p * a.ldo + n0 + (r >> 3) * 32 + (r & 7)] = Out(s * alpha * 256.0f);
       }
     }
     if (ranks > 1) {
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, GemvCfg<NT>::kCtas) gemv_kernel(cons
         float s = 0.0f;
         for (int i = 0; i < ranks; ++i) s += cluster.map_shared_rank(&sm.share[turn][m][r], i)[0];
         const int64_t p = a.ids ? sm.slots.pairs[m0 + m] : m0 + m;
-        out[p * a.ldo + n0 + (r >> 3) * 32 + (r & 7)] = Out(s * 256.0f * alpha);
+        out[p * a.ldo + n0 + (r >> 3) * 32 + (r & 7)] = Out(s * alpha * 256.0f);
       }
     }
     if (++tile == tiles) {
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_wide_kernel(const __grid_con
       sum += from_rank[NT * 8 * 129];
     }
     const int64_t p = a.ids ? sm.slots.pairs[m0 + m] : m0 + m;
-    out[p * a.ldo + atom * 128ll + r] = Out(sum * 256.0f * alpha);
+    out[p * a.ldo + atom * 128ll + r] = Out(sum * alpha * 256.0f);
   }
   if (ranks > 1) cluster.sync();   // no CTA leaves while its share is read
 }

@@ -88,19 +88,28 @@ __device__ __forceinline__ F group_value(F first, F second, bool pair) {
   return pair && second > -FLT_MAX ? first + second : first;
 }
 
-// The choice in 64 bits, for rows whose values in 32 bits are too near to one
-// another to be ordered: lane j < k gets the j-th expert, or -1.
+// Finite numbers in their order as unsigned ones above 0, -inf as 0.
+__device__ __forceinline__ unsigned long long ordered(double v) {
+  if (!(v > -INFINITY)) return 0ull;
+  const long long u = __double_as_longlong(v + 0.0);
+  return static_cast<unsigned long long>(u ^ ((u >> 63) | static_cast<long long>(0x8000000000000000ull)));
+}
+
+// The choice in 64 bits, by the whole warp, for rows whose values in 32 bits
+// are too near to one another to be ordered: lane j < k gets the j-th expert,
+// or -1.  c: E doubles of shared memory.
 template <typename Z>
 __device__ __noinline__ int choose_exactly(const Z* __restrict__ z, const RouteArgs& a, double* c, int lane) {
   const float low = lowest<Z>();
   const int E = static_cast<int>(a.E), k = static_cast<int>(a.k), G = static_cast<int>(a.groups), n = E / G;
   const double none = -INFINITY;
-  const bool direct = !a.bias && G == 1;
+  const bool direct = !a.bias && G == 1, softmax = a.score == NVFP4_ROUTE_SOFTMAX;
   float m = -INFINITY;
   double sum = 0.0;
-  if (!direct && a.score == NVFP4_ROUTE_SOFTMAX) {
+  if (!direct && softmax) {
     for (int e = lane; e < E; e += 32) m = fmaxf(m, as_float(z[e]));
     m = warp_max(m);
+#pragma unroll 4
     for (int e = lane; e < E; e += 32) sum += exp(static_cast<double>(as_float(z[e])) - m);
     sum = warp_sum(sum);
   }
@@ -108,7 +117,7 @@ __device__ __noinline__ int choose_exactly(const Z* __restrict__ z, const RouteA
   for (int e = lane; e < E; e += 32) {
     const float v = as_float(z[e]);
     double s = v;
-    if (!direct) s = a.score == NVFP4_ROUTE_SOFTMAX ? exp(s - m) / sum : 1.0 / (1.0 + exp(-s));
+    if (!direct) s = softmax ? exp(s - m) / sum : 1.0 / (1.0 + exp(-s));
     bool open = v > low;
     if (a.bias) {
       const float b = __ldg(a.bias + e);
@@ -118,8 +127,9 @@ __device__ __noinline__ int choose_exactly(const Z* __restrict__ z, const RouteA
     c[e] = open ? s : none;
   }
   __syncwarp();
+  unsigned kept = 1u;
+  int lanes = 32;   // of a group
   if (G > 1) {
-    int lanes = 32;   // of a group
     while (lanes * G > 32) lanes >>= 1;
     const int g = lane / lanes;
     double a1 = none, a2 = none;
@@ -135,33 +145,38 @@ __device__ __noinline__ int choose_exactly(const Z* __restrict__ z, const RouteA
       const double v = __shfl_sync(kAll, mine, h * lanes);
       better += v > mine || (v == mine && h < g);
     }
-    const unsigned kept = __ballot_sync(kAll, g < G && better < a.kept);
-    for (int e = lane; e < E; e += 32)
-      if (!(kept >> (e / n * lanes) & 1u)) c[e] = none;
-    __syncwarp();
+    kept = __ballot_sync(kAll, g < G && better < a.kept);
+  }
+  unsigned long long best = 0ull;   // this lane's largest, and its expert
+  int at = E;
+  for (int e = lane; e < E; e += 32) {
+    if (!(kept >> (e / n * lanes & 31) & 1u)) c[e] = none;
+    const unsigned long long v = ordered(c[e]);
+    if (v > best) {
+      best = v;
+      at = e;
+    }
   }
   int mine = -1;
   for (int j = 0; j < k; ++j) {
-    double best = none;
-    int at = E;
-    for (int e = lane; e < E; e += 32)
-      if (c[e] > best) {
-        best = c[e];
-        at = e;
-      }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const double v = __shfl_xor_sync(kAll, best, o);
-      const int i = __shfl_xor_sync(kAll, at, o);
-      if (v > best || (v == best && i < at)) {
-        best = v;
-        at = i;
+    const unsigned high = static_cast<unsigned>(best >> 32), top = __reduce_max_sync(kAll, high);
+    if (top == 0u) break;
+    const unsigned lo = high == top ? static_cast<unsigned>(best) : 0u, next = __reduce_max_sync(kAll, lo);
+    const int e = __reduce_min_sync(kAll, high == top && lo == next ? at : E);
+    if (lane == j) mine = e;
+    if (at == e) {
+      c[e] = none;
+      best = 0ull;
+      at = E;
+#pragma unroll 4
+      for (int i = lane; i < E; i += 32) {
+        const unsigned long long v = ordered(c[i]);
+        if (v > best) {
+          best = v;
+          at = i;
+        }
       }
     }
-    if (at == E) break;   // the same in every lane
-    if (lane == j) mine = at;
-    if (lane == (at & 31)) c[at] = none;
-    __syncwarp();
   }
   return mine;
 }
@@ -184,6 +199,40 @@ __device__ __forceinline__ float share_at(float z, bool got, float top, int scor
 
 __device__ __forceinline__ float share_of(float z, bool got, int score, bool renorm, float row_max, float row_sum) {
   return share_at(z, got, renorm ? warp_max(got ? z : -INFINITY) : row_max, score, renorm, row_sum);
+}
+
+// Bound of |32-bit c - c| (see the figures behind route_kernel); share: the
+// largest score, most_c: no less than any |c|.
+__device__ __forceinline__ float error_of(bool softmax, float share, float most_c) {
+  return (softmax ? 0x1p-18f * share : 0x1.8p-22f) + 0x1.1p-24f * most_c + FLT_MIN;
+}
+
+// What a row that has to be chosen in 64 bits holds in the place of its first
+// choice until then.  Such rows wait until a warp has been through its others:
+// the code for them would cost those registers.
+constexpr int kDoubtful = -2;
+
+template <typename Z>
+__device__ __noinline__ void finish_exactly(const RouteArgs& a, int64_t t, double* c, int lane) {
+  const Z* const row = static_cast<const Z*>(a.logits) + t * a.ldl;
+  const int k = static_cast<int>(a.k);
+  const int mine = choose_exactly<Z>(row, a, c, lane);
+  const bool softmax = a.score == NVFP4_ROUTE_SOFTMAX, renorm = a.flags & NVFP4_ROUTE_RENORM;
+  float row_max = -INFINITY, row_sum = 0.0f;
+  if (softmax && !renorm) {
+    for (int e = lane; e < a.E; e += 32) row_max = fmaxf(row_max, as_float(row[e]));
+    row_max = fmaxf(warp_max(row_max), -FLT_MAX);
+    for (int e = lane; e < a.E; e += 32) row_sum += ex2((as_float(row[e]) - row_max) * kLog2e);
+    row_sum = warp_sum(row_sum);
+  }
+  const bool got = mine >= 0;
+  const float share = share_of(got ? as_float(row[mine]) : 0.0f, got, a.score, renorm, row_max, row_sum);
+  const float sum = renorm ? warp_sum(share) : 1.0f;
+  if (lane < k) {
+    a.ids[t * k + lane] = mine;
+    a.weights[t * k + lane] = got ? a.scale * (renorm ? __fdiv_rn(share, sum) : share) : 0.0f;
+  }
+  __syncwarp();   // c is free
 }
 
 // V: values per lane, the power of two from E / 32 on.  kDirect: no bias and
@@ -230,6 +279,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRouteCtas<V>) route_kernel(const
     bmax = warp_max(bmax);
   }
 
+  bool doubts = false;   // uniform in the warp
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.T;
        t += static_cast<int64_t>(gridDim.x) * kWarps) {
     const Z* const row = logits + t * a.ldl;
@@ -271,7 +321,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRouteCtas<V>) route_kernel(const
     if (!kDirect) {
       const float share = softmax ? rcp(fmaxf(row_sum, FLT_MIN)) : 1.0f;
       most_c = share + bmax;
-      delta = (softmax ? 0x1p-18f * share : 0x1p-20f) + 0x1p-23f * static_cast<float>(V) * most_c + FLT_MIN;
+      delta = error_of(softmax, share, most_c) + 0x1p-23f * static_cast<float>(V) * most_c;
       if (softmax) {
 #pragma unroll
         for (int i = 0; i < V; ++i) c[i] = __fmaf_rn(c[i], share, bias[i]);
@@ -400,9 +450,9 @@ __global__ void __launch_bounds__(kWarps * 32, kRouteCtas<V>) route_kernel(const
       unsure = !(as_float(row[mine]) == as_float(row[next]) && (kDirect || !a.bias || __ldg(a.bias + mine) == __ldg(a.bias + next)));
     }
     if (near || __any_sync(kAll, unsure)) {
-      __syncwarp();
-      mine = choose_exactly<Z>(row, a, c64, lane);
-      __syncwarp();
+      if (lane == 0) a.ids[t * k] = kDoubtful;
+      doubts = true;
+      continue;
     }
     const bool got = mine >= 0;
     const float share = share_of(got ? as_float(row[mine]) : 0.0f, got, a.score, renorm, row_max, row_sum);
@@ -414,13 +464,20 @@ __global__ void __launch_bounds__(kWarps * 32, kRouteCtas<V>) route_kernel(const
       a.weights[t * k + lane] = got ? a.scale * (renorm ? __fdiv_rn(share, sum) : share) : 0.0f;
     }
   }
+  if (doubts) {
+    __syncwarp();
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.T; t += static_cast<int64_t>(gridDim.x) * kWarps)
+      if (__shfl_sync(kAll, lane == 0 ? a.ids[t * k] : 0, 0) == kDoubtful) finish_exactly<Z>(a, t, c64, lane);
+  }
 }
-// delta.  ex2.approx and rcp.approx are off by 2^-22 and 2^-23 relative; the
-// exponent's rounding makes that |z| 2^-23.5 more.  sigmoid: s (1 - s) |z| <=
-// 0.23, in all below 2^-21.  softmax with d = z - max: exp(-d) d <= 0.37 of
-// the largest share, and the row's sum is off by (mean d + 1) 2^-22 <=
-// (ln 1024 + 1) 2^-22 relative: below 2^-19 of the largest share.  The keys
-// drop log2 V bits of c: 2^-23 V |c|, and c's own rounding is in the slack.
+// error_of.  ex2.approx and rcp.approx are off by 2^-22 and 2^-23 relative;
+// the exponent's rounding (of the product and of log2 e) makes that
+// 1.5 |z| 2^-24 more.  sigmoid: s (1 - s) (2^-22 + 1.5 |z| 2^-24) + 1.5 s 2^-23
+// with s (1 - s) <= 1/4 and s (1 - s) |z| <= 0.23 is below 4.4 x 2^-24.  softmax
+// with d = z - max: exp(-d) d <= 0.37 of the largest share, and the row's sum
+// is off by (mean d + 1) 2^-22 <= (ln 1024 + 1) 2^-22 relative: below 2^-19 of
+// the largest share.  c's own rounding: 2^-24 |c|.  The keys drop log2 V bits of
+// c: 2^-23 V |c| more.  A sum of two is rounded by 2^-24 of up to 2 |c|.
 
 // ---------------------------------------------------------------------------
 // Many rows.  What a row costs beyond its values (reductions, rounds, the
@@ -447,16 +504,15 @@ __device__ __forceinline__ float share_max(float v) {
   return v;
 }
 
+// Values of a row in shared memory, four free ones after each 32: lanes that
+// read 16 bytes of different groups then meet different banks.
+__device__ __forceinline__ int place(int e) { return e + (e >> 5) * 4; }
+
 template <typename Z, int V, bool kDirect>
 __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(const __grid_constant__ RouteArgs a) {
-  constexpr int kPitch = V * kShare + V / 4;   // of a row's values in shared memory: one free after each 32
-  static_assert(V % 4 == 0);
-  // a warp's values in 32 bits (four rows) or in 64 (one row at a time)
-  constexpr int kValues = kDirect ? V * kShare : kRowsOfWarp * (kPitch + 8) / 2;
-  __shared__ double values[kWarps][kValues < kRowsOfWarp * 32 ? kRowsOfWarp * 32 : kValues];
-  __shared__ int16_t doubtful[kWarps][kRowsOfWarp][32];   // experts that may be among the choices
-  __shared__ int doubts[kWarps][kRowsOfWarp];
-  __shared__ int16_t order[kWarps][kRowsOfWarp][kShare];
+  constexpr int kPitch = V * kShare + V + 8;   // of a row's values in shared memory; rows 8 banks apart
+  // a warp's values in 32 bits (four rows), and in 64 (one row at a time)
+  __shared__ __align__(16) double values[kWarps][kDirect ? V * kShare : kRowsOfWarp * kPitch / 2];
   __shared__ __align__(16) float biases[kDirect ? 1 : V * kShare];
   __shared__ int bad_bias;
   __shared__ float most_bias[kWarps];
@@ -470,7 +526,7 @@ __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(c
   const bool whole = softmax && (!kDirect || !renorm);
   const unsigned inverse = ((1u << 20) + n - 1) / n;
   const unsigned before = ((1u << lane) - 1u) & (0xFFu << (lane & 24));   // lanes of this row in front of this one
-  float* const c32 = reinterpret_cast<float*>(values[warp]) + (kDirect ? 0 : r * (kPitch + 8));   // rows 8 banks apart
+  float* const c32 = reinterpret_cast<float*>(values[warp]) + (kDirect ? 0 : r * kPitch);
 
   float bmax = 0.0f;
   if (!kDirect) {
@@ -490,6 +546,7 @@ __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(c
     for (int i = 0; i < kWarps; ++i) bmax = fmaxf(bmax, most_bias[i]);
   }
 
+  bool doubts = false;
   for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRowsOfWarp; t0 < a.T;
        t0 += static_cast<int64_t>(gridDim.x) * (kWarps * kRowsOfWarp)) {
     const int64_t t = t0 + r < a.T ? t0 + r : a.T - 1;   // rows behind the last are the last again, and not written
@@ -514,11 +571,13 @@ __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(c
       for (int i = 0; i < V; ++i) row_sum += ex2((c[i] - row_max) * kLog2e);
       row_sum = share_sum(row_sum);
     }
-    float delta = 0.0f, most_c = 0.0f;
+    // |32-bit c - c| <= fine, and delta for the c of a key
+    float fine = 0.0f, delta = 0.0f, most_c = 0.0f;
     if (!kDirect) {
       const float share = softmax ? rcp(fmaxf(row_sum, FLT_MIN)) : 1.0f;
       most_c = share + bmax;
-      delta = (softmax ? 0x1p-18f * share : 0x1p-20f) + 0x1p-23f * static_cast<float>(V) * most_c + FLT_MIN;
+      fine = error_of(softmax, share, most_c);
+      delta = fine + 0x1p-23f * static_cast<float>(V) * most_c;
       if (softmax) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -532,19 +591,30 @@ __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(c
     unsigned kept = 0xFFu;
     if (!kDirect && G > 1) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) c32[i * kShare + sub + i / 4] = c[i];
+      for (int i = 0; i < V; ++i) c32[i * kShare + sub + i / 4 * 4] = c[i];
       __syncwarp();
       float a1 = -INFINITY, a2 = -INFINITY;
+      const auto add = [&](float v) {
+        a2 = fmaxf(a2, fminf(a1, v));
+        a1 = fmaxf(a1, v);
+      };
       if (sub < G) {
         const int first = sub * n;
-        for (int i = first; i < first + n; ++i) {
-          const float v = c32[i + (i >> 5)];
-          a2 = fmaxf(a2, fminf(a1, v));
-          a1 = fmaxf(a1, v);
+        if ((n & 3) == 0) {
+#pragma unroll 4
+          for (int i = first; i < first + n; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(c32 + place(i));
+            add(v.x);
+            add(v.y);
+            add(v.z);
+            add(v.w);
+          }
+        } else {
+          for (int i = first; i < first + n; ++i) add(c32[place(i)]);
         }
       }
-      __syncwarp();
-      const float mine = group_value(a1, a2, a.flags & NVFP4_ROUTE_GROUP_PAIR);   // -inf from lanes without a group
+      const bool pair = a.flags & NVFP4_ROUTE_GROUP_PAIR;
+      const float mine = group_value(a1, a2, pair);   // -inf from lanes without a group
       int better = 0;
 #pragma unroll
       for (int o = 1; o < kShare; ++o) {
@@ -554,7 +624,7 @@ __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(c
       const bool keep = better < a.kept;
       kept = __ballot_sync(kAll, keep) >> (lane & 24) & 0xFFu;
       const float least = -share_max(keep ? -mine : -INFINITY), most = share_max(keep ? -INFINITY : mine);
-      near = most >= -FLT_MAX && !(least - most > 4.0f * delta + 0x1p-21f * most_c);
+      near = !bad && most >= -FLT_MAX && !(least - most > 4.0f * fine + 0x1p-22f * most_c);
     }
     uint32_t key[V];
     uint32_t l0 = 0u, l1 = 0u, l2 = 0u, l3 = 0u;
@@ -599,74 +669,29 @@ __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(c
     uint32_t next_key = __shfl_down_sync(kAll, my_key, 1);
     if (sub == k - 1) next_key = w;
     int mine = had ? (V - 1 - static_cast<int>(my_key & (V - 1))) * kShare + holder[warp][r][sub] : -1;
+    // Neighbours whose keys do not part them: equal inputs are in order; of two
+    // that are both choices, so are those whose values themselves part them (any
+    // other expert's key is below both); the rest is unsure.
     bool unsure = false;
     if (had && next_key &&
         (kDirect ? (my_key ^ next_key) < static_cast<uint32_t>(V) : !(from_ordered(my_key) - from_ordered(next_key) > 2.0f * delta))) {
       const int next = (V - 1 - static_cast<int>(next_key & (V - 1))) * kShare + holder[warp][r][sub + 1];
-      unsure = !(as_float(row[mine]) == as_float(row[next]) && (kDirect || !a.bias || __ldg(a.bias + mine) == __ldg(a.bias + next)));
-    }
-    unsure = (__ballot_sync(kAll, unsure) >> (lane & 24) & 0xFFu) && !near && !bad;   // of the row
-    if (__any_sync(kAll, unsure)) {
-      // every expert whose 32-bit value could belong to a choice, in 64 bits
-      const uint32_t last = __reduce_min_sync(0xFFu << (lane & 24), had ? my_key : 0xFFFFFFFFu);
-      const uint32_t least = (kDirect ? last : ordered(from_ordered(last) - 2.0f * delta)) & ~static_cast<uint32_t>(V - 1);
-      if (sub == 0) doubts[warp][r] = 0;
-      __syncwarp();
-      if (unsure) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (key[i] && key[i] >= least) {
-            const int at = atomicAdd(&doubts[warp][r], 1);
-            if (at < 32) doubtful[warp][r][at] = static_cast<int16_t>(i * kShare + sub);
-          }
-      }
-      __syncwarp();
-      const int number = doubts[warp][r];
-      if (unsure && number > 32) {   // as many equal ones: the whole row
-        near = true;
-        unsure = false;
-      }
-      double* const v64 = values[warp] + r * 32;
-      double sum64 = 1.0;
-      if (!kDirect && softmax) {
-        sum64 = 0.0;
-        if (unsure)
-          for (int e = sub; e < E; e += kShare) sum64 += exp(static_cast<double>(as_float(row[e])) - row_max);
-#pragma unroll
-        for (int o = kShare / 2; o; o >>= 1) sum64 += __shfl_xor_sync(kAll, sum64, o);
-      }
-      if (unsure)
-        for (int m = sub; m < number; m += kShare) {
-          const int e = doubtful[warp][r][m];
-          double v = as_float(row[e]);
-          if (!kDirect) {
-            v = softmax ? exp(v - row_max) / sum64 : 1.0 / (1.0 + exp(-v));
-            if (a.bias) v += __ldg(a.bias + e);
-          }
-          v64[m] = v;
+      const float z1 = as_float(row[mine]), z2 = as_float(row[next]);
+      float c1 = z1, c2 = z2;
+      bool equal = z1 == z2;
+      if (!kDirect) {
+        const float b1 = biases[mine], b2 = biases[next];
+        equal &= b1 == b2;
+        if (!softmax) {
+          c1 = rcp(1.0f + ex2(-kLog2e * z1)) + b1;
+          c2 = rcp(1.0f + ex2(-kLog2e * z2)) + b2;
         }
-      __syncwarp();
-      if (unsure)
-        for (int m = sub; m < number; m += kShare) {
-          const int e = doubtful[warp][r][m];
-          const double v = v64[m];
-          int better = 0;
-          for (int i = 0; i < number; ++i) better += v64[i] > v || (v64[i] == v && doubtful[warp][r][i] < e);
-          if (better < k) order[warp][r][better] = static_cast<int16_t>(e);
-        }
-      __syncwarp();
-      if (unsure && had) mine = order[warp][r][sub];
+      }
+      unsure = !equal && !((kDirect || !softmax) && sub + 1 < k && c1 - c2 > 2.0f * fine);
     }
-    const unsigned again = __ballot_sync(kAll, near && !bad);   // its votes also part the uses of values
-    for (unsigned rows = again; rows;) {
-      const int of = (__ffs(rows) - 1) / kShare;
-      rows &= ~(0xFFu << (of * kShare));
-      const int64_t u = t0 + of < a.T ? t0 + of : a.T - 1;
-      const int e = choose_exactly<Z>(logits + u * a.ldl, a, values[warp], lane);
-      __syncwarp();
-      const int moved = __shfl_sync(kAll, e, sub);   // lane j of the warp has choice j
-      if (r == of) mine = sub < k ? moved : -1;
-    }
+    // its vote also parts the uses of values
+    const bool later = ((__ballot_sync(kAll, unsure) >> (lane & 24) & 0xFFu) || near) && !bad;   // of the row
+    doubts |= later;
     if (bad) mine = -1;
     const bool got = mine >= 0;
     const float z = got ? as_float(row[mine]) : 0.0f;
@@ -675,12 +700,20 @@ __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(c
     const float sum = renorm ? share_sum(share) : 1.0f;
     if (t0 + r < a.T) {
       if (bad && sub == 0 && a.status) *a.status = kStatusNonFinite;
-      if (sub < k) {
+      if (later) {
+        if (sub == 0) a.ids[t * k] = kDoubtful;
+      } else if (sub < k) {
         a.ids[t * k + sub] = mine;
         a.weights[t * k + sub] = got ? a.scale * (renorm ? __fdiv_rn(share, sum) : share) : 0.0f;
       }
     }
   }
+  if (__any_sync(kAll, doubts))
+    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRowsOfWarp; t0 < a.T;
+         t0 += static_cast<int64_t>(gridDim.x) * (kWarps * kRowsOfWarp)) {
+      unsigned rows = __ballot_sync(kAll, sub == 0 && t0 + r < a.T && a.ids[(t0 + r) * k] == kDoubtful);
+      for (; rows; rows &= rows - 1u) finish_exactly<Z>(a, t0 + (__ffs(rows) - 1) / kShare, values[warp], lane);
+    }
 }
 
 template <typename Z, int V>
@@ -725,61 +758,86 @@ cudaError_t route_launch_z(const RouteArgs& a, cudaStream_t st) {
 
 // ---------------------------------------------------------------------------
 // Gradient.  Softmax scores without renormalisation reach every expert: one
-// warp per row, the chosen experts' parts put together in shared memory in the
-// order of the choices (an expert that is named twice gets both).  Otherwise a
-// row is zeros but for its choices: a CTA computes the choices of its rows,
-// `span` lanes each, fills all of them with zeros in 16-byte pieces and then
-// puts the choices' values on top.
+// warp per row writes s_e (0 - sum s g) for all and then the choices' s_i (g_i -
+// sum s g) on top.  Otherwise a row is zeros but for its choices: a CTA
+// computes the choices of its rows, `span` lanes each, fills all of them with
+// zeros in 16-byte pieces and puts the choices' values on top.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-template <typename Z>
+// Sum of `v` over the choices j < k of the `span` lanes of a row that name
+// lane's own expert; *first: whether none before it does.
+__device__ __forceinline__ float sum_of_same(int id, float v, int k, int span, bool* first) {
+  float sum = 0.0f;
+  const int sub = threadIdx.x & (span - 1), from = threadIdx.x & 31 & ~(span - 1);
+  *first = id >= 0;
+  for (int j = 0; j < k; ++j) {
+    const int other = __shfl_sync(kAll, id, from + j);
+    const float part = __shfl_sync(kAll, v, from + j);
+    if (other == id) {
+      sum += part;
+      *first &= j >= sub;
+    }
+  }
+  return sum;
+}
+
+template <typename Z, int V>
 __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const __grid_constant__ RouteArgs a, const float* __restrict__ dweights,
                                                                      Z* dlogits, int64_t ldd) {
-  extern __shared__ float grad_smem[];
   pdl_entry();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = static_cast<int>(a.E), k = static_cast<int>(a.k);
-  float* const d = grad_smem + static_cast<size_t>(warp) * E;
   const Z* const logits = static_cast<const Z*>(a.logits);
-
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.T;
        t += static_cast<int64_t>(gridDim.x) * kWarps) {
     const Z* const row = logits + t * a.ldl;
     int id = lane < k ? __ldg(a.ids + t * k + lane) : -1;
-    const bool wrong = id < -1 || id >= E;
-    if (wrong) {
+    if (id < -1 || id >= E) {
       if (a.status) *a.status = kStatusArg;
       id = -1;
     }
-    const bool got = id >= 0;
-    const float z = got ? as_float(row[id]) : 0.0f;
-    const float g = got ? a.scale * __ldg(dweights + t * k + lane) : 0.0f;
+    const bool got = id >= 0, live = __any_sync(kAll, got);
+    float z[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = i * 32 + lane;
+      z[i] = i < V / 2 || e < E ? as_float(row[e]) : -INFINITY;   // E > 16 V
+    }
+    const float mine = got ? as_float(row[id]) : 0.0f, g = got ? a.scale * __ldg(dweights + t * k + lane) : 0.0f;
     float row_max = -INFINITY, row_sum = 0.0f;
-    const bool live = __any_sync(kAll, got);
-    if (live) {
-      for (int e = lane; e < E; e += 32) row_max = fmaxf(row_max, as_float(row[e]));
-      row_max = warp_max(row_max);
-      for (int e = lane; e < E; e += 32) row_sum += ex2((as_float(row[e]) - row_max) * kLog2e);
-      row_sum = warp_sum(row_sum);
+#pragma unroll
+    for (int i = 0; i < V; ++i) row_max = fmaxf(row_max, z[i]);
+    row_max = warp_max(row_max);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      z[i] = ex2((z[i] - row_max) * kLog2e);
+      row_sum += z[i];
     }
-    const float p = share_at(z, got, row_max, NVFP4_ROUTE_SOFTMAX, false, row_sum);
+    row_sum = warp_sum(row_sum);
+    const float p = share_at(mine, got, row_max, NVFP4_ROUTE_SOFTMAX, false, row_sum);
     const float dot = warp_sum(got ? p * g : 0.0f);
-    for (int e = lane; e < E; e += 32) d[e] = 0.0f;
-    __syncwarp();
-    for (int j = 0; j < k; ++j) {
-      const int e = __shfl_sync(kAll, id, j);
-      const float v = __shfl_sync(kAll, g, j);
-      if (e >= 0 && lane == (e & 31)) d[e] += v;
-    }
-    __syncwarp();
+    bool first;
+    const float sum = sum_of_same(id, g, k, 32, &first);
+    const float all = live ? -__fdiv_rn(dot, row_sum) : 0.0f;
     Z* const out = dlogits + t * ldd;
-    for (int e = lane; e < E; e += 32) {
-      put(out + e, live ? __fdiv_rn(ex2((as_float(row[e]) - row_max) * kLog2e), row_sum) * (d[e] - dot) : 0.0f);
+    __syncwarp();   // dlogits may be the logits
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = i * 32 + lane;
+      if (i < V / 2 || e < E) put(out + e, live ? z[i] * all : 0.0f);   // a row without a choice may hold anything
     }
     __syncwarp();
+    if (first) put(out + id, p * (sum - dot));
   }
+}
+
+template <typename Z, int V>
+cudaError_t route_backward_launch_v(const RouteArgs& a, const float* dweights, void* dlogits, int64_t ldd, cudaStream_t st) {
+  const int64_t want = (a.T + kWarps - 1) / kWarps;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(want, static_cast<int64_t>(sm_count()) * 12));
+  return launch_k(route_backward_kernel<Z, V>, dim3(grid), dim3(kWarps * 32), 0, st, 1, a, dweights, static_cast<Z*>(dlogits), ldd);
 }
 
 constexpr int kFillThreads = 256;
@@ -817,17 +875,8 @@ __global__ void __launch_bounds__(kFillThreads) route_backward_sparse_kernel(con
   if (!softmax) p *= z > 0.0f ? __fdiv_rn(expf(-z), 1.0f + expf(-z)) : __fdiv_rn(1.0f, 1.0f + expf(z));
   const float mine = got ? p * g : 0.0f;
   // an expert that is named more than once: the first one puts the sum
-  float sum = 0.0f;
-  bool first = got;
-  for (int j = 0; j < k; ++j) {
-    const int from = (tid & 31 & ~(span - 1)) + j;
-    const int other = __shfl_sync(kAll, id, from);
-    const float v = __shfl_sync(kAll, mine, from);
-    if (other == id) {
-      sum += v;
-      first &= j >= sub;
-    }
-  }
+  bool first;
+  const float sum = sum_of_same(id, mine, k, span, &first);
   __syncthreads();   // dlogits may be the logits
   if (ldd == E && (reinterpret_cast<uintptr_t>(dlogits) & 15) == 0) {
     // rows * E values are whole 16-byte pieces: rows is a multiple of 8
@@ -853,10 +902,12 @@ cudaError_t route_backward_launch_z(const RouteArgs& a, const float* dweights, v
     return launch_k(route_backward_sparse_kernel<Z>, dim3(static_cast<unsigned>((a.T + rows - 1) / rows)), dim3(kFillThreads), 0,
                     st, 1, a, dweights, static_cast<Z*>(dlogits), ldd, span);
   }
-  const int64_t want = (a.T + kWarps - 1) / kWarps;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(want, static_cast<int64_t>(sm_count()) * 16));
-  return launch_k(route_backward_kernel<Z>, dim3(grid), dim3(kWarps * 32), static_cast<size_t>(kWarps) * a.E * sizeof(float),
-                  st, 1, a, dweights, static_cast<Z*>(dlogits), ldd);
+  return a.E <= 32    ? route_backward_launch_v<Z, 1>(a, dweights, dlogits, ldd, st)
+         : a.E <= 64  ? route_backward_launch_v<Z, 2>(a, dweights, dlogits, ldd, st)
+         : a.E <= 128 ? route_backward_launch_v<Z, 4>(a, dweights, dlogits, ldd, st)
+         : a.E <= 256 ? route_backward_launch_v<Z, 8>(a, dweights, dlogits, ldd, st)
+         : a.E <= 512 ? route_backward_launch_v<Z, 16>(a, dweights, dlogits, ldd, st)
+                      : route_backward_launch_v<Z, 32>(a, dweights, dlogits, ldd, st);
 }
 
 }  // namespace

@@ -714,3 +714,50 @@ def test_streams_and_equal_calls(api):
     torch.cuda.synchronize()
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+@pytest.mark.parametrize("P", [1, 9, 20, 30])
+def test_gemv_numbers_far_apart(api, P):
+    """Rows whose numbers lie up to 250 powers of two apart, the largest often
+    next to codes of zero: every product counts, in fp32's range."""
+    N, K = 128, 640
+    W, sW, alpha, w = random_weight(1, N, K, seed=P)
+    g = torch.Generator().manual_seed(P)
+    mant = 1 + torch.randint(0, 128, (P, K), generator=g).double() / 128
+    for kind in range(4):
+        span = ((-120, 100), (-40, 0), (-133, -100), (60, 110))[kind]
+        ex = torch.randint(span[0], span[1] + 1, (P, K), generator=g).double()
+        x64 = mant * torch.pow(2.0, ex)
+        if kind < 2:
+            x64[:, : K // 2] = 0.0                       # and many that are nothing
+        x = x64.to(torch.bfloat16).cuda()
+        y = api.nvfp4_gemv(x, W[0], sW, alpha, out_dtype=1).double().cpu()
+        x64 = x.double().cpu()
+        want, mag = float(alpha[0]) * (x64 @ w[0].t()), float(alpha[0]) * (x64.abs() @ w[0].abs().t())
+        within(y, want, (2 * K + 40) * U * mag + 2.0 ** -126, f"kind {kind}")
+    # one number of 2^100 beside ones of 2^-60: weights of 0 leave the small ones' sum
+    x = torch.full((P, K), 2.0 ** -60, dtype=torch.bfloat16, device="cuda")
+    x[:, 7] = 2.0 ** 100
+    y = api.nvfp4_gemv(x, W[0], sW, alpha, out_dtype=1).double().cpu()
+    x64 = x.double().cpu()
+    want, mag = float(alpha[0]) * (x64 @ w[0].t()), float(alpha[0]) * (x64.abs() @ w[0].abs().t())
+    assert bool((w[0, :, 7] == 0).any())
+    within(y, want, (2 * K + 40) * U * mag, "beside 2^100")
+
+
+def test_gemv_infinities_of_both_kinds_and_numbers_far_apart(api):
+    N, K = 128, 512
+    W, sW, alpha, w = random_weight(1, N, K, seed=77)
+    x = rows_of(5, K, seed=1)
+    x[1, 3], x[2, 300], x[3, 5] = INF, -INF, math.nan
+    x[0, 9] = 2.0 ** -130
+    x[0, 10] = 2.0 ** 120
+    x[4] = 0.0
+    y = api.nvfp4_gemv(x, W[0], sW, alpha, out_dtype=1).cpu()
+    want = float(alpha[0]) * (x.double().cpu() @ w[0].t())
+    for r, k in ((1, 3), (2, 300)):
+        col = w[0, :, k]
+        assert bool((y[r][col != 0] == want[r][col != 0].float()).all()) and bool(torch.isnan(y[r][col == 0]).all())
+    assert bool(torch.isnan(y[3]).all()) and not bool(y[4].any())
+    mag = float(alpha[0]) * (x[0].double().cpu().abs() @ w[0].abs().t())
+    within(y[0], want[0], (2 * K + 40) * U * mag, "row 0")
