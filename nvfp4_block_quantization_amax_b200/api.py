@@ -657,34 +657,35 @@ def nvfp4_lora_backward(dy: torch.Tensor, x: torch.Tensor, h: torch.Tensor, A: t
 # ---------------------------------------------------------------------------
 # Around the experts' products: routing, sorting rows by expert, the way back,
 # and products of a few unquantized rows.  Their small calls are as long as
-# their host path: new tensors come from empty_strided (1.5 us, torch.empty
-# 2.3 us), tensors on another device than the current one take a second call
-# under that device instead of a context around the first, and the library's
-# functions are called without the names in _lib between.
+# their host path: new tensors come from empty_like (1.3 us) and empty_strided
+# (1.5 us; torch.empty 2.3 us), tensors on another device than the current one
+# take a second call under that device instead of a context around the first,
+# and the library's functions are called without the names in _lib between.
 # ---------------------------------------------------------------------------
-def _elsewhere(device) -> bool:
-    """Whether `device`, which must be a GPU, is not the current one."""
-    if device.type != "cuda":
-        raise TypeError(f"the tensors must be CUDA tensors, not on {device}")
-    return _current_device is None or _current_device() != device.index
-
-
 def _new(rows: int, cols: int, dtype, device) -> torch.Tensor:
     return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
+def _elsewhere(device) -> bool:
+    """Whether `device`, a GPU, is not the current one."""
+    return _current_device is None or _current_device() != device.index
+
+
 def _pairs(t: torch.Tensor, dtype, what: str, device):
     """Shape (T, k) of a contiguous tensor of one value per token and choice."""
-    if t.dim() != 2:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, need [T, k]")
-    _need(t, t.shape[0] * t.shape[1], dtype, what, device)
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what}: shape {tuple(shape)}, need [T, k]")
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _need(t, 0, dtype, what, device)
+    return shape
 
 
 def _like_pairs(t: torch.Tensor, shape, dtype, what: str, device):
     if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, need {tuple(shape)}")
-    _need(t, shape[0] * shape[1], dtype, what, device)
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _need(t, 0, dtype, what, device)
 
 
 def _logits(t: torch.Tensor, what: str):
@@ -698,9 +699,10 @@ def _logits(t: torch.Tensor, what: str):
     else:
         raise TypeError(f"{what}: dtype {t.dtype}, expected {torch.float32} or {torch.bfloat16}")
     T, E = t.shape
-    if T and E > 1 and t.stride(1) != 1:
+    stride = t.stride()
+    if T and E > 1 and stride[1] != 1:
         raise ValueError(f"{what} must have unit column stride")
-    return t.stride(0) if T > 1 else E, kind
+    return stride[0] if T > 1 else E, kind
 
 
 def nvfp4_route(logits: torch.Tensor, k: int, score: int = NVFP4_ROUTE_SOFTMAX, flags: int = 0,
@@ -730,8 +732,8 @@ def nvfp4_route(logits: torch.Tensor, k: int, score: int = NVFP4_ROUTE_SOFTMAX, 
     if ids is None:
         ids = _new(T, k, torch.int32, dev)
     if weights is None:
-        weights = _new(T, k, torch.float32, dev)
-    st = L.load().nvfp4_route(logits.data_ptr(), ldl, kind, _p(bias), T, E, k, groups, groups_kept, score, flags, scale,
+        weights = torch.empty_like(ids, dtype=torch.float32)
+    st = (L._lib or L.load()).nvfp4_route(logits.data_ptr(), ldl, kind, _p(bias), T, E, k, groups, groups_kept, score, flags, scale,
                               ids.data_ptr(), weights.data_ptr(), _p(status), _stream_of(dev))
     if st:
         _check(st, "nvfp4_route")
@@ -762,8 +764,8 @@ def nvfp4_route_backward(dweights: torch.Tensor, ids: torch.Tensor, logits: torc
     if status is not None:
         _check_status(status, dev)
     if out is None:
-        out = _new(T, E, logits.dtype, dev)
-    st = L.load().nvfp4_route_backward(dweights.data_ptr(), ids.data_ptr(), logits.data_ptr(), ldl, kind, T, E, shape[1],
+        out = torch.empty_like(logits) if logits.is_contiguous() else _new(T, E, logits.dtype, dev)
+    st = (L._lib or L.load()).nvfp4_route_backward(dweights.data_ptr(), ids.data_ptr(), logits.data_ptr(), ldl, kind, T, E, shape[1],
                                        score, flags, scale, out.data_ptr(), ldd, _p(status), _stream_of(dev))
     if st:
         _check(st, "nvfp4_route_backward")
@@ -802,12 +804,12 @@ def nvfp4_dispatch(x: Optional[torch.Tensor], ids: torch.Tensor, E: int, out: Op
     if status is not None:
         _check_status(status, dev)
     if rows is None:
-        rows = _new(T, k, torch.int32, dev)
+        rows = torch.empty_like(ids)
     if offsets is None:
         offsets = torch.empty_strided((max(E, 0) + 1,), (1,), dtype=torch.int32, device=dev)
     if x is not None and out is None:
         out = _new(T * k, C, torch.bfloat16, dev)
-    st = L.load().nvfp4_dispatch(_p(x), ldx, ids.data_ptr(), T, k, E, C, _p(out), ldo, offsets.data_ptr(), rows.data_ptr(),
+    st = (L._lib or L.load()).nvfp4_dispatch(_p(x), ldx, ids.data_ptr(), T, k, E, C, _p(out), ldo, offsets.data_ptr(), rows.data_ptr(),
                                  _p(status), _stream_of(dev))
     if st:
         _check(st, "nvfp4_dispatch")
@@ -849,8 +851,8 @@ def nvfp4_combine(y: torch.Tensor, rows: Optional[torch.Tensor], weights: Option
     if status is not None:
         _check_status(status, dev)
     if out is None:
-        out = _new(T, C, torch.bfloat16, dev)
-    st = L.load().nvfp4_combine(y.data_ptr(), ldy, R, _p(rows), _p(weights), T, k, C, _p(residual), ldr, out.data_ptr(), ldo,
+        out = torch.empty_like(residual) if residual is not None and residual.is_contiguous() else _new(T, C, torch.bfloat16, dev)
+    st = (L._lib or L.load()).nvfp4_combine(y.data_ptr(), ldy, R, _p(rows), _p(weights), T, k, C, _p(residual), ldr, out.data_ptr(), ldo,
                                 _p(status), _stream_of(dev))
     if st:
         _check(st, "nvfp4_combine")
@@ -886,7 +888,7 @@ def nvfp4_combine_backward(dout: torch.Tensor, rows: Optional[torch.Tensor], wei
     if need_dy and out is None:
         out = _new(R, C, torch.bfloat16, dev)
     dw = _new(shape[0], shape[1], torch.float32, dev) if need_dweights else None
-    st = L.load().nvfp4_combine_backward(dout.data_ptr(), lddo, y.data_ptr(), ldy, R, _p(rows), _p(weights), T, shape[1], C,
+    st = (L._lib or L.load()).nvfp4_combine_backward(dout.data_ptr(), lddo, y.data_ptr(), ldy, R, _p(rows), _p(weights), T, shape[1], C,
                                          _p(out), lddy, _p(dw), _p(status), _stream_of(dev))
     if st:
         _check(st, "nvfp4_combine_backward")
@@ -934,7 +936,7 @@ def nvfp4_gemv(x: torch.Tensor, W: torch.Tensor, sW: torch.Tensor, alphaW: torch
         _need_matrix(out, P, N, dt, "out", dev)
         if P > 1:
             ldo = out.stride(0)
-    st = L.load().nvfp4_gemv(x.data_ptr(), ldx, _p(ids), P, rep or 1, W.data_ptr(), sW.data_ptr(), alphaW.data_ptr(), E, N, K,
+    st = (L._lib or L.load()).nvfp4_gemv(x.data_ptr(), ldx, _p(ids), P, rep or 1, W.data_ptr(), sW.data_ptr(), alphaW.data_ptr(), E, N, K,
                              out.data_ptr(), out_dtype, ldo, _p(status), _stream_of(dev))
     if st:
         _check(st, "nvfp4_gemv")
