@@ -2,8 +2,8 @@
 //
 //   y[p, n] = alpha_e sum_k x[p / rep, k] q[e, n, k] Delta[e, n, k / 16],   e = ids[p]
 //
-// What bounds it is the weight, 0.5625 bytes per value, read once for all rows
-// that need it.  q Delta has at most 6 significant bits (2 of E2M1, 4 of
+// What it cannot do without is the weight, 0.5625 bytes per value, read once for
+// all rows that need it.  q Delta has at most 6 significant bits (2 of E2M1, 4 of
 // E4M3), so it is exact in bf16, and mma.sync m16n8k16 multiplies it with bf16
 // x into fp32: weight rows are the 16 rows of a product, up to 8 x rows its
 // columns.  A warp reads codes straight from memory into the operand's
@@ -16,13 +16,12 @@
 // q 2^-126 (denormals included), by one masked multiply; times Delta 2^118 that
 // is q Delta 2^-8, normal and exact.
 //
-// A CTA takes 32 weight rows, 8 b + g and 32, 64, 96 further of a 128-row
-// atom: with that choice 16 bytes of the scale layout hold the scales of a
-// lane's four rows.  Its 8 warps share out K; their sums are added in order.
+// Two kernels, by the rows that share a weight.  With up to 8 (one column group
+// of a product) x is small beside the weight and is read from memory; with more
+// it is not, and comes once per 128 weight rows.  24 rows, 4096 x 14336: 28 us in
+// the first form (with three column groups), 22 in the second.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <atomic>
@@ -179,29 +178,34 @@ __device__ __forceinline__ void clear_rows(const GemvArgs& a, Out* out, int me, 
   }
 }
 
-template <int NT>
-struct GemvCfg {
-  static constexpr int kDepth = NT == 1 ? 2 : NT == 2 ? 3 : 6;      // chunks of a lane on their way and in use
-  static constexpr int kCtas = NT == 1 ? 3 : NT == 2 ? 2 : 1;       // per SM
-  static constexpr int kParts = NT <= 2 ? 2 : 1;      // copies of the warps' sums
-  struct Smem {
-    uint4 ring[kDepth][kPieces][kThreads];            // every thread copies and reads its own pieces
-    float part[kParts][kWarps][NT * 8][kTileRows + 1];
-    float share[2][NT * 8][kTileRows];                // this CTA's sums, read by its cluster
-    Slots slots;
-  };
+// ---------------------------------------------------------------------------
+// Up to 8 rows of a weight.  A CTA (a cluster of `ranks` CTAs that share out K)
+// takes a run of items; an item is 32 weight rows, 8 b + g and 32, 64, 96
+// further of a 128-row atom, for up to 8 pairs of one expert (a slot), and its 8
+// warps share out K.  Weights stream through a ring of shared memory that every
+// thread fills for itself, across the items' borders, so that no item waits for
+// memory from its beginning.
+// 14336 x 4096, one row: 14.1 us, 2.4 TB/s (weights from memory; 5.05 us at the
+// measured rate).  8 weights of that size, 16 rows: 59 to 67 us, 4.0 to 4.5 TB/s.
+// What bounds it: unpacking, 19 cycles of the logic and multiply pipes per 8
+// codes and warp, 63% busy; next to it the item borders (one CTA's warps meet)
+// and, for one row, 448 items on 444 CTAs.  Two copies of the warps' sums and
+// one barrier less: 70 us (less L1 for x); two CTAs per SM with a deeper ring:
+// 15.8 and 68; four CTAs: 15.3 and 84; x a word ahead: 15.0 and 68.
+// ---------------------------------------------------------------------------
+constexpr int kDepth = 2;   // chunks of a lane on their way and in use
+constexpr int kCtas = 3;    // per SM
+struct Smem {
+  uint4 ring[kDepth][kPieces][kThreads];   // every thread copies and reads its own pieces
+  float part[kWarps][8][kTileRows + 1];
+  float share[2][8][kTileRows];            // this CTA's sums, read by its cluster
+  Slots slots;
 };
 
-// A CTA (a cluster of `ranks` CTAs that share out K) takes a run of items: an
-// item is 32 weight rows for up to 8 NT pairs of one expert, a slot.  Weights
-// stream through a ring of shared memory that every thread fills for itself,
-// across the items' borders.
-template <int NT, typename Out>
-__global__ void __launch_bounds__(kThreads, GemvCfg<NT>::kCtas) gemv_kernel(const __grid_constant__ GemvArgs a) {
-  using Cfg = GemvCfg<NT>;
-  constexpr int kDepth = Cfg::kDepth, kGroup = NT * 8;
+template <typename Out>
+__global__ void __launch_bounds__(kThreads, kCtas) gemv_kernel(const __grid_constant__ GemvArgs a) {
   extern __shared__ __align__(16) uint8_t gemv_smem[];
-  typename Cfg::Smem& sm = *reinterpret_cast<typename Cfg::Smem*>(gemv_smem);
+  Smem& sm = *reinterpret_cast<Smem*>(gemv_smem);
   pdl_entry();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   cg::cluster_group cluster = cg::this_cluster();
@@ -210,9 +214,9 @@ __global__ void __launch_bounds__(kThreads, GemvCfg<NT>::kCtas) gemv_kernel(cons
   const int64_t N = a.N, K = a.K;
   const int tiles = static_cast<int>(N / kTileRows);
   Out* const out = static_cast<Out*>(a.out);
-  int slots = (P + kGroup - 1) / kGroup;
+  int slots = (P + 7) / 8;
   if (a.ids) {
-    slots = find_slots<kGroup>(a, sm.slots, rank == 0);
+    slots = find_slots<8>(a, sm.slots, rank == 0);
     if (rank == 0) clear_rows<kTileRows>(a, out, blockIdx.x / ranks, gridDim.x / ranks);
   }
 
@@ -268,22 +272,16 @@ __global__ void __launch_bounds__(kThreads, GemvCfg<NT>::kCtas) gemv_kernel(cons
   int use = 0, turn = 0;
   for (; left; --left, turn ^= 1) {
     const int e = a.ids ? sm.slots.expert[slot] : 0;
-    const int m0 = a.ids ? sm.slots.begin[e] + sm.slots.pass[slot] * kGroup : slot * kGroup;
-    const int members = min((a.ids ? sm.slots.begin[e + 1] : P) - m0, kGroup);
+    const int m0 = a.ids ? sm.slots.begin[e] + sm.slots.pass[slot] * 8 : slot * 8;
+    const int members = min((a.ids ? sm.slots.begin[e + 1] : P) - m0, 8);
     // columns without a pair read the first one's row; their sums are dropped
-    const __nv_bfloat16* x[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int m = m0 + (i * 8 + g < members ? i * 8 + g : 0);
-      const uint32_t p = a.ids ? sm.slots.pairs[m] : m;
-      x[i] = a.x + static_cast<int64_t>(p / static_cast<uint32_t>(a.rep)) * a.ldx + start * 128 + c * 32;
-    }
-    float acc[NT][2][4] = {};
+    const int column = m0 + (g < members ? g : 0);
+    const uint32_t pair = a.ids ? sm.slots.pairs[column] : column;
+    const __nv_bfloat16* x = a.x + static_cast<int64_t>(pair / static_cast<uint32_t>(a.rep)) * a.ldx + start * 128 + c * 32;
+    float acc[2][4] = {};
     for (int j = 0, kc = start; j < mine; ++j, kc += stride) {
-      if (!tail && kc + 1 == chunks) {   // nothing here: no number in x's place may meet the zero weights
-#pragma unroll
-        for (int i = 0; i < NT; ++i) x[i] = reinterpret_cast<const __nv_bfloat16*>(kNothing);
-      }
+      // nothing here: no number in x's place may meet the zero weights
+      if (!tail && kc + 1 == chunks) x = reinterpret_cast<const __nv_bfloat16*>(kNothing);
       fill();
       asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
       uint32_t u[4][4];
@@ -304,41 +302,28 @@ __global__ void __launch_bounds__(kThreads, GemvCfg<NT>::kCtas) gemv_kernel(cons
       scale_pairs(sw.w, pick, sc[3]);
 #pragma unroll
       for (int word = 0; word < 4; ++word) {
-        uint32_t b[NT][4];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(x[i]) + word);
-          b[i][0] = __byte_perm(v.x, v.z, 0x5410);
-          b[i][1] = __byte_perm(v.x, v.z, 0x7632);
-          b[i][2] = __byte_perm(v.y, v.w, 0x5410);
-          b[i][3] = __byte_perm(v.y, v.w, 0x7632);
-        }
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(x) + word);
+        const uint32_t b[4] = {__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                               __byte_perm(v.y, v.w, 0x7632)};
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           uint32_t lo[4], hi[4];
           decode(u[2 * m][word], sc[2 * m][word >> 1], lo);
           decode(u[2 * m + 1][word], sc[2 * m + 1][word >> 1], hi);
           const uint32_t op0[4] = {lo[0], hi[0], lo[1], hi[1]}, op1[4] = {lo[2], hi[2], lo[3], hi[3]};
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            mma16(acc[i][m], op0, b[i][0], b[i][1]);
-            mma16(acc[i][m], op1, b[i][2], b[i][3]);
-          }
+          mma16(acc[m], op0, b[0], b[1]);
+          mma16(acc[m], op1, b[2], b[3]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < NT; ++i) x[i] += stride * 128;
+      x += stride * 128;
     }
-    auto& part = sm.part[Cfg::kParts == 2 ? turn : 0];
-    if (Cfg::kParts == 1) __syncthreads();   // read until here in the item before
+    __syncthreads();   // part is read until here in the item before
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-          // weight row: 32 (2 m + h / 2) + g; x row 2 c + h % 2 of the group
-          part[warp][i * 8 + 2 * c + (h & 1)][(2 * m + (h >> 1)) * 8 + g] = acc[i][m][h];
+      for (int h = 0; h < 4; ++h)
+        // weight row: 32 (2 m + h / 2) + g; x row 2 c + h % 2
+        sm.part[warp][2 * c + (h & 1)][(2 * m + (h >> 1)) * 8 + g] = acc[m][h];
     __syncthreads();
     const float alpha = __ldg(a.alphaW + e);
     const int64_t n0 = (tile >> 2) * 128ll + (tile & 3) * 8;
@@ -346,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, GemvCfg<NT>::kCtas) gemv_kernel(cons
       const int m = v / kTileRows, r = v % kTileRows;
       float s = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) s += part[i][m][r];
+      for (int i = 0; i < kWarps; ++i) s += sm.part[i][m][r];
       if (ranks > 1) {
         sm.share[turn][m][r] = s;
       } else {
@@ -378,6 +363,9 @@ __global__ void __launch_bounds__(kThreads, GemvCfg<NT>::kCtas) gemv_kernel(cons
 // whole 128-row atom: warp w its quarter w % 4 and, of each 256 values of K, half
 // w / 4; x comes once per CTA, through shared memory.  One item per cluster of
 // `ranks` CTAs, which share out K.
+// 4096 x 14336, 24 rows, fp32: 22 us (5.2 at the measured rate): 520 instructions
+// per 128 values of K and 32 weight rows, 48 of them products, on 256 CTAs, one
+// or two per SM, for 7 stages each between the start and the cluster's sum.
 // ---------------------------------------------------------------------------
 template <int NT>
 struct WideCfg {
@@ -545,19 +533,18 @@ cudaError_t allow_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t>& done)
 
 template <typename Out>
 cudaError_t launch_narrow(const GemvArgs& a, cudaStream_t st) {
-  using Cfg = GemvCfg<1>;
-  constexpr size_t smem = sizeof(typename Cfg::Smem);
+  constexpr size_t smem = sizeof(Smem);
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(gemv_kernel<1, Out>, smem, done);
+  const cudaError_t e = allow_smem(gemv_kernel<Out>, smem, done);
   if (e != cudaSuccess) return e;
   const int64_t slots = a.ids ? std::min(a.P, a.E) : (a.P + 7) / 8;
   const int64_t items = slots * (a.N / kTileRows), chunks = (a.K + 127) / 128;
-  const int64_t room = static_cast<int64_t>(sm_count()) * Cfg::kCtas;
+  const int64_t room = static_cast<int64_t>(sm_count()) * kCtas;
   int ranks = 1;
   while (ranks < 8 && items * ranks * 2 <= room && chunks >= 2 * ranks * kWarps) ranks *= 2;
   const int64_t crowd = std::max<int64_t>(1, std::min(items, room / ranks));
   note_launch();
-  return launch_k(gemv_kernel<1, Out>, dim3(static_cast<unsigned>(crowd * ranks)), dim3(kThreads), smem, st,
+  return launch_k(gemv_kernel<Out>, dim3(static_cast<unsigned>(crowd * ranks)), dim3(kThreads), smem, st,
                   static_cast<unsigned>(ranks), a);
 }
 

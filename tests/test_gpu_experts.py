@@ -117,13 +117,19 @@ def check_route(api, z, k, score, flags, bias=None, groups=1, kept=1, scale=1.0)
     assert torch.equal(ids.cpu(), want), torch.nonzero((ids.cpu() != want).any(1)).view(-1)[:8]
     within(w, w64, share_error(z.double().cpu(), want, score, flags) * w64.abs() + 2.0 ** -149, "weights")
     assert int(status) == 0
+    # the same rows many times over, which may take another kernel
+    times = -(-2100 // z.shape[0])
+    many, wm = api.nvfp4_route(z.repeat(times, 1), k, score, flags, bias=bias, groups=groups, groups_kept=kept, scale=scale, status=status)
+    assert torch.equal(many.cpu(), want.repeat(times, 1)) and int(status) == 0
+    within(wm, w64.repeat(times, 1), (share_error(z.double().cpu(), want, score, flags) * w64.abs() + 2.0 ** -149).repeat(times, 1), "weights")
     return ids, w
 
 
 @pytest.mark.parametrize("T,E,k,groups,kept", [
     (1, 1, 1, 1, 1), (1, 8, 2, 1, 1), (3, 7, 7, 1, 1), (5, 32, 32, 1, 1), (33, 33, 4, 3, 2), (64, 64, 6, 1, 1), (17, 160, 6, 8, 3),
     (40, 256, 8, 8, 4), (9, 100, 10, 4, 2), (130, 128, 5, 32, 7), (6, 512, 22, 1, 1), (4, 1000, 9, 10, 4), (3, 1024, 32, 32, 32),
-    (12, 24, 3, 12, 5), (10, 96, 4, 24, 9), (700, 16, 2, 2, 1)])
+    (12, 24, 3, 12, 5), (10, 96, 4, 24, 9), (700, 16, 2, 2, 1), (90, 512, 8, 8, 3), (60, 257, 8, 1, 1), (70, 72, 8, 8, 1), (80, 200, 7, 5, 4),
+    (50, 500, 3, 4, 4), (64, 40, 8, 8, 2)])
 @pytest.mark.parametrize("score,flags", [(SOFTMAX, 0), (SOFTMAX, RENORM | PAIR), (SIGMOID, PAIR), (SIGMOID, RENORM)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_route_shapes(api, T, E, k, groups, kept, score, flags, dtype):
@@ -207,6 +213,11 @@ def test_route_nonfinite_rows(api, bad):
     want = api.nvfp4_route(z.cuda(), 3)
     z[7, 29] = bad
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    wide = torch.cat([z, z], 1).repeat(150, 1).cuda()              # 60 experts, 3000 tokens
+    ids, w = api.nvfp4_route(wide, 3, status=status)
+    rest = torch.arange(3000) % 20 != 7
+    assert int(status) == -4 and bool((ids[~rest] == -1).all()) and not bool(w[~rest].any()) and bool((ids[rest] >= 0).all())
+    status.zero_()
     ids, w = api.nvfp4_route(z.cuda(), 3, status=status)
     assert int(status) == -4 and ids[7].tolist() == [-1] * 3 and w[7].tolist() == [0.0] * 3
     keep = [t for t in range(20) if t != 7]
@@ -587,6 +598,56 @@ def test_gemv_bad_ids_strides_and_infinities(api):
     assert bool((y[4].cpu()[col > 0] == INF).all()) and bool((y[4].cpu()[col < 0] == -INF).all())
     assert bool(torch.isnan(y[4].cpu()[col == 0]).all())
     assert api.nvfp4_gemv(x[:0], W[0], sW[0], alpha[:1]).shape == (0, 128)
+
+
+# ---------------------------------------------------------------------------
+# sizes past 2^31 elements
+# ---------------------------------------------------------------------------
+def test_rows_past_2_31_elements(api):
+    T, k, C, E = 70000, 8, 4096, 64
+    x = torch.randn((T, C), device="cuda", dtype=torch.bfloat16)
+    ids = (torch.arange(T * k, device="cuda").view(T, k) * 37 % E).to(torch.int32)
+    xs, rows, offsets = api.nvfp4_dispatch(x, ids, E)
+    want_rows, want_offsets = sort_reference(ids.cpu(), E)
+    assert torch.equal(rows.cpu(), want_rows) and torch.equal(offsets.cpu(), want_offsets)
+    at = torch.tensor([0, 1, T // 2, T - 2, T - 1], device="cuda")
+    assert torch.equal(xs[rows[at].long()], x[at].unsqueeze(1).expand(-1, k, -1))
+    w = torch.full((T, k), 0.125, device="cuda")
+    assert torch.equal(api.nvfp4_combine(xs, rows, w), x)         # eight eighths, exact
+    dy, dw = api.nvfp4_combine_backward(x, rows, w, xs, out=xs.new_zeros(xs.shape))
+    assert torch.equal(dy[rows[at].long()], (x[at] * 0.125).unsqueeze(1).expand(-1, k, -1))
+    want = x[at].double().square()
+    within(dw[at], want.sum(1, keepdim=True).expand(-1, k).cpu(), (C + 32) * U * want.sum(1, keepdim=True).expand(-1, k).cpu(), "dweights")
+
+
+def test_logits_past_2_31_elements(api):
+    T, E = (1 << 23) + 1000, 256
+    few = logits_of(512, E, torch.bfloat16, seed=1).cuda()
+    z = torch.empty((T, E), dtype=torch.bfloat16, device="cuda")
+    z[-512:] = few
+    z[:-512] = 0.0
+    ids, w = api.nvfp4_route(z, 4)
+    a, b = api.nvfp4_route(few, 4)
+    assert torch.equal(ids[-512:], a) and torch.allclose(w[-512:], b, rtol=64 * U, atol=0) and ids[0].tolist() == [0, 1, 2, 3]
+    dw = torch.ones((T, 4), device="cuda")
+    dw[:, 1:] = 0.5
+    for flags in (0, RENORM):
+        d = api.nvfp4_route_backward(dw, ids, z, flags=flags)
+        assert torch.equal(d[-512:], api.nvfp4_route_backward(dw[-512:], a, few, flags=flags))
+
+
+def test_weights_past_2_31_bytes(api):
+    E, N, K = 76, 14336, 4096
+    W = torch.randint(0, 256, (E, N, K // 2), device="cuda", dtype=torch.uint8)
+    sW = torch.randint(40, 70, (E, N * K // 16), device="cuda", dtype=torch.uint8)
+    alpha = torch.full((E,), 1e-3, device="cuda")
+    ids = torch.tensor([[E - 1, 0], [E - 1, 40]], dtype=torch.int32, device="cuda")
+    x = rows_of(2, K, seed=1)
+    y = api.nvfp4_gemv(x, W, sW, alpha, ids=ids, out_dtype=1)
+    for t in range(2):
+        for j in range(2):
+            e = int(ids[t, j])
+            assert torch.equal(y[2 * t + j], api.nvfp4_gemv(x[t:t + 1], W[e].clone(), sW[e].clone(), alpha[:1], out_dtype=1)[0])
 
 
 # ---------------------------------------------------------------------------
