@@ -113,7 +113,7 @@ __device__ __noinline__ int choose_exactly(const Z* __restrict__ z, const RouteA
     for (int e = lane; e < E; e += 32) sum += exp(static_cast<double>(as_float(z[e])) - m);
     sum = warp_sum(sum);
   }
-#pragma unroll 4
+#pragma unroll 8
   for (int e = lane; e < E; e += 32) {
     const float v = as_float(z[e]);
     double s = v;
@@ -147,11 +147,14 @@ __device__ __noinline__ int choose_exactly(const Z* __restrict__ z, const RouteA
     }
     kept = __ballot_sync(kAll, g < G && better < a.kept);
   }
-  unsigned long long best = 0ull;   // this lane's largest, and its expert
+  // values as ordered numbers, and this lane's largest with its expert
+  unsigned long long* const key = reinterpret_cast<unsigned long long*>(c);
+  unsigned long long best = 0ull;
   int at = E;
+#pragma unroll 4
   for (int e = lane; e < E; e += 32) {
-    if (!(kept >> (e / n * lanes & 31) & 1u)) c[e] = none;
-    const unsigned long long v = ordered(c[e]);
+    const unsigned long long v = kept >> (e / n * lanes & 31) & 1u ? ordered(c[e]) : 0ull;
+    key[e] = v;
     if (v > best) {
       best = v;
       at = e;
@@ -165,12 +168,12 @@ __device__ __noinline__ int choose_exactly(const Z* __restrict__ z, const RouteA
     const int e = __reduce_min_sync(kAll, high == top && lo == next ? at : E);
     if (lane == j) mine = e;
     if (at == e) {
-      c[e] = none;
+      key[e] = 0ull;
       best = 0ull;
       at = E;
-#pragma unroll 4
+#pragma unroll 8
       for (int i = lane; i < E; i += 32) {
-        const unsigned long long v = ordered(c[i]);
+        const unsigned long long v = key[i];
         if (v > best) {
           best = v;
           at = i;
@@ -207,10 +210,13 @@ __device__ __forceinline__ float error_of(bool softmax, float share, float most_
   return (softmax ? 0x1p-18f * share : 0x1.8p-22f) + 0x1.1p-24f * most_c + FLT_MIN;
 }
 
-// What a row that has to be chosen in 64 bits holds in the place of its first
-// choice until then.  Such rows wait until a warp has been through its others:
-// the code for them would cost those registers.
-constexpr int kDoubtful = -2;
+// Rows that have to be looked at in 64 bits wait until a warp has been through
+// its others (the code for them would cost those registers).  Until then the
+// first choice holds a mark: kDoubtful, if the row has to be chosen again, or
+// mark - e for a first choice e, if the choices, and the expert behind them,
+// whose number lies in the place of the first weight, only have to be put in
+// order.
+constexpr int kDoubtful = -2, kMark = -3;
 
 template <typename Z>
 __device__ __noinline__ void finish_exactly(const RouteArgs& a, int64_t t, double* c, int lane) {
@@ -235,6 +241,63 @@ __device__ __noinline__ void finish_exactly(const RouteArgs& a, int64_t t, doubl
   __syncwarp();   // c is free
 }
 
+// Put the choices of a row and the expert behind them in order, by their values
+// in 64 bits; c: 32 numbers of shared memory.  2.7 us (choose_exactly and the
+// weights, 256 experts: 5).  No softmax scores with a bias or groups: they need
+// the whole row.
+template <typename Z>
+__device__ __noinline__ void settle(const RouteArgs& a, int64_t t, double* c, int lane) {
+  const Z* const row = static_cast<const Z*>(a.logits) + t * a.ldl;
+  const int k = static_cast<int>(a.k);
+  const bool direct = !a.bias && a.groups == 1, softmax = a.score == NVFP4_ROUTE_SOFTMAX, renorm = a.flags & NVFP4_ROUTE_RENORM;
+  int e[2] = {lane < k ? a.ids[t * k + lane] : -1, __float_as_int(a.weights[t * k])};   // of this lane, and the last one
+  if (lane == 0) e[0] = kMark - e[0];
+  double v[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool is = e[i] >= 0;
+    v[i] = is ? as_float(row[e[i]]) : 0.0f;
+    if (!direct) v[i] = 1.0 / (1.0 + exp(-v[i])) + (is && a.bias ? __ldg(a.bias + e[i]) : 0.0f);
+    if (!is) v[i] = -INFINITY;
+  }
+  const auto before = [](double x, int ex, double y, int ey) { return x > y || (x == y && ex < ey); };
+  int better = before(v[1], e[1], v[0], e[0]);
+  for (int j = 0; j < k; ++j) {
+    const double o = __shfl_sync(kAll, v[0], j);
+    const int eo = __shfl_sync(kAll, e[0], j);
+    better += eo >= 0 && before(o, eo, v[0], e[0]);
+  }
+  int* const order = reinterpret_cast<int*>(c);
+  const int place = __popc(__ballot_sync(kAll, e[0] >= 0 && before(v[0], e[0], v[1], e[1])));   // of the last one
+  order[lane] = -1;
+  __syncwarp();
+  if (e[0] >= 0 && better < k) order[better] = e[0];
+  if (lane == 0 && e[1] >= 0 && place < k) order[place] = e[1];
+  __syncwarp();
+  const int mine = lane < k ? order[lane] : -1;
+  float row_max = -INFINITY, row_sum = 0.0f;
+  if (softmax && !renorm) {
+    for (int i = lane; i < a.E; i += 32) row_max = fmaxf(row_max, as_float(row[i]));
+    row_max = warp_max(row_max);
+    for (int i = lane; i < a.E; i += 32) row_sum += ex2((as_float(row[i]) - row_max) * kLog2e);
+    row_sum = warp_sum(row_sum);
+  }
+  const bool got = mine >= 0;
+  const float share = share_of(got ? as_float(row[mine]) : 0.0f, got, a.score, renorm, row_max, row_sum);
+  const float sum = renorm ? warp_sum(share) : 1.0f;
+  if (lane < k) {
+    a.ids[t * k + lane] = mine;
+    a.weights[t * k + lane] = got ? a.scale * (renorm ? __fdiv_rn(share, sum) : share) : 0.0f;
+  }
+  __syncwarp();   // c is free
+}
+
+template <typename Z>
+__device__ __forceinline__ void finish(const RouteArgs& a, int64_t t, int mark, double* c, int lane) {
+  if (mark == kDoubtful) finish_exactly<Z>(a, t, c, lane);
+  else settle<Z>(a, t, c, lane);
+}
+
 // V: values per lane, the power of two from E / 32 on.  kDirect: no bias and
 // no groups, so that the order is that of the logits themselves.
 //
@@ -255,7 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRouteCtas<V>) route_kernel(const
   pdl_entry();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = static_cast<int>(a.E), k = static_cast<int>(a.k), G = static_cast<int>(a.groups), n = E / G;
-  double* const c64 = route_smem + static_cast<size_t>(warp) * E;
+  double* const c64 = route_smem + static_cast<size_t>(warp) * max(E, 16);   // E values, or 32 numbers
   float* const c32 = reinterpret_cast<float*>(c64);   // padded: expert e at e + e / 32 <= 2 E - 1
   const Z* const logits = static_cast<const Z*>(a.logits);
   const float low = lowest<Z>();
@@ -412,8 +475,11 @@ __global__ void __launch_bounds__(kWarps * 32, kRouteCtas<V>) route_kernel(const
     bool spent = false;        // second is no longer known
     uint32_t my_key = 0u, w = 0u;   // lane j: the j-th choice's
     int my_src = 0, src = 0;
-    for (int j = 0; j <= k; ++j) {
-      w = __reduce_max_sync(kAll, top);
+    uint32_t behind = 0u;   // the key behind the last choice's next
+    for (int j = 0; j <= k + 1; ++j) {
+      behind = __reduce_max_sync(kAll, top);
+      if (j > k) break;
+      w = behind;
       if (w == 0u) break;
       src = __ffs(__ballot_sync(kAll, top == w)) - 1;
       if (lane == j) {
@@ -450,7 +516,18 @@ __global__ void __launch_bounds__(kWarps * 32, kRouteCtas<V>) route_kernel(const
       unsure = !(as_float(row[mine]) == as_float(row[next]) && (kDirect || !a.bias || __ldg(a.bias + mine) == __ldg(a.bias + next)));
     }
     if (near || __any_sync(kAll, unsure)) {
-      if (lane == 0) a.ids[t * k] = kDoubtful;
+      // the choices and the next one are all there is to it where what is behind
+      // them is further below; softmax values need the whole row
+      const uint32_t last = __shfl_sync(kAll, my_key, k - 1);
+      const bool whole_row = near || (!kDirect && softmax) ||
+                             (last && behind && (kDirect ? (last ^ behind) < static_cast<uint32_t>(V)
+                                                         : !(from_ordered(last) - from_ordered(behind) > 2.0f * delta)));
+      const int next = w ? (V - 1 - static_cast<int>(w & (V - 1))) * 32 + src : -1;
+      if (lane < k && !whole_row) a.ids[t * k + lane] = lane ? mine : kMark - mine;
+      if (lane == 0) {
+        if (whole_row) a.ids[t * k] = kDoubtful;
+        a.weights[t * k] = __int_as_float(next);
+      }
       doubts = true;
       continue;
     }
@@ -466,8 +543,10 @@ __global__ void __launch_bounds__(kWarps * 32, kRouteCtas<V>) route_kernel(const
   }
   if (doubts) {
     __syncwarp();
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.T; t += static_cast<int64_t>(gridDim.x) * kWarps)
-      if (__shfl_sync(kAll, lane == 0 ? a.ids[t * k] : 0, 0) == kDoubtful) finish_exactly<Z>(a, t, c64, lane);
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.T; t += static_cast<int64_t>(gridDim.x) * kWarps) {
+      const int mark = __shfl_sync(kAll, lane == 0 ? a.ids[t * k] : 0, 0);
+      if (mark <= kDoubtful) finish<Z>(a, t, mark, c64, lane);
+    }
   }
 }
 // error_of.  ex2.approx and rcp.approx are off by 2^-22 and 2^-23 relative;
@@ -491,7 +570,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRouteCtas<V>) route_kernel(const
 constexpr int kShare = 8;                 // lanes of a row
 constexpr int kRowsOfWarp = 32 / kShare;
 template <int V>
-constexpr int kManyCtas = V <= 16 ? 7 : V == 32 ? 5 : 4;   // per SM
+constexpr int kManyCtas = V <= 16 ? 7 : 5;   // per SM
 
 __device__ __forceinline__ float share_sum(float v) {
 #pragma unroll
@@ -642,11 +721,13 @@ __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(c
       l2 = max(l2, d1);
       l3 = max(l3, d2);
     }
-    uint32_t my_key = 0u, w = 0u;
-    for (int j = 0; j <= k; ++j) {
-      w = l0;
+    uint32_t my_key = 0u, w = 0u, behind = 0u;   // behind: the key behind the last choice's next
+    for (int j = 0; j <= k + 1; ++j) {
+      behind = l0;
 #pragma unroll
-      for (int o = kShare / 2; o; o >>= 1) w = max(w, __shfl_xor_sync(kAll, w, o));
+      for (int o = kShare / 2; o; o >>= 1) behind = max(behind, __shfl_xor_sync(kAll, behind, o));
+      if (j > k) break;
+      w = behind;
       const unsigned held = __ballot_sync(kAll, l0 == w);
       if (sub == j) my_key = w;
       if (l0 == w && !(held & before)) {
@@ -692,6 +773,11 @@ __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(c
     // its vote also parts the uses of values
     const bool later = ((__ballot_sync(kAll, unsure) >> (lane & 24) & 0xFFu) || near) && !bad;   // of the row
     doubts |= later;
+    const uint32_t last = __shfl_sync(kAll, my_key, (lane & 24) + k - 1);
+    // as in the kernel above
+    const bool whole_row = near || (!kDirect && softmax) ||
+                           (last && behind && (kDirect ? (last ^ behind) < static_cast<uint32_t>(V)
+                                                       : !(from_ordered(last) - from_ordered(behind) > 2.0f * delta)));
     if (bad) mine = -1;
     const bool got = mine >= 0;
     const float z = got ? as_float(row[mine]) : 0.0f;
@@ -701,19 +787,25 @@ __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(c
     if (t0 + r < a.T) {
       if (bad && sub == 0 && a.status) *a.status = kStatusNonFinite;
       if (later) {
-        if (sub == 0) a.ids[t * k] = kDoubtful;
+        if (sub < k) a.ids[t * k + sub] = sub ? mine : whole_row ? kDoubtful : kMark - mine;
+        if (sub == 0) a.weights[t * k] = __int_as_float(w ? (V - 1 - static_cast<int>(w & (V - 1))) * kShare + holder[warp][r][k] : -1);
       } else if (sub < k) {
         a.ids[t * k + sub] = mine;
         a.weights[t * k + sub] = got ? a.scale * (renorm ? __fdiv_rn(share, sum) : share) : 0.0f;
       }
     }
   }
-  if (__any_sync(kAll, doubts))
+  if (__any_sync(kAll, doubts)) {
+    __syncwarp();
     for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRowsOfWarp; t0 < a.T;
          t0 += static_cast<int64_t>(gridDim.x) * (kWarps * kRowsOfWarp)) {
-      unsigned rows = __ballot_sync(kAll, sub == 0 && t0 + r < a.T && a.ids[(t0 + r) * k] == kDoubtful);
-      for (; rows; rows &= rows - 1u) finish_exactly<Z>(a, t0 + (__ffs(rows) - 1) / kShare, values[warp], lane);
+      const int mark = sub == 0 && t0 + r < a.T ? a.ids[(t0 + r) * k] : 0;
+      for (unsigned rows = __ballot_sync(kAll, mark <= kDoubtful); rows; rows &= rows - 1u) {
+        const int from = __ffs(rows) - 1;
+        finish<Z>(a, t0 + from / kShare, __shfl_sync(kAll, mark, from), values[warp], lane);
+      }
     }
+  }
 }
 
 template <typename Z, int V>
@@ -733,7 +825,7 @@ constexpr int64_t kManyRows = 2048;
 template <typename Z, int V>
 cudaError_t route_launch_v(const RouteArgs& a, cudaStream_t st) {
   const bool direct = !a.bias && a.groups == 1;
-  const size_t smem = static_cast<size_t>(kWarps) * a.E * sizeof(double);
+  const size_t smem = static_cast<size_t>(kWarps) * std::max<int64_t>(a.E, 16) * sizeof(double);
   const int64_t want = (a.T + kWarps - 1) / kWarps;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(want, static_cast<int64_t>(sm_count()) * kRouteCtas<V>));
   note_launch();
@@ -743,11 +835,10 @@ cudaError_t route_launch_v(const RouteArgs& a, cudaStream_t st) {
 
 template <typename Z>
 cudaError_t route_launch_z(const RouteArgs& a, cudaStream_t st) {
-  if (a.T >= kManyRows && a.k <= kShare && a.groups <= kShare && a.E > 32 && a.E <= 512)
+  if (a.T >= kManyRows && a.k <= kShare && a.groups <= kShare && a.E > 32 && a.E <= 256)
     return a.E <= 64    ? route_many_launch_v<Z, 8>(a, st)
            : a.E <= 128 ? route_many_launch_v<Z, 16>(a, st)
-           : a.E <= 256 ? route_many_launch_v<Z, 32>(a, st)
-                        : route_many_launch_v<Z, 64>(a, st);
+                        : route_many_launch_v<Z, 32>(a, st);
   return a.E <= 32    ? route_launch_v<Z, 1>(a, st)
          : a.E <= 64  ? route_launch_v<Z, 2>(a, st)
          : a.E <= 128 ? route_launch_v<Z, 4>(a, st)

@@ -167,6 +167,30 @@ def test_route_orders_values_that_32_bits_cannot(api, score, base):
     check_route(api, z, 8, score, 0)
 
 
+@pytest.mark.parametrize("E,k,groups,kept", [(5, 2, 1, 1), (64, 8, 1, 1), (64, 4, 8, 3), (256, 8, 8, 4), (300, 20, 1, 1), (600, 32, 1, 1)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_pairs_that_32_bits_cannot_part(api, E, k, groups, kept, biased):
+    """One pair of neighbours in each row, among the choices or at their end,
+    whose values are a few 2^-27 apart or equal, in either order."""
+    g = torch.Generator().manual_seed(E + k)
+    T = 250
+    z = torch.argsort(torch.rand((T, E), generator=g), 1).float() * (8.0 / E) - 4.0    # far apart
+    bias = torch.randn(E, generator=g) * 0.1 if biased else None
+    b64 = bias.double() if biased else torch.zeros(E, dtype=torch.float64)
+    sig = biased or groups > 1
+    c = (1 / (1 + torch.exp(-z.double())) if sig else z.double()) + b64
+    order = torch.argsort(c, 1, descending=True)
+    for t in range(T):
+        r = min(t % (k + 1), E - 2)
+        first, second = int(order[t, r]), int(order[t, r + 1])
+        target = c[t, first] - b64[second] + (t % 5 - 2) * 2.0 ** -27
+        if sig and not 0 < target < 1:
+            continue
+        z[t, second] = torch.log(target / (1 - target)).float() if sig else z[t, first] * (1 + (t % 5 - 2) * 2.0 ** -23)
+    check_route(api, z, k, SIGMOID, RENORM, bias=bias, groups=groups, kept=kept)
+    check_route(api, z, k, SOFTMAX, 0, bias=bias, groups=groups, kept=kept)
+
+
 @pytest.mark.parametrize("score,flags", [(SOFTMAX, 0), (SOFTMAX, RENORM), (SIGMOID, 0), (SIGMOID, RENORM)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_route_far_logits(api, score, flags, dtype):
