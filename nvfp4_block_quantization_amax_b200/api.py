@@ -13,7 +13,8 @@ from . import _lib as L
 from ._lib import (NVFP4_ALPHA_PROVIDED, NVFP4_AMAX_PROVIDED, NVFP4_BLOCK2D, NVFP4_COLWISE, NVFP4_FOUR_SIX,  # noqa: F401
                    NVFP4_GEMM_SCALE_LAYOUT, NVFP4_HEADROOM, NVFP4_INVERSE_RHT, NVFP4_MS_EDEN, NVFP4_OUT_BF16,
                    NVFP4_OUT_DTYPE_BF16, NVFP4_OUT_DTYPE_FP32, NVFP4_RHT, NVFP4_RHT_SR, NVFP4_RHT_SR_HW,
-                   NVFP4_ROUTE_GROUP_PAIR, NVFP4_ROUTE_RENORM, NVFP4_ROUTE_SIGMOID, NVFP4_ROUTE_SOFTMAX, NVFP4_ROWWISE, NVFP4_RTN, NVFP4_SINGLE_PASS, NVFP4_VECTOR_SCALES)
+                   NVFP4_ROUTE_GROUP_PAIR, NVFP4_ROUTE_RENORM, NVFP4_ROUTE_SIGMOID, NVFP4_ROUTE_SOFTMAX,
+                   NVFP4_ROWWISE, NVFP4_RTN, NVFP4_SINGLE_PASS, NVFP4_VECTOR_SCALES)
 
 
 class NVFP4Error(RuntimeError):
@@ -733,8 +734,9 @@ def nvfp4_route(logits: torch.Tensor, k: int, score: int = NVFP4_ROUTE_SOFTMAX, 
         ids = _new(T, k, torch.int32, dev)
     if weights is None:
         weights = torch.empty_like(ids, dtype=torch.float32)
-    st = (L._lib or L.load()).nvfp4_route(logits.data_ptr(), ldl, kind, _p(bias), T, E, k, groups, groups_kept, score, flags, scale,
-                              ids.data_ptr(), weights.data_ptr(), _p(status), _stream_of(dev))
+    st = (L._lib or L.load()).nvfp4_route(
+        logits.data_ptr(), ldl, kind, _p(bias), T, E, k, groups, groups_kept, score, flags, scale, ids.data_ptr(),
+        weights.data_ptr(), _p(status), _stream_of(dev))
     if st:
         _check(st, "nvfp4_route")
     return ids, weights
@@ -765,8 +767,9 @@ def nvfp4_route_backward(dweights: torch.Tensor, ids: torch.Tensor, logits: torc
         _check_status(status, dev)
     if out is None:
         out = torch.empty_like(logits) if logits.is_contiguous() else _new(T, E, logits.dtype, dev)
-    st = (L._lib or L.load()).nvfp4_route_backward(dweights.data_ptr(), ids.data_ptr(), logits.data_ptr(), ldl, kind, T, E, shape[1],
-                                       score, flags, scale, out.data_ptr(), ldd, _p(status), _stream_of(dev))
+    st = (L._lib or L.load()).nvfp4_route_backward(
+        dweights.data_ptr(), ids.data_ptr(), logits.data_ptr(), ldl, kind, T, E, shape[1], score, flags, scale,
+        out.data_ptr(), ldd, _p(status), _stream_of(dev))
     if st:
         _check(st, "nvfp4_route_backward")
     return out
@@ -809,8 +812,9 @@ def nvfp4_dispatch(x: Optional[torch.Tensor], ids: torch.Tensor, E: int, out: Op
         offsets = torch.empty_strided((max(E, 0) + 1,), (1,), dtype=torch.int32, device=dev)
     if x is not None and out is None:
         out = _new(T * k, C, torch.bfloat16, dev)
-    st = (L._lib or L.load()).nvfp4_dispatch(_p(x), ldx, ids.data_ptr(), T, k, E, C, _p(out), ldo, offsets.data_ptr(), rows.data_ptr(),
-                                 _p(status), _stream_of(dev))
+    st = (L._lib or L.load()).nvfp4_dispatch(
+        _p(x), ldx, ids.data_ptr(), T, k, E, C, _p(out), ldo, offsets.data_ptr(), rows.data_ptr(), _p(status),
+        _stream_of(dev))
     if st:
         _check(st, "nvfp4_dispatch")
     return out, rows, offsets
@@ -851,16 +855,20 @@ def nvfp4_combine(y: torch.Tensor, rows: Optional[torch.Tensor], weights: Option
     if status is not None:
         _check_status(status, dev)
     if out is None:
-        out = torch.empty_like(residual) if residual is not None and residual.is_contiguous() else _new(T, C, torch.bfloat16, dev)
-    st = (L._lib or L.load()).nvfp4_combine(y.data_ptr(), ldy, R, _p(rows), _p(weights), T, k, C, _p(residual), ldr, out.data_ptr(), ldo,
-                                _p(status), _stream_of(dev))
+        if residual is not None and residual.is_contiguous():
+            out = torch.empty_like(residual)
+        else:
+            out = _new(T, C, torch.bfloat16, dev)
+    st = (L._lib or L.load()).nvfp4_combine(
+        y.data_ptr(), ldy, R, _p(rows), _p(weights), T, k, C, _p(residual), ldr, out.data_ptr(), ldo, _p(status),
+        _stream_of(dev))
     if st:
         _check(st, "nvfp4_combine")
     return out
 
 
-def nvfp4_combine_backward(dout: torch.Tensor, rows: Optional[torch.Tensor], weights: Optional[torch.Tensor], y: torch.Tensor,
-                           need_dy: bool = True, need_dweights: bool = True, out: Optional[torch.Tensor] = None,
+def nvfp4_combine_backward(dout: torch.Tensor, rows: Optional[torch.Tensor], weights: Optional[torch.Tensor],
+                           y: torch.Tensor, need_dy: bool = True, need_dweights: bool = True, out: Optional[torch.Tensor] = None,
                            status: Optional[torch.Tensor] = None):
     """Gradients of nvfp4_combine for dout [T, C]: returns (dy [R, C], dweights
     [T, k]), None in the place of one that is not needed.  rows, weights and y
@@ -888,8 +896,9 @@ def nvfp4_combine_backward(dout: torch.Tensor, rows: Optional[torch.Tensor], wei
     if need_dy and out is None:
         out = _new(R, C, torch.bfloat16, dev)
     dw = _new(shape[0], shape[1], torch.float32, dev) if need_dweights else None
-    st = (L._lib or L.load()).nvfp4_combine_backward(dout.data_ptr(), lddo, y.data_ptr(), ldy, R, _p(rows), _p(weights), T, shape[1], C,
-                                         _p(out), lddy, _p(dw), _p(status), _stream_of(dev))
+    st = (L._lib or L.load()).nvfp4_combine_backward(
+        dout.data_ptr(), lddo, y.data_ptr(), ldy, R, _p(rows), _p(weights), T, shape[1], C, _p(out), lddy, _p(dw),
+        _p(status), _stream_of(dev))
     if st:
         _check(st, "nvfp4_combine_backward")
     return out, dw
@@ -936,8 +945,9 @@ def nvfp4_gemv(x: torch.Tensor, W: torch.Tensor, sW: torch.Tensor, alphaW: torch
         _need_matrix(out, P, N, dt, "out", dev)
         if P > 1:
             ldo = out.stride(0)
-    st = (L._lib or L.load()).nvfp4_gemv(x.data_ptr(), ldx, _p(ids), P, rep or 1, W.data_ptr(), sW.data_ptr(), alphaW.data_ptr(), E, N, K,
-                             out.data_ptr(), out_dtype, ldo, _p(status), _stream_of(dev))
+    st = (L._lib or L.load()).nvfp4_gemv(
+        x.data_ptr(), ldx, _p(ids), P, rep or 1, W.data_ptr(), sW.data_ptr(), alphaW.data_ptr(), E, N, K, out.data_ptr(),
+        out_dtype, ldo, _p(status), _stream_of(dev))
     if st:
         _check(st, "nvfp4_gemv")
     return out

@@ -407,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_wide_kernel(const __grid_con
   const int m0 = a.ids ? sm.slots.begin[e] + sm.slots.pass[slot] * kGroup : slot * kGroup;
   const int members = min((a.ids ? sm.slots.begin[e + 1] : static_cast<int>(a.P)) - m0, kGroup);
   const int stages = static_cast<int>((K + 255) / 256);
-  const int from = static_cast<int>(static_cast<int64_t>(stages) * rank / ranks), to = static_cast<int>(static_cast<int64_t>(stages) * (rank + 1) / ranks);
+  const int from = static_cast<int>(static_cast<int64_t>(stages) * rank / ranks);
+  const int to = static_cast<int>(static_cast<int64_t>(stages) * (rank + 1) / ranks);
 
   const int row0 = (warp & 3) * 8 + g;   // of the atom; its others 32, 64, 96 further
   const uint8_t* codes = a.W + (e * N + atom * 128ll + row0) * (K / 2) + (from * 2ll + part) * 64 + c * 16;
