@@ -54,7 +54,8 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 
 // Two E4M3 bytes of a word, picked by a byte selector, as bf16 pairs (each in
 // both halves) times 2^118: a byte's bits e e e e, m m m at a bf16's bits 10 .. 7,
-// 6 .. 4 are Delta 2^-120, denormals included.
+// 6 .. 4 are Delta 2^-120, denormals included (0x7F, which no quantizer writes,
+// would be 480, not NaN).
 __device__ __forceinline__ void scale_pairs(uint32_t word, uint32_t pick, uint32_t* s) {
   constexpr uint32_t up = 0x7B007B00u;   // 2^119 twice
   const uint32_t v = mul2(mul2(__byte_perm(word, 0u, pick) << 4, up), up);
