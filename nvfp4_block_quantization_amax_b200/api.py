@@ -3,6 +3,7 @@ memory and the current stream are the only things torch supplies) and call
 libnvfp4.so.  Every step of the computation runs in the library's kernels.
 """
 import contextlib
+import ctypes
 import math
 from dataclasses import dataclass
 from typing import Optional
@@ -663,6 +664,26 @@ def nvfp4_lora_backward(dy: torch.Tensor, x: torch.Tensor, h: torch.Tensor, A: t
 # take a second call under that device instead of a context around the first,
 # and the library's functions are called without the names in _lib between.
 # ---------------------------------------------------------------------------
+_fast = None
+
+
+def _load_fast():
+    """The small calls' C++ host path, with the library's entry points.  Its
+    functions return the results, a status, or None where a call is not of the
+    plain form: then the checks below say what is wrong, or make the call."""
+    global _fast
+    lib = L.load()
+    try:
+        from . import _fastcall
+    except ImportError as e:
+        raise RuntimeError("_fastcall.so is missing or of another torch: build it with "
+                           "nvfp4_block_quantization_amax_b200/build.py") from e
+    names = ("route", "route_backward", "dispatch", "combine", "combine_backward", "gemv")
+    _fastcall.use(*(ctypes.cast(getattr(lib, "nvfp4_" + n), ctypes.c_void_p).value for n in names))
+    _fast = _fastcall
+    return _fast
+
+
 def _new(rows: int, cols: int, dtype, device) -> torch.Tensor:
     return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
@@ -716,6 +737,11 @@ def nvfp4_route(logits: torch.Tensor, k: int, score: int = NVFP4_ROUTE_SOFTMAX, 
     for the choice alone; groups / groups_kept restrict it to the best groups
     of experts; flags: NVFP4_ROUTE_RENORM, NVFP4_ROUTE_GROUP_PAIR.  Experts
     with a logit of -inf are never chosen; -1 stands where none is left."""
+    done = (_fast or _load_fast()).route(logits, k, score, flags, bias, groups, groups_kept, scale, ids, weights, status)
+    if done.__class__ is tuple:
+        return done
+    if done is not None:
+        _check(done, "nvfp4_route")
     ldl, kind = _logits(logits, "logits")
     dev = logits.device
     if _elsewhere(dev):
@@ -748,6 +774,11 @@ def nvfp4_route_backward(dweights: torch.Tensor, ids: torch.Tensor, logits: torc
     """Gradient of nvfp4_route's weights with respect to the logits ([T, E],
     the logits' type) for dweights [T, k]; ids, score, flags and scale as in
     the forward call.  out may be the logits."""
+    done = (_fast or _load_fast()).route_backward(dweights, ids, logits, score, flags, scale, out, status)
+    if done.__class__ is tuple:
+        return done[0]
+    if done is not None:
+        _check(done, "nvfp4_route_backward")
     ldl, kind = _logits(logits, "logits")
     dev = logits.device
     if _elsewhere(dev):
@@ -783,6 +814,11 @@ def nvfp4_dispatch(x: Optional[torch.Tensor], ids: torch.Tensor, E: int, out: Op
     nvfp4_quantize_grouped, rows those of nvfp4_combine.  Rows of xs from
     offsets[E] on are left as they are (unspecified in a new tensor).  Without
     x only rows and offsets are computed (xs is None)."""
+    done = (_fast or _load_fast()).dispatch(x, ids, E, out, rows, offsets, status)
+    if done.__class__ is tuple:
+        return done
+    if done is not None:
+        _check(done, "nvfp4_dispatch")
     if not ids.is_cuda:
         raise TypeError("ids must be a 2D int32 CUDA tensor")
     dev = ids.device
@@ -841,6 +877,11 @@ def nvfp4_combine(y: torch.Tensor, rows: Optional[torch.Tensor], weights: Option
     returned them (-1: nothing), or None: y's rows are those of the pairs in
     order, as nvfp4_gemv returns them; weights [T, k] fp32, or all 1; residual
     optional, may be out.  Without weights it is nvfp4_dispatch's gradient."""
+    done = (_fast or _load_fast()).combine(y, rows, weights, residual, out, status)
+    if done.__class__ is tuple:
+        return done[0]
+    if done is not None:
+        _check(done, "nvfp4_combine")
     if y.dtype != torch.bfloat16 or y.dim() != 2 or not y.is_cuda:
         raise TypeError("y must be a 2D bfloat16 CUDA tensor")
     dev = y.device
@@ -874,6 +915,11 @@ def nvfp4_combine_backward(dout: torch.Tensor, rows: Optional[torch.Tensor], wei
     [T, k]), None in the place of one that is not needed.  rows, weights and y
     as in the forward call; no place may occur twice in rows.  Rows of dy that
     do not occur are left as they are in `out` (unspecified in a new tensor)."""
+    done = (_fast or _load_fast()).combine_backward(dout, rows, weights, y, need_dy, need_dweights, out, status)
+    if done.__class__ is tuple:
+        return done
+    if done is not None:
+        _check(done, "nvfp4_combine_backward")
     if dout.dtype != torch.bfloat16 or dout.dim() != 2 or not dout.is_cuda:
         raise TypeError("dout must be a 2D bfloat16 CUDA tensor")
     dev = dout.device
@@ -912,6 +958,11 @@ def nvfp4_gemv(x: torch.Tensor, W: torch.Tensor, sW: torch.Tensor, alphaW: torch
     With ids [T, k]: W codes [E, N, K/2], and x [T, K] (a token's choices share
     its row) or [T k, K] (a row each) -> [T k, N], zeros for a choice of -1.
     Scales in the GEMM layout, alphaW one float per weight."""
+    done = (_fast or _load_fast()).gemv(x, W, sW, alphaW, ids, out_dtype, out, status)
+    if done.__class__ is tuple:
+        return done[0]
+    if done is not None:
+        _check(done, "nvfp4_gemv")
     if x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_cuda:
         raise TypeError("x must be a 2D bfloat16 CUDA tensor")
     dev = x.device

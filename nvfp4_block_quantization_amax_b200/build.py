@@ -1,4 +1,5 @@
-"""Build libnvfp4.so in-tree with nvcc for sm_100a.
+"""Build libnvfp4.so in-tree with nvcc for sm_100a, and _fastcall.so, the C++
+host path of the small calls, with the host compiler against torch's headers.
 
 The library is plain CUDA C++ behind the C ABI of include/nvfp4.h.  Every
 translation unit is compiled with -fmad=false so no multiply-add is fused:
@@ -15,6 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libnvfp4.so")
+FASTCALL = os.path.join(PKG, "_fastcall.so")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo", "-fmad=false",
@@ -37,7 +39,30 @@ def _stale():
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_fastcall(force=False, verbose=False):
+    src = os.path.join(CSRC, "fastcall.cpp")
+    deps = (src, os.path.join(INCLUDE, "nvfp4.h"))
+    if not force and os.path.exists(FASTCALL) and all(os.path.getmtime(d) <= os.path.getmtime(FASTCALL) for d in deps):
+        return FASTCALL
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    headers = [*include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           *(f for h in headers for f in ("-isystem", h)), src, "-o", FASTCALL + ".tmp",
+           *(f"-L{d}" for d in library_paths()), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    os.replace(FASTCALL + ".tmp", FASTCALL)
+    return FASTCALL
+
+
 def build(force=False, verbose=False, extra=()):
+    build_fastcall(force, verbose)
     if not force and not _stale():
         return LIB
     nvcc = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")

@@ -122,3 +122,21 @@ def test_binding_refuses_wrong_tensors():
                  lambda: api.nvfp4_route_backward(torch.zeros((5, 2)), ids, bf)):
         with pytest.raises(TypeError, match="CUDA"):
             call()
+
+
+def test_fast_host_path_declines_what_is_not_on_the_gpu():
+    """The C++ host path leaves every call it does not know to the binding's
+    checks: nothing is done, None is the answer."""
+    f = api._load_fast()
+    z, ids, w = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    x, codes, alpha = torch.zeros(4, 32).bfloat16(), torch.zeros(8, 16, dtype=torch.uint8), torch.ones(1)
+    assert f.route(z, 2, 0, 0, None, 1, 1, 1.0, None, None, None) is None
+    assert f.route(None, "2", 0, 0, None, 1, 1, 1.0, None, None, None) is None
+    assert f.route_backward(w, ids, z, 0, 0, 1.0, None, None) is None
+    assert f.dispatch(x, ids, 8, None, None, None, None) is None
+    assert f.combine(x, ids, w, None, None, None) is None
+    assert f.combine_backward(x, ids, w, x, True, True, None, None) is None
+    assert f.gemv(x, codes, codes, alpha, None, 0, None, None) is None
+    assert f.route() is None and f.gemv(x) is None
+    with pytest.raises(ValueError):
+        f.use(1, 2)

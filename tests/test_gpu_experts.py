@@ -846,3 +846,117 @@ def test_gemv_infinities_of_both_kinds_and_numbers_far_apart(api):
     assert bool(torch.isnan(y[3]).all()) and not bool(y[4].any())
     mag = float(alpha[0]) * (x[0].double().cpu().abs() @ w[0].abs().t())
     within(y[0], want[0], (2 * K + 40) * U * mag, "row 0")
+
+
+# ---------------------------------------------------------------------------
+# the two host paths
+# ---------------------------------------------------------------------------
+class Declines:
+    """A C++ host path that takes no call: the binding's checks make them all."""
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+class Answers:
+    """The C++ host path; counts the calls that it made."""
+    def __init__(self, fast):
+        self.fast, self.made = fast, []
+
+    def __getattr__(self, name):
+        def call(*args):
+            done = getattr(self.fast, name)(*args)
+            if type(done) is tuple:
+                self.made.append(name)
+            return done
+        return call
+
+
+def every_call(api, given, strided):
+    """Results of the six calls; outputs and status given, or new; rows of
+    their own stride, or contiguous."""
+    T, k, E, C, N = 13, 3, 9, 64, 128
+    g = torch.Generator().manual_seed(5)
+
+    def rows(n, c, dtype=torch.bfloat16):
+        t = torch.randn(n, c + 8, generator=g).cuda().to(dtype)
+        return t[:, :c] if strided else t[:, :c].contiguous()
+
+    def new(n, c, dtype=torch.bfloat16):
+        return torch.zeros(n, c, dtype=dtype, device="cuda") if given else None
+
+    status = torch.zeros(1, dtype=torch.int32, device="cuda") if given else None
+    z = rows(T, 16)[:, :E] if strided else rows(T, E)
+    bias = torch.randn(E, generator=g).cuda() if given else None
+    ids, w = api.nvfp4_route(z, k, 0, 0, bias, ids=new(T, k, torch.int32), weights=new(T, k, torch.float32), status=status)
+    dz = api.nvfp4_route_backward(w, ids, z, 0, 0, 2.0, out=new(T, E), status=status)
+    x = rows(T, C)
+    xs, places, offsets = api.nvfp4_dispatch(
+        x, ids, E, out=new(T * k, C), rows=new(T, k, torch.int32),
+        offsets=torch.zeros(E + 1, dtype=torch.int32, device="cuda") if given else None, status=status)
+    out = api.nvfp4_combine(xs, places, w, residual=x if given else None, out=new(T, C), status=status)
+    back = api.nvfp4_combine_backward(x, places, w, xs, out=new(T * k, C), status=status)
+    W = torch.randint(0, 256, (E, N, C // 2), generator=g, dtype=torch.uint8).cuda()
+    sW = torch.randint(40, 80, (E, N * (C // 16)), generator=g, dtype=torch.uint8).cuda()
+    y = api.nvfp4_gemv(x, W, sW, torch.ones(E, device="cuda"), ids, out=new(T * k, N), status=status)
+    return [ids, w, dz, xs, places, offsets, out, *back, y]
+
+
+SIX = ["route", "route_backward", "dispatch", "combine", "combine_backward", "gemv"]
+
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("strided", [False, True])
+def test_both_host_paths_make_the_same_call(api, monkeypatch, given, strided):
+    fast = Answers(api._load_fast())
+    monkeypatch.setattr(api, "_fast", fast)
+    a = every_call(api, given, strided)
+    assert fast.made == SIX
+    monkeypatch.setattr(api, "_fast", Declines())
+    b = every_call(api, given, strided)
+    for u, v in zip(a, b):
+        assert u.shape == v.shape and u.dtype == v.dtype and u.is_contiguous() and torch.equal(u, v)
+
+
+def test_fast_host_path_gives_back_the_callers_tensors(api):
+    z = torch.randn(4, 8, device="cuda")
+    ids, w = torch.zeros(4, 2, dtype=torch.int32, device="cuda"), torch.zeros(4, 2, device="cuda")
+    got = api._load_fast().route(z, 2, 0, 0, None, 1, 1, 1.0, ids, w, None)
+    assert got[0] is ids and got[1] is w
+    assert api._load_fast().dispatch(None, ids, 8, None, None, None, None)[0] is None
+
+
+def test_fast_host_path_refuses_as_the_checks_do(api):
+    """Host-side refusals: nothing is launched."""
+    z = torch.zeros(4, 8, device="cuda")
+    ids, w = torch.zeros(4, 2, dtype=torch.int32, device="cuda"), torch.zeros(4, 2, device="cuda")
+    y = torch.zeros(8, 64, device="cuda").bfloat16()
+    fast = api._load_fast()
+    for bad in ((ids[:3], None, None), (ids.long(), None, None), (None, w[:, :1], None), (None, w.cpu(), None), (None, None, w)):
+        assert fast.route(z, 2, 0, 0, None, 1, 1, 1.0, *bad) is None
+        with pytest.raises((TypeError, ValueError)):
+            api.nvfp4_route(z, 2, ids=bad[0], weights=bad[1], status=bad[2])
+    for kw in (dict(score=7), dict(flags=9), dict(groups=3), dict(k=9), dict(k=0)):
+        with pytest.raises(api.NVFP4Error):
+            api.nvfp4_route(z, **{"k": 2, **kw})
+    with pytest.raises(api.NVFP4Error):
+        api.nvfp4_combine(y[:, :60], ids, w)                      # C not a multiple of 8
+    with pytest.raises(ValueError):
+        api.nvfp4_combine(y, ids, w, out=torch.zeros(4, 32, device="cuda").bfloat16())
+    with pytest.raises(ValueError):
+        api.nvfp4_combine_backward(y[:4], ids, w, y, need_dy=False, out=y)
+    with pytest.raises(ValueError):
+        api.nvfp4_dispatch(None, ids, 8, out=y)
+    with pytest.raises(ValueError):
+        api.nvfp4_gemv(y, torch.zeros(8, 30, dtype=torch.uint8, device="cuda"), ids.byte(), w.view(-1))
+
+
+def test_fast_host_path_takes_the_current_stream(api):
+    """The call goes to the stream that is current, behind its earlier work."""
+    z = torch.zeros(64, 64, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        z.add_(torch.arange(64, device="cuda"))
+        ids, _ = api.nvfp4_route(z, 2)
+    torch.cuda.current_stream().wait_stream(s)
+    assert ids.cpu().tolist() == [[63, 62]] * 64
