@@ -5,9 +5,8 @@
 // 11 us a call (checks, two or three new tensors, a dozen arguments converted).
 // Here the whole call takes 3.9 to 5.4 us, 2.7 of them the launch (routing 64
 // tokens 10.5 -> 5.1 us per pass, dispatch 11.1 -> 5.0, combine 9.7 -> 4.8).
-// These functions
-// take the same arguments as api.py's, in order, check them, allocate the
-// results and call the library.  They answer
+// These functions take the same arguments as api.py's, in order, check them,
+// allocate the results and call the library.  They answer
 //   a tuple      the call was made: its results
 //   a number     the library's status, where it is not NVFP4_OK
 //   None         something is not as expected (a type, a shape, a device that
