@@ -222,14 +222,14 @@ __device__ __forceinline__ float error_of(bool softmax, float share, float most_
 // first choice holds a mark: kDoubtful, if the row has to be chosen again, or
 // mark - e for a first choice e, if the choices, and the expert behind them,
 // whose number lies in the place of the first weight, only have to be put in
-// order.
-constexpr int kDoubtful = -2, kMark = -3;
+// order.  kTied in that place: the choices stand if no other expert belongs
+// above the last one.
+constexpr int kDoubtful = -2, kMark = -3, kTied = -2;
 
+// The choices of a row (lane j: the j-th, or -1) with their weights.
 template <typename Z>
-__device__ __noinline__ void finish_exactly(const RouteArgs& a, int64_t t, double* c, int lane) {
-  const Z* const row = static_cast<const Z*>(a.logits) + t * a.ldl;
+__device__ __forceinline__ void write_row(const RouteArgs& a, int64_t t, const Z* row, int mine, int lane) {
   const int k = static_cast<int>(a.k);
-  const int mine = choose_exactly<Z>(row, a, c, lane);
   const bool softmax = a.score == NVFP4_ROUTE_SOFTMAX, renorm = a.flags & NVFP4_ROUTE_RENORM;
   float row_max = -INFINITY, row_sum = 0.0f;
   if (softmax && !renorm) {
@@ -245,6 +245,12 @@ __device__ __noinline__ void finish_exactly(const RouteArgs& a, int64_t t, doubl
     a.ids[t * k + lane] = mine;
     a.weights[t * k + lane] = got ? a.scale * (renorm ? __fdiv_rn(share, sum) : share) : 0.0f;
   }
+}
+
+template <typename Z>
+__device__ __noinline__ void finish_exactly(const RouteArgs& a, int64_t t, double* c, int lane) {
+  const Z* const row = static_cast<const Z*>(a.logits) + t * a.ldl;
+  write_row<Z>(a, t, row, choose_exactly<Z>(row, a, c, lane), lane);
   __syncwarp();   // c is free
 }
 
@@ -256,7 +262,7 @@ template <typename Z>
 __device__ __noinline__ void settle(const RouteArgs& a, int64_t t, double* c, int lane) {
   const Z* const row = static_cast<const Z*>(a.logits) + t * a.ldl;
   const int k = static_cast<int>(a.k);
-  const bool direct = !a.bias && a.groups == 1, softmax = a.score == NVFP4_ROUTE_SOFTMAX, renorm = a.flags & NVFP4_ROUTE_RENORM;
+  const bool direct = !a.bias && a.groups == 1;
   int e[2] = {lane < k ? a.ids[t * k + lane] : -1, __float_as_int(a.weights[t * k])};   // of this lane, and the last one
   if (lane == 0) e[0] = kMark - e[0];
   double v[2];
@@ -281,27 +287,40 @@ __device__ __noinline__ void settle(const RouteArgs& a, int64_t t, double* c, in
   if (e[0] >= 0 && better < k) order[better] = e[0];
   if (lane == 0 && e[1] >= 0 && place < k) order[place] = e[1];
   __syncwarp();
-  const int mine = lane < k ? order[lane] : -1;
-  float row_max = -INFINITY, row_sum = 0.0f;
-  if (softmax && !renorm) {
-    for (int i = lane; i < a.E; i += 32) row_max = fmaxf(row_max, as_float(row[i]));
-    row_max = warp_max(row_max);
-    for (int i = lane; i < a.E; i += 32) row_sum += ex2((as_float(row[i]) - row_max) * kLog2e);
-    row_sum = warp_sum(row_sum);
-  }
-  const bool got = mine >= 0;
-  const float share = share_of(got ? as_float(row[mine]) : 0.0f, got, a.score, renorm, row_max, row_sum);
-  const float sum = renorm ? warp_sum(share) : 1.0f;
-  if (lane < k) {
-    a.ids[t * k + lane] = mine;
-    a.weights[t * k + lane] = got ? a.scale * (renorm ? __fdiv_rn(share, sum) : share) : 0.0f;
-  }
+  write_row<Z>(a, t, row, lane < k ? order[lane] : -1, lane);
   __syncwarp();   // c is free
+}
+
+// A row where the last choice and the expert behind it are equal and others are
+// as close to them: the choices stand if those are no more than equal.  An
+// expert that is unlike the last choice and not surely below it (error_of) has
+// to be a choice itself, so both are counted.  Softmax scores need the whole
+// row.  Logits without a bias or groups do not come here.
+template <typename Z>
+__device__ __noinline__ void finish_tied(const RouteArgs& a, int64_t t, double* c, int lane) {
+  if (a.score == NVFP4_ROUTE_SOFTMAX) return finish_exactly<Z>(a, t, c, lane);
+  const Z* const row = static_cast<const Z*>(a.logits) + t * a.ldl;
+  const int k = static_cast<int>(a.k), E = static_cast<int>(a.E);
+  const int id = lane < k ? a.ids[t * k + lane] : -1, mine = lane ? id : kMark - id;
+  const int last = __shfl_sync(kAll, mine, k - 1);
+  const float z_last = as_float(row[last]), b_last = a.bias ? __ldg(a.bias + last) : 0.0f;
+  const float c_last = rcp(1.0f + ex2(-kLog2e * z_last)) + b_last;
+  const auto above = [&](int e) {
+    const float z = as_float(row[e]), b = a.bias ? __ldg(a.bias + e) : 0.0f;
+    if ((z == z_last && b == b_last) || !(z > lowest<Z>()) || !(b > -FLT_MAX)) return false;
+    const float v = rcp(1.0f + ex2(-kLog2e * z)) + b;
+    return v - c_last > -2.0f * error_of(false, 1.0f, 1.0f + fmaxf(fabsf(b), fabsf(b_last)));
+  };
+  int n = 0;
+  for (int e = lane; e < E; e += 32) n += above(e);
+  if (__reduce_add_sync(kAll, n) != __popc(__ballot_sync(kAll, mine >= 0 && above(mine)))) return finish_exactly<Z>(a, t, c, lane);
+  write_row<Z>(a, t, row, mine, lane);
 }
 
 template <typename Z>
 __device__ __forceinline__ void finish(const RouteArgs& a, int64_t t, int mark, double* c, int lane) {
   if (mark == kDoubtful) finish_exactly<Z>(a, t, c, lane);
+  else if (__float_as_int(a.weights[t * a.k]) == kTied) finish_tied<Z>(a, t, c, lane);
   else settle<Z>(a, t, c, lane);
 }
 
@@ -318,7 +337,13 @@ __device__ __forceinline__ void finish(const RouteArgs& a, int64_t t, int mark, 
 // every lane keeps, and looks for a third only when it wins again.
 // Values as near as the error of their 32-bit form (delta), or with the same
 // key, may stand in the wrong order; rows with such a pair among the chosen
-// and the next one, or with such groups, are chosen again in 64 bits.
+// and the next one, or with such groups, are chosen again in 64 bits.  Equal
+// inputs are in order; but where the last choice and the next one are equal,
+// any expert behind them that is as near may be unlike them and belong above
+// both (`tied`).  Logits that are ordered as they are show it at once (bf16 has
+// no two values as near); other values wait for finish_tied.
+template <typename Z, bool kDirect>
+constexpr bool kTies = !(kDirect && sizeof(Z) == 2);
 template <int V>
 constexpr int kRouteCtas = V <= 8 ? 8 : V == 16 ? 5 : 3;   // per SM
 
@@ -519,20 +544,30 @@ __global__ void __launch_bounds__(kWarps * 32, kRouteCtas<V>) route_kernel(const
     }
     int mine = had ? (V - 1 - static_cast<int>(my_key & (V - 1))) * 32 + my_src : -1;
     // neighbours that may stand in the wrong order; equal inputs do not
-    bool unsure = false;
-    if (had && next_key &&
-        (kDirect ? (my_key ^ next_key) < static_cast<uint32_t>(V) : !(from_ordered(my_key) - from_ordered(next_key) > 2.0f * delta))) {
+    const auto close = [&](uint32_t above, uint32_t below) {
+      return kDirect ? (above ^ below) < static_cast<uint32_t>(V) : !(from_ordered(above) - from_ordered(below) > 2.0f * delta);
+    };
+    bool unsure = false, tied = false;
+    if (had && next_key && close(my_key, next_key)) {
       const int next = (V - 1 - static_cast<int>(next_key & (V - 1))) * 32 + next_src;
       unsure = !(as_float(row[mine]) == as_float(row[next]) && (kDirect || !a.bias || __ldg(a.bias + mine) == __ldg(a.bias + next)));
+      tied = kTies<Z, kDirect> && !unsure && lane == k - 1 && behind && close(my_key, behind);
     }
-    if (near || __any_sync(kAll, unsure)) {
+    if (kDirect && kTies<Z, kDirect> && __any_sync(kAll, tied)) {
+      const uint32_t last = __shfl_sync(kAll, my_key, k - 1);
+      const float z_last = as_float(row[__shfl_sync(kAll, mine, k - 1)]);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (key[i] && key[i] <= last && close(last, key[i])) unsure |= as_float(row[i * 32 + lane]) > z_last;
+      tied = false;
+    }
+    if (near || __any_sync(kAll, unsure || tied)) {
       // the choices and the next one are all there is to it where what is behind
       // them is further below; softmax values need the whole row
       const uint32_t last = __shfl_sync(kAll, my_key, k - 1);
-      const bool whole_row = near || (!kDirect && softmax) ||
-                             (last && behind && (kDirect ? (last ^ behind) < static_cast<uint32_t>(V)
-                                                         : !(from_ordered(last) - from_ordered(behind) > 2.0f * delta)));
-      const int next = w ? (V - 1 - static_cast<int>(w & (V - 1))) * 32 + src : -1;
+      const bool only_tied = !near && !__any_sync(kAll, unsure);
+      const bool whole_row = !only_tied && (near || (!kDirect && softmax) || (last && behind && close(last, behind)));
+      const int next = only_tied ? kTied : w ? (V - 1 - static_cast<int>(w & (V - 1))) * 32 + src : -1;
       if (lane < k && !whole_row) a.ids[t * k + lane] = lane ? mine : kMark - mine;
       if (lane == 0) {
         if (whole_row) a.ids[t * k] = kDoubtful;
@@ -763,9 +798,11 @@ __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(c
     // Neighbours whose keys do not part them: equal inputs are in order; of two
     // that are both choices, so are those whose values themselves part them (any
     // other expert's key is below both); the rest is unsure.
-    bool unsure = false;
-    if (had && next_key &&
-        (kDirect ? (my_key ^ next_key) < static_cast<uint32_t>(V) : !(from_ordered(my_key) - from_ordered(next_key) > 2.0f * delta))) {
+    const auto close = [&](uint32_t above, uint32_t below) {
+      return kDirect ? (above ^ below) < static_cast<uint32_t>(V) : !(from_ordered(above) - from_ordered(below) > 2.0f * delta);
+    };
+    bool unsure = false, tied = false;
+    if (had && next_key && close(my_key, next_key)) {
       const int next = (V - 1 - static_cast<int>(next_key & (V - 1))) * kShare + holder[warp][r][sub + 1];
       const float z1 = as_float(row[mine]), z2 = as_float(row[next]);
       float c1 = z1, c2 = z2;
@@ -779,15 +816,27 @@ __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(c
         }
       }
       unsure = !equal && !((kDirect || !softmax) && sub + 1 < k && c1 - c2 > 2.0f * fine);
+      tied = kTies<Z, kDirect> && equal && sub == k - 1 && behind && close(my_key, behind);
+    }
+    if (kDirect && kTies<Z, kDirect> && __any_sync(kAll, tied)) {
+      const int from = (lane & 24) + k - 1;
+      const uint32_t last = __shfl_sync(kAll, my_key, from);
+      const int at = __shfl_sync(kAll, mine, from);
+      if (__shfl_sync(kAll, tied, from)) {
+        const float z_last = as_float(row[at]);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (key[i] && key[i] <= last && close(last, key[i])) unsure |= as_float(row[i * kShare + sub]) > z_last;
+      }
+      tied = false;
     }
     // its vote also parts the uses of values
-    const bool later = ((__ballot_sync(kAll, unsure) >> (lane & 24) & 0xFFu) || near) && !bad;   // of the row
+    const bool only_tied = !(__ballot_sync(kAll, unsure) >> (lane & 24) & 0xFFu) && !near;   // of the row, if it is
+    const bool later = ((__ballot_sync(kAll, tied) >> (lane & 24) & 0xFFu) || !only_tied) && !bad;
     doubts |= later;
     const uint32_t last = __shfl_sync(kAll, my_key, (lane & 24) + k - 1);
     // as in the kernel above
-    const bool whole_row = near || (!kDirect && softmax) ||
-                           (last && behind && (kDirect ? (last ^ behind) < static_cast<uint32_t>(V)
-                                                       : !(from_ordered(last) - from_ordered(behind) > 2.0f * delta)));
+    const bool whole_row = !only_tied && (near || (!kDirect && softmax) || (last && behind && close(last, behind)));
     if (bad) mine = -1;
     const bool got = mine >= 0;
     const float z = got ? as_float(row[mine]) : 0.0f;
@@ -798,7 +847,9 @@ __global__ void __launch_bounds__(kWarps * 32, kManyCtas<V>) route_many_kernel(c
       if (bad && sub == 0 && a.status) *a.status = kStatusNonFinite;
       if (later) {
         if (sub < k) a.ids[t * k + sub] = sub ? mine : whole_row ? kDoubtful : kMark - mine;
-        if (sub == 0) a.weights[t * k] = __int_as_float(w ? (V - 1 - static_cast<int>(w & (V - 1))) * kShare + holder[warp][r][k] : -1);
+        if (sub == 0)
+          a.weights[t * k] =
+              __int_as_float(only_tied ? kTied : w ? (V - 1 - static_cast<int>(w & (V - 1))) * kShare + holder[warp][r][k] : -1);
       } else if (sub < k) {
         a.ids[t * k + sub] = mine;
         a.weights[t * k + sub] = got ? a.scale * (renorm ? __fdiv_rn(share, sum) : share) : 0.0f;

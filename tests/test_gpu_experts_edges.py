@@ -1,0 +1,52 @@
+"""Routing, dispatch and the few-row products where their fast paths end.
+Tolerances as in test_gpu_experts.py."""
+import pytest
+import torch
+
+from test_gpu_experts import PAIR, RENORM, SIGMOID, SOFTMAX, api, check_route  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# routing
+# ---------------------------------------------------------------------------
+def tied_rows(T, E, k, step, seed):
+    """Logits far apart but for three neighbours at the end of the k choices:
+    two equal ones and one `step` units in the last place away, in any order."""
+    g = torch.Generator().manual_seed(seed)
+    order = torch.argsort(torch.rand((T, E), generator=g), 1)
+    z = torch.zeros((T, E))
+    z.scatter_(1, order, (4.0 - torch.arange(E) * (8.0 / E)).expand(T, E).contiguous())
+    at = order[:, k - 1:k + 2]
+    v = torch.round(z.gather(1, at[:, 1:2]) * 32) / 32 + 0.0
+    odd = torch.randint(0, 3, (T, 1), generator=g)
+    three = v.expand(T, 3).clone()
+    three.scatter_(1, odd, (v.double() + step * (2.0 ** torch.floor(torch.log2(v.double().abs().clamp(min=0.03)))) * 2.0 ** -23).float())
+    return z.scatter_(1, at, three)
+
+
+@pytest.mark.parametrize("E,k", [(5, 1), (33, 1), (64, 1), (64, 6), (100, 3), (128, 8), (160, 2), (256, 8), (300, 20), (500, 1), (700, 9), (1024, 32)])
+@pytest.mark.parametrize("step", [1, 3, -2])
+def test_route_equal_experts_at_the_end_hide_no_better_one(api, E, k, step):
+    z = tied_rows(150, E, k, step, seed=E + k)
+    check_route(api, z, k, SOFTMAX, 0)
+    check_route(api, z, k, SIGMOID, RENORM)
+    bias = torch.zeros(E)
+    check_route(api, z, k, SIGMOID, 0, bias=bias)
+    check_route(api, z, k, SOFTMAX, RENORM, bias=bias)
+
+
+@pytest.mark.parametrize("E,k", [(64, 6), (256, 8), (512, 4)])
+def test_route_many_equal_experts_around_the_end(api, E, k):
+    """Rows of one value but for one or two experts a step above or below."""
+    g = torch.Generator().manual_seed(E)
+    z = torch.full((120, E), 1.5)
+    z[40:80] = torch.tensor([1.5, 1.25])[torch.randint(0, 2, (40, E), generator=g)]
+    z[torch.arange(120), torch.randint(0, E, (120,), generator=g)] = 1.5 + 2.0 ** -23
+    z[torch.arange(100), torch.randint(0, E, (100,), generator=g)] = 1.5 - 2.0 ** -23
+    z[110:] = 0.0
+    for bias in (None, torch.zeros(E)):
+        check_route(api, z, k, SOFTMAX, 0, bias=bias)
+        check_route(api, z, k, SIGMOID, RENORM, bias=bias)
+    check_route(api, z, k, SIGMOID, PAIR, groups=8, kept=3)
