@@ -89,10 +89,14 @@ __device__ __forceinline__ void merge_two(F& a1, F& a2, F b1, F b2) {
   a2 = low < two ? two : low;
 }
 
-// A group's value from its two largest (-inf: there is none).
-template <typename F>
-__device__ __forceinline__ F group_value(F first, F second, bool pair) {
-  return pair && second > -FLT_MAX ? first + second : first;
+// A group's value from its two largest (-inf: there is none).  A sum below the
+// finite numbers of 32 bits becomes the lowest, which still stands above a group
+// without any; groups as near as that are parted in 64 bits.
+__device__ __forceinline__ float group_value(float first, float second, bool pair) {
+  return pair && second > -INFINITY ? fmaxf(first + second, -FLT_MAX) : first;
+}
+__device__ __forceinline__ double group_value(double first, double second, bool pair) {
+  return pair && second > -INFINITY ? first + second : first;
 }
 
 // Finite numbers in their order as unsigned ones above 0, -inf as 0.

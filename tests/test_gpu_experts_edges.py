@@ -3,7 +3,7 @@ Tolerances as in test_gpu_experts.py."""
 import pytest
 import torch
 
-from test_gpu_experts import PAIR, RENORM, SIGMOID, SOFTMAX, api, check_route  # noqa: F401
+from test_gpu_experts import INF, PAIR, RENORM, SIGMOID, SOFTMAX, api, check_route  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,23 @@ def test_route_many_equal_experts_around_the_end(api, E, k):
         check_route(api, z, k, SOFTMAX, 0, bias=bias)
         check_route(api, z, k, SIGMOID, RENORM, bias=bias)
     check_route(api, z, k, SIGMOID, PAIR, groups=8, kept=3)
+
+
+@pytest.mark.parametrize("E,groups", [(40, 4), (128, 4), (256, 8), (512, 4), (96, 12)])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+def test_route_group_values_past_32_bits(api, E, groups, score):
+    """Sums of two biases below -FLT_MAX are still ordered, and stand above a
+    group without an open expert; sums above FLT_MAX are as well."""
+    n = E // groups
+    z = torch.randn((20, E), generator=torch.Generator().manual_seed(E))
+    low = torch.finfo(torch.float32).min
+    for values in ([-INF, -3.0e38, -2.5e38, -3.2e38], [-3.3e38, low, -3.1e38, -2.0e38], [3.0e38, 2.6e38, -3.0e38, 3.2e38],
+                   [-3.0e38, -3.0e38, -INF, -3.0e38]):
+        bias = torch.tensor(values).repeat(groups // 4).repeat_interleave(n)
+        for kept in (1, 2, groups - 1):
+            check_route(api, z, 3, score, PAIR, bias=bias, groups=groups, kept=kept)
+    # the second value next to the lowest number
+    bias = torch.zeros(E)
+    bias[:n] = torch.nextafter(torch.tensor(low), torch.tensor(0.0))
+    bias[0] = 2.0
+    check_route(api, z, 2, score, PAIR, bias=bias, groups=groups, kept=1)
