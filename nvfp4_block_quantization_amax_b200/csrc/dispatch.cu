@@ -23,6 +23,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "launch.cuh"
@@ -385,14 +386,15 @@ cudaError_t rows_launch(Kernel kernel, const RowArgs& a, cudaStream_t st, int pe
 template <int kBits>
 cudaError_t sort_launch(const RowArgs& a, const int32_t* ids, int64_t P, int64_t E, int32_t* offsets, int32_t* rows,
                         cudaStream_t st) {
-  const size_t smem = static_cast<size_t>(kSortWarps + 2) * E * sizeof(int);
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(sort_kernel<kBits>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  constexpr auto bytes = [](int64_t experts) { return static_cast<size_t>(kSortWarps + 2) * experts * sizeof(int); };
+  constexpr size_t most = bytes(int64_t(1) << kBits);
+  if constexpr (most > 48 * 1024) {
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(sort_kernel<kBits>, most, done);
     if (e != cudaSuccess) return e;
   }
   note_launch();
-  return launch_k(sort_kernel<kBits>, dim3(kSortCtas), dim3(kSortThreads), smem, st, kSortCtas, ids, P, static_cast<int>(E),
+  return launch_k(sort_kernel<kBits>, dim3(kSortCtas), dim3(kSortThreads), bytes(E), st, kSortCtas, ids, P, static_cast<int>(E),
                   offsets, rows, a.status);
 }
 

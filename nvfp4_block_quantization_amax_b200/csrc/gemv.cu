@@ -24,7 +24,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
-#include <atomic>
 #include <cstdint>
 
 #include "launch.cuh"
@@ -520,17 +519,6 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_wide_kernel(const __grid_con
     out[p * a.ldo + atom * 128ll + r] = Out(sum * alpha * 256.0f);
   }
   if (ranks > 1) cluster.sync();   // no CTA leaves while its share is read
-}
-
-// The dynamic shared memory of a kernel, asked for once per device.
-template <typename Kernel>
-cudaError_t allow_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (dev < 64 && done.load(std::memory_order_relaxed) >> dev & 1)) return e;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
-  return e;
 }
 
 template <typename Out>

@@ -1,9 +1,11 @@
 """Routing, dispatch and the few-row products where their fast paths end.
 Tolerances as in test_gpu_experts.py."""
+import threading
+
 import pytest
 import torch
 
-from test_gpu_experts import INF, PAIR, RENORM, SIGMOID, SOFTMAX, api, check_route  # noqa: F401
+from test_gpu_experts import INF, PAIR, RENORM, SIGMOID, SOFTMAX, api, check_route, choices, sort_reference  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +72,35 @@ def test_route_group_values_past_32_bits(api, E, groups, score):
     bias[:n] = torch.nextafter(torch.tensor(low), torch.tensor(0.0))
     bias[0] = 2.0
     check_route(api, z, 2, score, PAIR, bias=bias, groups=groups, kept=1)
+
+
+# ---------------------------------------------------------------------------
+# dispatch
+# ---------------------------------------------------------------------------
+def test_dispatch_from_two_host_threads(api):
+    """Calls of different numbers of experts, whose sorts need different
+    amounts of shared memory, at once: each thread has its own stream."""
+    T, k = 700, 8
+    cases = {E: choices(T, k, E, seed=E) for E in (400, 1024, 600, 1000)}
+    want = {E: sort_reference(ids, E) for E, ids in cases.items()}
+    gpu = {E: ids.cuda() for E, ids in cases.items()}
+    failures = []
+    start = threading.Barrier(len(cases))
+
+    def work(E):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                start.wait()
+                for _ in range(400):
+                    _, rows, offsets = api.nvfp4_dispatch(None, gpu[E], E)
+                assert torch.equal(rows.cpu(), want[E][0]) and torch.equal(offsets.cpu(), want[E][1])
+        except Exception as e:   # noqa: BLE001
+            failures.append((E, e))
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(E,)) for E in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, failures
