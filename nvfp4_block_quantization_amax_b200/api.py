@@ -4,6 +4,7 @@ libnvfp4.so.  Every step of the computation runs in the library's kernels.
 """
 import contextlib
 import ctypes
+import importlib.util
 import math
 from dataclasses import dataclass
 from typing import Optional
@@ -11,6 +12,7 @@ from typing import Optional
 import torch
 
 from . import _lib as L
+from .build import fastcall_path
 from ._lib import (NVFP4_ALPHA_PROVIDED, NVFP4_AMAX_PROVIDED, NVFP4_BLOCK2D, NVFP4_COLWISE, NVFP4_FOUR_SIX,  # noqa: F401
                    NVFP4_GEMM_SCALE_LAYOUT, NVFP4_HEADROOM, NVFP4_INVERSE_RHT, NVFP4_MS_EDEN, NVFP4_OUT_BF16,
                    NVFP4_OUT_DTYPE_BF16, NVFP4_OUT_DTYPE_FP32, NVFP4_RHT, NVFP4_RHT_SR, NVFP4_RHT_SR_HW,
@@ -674,9 +676,11 @@ def _load_fast():
     global _fast
     lib = L.load()
     try:
-        from . import _fastcall
+        spec = importlib.util.spec_from_file_location(f"{__package__}._fastcall", fastcall_path())
+        _fastcall = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_fastcall)
     except ImportError as e:
-        raise RuntimeError("_fastcall.so is missing or of another torch: build it with "
+        raise RuntimeError("_fastcall is not built for this torch and Python: build it with "
                            "nvfp4_block_quantization_amax_b200/build.py") from e
     names = ("route", "route_backward", "dispatch", "combine", "combine_backward", "gemv")
     _fastcall.use(*(ctypes.cast(getattr(lib, "nvfp4_" + n), ctypes.c_void_p).value for n in names))

@@ -1,4 +1,4 @@
-"""Build libnvfp4.so in-tree with nvcc for sm_100a, and _fastcall.so, the C++
+"""Build libnvfp4.so in-tree with nvcc for sm_100a, and _fastcall.*.so, the C++
 host path of the small calls, with the host compiler against torch's headers.
 
 The library is plain CUDA C++ behind the C ABI of include/nvfp4.h.  Every
@@ -10,6 +10,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,7 +18,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libnvfp4.so")
-FASTCALL = os.path.join(PKG, "_fastcall.so")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo", "-fmad=false",
@@ -40,26 +40,32 @@ def _stale():
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def fastcall_path():
+    """The small calls' host path for this torch and this Python, whose layouts
+    are compiled into it: its name says which, so that no other one's is taken."""
+    import torch
+    return os.path.join(PKG, f"_fastcall.torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_fastcall(force=False, verbose=False):
+    out = fastcall_path()
     src = os.path.join(CSRC, "fastcall.cpp")
     deps = (src, os.path.join(INCLUDE, "nvfp4.h"))
-    if not force and os.path.exists(FASTCALL) and all(os.path.getmtime(d) <= os.path.getmtime(FASTCALL) for d in deps):
-        return FASTCALL
-    import sysconfig
-
+    if not force and os.path.exists(out) and all(os.path.getmtime(d) <= os.path.getmtime(out) for d in deps):
+        return out
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     headers = [*include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
-           *(f for h in headers for f in ("-isystem", h)), src, "-o", FASTCALL + ".tmp",
+           *(f for h in headers for f in ("-isystem", h)), src, "-o", out + ".tmp",
            *(f"-L{d}" for d in library_paths()), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
-    os.replace(FASTCALL + ".tmp", FASTCALL)
-    return FASTCALL
+    os.replace(out + ".tmp", out)
+    return out
 
 
 def build(force=False, verbose=False, extra=()):
@@ -70,7 +76,7 @@ def build(force=False, verbose=False, extra=()):
     try:
         build_fastcall(force, verbose)
     except (ImportError, OSError, subprocess.CalledProcessError) as e:
-        warnings.warn(f"_fastcall.so was not built: {e}", RuntimeWarning, stacklevel=2)
+        warnings.warn(f"_fastcall, the small calls' host path, was not built: {e}", RuntimeWarning, stacklevel=2)
     return LIB
 
 

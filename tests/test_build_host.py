@@ -59,3 +59,19 @@ def test_a_failing_library_is_an_error(record, monkeypatch):
     with pytest.raises(subprocess.CalledProcessError):
         build.build(force=True)
     assert not r.commands
+
+
+def test_host_path_belongs_to_one_torch_and_python(record, monkeypatch):
+    """Another torch or Python has another file: the one of this torch does not
+    count as built for it, nor is it taken in its place."""
+    import torch
+    here = build.build_fastcall()
+    assert here == build.fastcall_path() and os.path.exists(here)
+    r = record()
+    assert build.build_fastcall() == here and not r.commands
+    monkeypatch.setattr(torch, "__version__", "2.12.0+cu130")
+    other = build.fastcall_path()
+    assert other != here and build.build_fastcall() == other and len(r.commands) == 1
+    monkeypatch.undo()
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: ".cpython-313-x86_64-linux-gnu.so")
+    assert build.fastcall_path() not in (here, other) and not os.path.exists(build.fastcall_path())
