@@ -6,6 +6,8 @@ import contextlib
 import ctypes
 import importlib.util
 import math
+import types
+import warnings
 from dataclasses import dataclass
 from typing import Optional
 
@@ -666,26 +668,28 @@ def nvfp4_lora_backward(dy: torch.Tensor, x: torch.Tensor, h: torch.Tensor, A: t
 # take a second call under that device instead of a context around the first,
 # and the library's functions are called without the names in _lib between.
 # ---------------------------------------------------------------------------
+_SMALL = ("route", "route_backward", "dispatch", "combine", "combine_backward", "gemv")
 _fast = None
 
 
 def _load_fast():
     """The small calls' C++ host path, with the library's entry points.  Its
     functions return the results, a status, or None where a call is not of the
-    plain form: then the checks below say what is wrong, or make the call."""
+    plain form: then the checks below say what is wrong, or make the call.
+    Where it is not built for this torch and Python they make every call."""
     global _fast
     lib = L.load()
     try:
         spec = importlib.util.spec_from_file_location(f"{__package__}._fastcall", fastcall_path())
-        _fastcall = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_fastcall)
+        fast = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(fast)
+        fast.use(*(ctypes.cast(getattr(lib, "nvfp4_" + n), ctypes.c_void_p).value for n in _SMALL))
     except ImportError as e:
-        raise RuntimeError("_fastcall is not built for this torch and Python: build it with "
-                           "nvfp4_block_quantization_amax_b200/build.py") from e
-    names = ("route", "route_backward", "dispatch", "combine", "combine_backward", "gemv")
-    _fastcall.use(*(ctypes.cast(getattr(lib, "nvfp4_" + n), ctypes.c_void_p).value for n in names))
-    _fast = _fastcall
-    return _fast
+        warnings.warn(f"the small calls take about 5 us longer: their C++ host path is not built for this torch and Python "
+                      f"(nvfp4_block_quantization_amax_b200/build.py builds it): {e}", RuntimeWarning, stacklevel=3)
+        fast = types.SimpleNamespace(**{n: lambda *args: None for n in _SMALL})
+    _fast = fast
+    return fast
 
 
 def _new(rows: int, cols: int, dtype, device) -> torch.Tensor:

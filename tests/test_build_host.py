@@ -75,3 +75,21 @@ def test_host_path_belongs_to_one_torch_and_python(record, monkeypatch):
     monkeypatch.undo()
     monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: ".cpython-313-x86_64-linux-gnu.so")
     assert build.fastcall_path() not in (here, other) and not os.path.exists(build.fastcall_path())
+
+
+def test_binding_makes_the_calls_without_the_host_path(record, monkeypatch):
+    """With another torch, say: one warning, and the binding's own checks."""
+    import torch
+
+    from nvfp4_block_quantization_amax_b200 import api
+    monkeypatch.setattr(api, "_fast", None)
+    monkeypatch.setattr(torch, "__version__", "2.12.0+cu130")
+    with pytest.warns(RuntimeWarning, match="host path"):
+        fast = api._load_fast()
+    assert api._fast is fast
+    for name in ("route", "route_backward", "dispatch", "combine", "combine_backward", "gemv"):
+        assert getattr(fast, name)(1, 2, 3) is None
+    with pytest.raises(TypeError, match="CUDA"):
+        api.nvfp4_route(torch.zeros(4, 8), 2)
+    with pytest.raises(TypeError, match="CUDA"):
+        api.nvfp4_combine(torch.zeros(4, 8).bfloat16(), None, torch.zeros(4, 1))
