@@ -698,7 +698,7 @@ def _new(rows: int, cols: int, dtype, device) -> torch.Tensor:
 
 def _elsewhere(device) -> bool:
     """Whether `device`, a GPU, is not the current one."""
-    return _current_device is None or _current_device() != device.index
+    return (_current_device or torch.cuda.current_device)() != device.index
 
 
 def _pairs(t: torch.Tensor, dtype, what: str, device):
