@@ -5,7 +5,8 @@ import threading
 import pytest
 import torch
 
-from test_gpu_experts import INF, PAIR, RENORM, SIGMOID, SOFTMAX, api, check_route, choices, sort_reference  # noqa: F401
+from test_gpu_experts import (INF, PAIR, RENORM, SIGMOID, SOFTMAX, api, check_gemv, check_route, choices,  # noqa: F401
+                              random_weight, rows_of, sort_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +105,34 @@ def test_dispatch_from_two_host_threads(api):
     for t in threads:
         t.join()
     assert not failures, failures
+
+
+# ---------------------------------------------------------------------------
+# few-row products
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("hot,T,k,E", [(9, 40, 1, 64), (40, 64, 2, 128), (300, 500, 1, 300)])
+def test_gemv_a_hot_expert_among_many(api, hot, T, k, E):
+    """More than 8 rows of one weight where few are likely, in several passes."""
+    W, sW, alpha, w = random_weight(E, 128, 192, seed=E)
+    ids = choices(T, k, E, seed=T, none=0.1)
+    ids.view(-1)[torch.randperm(T * k, generator=torch.Generator().manual_seed(hot))[:hot]] = E - 2
+    for rows in (T, T * k):
+        x = rows_of(rows, 192, seed=rows)
+        check_gemv(api, x, W, sW, alpha, w, ids.cuda(), api.NVFP4_OUT_DTYPE_FP32)
+
+
+@pytest.mark.parametrize("T,k,E,K", [(20, 2, 4, 448), (36, 1, 4, 64), (30, 2, 5, 1024), (45, 1, 3, 320), (64, 2, 8, 128), (90, 1, 2, 192)])
+def test_gemv_nine_to_45_rows_of_each_expert(api, T, k, E, K):
+    W, sW, alpha, w = random_weight(E, 256, K, seed=E + K)
+    ids = choices(T, k, E, seed=T, none=0.05).cuda()
+    for rows in (T, T * k):
+        x = rows_of(rows, K, seed=rows)
+        check_gemv(api, x, W, sW, alpha, w, ids, api.NVFP4_OUT_DTYPE_FP32)
+        check_gemv(api, x, W, sW, alpha, w, ids, api.NVFP4_OUT_DTYPE_BF16)
+
+
+@pytest.mark.parametrize("P", [25, 31, 32])
+@pytest.mark.parametrize("N,K", [(128, 64), (128, 14336), (4096, 1088)])
+def test_gemv_25_to_32_rows(api, P, N, K):
+    W, sW, alpha, w = random_weight(1, N, K, seed=N + K)
+    check_gemv(api, rows_of(P, K, seed=P), W, sW, alpha, w, None, api.NVFP4_OUT_DTYPE_FP32)
