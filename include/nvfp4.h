@@ -613,7 +613,7 @@ NVFP4_API nvfp4_status_t nvfp4_combine_backward(const void* dout, int64_t lddo, 
  * nvfp4_gemm does).  Products are exact and summed in fp32; out is bf16 or
  * fp32 with row stride ldo.  A pair of -1 gets zeros, an id outside -1 .. E - 1
  * sets NVFP4_ERR_ARG and does too.  A weight is read once for each 8 to 32 rows
- * that take it (by P and E).  0 <= P <= 1024 (more rows: nvfp4_gemm,
+ * that take it (by P, E and K).  0 <= P <= 1024 (more rows: nvfp4_gemm,
  * nvfp4_gemm_grouped), N % 128 == 0, N <= 2^25, K % 64 == 0, 1 <= E <= 1024; W
  * and sW 16-byte aligned, out aligned to its type. */
 NVFP4_API nvfp4_status_t nvfp4_gemv(const void* x, int64_t ldx, const int32_t* ids, int64_t P, int64_t rep,

@@ -559,13 +559,38 @@ cudaError_t launch_wide(const GemvArgs& a, cudaStream_t st) {
                   static_cast<unsigned>(ranks), a);
 }
 
+// The kernel goes by the rows that a weight is likely to have: P without ids,
+// else the mean of the weights that can be taken.  More than 8 are cut into as
+// few passes of up to 32 as there can be, of as few columns as that takes.
+// Even / uneven choices (weights proportional to exp of a normal), us:
+//   rows of each                    6           8          12          16          24
+//   8 experts of 14336 x 4096
+//     first kernel            86 /  96    89 / 126   161 / 160   164 / 197   248 / 274
+//     16 columns             116 /  92   117 / 118   119 / 139   121 / 155   220 / 226
+//     24 columns             137 / 111   138 / 139   139 / 141   141 / 168   145 / 201
+//     32 columns             192 / 129   195 / 195   197 / 177   199 / 198   204 / 267
+//   128 experts of 1408 x 2048
+//     first kernel            91 / 103    99 / 127
+//     16 columns             141 / 130   163 / 160
+//   32 experts of 1024 x 1024
+//     first kernel          17.4 / 18.2  19.7 / 22.3 29.2 / 27.0 32.2 / 34.2
+//     16 columns            15.1 / 14.8  17.0 / 17.5 23.0 / 27.7 25.4 / 31.9 42.9 / 37.6
+//     24 columns            18.4 / 18.4  19.5 / 20.3 21.6 / 22.0 27.3 / 32.2 33.3 / 39.2
+// Up to K = 1024 a spare column costs less than another pass, so half as many
+// rows again are taken for likely.  One weight, 40 rows, 24 / 32 columns: 4096 x
+// 14336 37 / 47, 14336 x 4096 43 / 62, 4096 x 4096 15 / 18.
 template <typename Out>
 cudaError_t launch_out(const GemvArgs& a, cudaStream_t st) {
-  const int64_t rows = a.ids ? std::max<int64_t>(1, a.P / std::min(a.P, a.E) * 2) : a.P;   // likely ones of a weight
-  return rows <= 8    ? launch_narrow<Out>(a, st)
-         : rows <= 16 ? launch_wide<2, Out>(a, st)
-         : rows <= 24 ? launch_wide<3, Out>(a, st)
-                      : launch_wide<4, Out>(a, st);
+  int64_t rows = a.P;
+  if (a.ids) {
+    const int64_t weights = std::min(a.P, a.E), likely = a.K > 1024 ? 2 * a.P : 3 * a.P;
+    rows = (likely + 2 * weights - 1) / (2 * weights);
+  }
+  const int64_t passes = (rows + 31) / 32, columns = (rows + passes - 1) / passes;
+  return rows <= 8       ? launch_narrow<Out>(a, st)
+         : columns <= 16 ? launch_wide<2, Out>(a, st)
+         : columns <= 24 ? launch_wide<3, Out>(a, st)
+                         : launch_wide<4, Out>(a, st);
 }
 
 }  // namespace

@@ -121,8 +121,9 @@ def test_gemv_a_hot_expert_among_many(api, hot, T, k, E):
         check_gemv(api, x, W, sW, alpha, w, ids.cuda(), api.NVFP4_OUT_DTYPE_FP32)
 
 
-@pytest.mark.parametrize("T,k,E,K", [(20, 2, 4, 448), (36, 1, 4, 64), (30, 2, 5, 1024), (45, 1, 3, 320), (64, 2, 8, 128), (90, 1, 2, 192)])
-def test_gemv_nine_to_45_rows_of_each_expert(api, T, k, E, K):
+@pytest.mark.parametrize("T,k,E,K", [(20, 2, 4, 448), (36, 1, 4, 64), (30, 2, 5, 1024), (45, 1, 3, 320), (64, 2, 8, 128), (90, 1, 2, 192),
+                                      (14, 1, 2, 1152), (16, 2, 2, 1152), (40, 1, 2, 1088), (60, 1, 2, 1088), (150, 1, 3, 1088)])
+def test_gemv_7_to_50_rows_of_each_expert(api, T, k, E, K):
     W, sW, alpha, w = random_weight(E, 256, K, seed=E + K)
     ids = choices(T, k, E, seed=T, none=0.05).cuda()
     for rows in (T, T * k):
@@ -131,8 +132,8 @@ def test_gemv_nine_to_45_rows_of_each_expert(api, T, k, E, K):
         check_gemv(api, x, W, sW, alpha, w, ids, api.NVFP4_OUT_DTYPE_BF16)
 
 
-@pytest.mark.parametrize("P", [25, 31, 32])
+@pytest.mark.parametrize("P", [25, 31, 32, 40, 65, 72, 100])
 @pytest.mark.parametrize("N,K", [(128, 64), (128, 14336), (4096, 1088)])
-def test_gemv_25_to_32_rows(api, P, N, K):
+def test_gemv_25_rows_and_more(api, P, N, K):
     W, sW, alpha, w = random_weight(1, N, K, seed=N + K)
     check_gemv(api, rows_of(P, K, seed=P), W, sW, alpha, w, None, api.NVFP4_OUT_DTYPE_FP32)
