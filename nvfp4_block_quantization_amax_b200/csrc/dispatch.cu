@@ -217,11 +217,20 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowArgs a, 
 
 // Few pairs: every CTA counts for itself where its tokens' rows go (the pairs
 // with a lower expert and the earlier ones with the same), one warp per pair,
-// and copies them; the experts' offsets are shared out over all warps.  The work
-// grows with the square of the pairs: against the sort and the copy, 8 choices
-// of 256 experts, C = 4096, us: 64 tokens 3.7 / 7.6, 256 5.8 / 10.5, 512 11.3 /
-// 12.9, 1024 32.8 / 18.5.
-constexpr int kFewPairs = 4096;
+// and copies them; the experts' offsets are shared out over all warps.  What it
+// costs is the rounds that a CTA makes (a token at a time, eight choices at a
+// time) over all pairs, against the sort and the copy.  C = 4096, 64 experts,
+// us for rounds x pairs:
+//   1 choice    1024 tokens  4 x 1024   6.0 /  8.8   1536  6 x 1536   9.2 /  9.4
+//               2048         7 x 2048  11.3 / 10.0   4096 14 x 4096  28.0 / 13.4
+//   2 choices   1024         4 x 2048   9.2 /  9.8   1500  6 x 3000  15.9 / 11.0
+//   4 choices    512         2 x 2048   6.7 /  9.8    750  3 x 3000  11.3 / 11.1
+//   6 choices    500         2 x 3000   9.5 / 10.7    682  3 x 4092  14.5 / 11.9
+//   8 choices    256         1 x 2048   5.6 /  9.2    512  2 x 4096  11.3 / 12.4
+//  16 choices    256         2 x 4096  11.6 / 11.8
+//  32 choices     64         4 x 2048  10.4 / 12.0    128  4 x 4096  15.1 / 12.3
+constexpr int kFewPairs = 4096;                      // shared memory
+constexpr int64_t kFewWork = 9 * 1024;               // rounds x pairs
 constexpr int kFewThreads = 256;
 
 __global__ void __launch_bounds__(kFewThreads) dispatch_few_kernel(const RowArgs a, const int32_t* __restrict__ ids, int E,
@@ -403,9 +412,10 @@ cudaError_t sort_launch(const RowArgs& a, const int32_t* ids, int64_t P, int64_t
 // Without rows to copy (in null) only the places and offsets.
 cudaError_t dispatch_launch(const RowArgs& a, const int32_t* ids, int64_t E, int32_t* offsets, int32_t* rows, cudaStream_t st) {
   const int64_t P = a.T * a.k;
-  if (P <= kFewPairs) {
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(a.T, 32), 2 * sm_count()));
+  const int64_t rounds = (a.T + grid - 1) / grid * ((a.k + kFewThreads / 32 - 1) / (kFewThreads / 32));
+  if (P <= kFewPairs && rounds * P <= kFewWork) {
     note_launch();
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(a.T, 32), 2 * sm_count()));
     return launch_k(dispatch_few_kernel, dim3(grid), dim3(kFewThreads), 0, st, 1, a, ids, static_cast<int>(E), offsets, rows);
   }
   const cudaError_t e = E <= 64    ? sort_launch<6>(a, ids, P, E, offsets, rows, st)

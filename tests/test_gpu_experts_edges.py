@@ -107,6 +107,31 @@ def test_dispatch_from_two_host_threads(api):
     assert not failures, failures
 
 
+@pytest.mark.parametrize("T,k,E", [(1, 1, 5), (300, 1, 7), (1024, 1, 256), (1023, 2, 16), (2048, 2, 64), (4096, 1, 128), (4095, 1, 1000),
+                                   (1365, 3, 8), (4097, 1, 60)])
+def test_dispatch_one_or_two_choices(api, T, k, E):
+    ids = choices(T, k, E, seed=T, none=0.05)
+    x = rows_of(T, 72, seed=T)
+    xs, rows, offsets = api.nvfp4_dispatch(x, ids.cuda(), E)
+    want_rows, want_offsets = sort_reference(ids, E)
+    assert torch.equal(rows.cpu(), want_rows) and torch.equal(offsets.cpu(), want_offsets)
+    live = (want_rows.view(-1) >= 0).cuda()
+    assert torch.equal(xs[want_rows.view(-1).cuda()[live].long()], x.repeat_interleave(k, 0)[live])
+
+
+@pytest.mark.parametrize("T,k,launches", [(64, 8, 1), (512, 8, 1), (1024, 1, 1), (1024, 2, 1), (2048, 1, 2), (4096, 1, 2), (2048, 2, 2),
+                                          (1024, 4, 2), (682, 6, 2), (128, 32, 2), (700, 8, 2), (1, 32, 1)])
+def test_dispatch_goes_by_rounds_and_pairs(api, T, k, launches):
+    """One launch where its count is the cheaper one, else sort and copy."""
+    from nvfp4_block_quantization_amax_b200 import _lib
+    if torch.cuda.get_device_properties(0).multi_processor_count != 148:
+        pytest.skip("the sizes are those of 148 SMs")
+    ids, x = choices(T, k, 64, seed=T).cuda(), rows_of(T, 64, seed=T)
+    before = _lib.nvfp4_launch_count()
+    api.nvfp4_dispatch(x, ids, 64)
+    assert _lib.nvfp4_launch_count() - before == launches
+
+
 # ---------------------------------------------------------------------------
 # few-row products
 # ---------------------------------------------------------------------------
