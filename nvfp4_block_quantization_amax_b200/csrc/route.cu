@@ -598,14 +598,20 @@ __global__ void __launch_bounds__(kWarps * 32, kRouteCtas<V>) route_kernel(const
     }
   }
 }
-// error_of.  ex2.approx and rcp.approx are off by 2^-22 and 2^-23 relative;
-// the exponent's rounding (of the product and of log2 e) makes that
-// 1.5 |z| 2^-24 more.  sigmoid: s (1 - s) (2^-22 + 1.5 |z| 2^-24) + 1.5 s 2^-23
-// with s (1 - s) <= 1/4 and s (1 - s) |z| <= 0.23 is below 4.4 x 2^-24.  softmax
-// with d = z - max: exp(-d) d <= 0.37 of the largest share, and the row's sum
-// is off by (mean d + 1) 2^-22 <= (ln 1024 + 1) 2^-22 relative: below 2^-19 of
-// the largest share.  c's own rounding: 2^-24 |c|.  The keys drop log2 V bits of
-// c: 2^-23 V |c| more.  A sum of two is rounded by 2^-24 of up to 2 |c|.
+// error_of, in u = 2^-24, half a step of 32 bits.  ex2.approx is off by 4 u,
+// rcp.approx by 2 u, both relative.
+//   sigmoid: log2 e and its product with z are rounded, 1.25 |z| u relative to
+// exp(-z), which reaches s with the factor 1 - s; 1 + exp(-z) and its reciprocal
+// add 3 u s.  s (1 - s) <= 1/4 and s (1 - s) |z| <= 0.23 make that less than
+// 4.4 u; the code takes 6.
+//   softmax, d = max - z: d is rounded too, so exp(-d) is off by (4 + 2.25 d) u
+// relative, that is by at most 4 u of the largest score's (at d = 0).  What all
+// scores of a row share comes on top: the sum's terms, 4 + 2.25 times their mean
+// d, which is at most ln 1024 (the entropy less the sum's logarithm); its
+// additions, 31 in a lane and 5 across them; the reciprocal, 2.  In all
+// 4 + (4 + 15.6) + 36 + 2 < 62 u of the largest score; the code takes 64.
+//   c is rounded once more, u |c|.  The keys drop log2 V bits of c: 2 V u |c|.
+// A sum of two is rounded by u of up to 2 |c|.
 
 // ---------------------------------------------------------------------------
 // Many rows.  What a row costs beyond its values (reductions, rounds, the
