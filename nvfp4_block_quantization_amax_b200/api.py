@@ -696,6 +696,12 @@ def _new(rows: int, cols: int, dtype, device) -> torch.Tensor:
     return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
+def _within(v: int, most: int, what: str):
+    """Raise unless 1 <= v <= most: a size of tensors that are yet to be made."""
+    if not 1 <= v <= most:
+        raise NVFP4Error(L.NVFP4_ERR_SHAPE, what)
+
+
 def _elsewhere(device) -> bool:
     """Whether `device`, a GPU, is not the current one."""
     return (_current_device or torch.cuda.current_device)() != device.index
@@ -756,6 +762,7 @@ def nvfp4_route(logits: torch.Tensor, k: int, score: int = NVFP4_ROUTE_SOFTMAX, 
         with torch.cuda.device(dev):
             return nvfp4_route(logits, k, score, flags, bias, groups, groups_kept, scale, ids, weights, status)
     T, E = logits.shape
+    _within(k, 32, "nvfp4_route")
     if bias is not None:
         _need(bias, E, torch.float32, "bias", dev)
     if ids is not None:
@@ -834,6 +841,7 @@ def nvfp4_dispatch(x: Optional[torch.Tensor], ids: torch.Tensor, E: int, out: Op
         with torch.cuda.device(dev):
             return nvfp4_dispatch(x, ids, E, out, rows, offsets, status)
     T, k = _pairs(ids, torch.int32, "ids", dev)
+    _within(E, 1024, "nvfp4_dispatch")
     C = ldx = ldo = 8
     if x is not None:
         if x.dim() != 2:
@@ -853,7 +861,7 @@ def nvfp4_dispatch(x: Optional[torch.Tensor], ids: torch.Tensor, E: int, out: Op
     if rows is None:
         rows = torch.empty_like(ids)
     if offsets is None:
-        offsets = torch.empty_strided((max(E, 0) + 1,), (1,), dtype=torch.int32, device=dev)
+        offsets = torch.empty_strided((E + 1,), (1,), dtype=torch.int32, device=dev)
     if x is not None and out is None:
         out = _new(T * k, C, torch.bfloat16, dev)
     st = (L._lib or L.load()).nvfp4_dispatch(
@@ -990,6 +998,8 @@ def nvfp4_gemv(x: torch.Tensor, W: torch.Tensor, sW: torch.Tensor, alphaW: torch
             rep = k
         elif X != P:
             raise ValueError(f"x: {X} rows, need {T} or {P}")
+    if P:
+        _within(P, 1024, "nvfp4_gemv")
     ldx = _rows(x, X, K, "x", dev)
     _need(W, E * N * (K // 2), torch.uint8, "W", dev)
     _need(sW, E * N * (K // 16), torch.uint8, "sW", dev)

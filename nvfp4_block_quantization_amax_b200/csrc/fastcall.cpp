@@ -333,6 +333,7 @@ PyObject* gemv(Call& c) {
     if (X == ids->size(0)) rep = ids->size(1);
     else if (X != P) return decline();
   }
+  if (P > 1024) return decline();   // before its results are allocated
   const at::Tensor* sW = c.flat(2, at::kByte, E * N * (K / 16));
   const at::Tensor* alpha = c.flat(3, kFloat, E);
   const at::ScalarType type = kind == NVFP4_OUT_DTYPE_FP32 ? kFloat : kBF16;

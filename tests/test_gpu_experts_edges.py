@@ -162,3 +162,25 @@ def test_gemv_7_to_50_rows_of_each_expert(api, T, k, E, K):
 def test_gemv_25_rows_and_more(api, P, N, K):
     W, sW, alpha, w = random_weight(1, N, K, seed=N + K)
     check_gemv(api, rows_of(P, K, seed=P), W, sW, alpha, w, None, api.NVFP4_OUT_DTYPE_FP32)
+
+
+# ---------------------------------------------------------------------------
+# refusals
+# ---------------------------------------------------------------------------
+def test_sizes_are_refused_before_results_of_them_are_allocated(api):
+    """Host-side refusals: nothing is launched, and no memory asked for."""
+    z = torch.zeros((64, 64), device="cuda")
+    ids = torch.zeros((1 << 16, 32), dtype=torch.int32, device="cuda")
+    W, sW, alpha, _ = random_weight(1, 128, 64, seed=1)
+    x = torch.zeros((1 << 16, 64), dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    used = torch.cuda.memory_allocated()
+    for call in [lambda k=k: api.nvfp4_route(z, k) for k in (-1, 0, 33, 1 << 33, 1 << 70)] + \
+                [lambda E=E: api.nvfp4_dispatch(None, ids[:8], E) for E in (-5, 0, 1025, 1 << 40, 1 << 70)] + \
+                [lambda: api.nvfp4_gemv(x, W[0], sW[0], alpha), lambda: api.nvfp4_gemv(x, W, sW, alpha, ids=ids),
+                 lambda: api.nvfp4_gemv(x[:1025], W, sW, alpha, ids=ids[:1025, :1].contiguous())]:
+        with pytest.raises(api.NVFP4Error) as e:
+            call()
+        assert e.value.status == -2
+    assert torch.cuda.max_memory_allocated() - used < 1 << 20
