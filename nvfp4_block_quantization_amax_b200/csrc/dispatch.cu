@@ -28,6 +28,7 @@
 
 #include "launch.cuh"
 #include "nvfp4_internal.h"
+#include "smem.cuh"
 
 namespace cg = cooperative_groups;
 
