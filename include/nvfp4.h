@@ -610,7 +610,8 @@ NVFP4_API nvfp4_status_t nvfp4_combine_backward(const void* dout, int64_t lddo, 
  * read its row, 1 where each pair has its own.  ids NULL: E = 1 and every row
  * takes the one weight.  W: codes [E, N, K/2] and sW: scales in the GEMM layout
  * of E N rows, alphaW: E floats, as nvfp4_gemm_grouped takes them (E = 1: as
- * nvfp4_gemm does).  Products are exact and summed in fp32; out is bf16 or
+ * nvfp4_gemm does); scale bytes are 0 .. 0x7E, as the quantizers write them for
+ * finite input.  Products are exact and summed in fp32; out is bf16 or
  * fp32 with row stride ldo.  A pair of -1 gets zeros, an id outside -1 .. E - 1
  * sets NVFP4_ERR_ARG and does too.  A weight is read once for each 8 to 32 rows
  * that take it (by P, E and K).  0 <= P <= 1024 (more rows: nvfp4_gemm,

@@ -663,10 +663,10 @@ def nvfp4_lora_backward(dy: torch.Tensor, x: torch.Tensor, h: torch.Tensor, A: t
 # ---------------------------------------------------------------------------
 # Around the experts' products: routing, sorting rows by expert, the way back,
 # and products of a few unquantized rows.  Their small calls are as long as
-# their host path: new tensors come from empty_like (1.3 us) and empty_strided
-# (1.5 us; torch.empty 2.3 us), tensors on another device than the current one
-# take a second call under that device instead of a context around the first,
-# and the library's functions are called without the names in _lib between.
+# their host path, so each goes to C++ first (csrc/fastcall.cpp: 4 to 5 us a
+# call).  What that declines, and every call where it is not built, goes through
+# the checks below it: they say what is wrong, or make the call (9 to 11 us).
+# Tensors on another device than the current one take a second call under it.
 # ---------------------------------------------------------------------------
 _SMALL = ("route", "route_backward", "dispatch", "combine", "combine_backward", "gemv")
 _fast = None
@@ -775,7 +775,7 @@ def nvfp4_route(logits: torch.Tensor, k: int, score: int = NVFP4_ROUTE_SOFTMAX, 
         ids = _new(T, k, torch.int32, dev)
     if weights is None:
         weights = torch.empty_like(ids, dtype=torch.float32)
-    st = (L._lib or L.load()).nvfp4_route(
+    st = L.nvfp4_route(
         logits.data_ptr(), ldl, kind, _p(bias), T, E, k, groups, groups_kept, score, flags, scale, ids.data_ptr(),
         weights.data_ptr(), _p(status), _stream_of(dev))
     if st:
@@ -813,7 +813,7 @@ def nvfp4_route_backward(dweights: torch.Tensor, ids: torch.Tensor, logits: torc
         _check_status(status, dev)
     if out is None:
         out = torch.empty_like(logits) if logits.is_contiguous() else _new(T, E, logits.dtype, dev)
-    st = (L._lib or L.load()).nvfp4_route_backward(
+    st = L.nvfp4_route_backward(
         dweights.data_ptr(), ids.data_ptr(), logits.data_ptr(), ldl, kind, T, E, shape[1], score, flags, scale,
         out.data_ptr(), ldd, _p(status), _stream_of(dev))
     if st:
@@ -864,7 +864,7 @@ def nvfp4_dispatch(x: Optional[torch.Tensor], ids: torch.Tensor, E: int, out: Op
         offsets = torch.empty_strided((E + 1,), (1,), dtype=torch.int32, device=dev)
     if x is not None and out is None:
         out = _new(T * k, C, torch.bfloat16, dev)
-    st = (L._lib or L.load()).nvfp4_dispatch(
+    st = L.nvfp4_dispatch(
         _p(x), ldx, ids.data_ptr(), T, k, E, C, _p(out), ldo, offsets.data_ptr(), rows.data_ptr(), _p(status),
         _stream_of(dev))
     if st:
@@ -916,7 +916,7 @@ def nvfp4_combine(y: torch.Tensor, rows: Optional[torch.Tensor], weights: Option
             out = torch.empty_like(residual)
         else:
             out = _new(T, C, torch.bfloat16, dev)
-    st = (L._lib or L.load()).nvfp4_combine(
+    st = L.nvfp4_combine(
         y.data_ptr(), ldy, R, _p(rows), _p(weights), T, k, C, _p(residual), ldr, out.data_ptr(), ldo, _p(status),
         _stream_of(dev))
     if st:
@@ -958,7 +958,7 @@ def nvfp4_combine_backward(dout: torch.Tensor, rows: Optional[torch.Tensor], wei
     if need_dy and out is None:
         out = _new(R, C, torch.bfloat16, dev)
     dw = _new(shape[0], shape[1], torch.float32, dev) if need_dweights else None
-    st = (L._lib or L.load()).nvfp4_combine_backward(
+    st = L.nvfp4_combine_backward(
         dout.data_ptr(), lddo, y.data_ptr(), ldy, R, _p(rows), _p(weights), T, shape[1], C, _p(out), lddy, _p(dw),
         _p(status), _stream_of(dev))
     if st:
@@ -1014,7 +1014,7 @@ def nvfp4_gemv(x: torch.Tensor, W: torch.Tensor, sW: torch.Tensor, alphaW: torch
         _need_matrix(out, P, N, dt, "out", dev)
         if P > 1:
             ldo = out.stride(0)
-    st = (L._lib or L.load()).nvfp4_gemv(
+    st = L.nvfp4_gemv(
         x.data_ptr(), ldx, _p(ids), P, rep or 1, W.data_ptr(), sW.data_ptr(), alphaW.data_ptr(), E, N, K, out.data_ptr(),
         out_dtype, ldo, _p(status), _stream_of(dev))
     if st:

@@ -17,7 +17,7 @@
 // 16384 tokens, 8 choices, C = 4096, and what memory alone takes at the measured
 // rate, us: copying 198 (185: 5.98 TB/s, 1.07 GB of it written), the sort in
 // front of it 16; combine, 6 choices, 16301 tokens 158 (143: 5.6 to 5.9 TB/s);
-// backward 403 (349: 5.96 TB/s, half read, half written).  64 tokens: 4.1 and 4.9,
+// backward 403 (349: 5.96 TB/s, half read, half written).  64 tokens: 3.8 and 5.1,
 // a launch and two or three dependent loads.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>

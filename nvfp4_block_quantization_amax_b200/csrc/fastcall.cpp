@@ -12,7 +12,8 @@
 //   None         something is not as expected (a type, a shape, a device that
 //                is not the current one, no tokens): nothing was done, and
 //                api.py's own checks say what is wrong or make the call.
-// So every condition here is at least as strict as api.py's.
+// So every condition here is at least as strict as api.py's, which makes all the
+// calls where this file is not built for the torch and the Python at hand.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -186,11 +186,13 @@ __device__ __forceinline__ void clear_rows(const GemvArgs& a, Out* out, int me, 
 // warps share out K.  Weights stream through a ring of shared memory that every
 // thread fills for itself, across the items' borders, so that no item waits for
 // memory from its beginning.
-// 14336 x 4096, one row: 14.1 us, 2.4 TB/s (weights from memory; 5.05 us at the
-// measured rate).  8 weights of that size, 16 rows: 59 to 67 us, 4.0 to 4.5 TB/s.
-// What bounds it: unpacking, 19 cycles of the logic and multiply pipes per 8
-// codes and warp, 63% busy; next to it the item borders (one CTA's warps meet)
-// and, for one row, 448 items on 444 CTAs.  Two copies of the warps' sums and
+// 14336 x 4096, one row: 14.2 us, 2.3 TB/s (weights from memory; 5.05 us at the
+// measured rate).  8 weights of that size, 16 rows: 57 to 66 us, 4.0 to 4.7 TB/s.
+// What bounds the larger: instructions (issue 70% of the active cycles), of them
+// unpacking, 19 cycles of the logic and multiply pipes per 8 codes and warp (59%
+// and 52% busy), and the item borders (one CTA's warps meet).  One row is bound by
+// its start, its end and its balance: 448 items on 444 CTAs, an SM active 21
+// thousand cycles on average, 27 at most, of 32; the logic pipe is 35% busy.  Two copies of the warps' sums and
 // one barrier less: 70 us (less L1 for x); two CTAs per SM with a deeper ring:
 // 15.8 and 68; four CTAs: 15.3 and 84; x a word ahead: 15.0 and 68.
 // ---------------------------------------------------------------------------

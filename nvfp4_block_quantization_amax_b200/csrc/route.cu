@@ -12,12 +12,20 @@
 // The order is that of the values in 64 bits, so that equal results come from
 // any machine that computes them so.  It is found on values in 32 bits with a
 // bound of their error (error_of); rows in which that bound does not part the
-// choices, about one in a thousand, are looked at in 64 bits.
+// choices are looked at in 64 bits.  How many those are goes by the values: with
+// a bias, or without bias and groups, one in a hundred to one in a thousand;
+// softmax or sigmoid scores in groups without a bias have more the farther the
+// logits are apart, since the bound goes by the largest score: 32768 tokens, 160
+// experts, softmax, 3 of 8 groups, logits of standard deviation 1.5 / 3 / 5 / 8:
+// 46 / 46 / 73 / 103 us (bf16), 34 / 41 / 59 / 108 (fp32); 256 experts, sigmoid, 4
+// of 8 groups of pairs 36 / 36 / 70 / 170, with a bias 34 / 36 / 32 / 35.
 //
 // What bounds the choice is its instructions, not memory: of 32768 tokens of 256
-// experts (sigmoid, bias, 4 of 8 groups, 8 choices) 36 us, 518 warp
-// instructions per token at half the issue rate; the logits alone are 5.1 us at
-// the measured rate, the same without bias and groups 18 us.  The gradient is
+// experts (sigmoid, bias, 4 of 8 groups, 8 choices) 36 us (34 to 38 with the
+// rows that are in doubt), 528 warp instructions per token at half the issue
+// rate, and an end at which few warps still finish such rows (an SM is active
+// 56 thousand cycles on average, 98 at most); the logits alone are 5.1 us at the
+// measured rate, the same without bias and groups 18 to 20 us.  The gradient is
 // bound by its launch and its zeros: 11.6 us for the same sizes (5.6).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -895,6 +903,10 @@ cudaError_t route_many_launch_v(const RouteArgs& a, cudaStream_t st) {
 // 4.7 / 4.5, 32768 tokens 24 / 8.5 and 37 / 16; 256 experts, 512 tokens 3.1 / 4.0
 // and 4.5 / 8.0, 2048 3.7 / 3.9 and 7.8 / 8.2, 4096 5.1 / 4.7 and 13.7 / 11.3, 32768
 // 27 / 18 and 52 / 36; 512 experts, 32768 tokens 46 / 36 and 77 / 95 (not built).
+// One bound for all sizes, which gives away up to 0.4 us at 256 experts.  Up to 32
+// experts a row is one value per lane: 32768 tokens of 8, 16 and 32 experts take
+// 13.4, 13.4 and 16.4 us (eight lanes a row: not built); more than 8 choices or
+// groups stay on the first kernel as well.
 constexpr int64_t kManyRows = 2048;
 
 template <typename Z, int V>
