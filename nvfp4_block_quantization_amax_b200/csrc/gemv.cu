@@ -193,9 +193,9 @@ __device__ __forceinline__ void clear_rows(const GemvArgs& a, Out* out, int me, 
 // and 52% busy), and the item borders (one CTA's warps meet).  One row is bound by
 // its start, its end and its balance: 448 items on 444 CTAs, an SM active 21
 // thousand cycles on average, 27 at most, of 32; the logic pipe is 35% busy.  Two
-// copies of the warps' sums and
-// one barrier less: 70 us (less L1 for x); two CTAs per SM with a deeper ring:
-// 15.8 and 68; four CTAs: 15.3 and 84; x a word ahead: 15.0 and 68.
+// copies of the warps' sums and one barrier less: 70 us (less L1 for x); two CTAs
+// per SM with a deeper ring: 15.8 and 68; four CTAs: 15.3 and 84; x a word ahead:
+// 15.0 and 68.
 // ---------------------------------------------------------------------------
 constexpr int kDepth = 2;   // chunks of a lane on their way and in use
 constexpr int kCtas = 3;    // per SM

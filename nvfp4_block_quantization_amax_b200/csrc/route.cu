@@ -13,11 +13,12 @@
 // any machine that computes them so.  It is found on values in 32 bits with a
 // bound of their error (error_of); rows in which that bound does not part the
 // choices are looked at in 64 bits.  How many those are goes by the values: with
-// a bias, or without bias and groups, mostly below one in a hundred; softmax or sigmoid scores in groups without a bias have more the farther the
-// logits are apart, since the bound goes by the largest score: 32768 tokens, 160
-// experts, softmax, 3 of 8 groups, logits of standard deviation 1.5 / 3 / 5 / 8:
-// 46 / 46 / 73 / 103 us (bf16), 34 / 41 / 59 / 108 (fp32); 256 experts, sigmoid, 4
-// of 8 groups of pairs 36 / 36 / 70 / 170, with a bias 34 / 36 / 32 / 35.
+// a bias, or without bias and groups, mostly below one in a hundred; scores in
+// groups without a bias have more the farther the logits are apart, since the
+// bound goes by the largest score: 32768 tokens, logits of standard deviation 1.5
+// / 3 / 5 / 8: 160 experts, softmax, 3 of 8 groups 46 / 46 / 73 / 103 us (bf16), 34
+// / 41 / 59 / 108 (fp32); 256 experts, sigmoid, 4 of 8 groups of pairs 36 / 36 / 70
+// / 170, with a bias 34 / 36 / 32 / 35.
 //
 // What bounds the choice is its instructions, not memory: of 32768 tokens of 256
 // experts (sigmoid, bias, 4 of 8 groups, 8 choices) 36 us (34 to 38 with the
